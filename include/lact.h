@@ -287,6 +287,177 @@ lact_status lact_layer_forward_noalloc(const lact_problem* p, const void* q, con
                                        float* W3, float* M1, float* M2, float* M3, void* o,
                                        void* stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Operators of a block around the fast-weight layer: window attention, rotary
+ * positions, and the residual stream's addition and norm.  They follow the
+ * conventions above (device pointers, validation before any device work,
+ * asynchronous on `stream`, nothing allocated or kept, LACT_ERR_HIP leaves
+ * the outputs undefined), with these of their own: all work runs on `stream`
+ * itself, so that calls with workspaces of their own may overlap; every call
+ * may be captured into a HIP graph; results are bitwise reproducible.
+ *
+ * A [batch, heads, tokens, d] tensor is a pointer and its strides in
+ * elements, d contiguous: head-major memory, token-major memory and slices of
+ * a joint projection alike.
+ */
+typedef struct {
+    int64_t batch, head, token;   /* elements; that of a dimension of size <= 1 is not looked at */
+} lact_strides;
+
+/*
+ * Window attention ("LaCT架构核心思想解析" §1.1 and "大块测试时训练（LaCT）技术解析"
+ * §2.1: the causal sliding-window branch beside the fast-weight layer) with
+ * first tokens that stay visible.  Row r < q_len[b] of sequence b stands at
+ * position p = k_len[b] - q_len[b] + r and sees the keys j with
+ *
+ *     0 <= j <= p  and  (j > p - window or j < sinks),      window = 0: j <= p
+ *
+ *     s_j = scale q_r . k_j,  lse_r = log sum_j exp(s_j),  o_r = sum_j exp(s_j - lse_r) v_j
+ *
+ * so that with q_len = k_len it is a whole sequence's causal attention, and
+ * with few rows the next tokens' over a cache.  A row that sees nothing
+ * (p < 0) gets o = 0 and lse = -infinity.  Query head h reads key head
+ * h / (heads / kv_heads).
+ */
+typedef struct {
+    int32_t batch;      /* >= 0 */
+    int32_t heads;      /* query heads, a multiple of kv_heads */
+    int32_t kv_heads;   /* >= 1 */
+    int32_t d;          /* width of a head: a multiple of 8 in [8, 128] */
+    int32_t io_dtype;   /* lact_dtype of q, k, v, o and their gradients */
+    float scale;        /* finite, > 0 */
+    int64_t q_len;      /* rows of q and o, 0 <= q_len < 2^30 */
+    int64_t k_len;      /* rows of k and v, 0 <= k_len < 2^30 */
+    int64_t window;     /* >= 0; 0: no limit */
+    int64_t sinks;      /* >= 0 */
+} lact_attention;
+
+/*
+ * q, o [batch, heads, q_len, d], k, v [batch, kv_heads, k_len, d]: 16-byte
+ * aligned, strides multiples of 16 bytes, inputs' strides >= 0 (0 repeats a
+ * row, head or sequence), outputs' rows distinct.  q_lens, k_lens: device
+ * arrays [batch] of each sequence's rows and keys (clamped to q_len and k_len), NULL: all.
+ * Rows of o and lse behind a sequence's q_lens are left as they were; q, k
+ * and v behind the lengths are not read.  A NaN or infinity in k or v reaches
+ * only rows that see it.  lse [batch, heads, q_len] float32, or NULL.
+ * ws: lact_window_attention_workspace_size bytes, 256-B aligned (may be NULL
+ * where that is 0).  o must not overlap an input.
+ */
+size_t lact_window_attention_workspace_size(const lact_attention* p);
+lact_status lact_window_attention_forward(const lact_attention* p, const void* q, const lact_strides* sq,
+                                          const void* k, const lact_strides* sk, const void* v,
+                                          const lact_strides* sv, const int64_t* q_lens,
+                                          const int64_t* k_lens, void* o, const lact_strides* so,
+                                          float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Gradients of sum(dO * o) with respect to q, k, v, from the forward's o and
+ * lse (lse's own gradient is zero).  dq, dk, dv in io_dtype, shapes of q, k,
+ * v, fully written: zero behind the lengths.  Sums are held in float32 and
+ * rounded once; a key head's gradient is the sum over its query heads.  dO
+ * behind q_lens is not read.  Non-finite inputs give non-finite gradients to
+ * what they reach.
+ */
+size_t lact_window_attention_backward_workspace_size(const lact_attention* p);
+lact_status lact_window_attention_backward(const lact_attention* p, const void* q, const lact_strides* sq,
+                                           const void* k, const lact_strides* sk, const void* v,
+                                           const lact_strides* sv, const int64_t* q_lens,
+                                           const int64_t* k_lens, const void* o, const lact_strides* so,
+                                           const float* lse, const void* dO, const lact_strides* sdo,
+                                           void* dq, const lact_strides* sdq, void* dk,
+                                           const lact_strides* sdk, void* dv, const lact_strides* sdv,
+                                           void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Rotary positions.  Features (i, i + pairs) of a head -- or (2i, 2i + 1)
+ * with interleaved -- for i < pairs turn by the angle position * freqs[i]:
+ *     (x, y) -> mscale (x cos - y sin, x sin + y cos)
+ * and the features from 2 pairs on are copied.  LACT_ROTARY_INVERSE turns the
+ * other way: with the same mscale, the gradient's way back.
+ */
+#define LACT_ROTARY_INTERLEAVED 1u
+#define LACT_ROTARY_INVERSE 2u
+typedef struct {
+    int32_t batch, heads, kv_heads;   /* kv_heads = 0: q alone */
+    int32_t d;                        /* width of a head, 1..8192 */
+    int32_t pairs;                    /* 0 <= 2 pairs <= d, pairs <= 2048 */
+    int32_t io_dtype;
+    uint32_t flags;                   /* LACT_ROTARY_* */
+    float mscale;
+    int64_t tokens;                   /* 0 <= tokens < 2^30 */
+    int64_t start;                    /* position of token 0 where positions is NULL */
+} lact_rotary_problem;
+
+/*
+ * q, q_out [batch, heads, tokens, d], k, k_out [batch, kv_heads, tokens, d],
+ * aligned to their elements; q_out may be q itself and k_out k (with the same
+ * strides), and must not overlap an input otherwise.  freqs: device float64
+ * [pairs].  positions: device int64 [batch, tokens] contiguous, or NULL:
+ * start + token.  The angle is formed and reduced to a turn in float64.
+ */
+lact_status lact_rotary(const lact_rotary_problem* p, const void* q, const lact_strides* sq, const void* k,
+                        const lact_strides* sk, const double* freqs, const int64_t* positions, void* q_out,
+                        const lact_strides* sqo, void* k_out, const lact_strides* sko, void* stream);
+
+/* Frequencies of `pairs` pairs on the host, freqs[i] = base^(-i / pairs) and
+ * then, for contexts `factor` times the original `context` tokens:
+ *   LACT_ROTARY_PLAIN   as they are;
+ *   LACT_ROTARY_LINEAR  all divided by factor;
+ *   LACT_ROTARY_NTK     the base raised so that the last one is divided by
+ *                       factor: base * factor^(pairs / (pairs - 1));
+ *   LACT_ROTARY_YARN    divided by factor where a pair turns less than `slow`
+ *                       times within the original context, kept where it
+ *                       turns more than `fast` times, and between the two
+ *                       blended linearly in the number of turns; *mscale is
+ *                       0.1 ln(factor) + 1 (1 for the others).
+ * mscale may be NULL. */
+#define LACT_ROTARY_PLAIN 0
+#define LACT_ROTARY_LINEAR 1
+#define LACT_ROTARY_NTK 2
+#define LACT_ROTARY_YARN 3
+lact_status lact_rotary_frequencies(int32_t pairs, double base, int32_t scaling, double factor, int64_t context,
+                                    double slow, double fast, double* freqs, float* mscale);
+
+/*
+ * Residual addition and root-mean-square norm of rows of `cols` values:
+ *     h = x + residual,   y = h weight / sqrt(mean(h^2) + eps).
+ * The norm takes the float32 sum; h is stored rounded to io_dtype.  y8 and
+ * scales: y in 8-bit floating point (e4m3, OCP), every group of 128 columns
+ * of a row divided by its own scale max(largest |y|, 2^-100) / 448.
+ */
+typedef struct {
+    int64_t rows;       /* >= 0 */
+    int32_t cols;       /* 1..32768 */
+    int32_t io_dtype;   /* lact_dtype of x, residual, h, y and the gradients but dw */
+    float eps;          /* finite, >= 0 */
+} lact_norm_problem;
+#define LACT_NORM_GROUP 128
+
+/*
+ * x, residual (NULL: none), h (may be NULL), y (NULL if y8 is given), y8
+ * (NULL: none) [rows, cols], each with its row stride in elements (>= cols;
+ * inputs also 0: one row for all), aligned to their elements; weight [cols]
+ * float32; scales [rows, ceil(cols / 128)] float32, with y8.  h and y may be
+ * x or residual themselves (same row stride), not partly overlap them.
+ */
+lact_status lact_add_rmsnorm_forward(const lact_norm_problem* p, const void* x, int64_t ldx, const void* residual,
+                                     int64_t ldr, const float* weight, void* h, int64_t ldh, void* y,
+                                     int64_t ldy, uint8_t* y8, int64_t ldy8, float* scales, void* stream);
+
+/*
+ * Gradients from the stored h: with f = 1 / sqrt(mean(h^2) + eps),
+ *     dx = f (weight dy - h f^2 mean(weight dy h)) + dh,   dw = sum over rows of dy h f.
+ * dx is the gradient of x and of residual alike; dh (NULL: none) is what
+ * reaches h from its other use; dx may be dy or dh itself (same row stride).
+ * dw [cols] float32, or NULL.  ws: lact_add_rmsnorm_backward_workspace_size
+ * bytes, 256-B aligned.
+ */
+size_t lact_add_rmsnorm_backward_workspace_size(const lact_norm_problem* p);
+lact_status lact_add_rmsnorm_backward(const lact_norm_problem* p, const void* h, int64_t ldh, const float* weight,
+                                      const void* dy, int64_t ldy, const void* dh, int64_t lddh, void* dx,
+                                      int64_t lddx, float* dw, void* ws, size_t ws_bytes, void* stream);
+
 /* Static text for a status code. */
 const char* lact_status_str(lact_status s);
 
@@ -318,7 +489,11 @@ const char* lact_last_error(void);
 #define LACT_K_BWD_ELEM 9  /* backward: elementwise, row and reduction kernels */
 #define LACT_K_NSRED 10    /* Newton-Schulz input: the sum of the split partials with its row
                               sums of squares (and, with momentum, the new momentum) */
-#define LACT_K_COUNT 11
+#define LACT_K_ATTN 11     /* window attention forward (the join of split keys included) */
+#define LACT_K_ATTN_BWD 12 /* window attention backward */
+#define LACT_K_ROTARY 13   /* rotary positions */
+#define LACT_K_NORM 14     /* add and norm, forward and backward */
+#define LACT_K_COUNT 15
 lact_status lact_timing_enable(int32_t kclass, int32_t on);
 lact_status lact_timing_read(int32_t kclass, double* total_ms, int64_t* launches);
 

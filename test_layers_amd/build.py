@@ -10,7 +10,7 @@ import time
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-SRC = os.path.join(PKG, "csrc", "lact.hip")
+SRC = os.path.join(PKG, "csrc", "liblact.hip")
 OUT = os.path.join(PKG, "liblact.so")
 
 HIPCC_FLAGS = [

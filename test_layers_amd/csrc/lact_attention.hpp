@@ -1,0 +1,831 @@
+// Sliding-window attention with sinks, forward and backward, on the 32x32
+// MFMA tiles of gfx950.
+//
+// Row r of a sequence stands at p = k_len - q_len + r and sees the keys
+// j <= p with j > p - window or j < sinks.  With s = scale q.k:
+//   lse = log sum_j exp(s_j),  o = sum_j exp(s_j - lse) v_j
+//   P = exp(s - lse), D = dO.o, dS = P (dO.v - D)
+//   dq = scale sum_j dS k_j,  dk_j = scale sum_r dS q_r,  dv_j = sum_r P dO_r.
+//
+// Layout trick all kernels share.  A product runs transposed, so that the
+// result's column -- the lane -- is the index that the next product keeps:
+// S^T = K Q^T leaves lane n with row n's scores of 16 of a block's 32 keys
+// (register r of lane half h holds key 8 (r/4) + 4 h + r%4).  The softmax is
+// then lane-local, and since the order of a contraction is free, registers
+// 8i .. 8i+7 already are a B operand of O^T = V^T P^T if the A operand reads
+// its keys in the same order: V^T comes out of LDS by two transposing 4-row
+// reads per fragment, and P never passes through LDS.  The backward's dK and
+// dV swap the roles of keys and rows.
+//
+// Numbers: scores, softmax statistics and all sums are fp32.  For bf16
+// tensors P and dS are rounded to bf16 once, as operands of their products
+// (half a step, 2^-9 of the value, against the same half step of the rounded
+// result); for fp32 tensors every product is an fp32 MFMA and nothing is
+// rounded.
+#pragma once
+#include "lact_direct.hpp"
+
+namespace lact {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float LN2 = 0.6931471805599453f;
+
+// byte strides of a [batch, heads, tokens, d] tensor with d contiguous
+struct AttnStride {
+  int64_t b, h, l;
+};
+
+struct AttnArgs {
+  const char *q, *k, *v, *o, *dO;
+  char *out, *dq, *dk, *dv;
+  AttnStride sq, sk, sv, so, sdo, sdq, sdk, sdv;
+  const int64_t *q_lens, *k_lens;  // device, or null: Lq, Lk
+  float* lse;                      // [B, H, Lq], or null (forward)
+  float* delta;                    // [B, H, Lq]: D = dO.o
+  float* part;                     // partial sums (few-row forward: O; backward: dK, dV of sink tiles)
+  float* part_ml;                  // few-row forward: running maximum and sum of each split
+  int32_t B, H, Hk, G;             // G = H / Hk query heads share a key head
+  int32_t d, Lq, Lk;
+  int32_t window, sinks;           // window: 1 << 30 where there is none
+  int32_t tiles;                   // row tiles (forward, dq), key tiles (dk, dv), per head
+  int32_t splits;                  // few-row forward: key splits; backward: row splits of a sink tile
+  int32_t sink_tiles, span;        // backward: key tiles with sinks; rows of one of their splits
+  float c;                         // scale * log2(e): exp(scale s) = exp2(c s)
+  float scale;
+};
+
+// ------------------------------------------------------------------ tiles
+// One LDS tile holds R rows of DP elements (DP = d rounded up to 64 or 128)
+// as 16-byte chunks.  Chunk c of row r lies in slot c ^ f(r): the 16-byte
+// reads of 16 consecutive rows then fall in 16 different slots, and for bf16
+// the transposing reads of 4 rows x 64 bytes in four different 64-byte groups.
+template <typename T, int DP>
+struct AttnTile {
+  static constexpr int CPR = DP * (int)sizeof(T) / 16;  // chunks per row
+  static constexpr int STEPS = CPR / 2;                 // chunk pairs: contraction steps of a row product
+  static constexpr int DB = DP / 32;                    // 32-wide blocks of d
+  __device__ static __forceinline__ int f(int r) {
+    if constexpr (sizeof(T) == 4) return r & 15;
+    else if constexpr (CPR == 16) return ((r & 3) << 2) | ((r >> 2) & 3);
+    else return (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
+  }
+  __device__ static __forceinline__ int at(int r, int c) { return (r * CPR + (c ^ f(r))) * 16; }
+
+  // Copies rows row0 .. row0 + R - 1 of a matrix (row stride in bytes) to the
+  // tile, by NW waves.  Rows outside 0 .. rmax and chunks behind the head's
+  // last are read from the nearest one inside: what lies there is masked, or
+  // meets a zero, by whoever uses the tile, and no memory outside is touched.
+  template <int R, int NW>
+  __device__ static __forceinline__ void stage(char* tile, const char* base, int64_t stride, int row0, int rmax,
+                                               int cmax, int wave, int lane) {
+    constexpr int N = R * CPR / (WAVE * NW);
+    static_assert(R * CPR % (WAVE * NW) == 0, "whole copies");
+    const uint32_t m0 = __builtin_amdgcn_readfirstlane(lds_off(tile) + (uint32_t)(wave * WAVE * 16));
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int s = (i * NW + wave) * WAVE + lane;
+      const int row = s / CPR, c = min((s % CPR) ^ f(row), cmax);
+      const int gr = max(0, min(row0 + row, rmax));
+      dma16(base + (int64_t)gr * stride + c * 16, m0 + (uint32_t)(i * NW * WAVE * 16));
+    }
+  }
+};
+
+// ------------------------------------------------------------------ products
+// A 16-byte chunk per lane is the unit of a row product's operand.  Lane l
+// supplies row l % 32 and chunk 2 s + l / 32 of step s, for A and B alike:
+// which elements of the contraction that pairs is the same on both sides.
+template <typename T> struct AttnFrag;
+template <> struct AttnFrag<bf16_t> { using type = bf16x8; };
+template <> struct AttnFrag<float> { using type = f32x4; };
+template <typename T> using Frag = typename AttnFrag<T>::type;
+
+__device__ __forceinline__ f32x16 mma32(bf16x8 a, bf16x8 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mma32(f32x4 a, f32x4 b, f32x16 c) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[i], b[i], c, 0, 0, 0);
+  return c;
+}
+
+template <typename T, int DP>
+__device__ __forceinline__ Frag<T> row_frag(const char* tile, int row0, int s, int lane) {
+  return *reinterpret_cast<const Frag<T>*>(
+      tile + AttnTile<T, DP>::at(row0 + (lane & 31), 2 * s + (lane >> 5)));
+}
+
+// the same operand straight from a row in memory; chunks behind the last are zero
+template <typename F, int STEPS>
+__device__ __forceinline__ void load_rows(F (&f)[STEPS], const char* row, int cmax, int lane) {
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s) {
+    const int c = 2 * s + (lane >> 5);
+    uint4 x = zero4();
+    if (c <= cmax) x = *reinterpret_cast<const uint4*>(row + c * 16);
+    f[s] = __builtin_bit_cast(F, x);
+  }
+}
+
+__device__ __forceinline__ f32x16 zero16() {
+  f32x16 z;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) z[i] = 0.f;
+  return z;
+}
+
+// bf16: A fragment of rows row0 + 16 kb .. + 15 transposed, columns 32 db .. + 31
+template <int DP>
+__device__ __forceinline__ bf16x8 trans_frag(const char* tile, int row0, int kb, int db, int lane) {
+  const int j = lane & 15;
+  const int row = row0 + 16 * kb + 4 * (lane >> 5) + (j >> 2);
+  const int chunk = 4 * db + 2 * ((lane >> 4) & 1) + ((j & 3) >> 1), half = (j & 1) * 8;
+  const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+      (__attribute__((address_space(3))) v4s*)(tile + AttnTile<bf16_t, DP>::at(row, chunk) + half));
+  const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+      (__attribute__((address_space(3))) v4s*)(tile + AttnTile<bf16_t, DP>::at(row + 8, chunk) + half));
+  typedef short v8s __attribute__((ext_vector_type(8)));
+  const v8s v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+  return __builtin_bit_cast(bf16x8, v);
+}
+// fp32: element (row 8 (r/4) + 4 h + r%4, column 32 db + l%32)
+template <int DP>
+__device__ __forceinline__ float trans_elem(const char* tile, int row0, int r, int db, int lane) {
+  const int row = row0 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3), col = 32 * db + (lane & 31);
+  return *reinterpret_cast<const float*>(tile + AttnTile<float, DP>::at(row, col >> 2) + (col & 3) * 4);
+}
+
+// acc^T[d x lane] += sum over the tile's 32 rows from row0 of row^T p, with p
+// in the layout a 32x32 product leaves.  GUARD: some p are masked (zero), and
+// a NaN or infinity in a row that only they would meet must not get through
+// 0 * NaN.  Such values are taken out of the product and what the others
+// make of them is put back: a row product with their places as ones, > 0
+// where a lane meets one.  FWD: p >= 0 are probabilities, infinities keep
+// their sign; else anything non-finite gives NaN.
+template <typename T, int DP, bool FWD>
+__device__ __forceinline__ void mma_trans(f32x16 (&acc)[DP / 32], const f32x16& p, const char* tile, int row0,
+                                          int lane, bool guard) {
+  constexpr int DB = DP / 32;
+  constexpr float INF = __builtin_huge_valf();
+  if constexpr (sizeof(T) == 2) {
+    bf16x8 b[2];
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      uint4 x = make_uint4(pack_bf16x2(p[8 * kb], p[8 * kb + 1]), pack_bf16x2(p[8 * kb + 2], p[8 * kb + 3]),
+                           pack_bf16x2(p[8 * kb + 4], p[8 * kb + 5]), pack_bf16x2(p[8 * kb + 6], p[8 * kb + 7]));
+      b[kb] = __builtin_bit_cast(bf16x8, x);
+    }
+    if (guard) {
+      bool bad = false;
+#pragma unroll 1
+      for (int i = 0; i < 2 * DB; ++i) {
+        const uint4 a = __builtin_bit_cast(uint4, trans_frag<DP>(tile, row0, i & 1, i >> 1, lane));
+        for (uint32_t w : {a.x, a.y, a.z, a.w})
+          bad |= (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+      }
+      if (__any(bad)) {
+#pragma unroll
+        for (int db = 0; db < DB; ++db) {
+          __builtin_amdgcn_sched_barrier(0);  // one block's registers at a time
+          f32x16 pos = zero16(), neg = zero16();
+#pragma unroll
+          for (int kb = 0; kb < 2; ++kb) {
+            const uint4 a4 = __builtin_bit_cast(uint4, trans_frag<DP>(tile, row0, kb, db, lane));
+            const uint4 b4 = __builtin_bit_cast(uint4, b[kb]);
+            const uint32_t a[4] = {a4.x, a4.y, a4.z, a4.w}, bb[4] = {b4.x, b4.y, b4.z, b4.w};
+            uint32_t fine[4], up[4], dn[4], mag[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              fine[e] = up[e] = dn[e] = 0;
+              mag[e] = bb[e] & 0x7fff7fffu;
+#pragma unroll
+              for (int s = 0; s < 32; s += 16) {
+                const uint32_t x = (a[e] >> s) & 0xffffu;
+                const bool non = (x & 0x7f80u) == 0x7f80u, nan = (x & 0x7fffu) > 0x7f80u;
+                if (!non) fine[e] |= x << s;
+                if (non && (nan || !(x & 0x8000u))) up[e] |= 0x3f80u << s;
+                if (non && (nan || (x & 0x8000u))) dn[e] |= 0x3f80u << s;
+              }
+            }
+            auto frag = [](const uint32_t(&w)[4]) {
+              return __builtin_bit_cast(bf16x8, make_uint4(w[0], w[1], w[2], w[3]));
+            };
+            acc[db] = mma32(frag(fine), b[kb], acc[db]);
+            pos = mma32(frag(up), frag(mag), pos);
+            neg = mma32(frag(dn), frag(mag), neg);
+          }
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const float u = pos[r] > 0.f ? INF : 0.f, w = neg[r] > 0.f ? -INF : 0.f;
+            acc[db][r] += FWD ? u + w : (u - w == 0.f ? 0.f : __builtin_nanf(""));
+          }
+        }
+        return;
+      }
+    }
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int db = 0; db < DB; ++db) acc[db] = mma32(trans_frag<DP>(tile, row0, kb, db, lane), b[kb], acc[db]);
+  } else {
+    if (guard) {
+      bool bad = false;
+#pragma unroll 1
+      for (int db = 0; db < DB; ++db)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) bad |= !__builtin_isfinite(trans_elem<DP>(tile, row0, r, db, lane));
+      if (__any(bad)) {
+#pragma unroll
+        for (int db = 0; db < DB; ++db) {
+          __builtin_amdgcn_sched_barrier(0);  // one block's registers at a time
+          f32x16 pos = zero16(), neg = zero16();
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const float x = trans_elem<DP>(tile, row0, r, db, lane);
+            const bool non = !__builtin_isfinite(x), nan = x != x;
+            acc[db] = __builtin_amdgcn_mfma_f32_32x32x2f32(non ? 0.f : x, p[r], acc[db], 0, 0, 0);
+            pos = __builtin_amdgcn_mfma_f32_32x32x2f32(nan || x == INF ? 1.f : 0.f, fabsf(p[r]), pos, 0, 0, 0);
+            neg = __builtin_amdgcn_mfma_f32_32x32x2f32(nan || x == -INF ? 1.f : 0.f, fabsf(p[r]), neg, 0, 0, 0);
+          }
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const float u = pos[r] > 0.f ? INF : 0.f, w = neg[r] > 0.f ? -INF : 0.f;
+            acc[db][r] += FWD ? u + w : (u - w == 0.f ? 0.f : __builtin_nanf(""));
+          }
+        }
+        return;
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+#pragma unroll
+      for (int db = 0; db < DB; ++db)
+        acc[db] = __builtin_amdgcn_mfma_f32_32x32x2f32(trans_elem<DP>(tile, row0, r, db, lane), p[r], acc[db], 0, 0, 0);
+  }
+}
+
+// maximum and sum of a lane and its partner 32 away
+__device__ __forceinline__ float pair_max(float x) {
+  const uint32_t u = __float_as_uint(x);
+  const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float pair_sum(float x) {
+  const uint32_t u = __float_as_uint(x);
+  const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+__device__ __forceinline__ int seq_len(const int64_t* lens, int b, int most) {
+  if (!lens) return most;
+  const int64_t n = lens[b];
+  return (int)(n < 0 ? 0 : n > most ? most : n);
+}
+
+// The key tiles of BN keys that rows at positions p_lo .. p_hi can see: the
+// `ns` first ones for the sinks, then those from `tl` on for the window.
+struct KeyTiles {
+  int ns = 0, tl = 0, total = 0;
+  __device__ KeyTiles(int p_lo, int p_hi, int window, int sinks, int BN) {
+    if (p_hi < 0) return;
+    ns = (min(sinks, p_hi + 1) + BN - 1) / BN;
+    tl = max(ns, max(0, p_lo - window + 1) / BN);
+    total = ns + max(0, p_hi / BN - tl + 1);
+  }
+  __device__ int at(int i) const { return i < ns ? i : tl + (i - ns); }
+};
+
+// ------------------------------------------------------------------ forward
+// A wave's 32 rows: running maximum and sum, and O^T.
+template <typename T, int DP>
+struct AttnRows {
+  static constexpr int STEPS = AttnTile<T, DP>::STEPS, DB = DP / 32;
+  Frag<T> q[STEPS];
+  f32x16 o[DB];
+  float m, l;   // maximum (in units of log2, at most 8 behind), this lane's half of the sum
+  int p;        // position of lane l % 32's row
+  int w_lo, w_hi;  // lowest and highest position of the wave's rows
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int db = 0; db < DB; ++db) o[db] = zero16();
+    m = -__builtin_huge_valf();
+    l = 0.f;
+  }
+
+  // keys k0 .. k0 + 32 SB - 1, in LDS tiles of as many rows
+  template <int SB>
+  __device__ __forceinline__ void step(const char* kt, const char* vt, int k0, int window, int sinks, float c,
+                                       int lane) {
+    const int k1 = k0 + 32 * SB - 1;
+    if (k0 > w_hi || (k1 <= w_lo - window && k0 >= sinks)) return;  // no row sees any of it
+    const bool whole = k1 <= w_lo && (k0 > w_hi - window || k1 < sinks);
+    f32x16 s[SB];
+#pragma unroll
+    for (int i = 0; i < SB; ++i) s[i] = zero16();
+#pragma unroll
+    for (int t = 0; t < STEPS; ++t)
+#pragma unroll
+      for (int i = 0; i < SB; ++i) s[i] = mma32(row_frag<T, DP>(kt, 32 * i, t, lane), q[t], s[i]);
+    if (!whole) {
+      const int h4 = 4 * (lane >> 5), lo = p - window;
+#pragma unroll
+      for (int i = 0; i < SB; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int key = k0 + 32 * i + 8 * (r >> 2) + (r & 3) + h4;
+          if (!(key <= p && (key > lo || key < sinks))) s[i][r] = -__builtin_huge_valf();
+        }
+    }
+    float top = s[0][0];
+#pragma unroll
+    for (int i = 0; i < SB; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) top = fmaxf(top, s[i][r]);
+    top = pair_max(top) * c;
+    // The sums are taken relative to m, which may lag: exp2 of up to 8 loses
+    // nothing in fp32, and most tiles then rescale nothing.
+    if (__any(top > m + 8.f)) {
+      const float to = fmaxf(m, top);
+      const float a = to == m ? 1.f : __builtin_amdgcn_exp2f(m - to);
+      m = to;
+      l *= a;
+#pragma unroll
+      for (int db = 0; db < DB; ++db)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) o[db][r] *= a;
+    }
+    const float ref = m == -__builtin_huge_valf() ? 0.f : m;  // nothing seen yet: every term is exp2(-inf)
+#pragma unroll
+    for (int i = 0; i < SB; ++i) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        s[i][r] = __builtin_amdgcn_exp2f(fmaf(s[i][r], c, -ref));
+        l += s[i][r];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < SB; ++i) mma_trans<T, DP, true>(o, s[i], vt, 32 * i, lane, !whole);
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ void store_row4(char* row, int d, const float (&v)[4]) {
+  store4(reinterpret_cast<T*>(row) + d, v);
+}
+
+// O^T of a wave to memory: lane l holds row l % 32, 4 consecutive d at a time
+template <typename T, int DP>
+__device__ __forceinline__ void store_rows(const f32x16 (&o)[DP / 32], float f, char* row, int d, int lane) {
+#pragma unroll
+  for (int db = 0; db < DP / 32; ++db)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int c = 32 * db + 8 * g + 4 * (lane >> 5);
+      const float v[4] = {o[db][4 * g] * f, o[db][4 * g + 1] * f, o[db][4 * g + 2] * f, o[db][4 * g + 3] * f};
+      if (c < d) store_row4<T>(row, c, v);
+    }
+}
+
+// waves a SIMD: two where 256 registers hold a wave's 32 rows
+template <typename T, int DP>
+constexpr int attn_waves() { return DP * (int)sizeof(T) > 256 ? 1 : 2; }
+
+// keys of a tile: 16 KB of K and of V, or 64 keys
+template <typename T, int DP>
+constexpr int attn_bn() { return DP * (int)sizeof(T) > 256 ? 32 : 64; }
+
+// Where a workgroup works: head and tile.  Query heads that share a key head
+// come next to each other, then tiles, so that those reading the same keys
+// run together, and (xcd_remap) mostly on one XCD with its L2.
+struct AttnPlace {
+  int b, hk, h, tile;
+  __device__ AttnPlace(int id, const AttnArgs& a) {
+    h = id % a.G;
+    id /= a.G;
+    tile = a.tiles - 1 - id % a.tiles;  // where rows have unequal work the long ones go first
+    id /= a.tiles;
+    hk = id % a.Hk;
+    b = id / a.Hk;
+    h += hk * a.G;
+  }
+};
+
+// Four waves x 32 rows; K and V tiles in a two-deep ring of direct loads.
+template <typename T, int DP>
+__global__ __launch_bounds__(256, (attn_waves<T, DP>())) void attn_fwd_kernel(AttnArgs a) {
+  using Tile = AttnTile<T, DP>;
+  constexpr int NW = 4, BM = 32 * NW, BN = attn_bn<T, DP>(), TB = BN * Tile::CPR * 16;
+  __shared__ __align__(1024) char lds[4 * TB];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const AttnPlace at(xcd_remap(blockIdx.x, gridDim.x), a);
+  const int qlen = seq_len(a.q_lens, at.b, a.Lq), klen = seq_len(a.k_lens, at.b, a.Lk);
+  const int r0 = at.tile * BM, off = klen - qlen;
+  if (r0 >= qlen) return;
+  const int row = r0 + 32 * wave + (lane & 31), cmax = a.d * (int)sizeof(T) / 16 - 1;
+  const char* kb = a.k + at.b * a.sk.b + at.hk * a.sk.h;
+  const char* vb = a.v + at.b * a.sv.b + at.hk * a.sv.h;
+  AttnRows<T, DP> w;
+  w.clear();
+  load_rows(w.q, a.q + at.b * a.sq.b + at.h * a.sq.h + (int64_t)min(row, qlen - 1) * a.sq.l, cmax, lane);
+  w.p = off + row;
+  w.w_lo = off + r0 + 32 * wave;
+  w.w_hi = off + min(r0 + 32 * wave + 31, qlen - 1);
+  const KeyTiles kt(off + r0, off + min(r0 + BM, qlen) - 1, a.window, a.sinks, BN);
+  auto issue = [&](int i) {
+    char* t = lds + (i & 1) * 2 * TB;
+    const int k0 = kt.at(i) * BN;
+    Tile::template stage<BN, NW>(t, kb, a.sk.l, k0, klen - 1, cmax, wave, lane);
+    Tile::template stage<BN, NW>(t + TB, vb, a.sv.l, k0, klen - 1, cmax, wave, lane);
+  };
+  if (kt.total > 0) issue(0);
+  for (int i = 0; i < kt.total; ++i) {
+    wait_lgkm0();
+    wait_vm<0>();
+    bar();
+    if (i + 1 < kt.total) issue(i + 1);
+    if (w.w_lo <= w.w_hi) {
+      const char* t = lds + (i & 1) * 2 * TB;
+      w.template step<BN / 32>(t, t + TB, kt.at(i) * BN, a.window, a.sinks, a.c, lane);
+    }
+  }
+  const float l = pair_sum(w.l);
+  if (row < qlen) {
+    store_rows<T, DP>(w.o, l > 0.f || l != l ? 1.f / l : 0.f, a.out + at.b * a.so.b + at.h * a.so.h + row * a.so.l,
+                      a.d, lane);
+    if (a.lse && lane < 32)
+      a.lse[((int64_t)at.b * a.H + at.h) * a.Lq + row] = l == 0.f ? -__builtin_huge_valf() : w.m * LN2 + logf(l);
+  }
+}
+
+// ------------------------------------------------------------------ forward, few rows
+// At most 32 rows a key head (its query heads x tokens): the work is reading
+// keys, so the keys are split, over workgroups and again over a workgroup's
+// waves.  Each wave runs its own ring of 32-key tiles with no barrier; the
+// waves join in LDS, the workgroups through `part` in attn_join_kernel.
+template <typename T, int DP, int NW>
+__global__ __launch_bounds__(64 * NW) void attn_few_kernel(AttnArgs a) {
+  using Tile = AttnTile<T, DP>;
+  constexpr int TB = 32 * Tile::CPR * 16, WB = 4 * TB > 32 * DP * 4 + 256 ? 4 * TB : 32 * DP * 4 + 256;
+  __shared__ __align__(1024) char lds[NW * WB];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int split = blockIdx.x % a.splits, bk = blockIdx.x / a.splits;
+  const int hk = bk % a.Hk, b = bk / a.Hk;
+  const int qlen = seq_len(a.q_lens, b, a.Lq), klen = seq_len(a.k_lens, b, a.Lk);
+  if (qlen == 0) return;
+  const int off = klen - qlen, rows = a.G * a.Lq, n = lane & 31;
+  const int row = n < rows ? n : 0, tok = row % a.Lq, cmax = a.d * (int)sizeof(T) / 16 - 1;
+  const char* kb = a.k + b * a.sk.b + hk * a.sk.h;
+  const char* vb = a.v + b * a.sv.b + hk * a.sv.h;
+  AttnRows<T, DP> w;
+  w.clear();
+  load_rows(w.q, a.q + b * a.sq.b + (int64_t)(hk * a.G + row / a.Lq) * a.sq.h +
+                            (int64_t)min(tok, qlen - 1) * a.sq.l, cmax, lane);
+  w.p = off + min(tok, qlen - 1);
+  w.w_lo = off;
+  w.w_hi = klen - 1;
+  const KeyTiles kt(w.w_lo, w.w_hi, a.window, a.sinks, 32);
+  const int i0 = (int)((int64_t)kt.total * split / a.splits), i1 = (int)((int64_t)kt.total * (split + 1) / a.splits);
+  char* ring = lds + wave * WB;
+  auto issue = [&](int i, int buf) {
+    char* t = ring + buf * 2 * TB;
+    Tile::template stage<32, 1>(t, kb, a.sk.l, kt.at(i) * 32, klen - 1, cmax, 0, lane);
+    Tile::template stage<32, 1>(t + TB, vb, a.sv.l, kt.at(i) * 32, klen - 1, cmax, 0, lane);
+  };
+  if (i0 + wave < i1) issue(i0 + wave, 0);
+  int buf = 0;
+  for (int i = i0 + wave; i < i1; i += NW, buf ^= 1) {
+    wait_lgkm0();  // the tile that the next copies overwrite has been read
+    if (i + NW < i1) {
+      issue(i + NW, buf ^ 1);
+      wait_vm<Tile::CPR>();  // the 2 x CPR / 2 copies of the tile before them have landed
+    } else {
+      wait_vm<0>();
+    }
+    asm volatile("" ::: "memory");
+    const char* t = ring + buf * 2 * TB;
+    w.template step<1>(t, t + TB, kt.at(i) * 32, a.window, a.sinks, a.c, lane);
+  }
+  // join the waves: O as [d][row] and the statistics behind it
+  wait_lgkm0();
+  float* mine = reinterpret_cast<float*>(ring);
+#pragma unroll
+  for (int db = 0; db < DP / 32; ++db)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) mine[(32 * db + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) * 32 + n] = w.o[db][r];
+  const float lsum = pair_sum(w.l);
+  if (lane < 32) {
+    mine[DP * 32 + n] = w.m;
+    mine[DP * 32 + 32 + n] = lsum;
+  }
+  __syncthreads();
+  auto other = [&](int v) { return reinterpret_cast<const float*>(lds + v * WB); };
+  float m = -__builtin_huge_valf(), l = 0.f, f[NW];
+#pragma unroll
+  for (int v = 0; v < NW; ++v) m = fmaxf(m, other(v)[DP * 32 + n]);
+#pragma unroll
+  for (int v = 0; v < NW; ++v) {
+    const float x = other(v)[DP * 32 + n];
+    f[v] = x == -__builtin_huge_valf() ? 0.f : __builtin_amdgcn_exp2f(x - m);
+    // a wave that met a NaN has a NaN sum whatever its maximum
+    l += other(v)[DP * 32 + 32 + n] == 0.f ? 0.f : other(v)[DP * 32 + 32 + n] * (f[v] == 0.f && x == -__builtin_huge_valf() ? 1.f : f[v]);
+  }
+  if (n >= rows || tok >= qlen) return;
+  constexpr int PER = DP / (2 * NW);  // columns of a thread
+  const int c0 = (int)(threadIdx.x >> 5) * PER;
+  float* pr = a.part + (((int64_t)bk * rows + n) * a.splits + split) * a.d;
+  char* orow = a.out + b * a.so.b + (int64_t)(hk * a.G + row / a.Lq) * a.so.h + (int64_t)tok * a.so.l;
+  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+#pragma unroll
+  for (int j = 0; j < PER; j += 4) {
+    if (c0 + j >= a.d) break;
+    float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+      for (int v = 0; v < NW; ++v) x[e] += f[v] == 0.f ? 0.f : f[v] * other(v)[(c0 + j + e) * 32 + n];
+    if (a.splits > 1) {
+      store4(pr + c0 + j, x);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] *= inv;
+      store_row4<T>(orow, c0 + j, x);
+    }
+  }
+  if (threadIdx.x < 32) {
+    if (a.splits > 1) {
+      float* ml = a.part_ml + (((int64_t)bk * rows + n) * a.splits + split) * 2;
+      ml[0] = m;
+      ml[1] = l;
+    } else if (a.lse) {
+      a.lse[((int64_t)b * a.H + hk * a.G + row / a.Lq) * a.Lq + tok] =
+          l == 0.f ? -__builtin_huge_valf() : m * LN2 + logf(l);
+    }
+  }
+}
+
+// One wave a row: the splits' sums, rescaled to their common maximum.
+template <typename T>
+__global__ __launch_bounds__(64) void attn_join_kernel(AttnArgs a) {
+  const int rows = a.G * a.Lq, n = blockIdx.x % rows, bk = blockIdx.x / rows;
+  const int hk = bk % a.Hk, b = bk / a.Hk, tok = n % a.Lq, h = hk * a.G + n / a.Lq;
+  const int qlen = seq_len(a.q_lens, b, a.Lq), lane = threadIdx.x;
+  if (tok >= qlen) return;
+  const float* ml = a.part_ml + ((int64_t)bk * rows + n) * a.splits * 2;
+  const float* pr = a.part + ((int64_t)bk * rows + n) * a.splits * a.d;
+  float m = -__builtin_huge_valf(), l = 0.f;
+  for (int s = 0; s < a.splits; ++s) m = fmaxf(m, ml[2 * s]);
+  float x[2] = {0.f, 0.f};
+  for (int s = 0; s < a.splits; ++s) {
+    const float ms = ml[2 * s], ls = ml[2 * s + 1];
+    if (ls == 0.f) continue;
+    const float f = ms == -__builtin_huge_valf() ? 1.f : __builtin_amdgcn_exp2f(ms - m);
+    l += ls * f;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (lane + 64 * j < a.d) x[j] += f * pr[(int64_t)s * a.d + lane + 64 * j];
+  }
+  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+  T* orow = reinterpret_cast<T*>(a.out + b * a.so.b + (int64_t)h * a.so.h + (int64_t)tok * a.so.l);
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    if (lane + 64 * j < a.d) io_traits<T>::store(orow + lane + 64 * j, x[j] * inv);
+  if (a.lse && lane == 0)
+    a.lse[((int64_t)b * a.H + h) * a.Lq + tok] = l == 0.f ? -__builtin_huge_valf() : m * LN2 + logf(l);
+}
+
+// ------------------------------------------------------------------ backward: dq
+// As the forward, with dP^T = V dO^T beside S^T and dq^T += K^T dS^T.  Lane n
+// holds half of its row's dO and o: D = dO.o costs no launch of its own and
+// is left in `delta` for the dk, dv kernel.
+template <typename T, int DP>
+__global__ __launch_bounds__(256, (attn_waves<T, DP>())) void attn_dq_kernel(AttnArgs a) {
+  using Tile = AttnTile<T, DP>;
+  constexpr int NW = 4, BM = 32 * NW, BN = attn_bn<T, DP>(), TB = BN * Tile::CPR * 16, STEPS = Tile::STEPS;
+  __shared__ __align__(1024) char lds[4 * TB];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const AttnPlace at(xcd_remap(blockIdx.x, gridDim.x), a);
+  const int qlen = seq_len(a.q_lens, at.b, a.Lq), klen = seq_len(a.k_lens, at.b, a.Lk);
+  const int r0 = at.tile * BM, off = klen - qlen, n = lane & 31;
+  const int row = r0 + 32 * wave + n, cmax = a.d * (int)sizeof(T) / 16 - 1;
+  const int64_t stat = ((int64_t)at.b * a.H + at.h) * a.Lq + row;
+  char* dqrow = a.dq + at.b * a.sdq.b + at.h * a.sdq.h + (int64_t)row * a.sdq.l;
+  f32x16 dq[DP / 32];
+#pragma unroll
+  for (int db = 0; db < DP / 32; ++db) dq[db] = zero16();
+  if (r0 < qlen) {
+    const char* kb = a.k + at.b * a.sk.b + at.hk * a.sk.h;
+    const char* vb = a.v + at.b * a.sv.b + at.hk * a.sv.h;
+    const int64_t rc = min(row, qlen - 1);
+    Frag<T> q[STEPS], g[STEPS];
+    float delta = 0.f;
+    {
+      Frag<T> o[STEPS];
+      load_rows(q, a.q + at.b * a.sq.b + at.h * a.sq.h + rc * a.sq.l, cmax, lane);
+      load_rows(g, a.dO + at.b * a.sdo.b + at.h * a.sdo.h + rc * a.sdo.l, cmax, lane);
+      load_rows(o, a.o + at.b * a.so.b + at.h * a.so.h + rc * a.so.l, cmax, lane);
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+        for (int e = 0; e < 16 / (int)sizeof(T); ++e) delta = fmaf((float)g[s][e], (float)o[s][e], delta);
+    }
+    delta = pair_sum(delta);
+    if (row < qlen && lane < 32) a.delta[stat] = delta;
+    const float lse2 = (row < qlen ? a.lse[stat] : 0.f) * LOG2E;
+    const int p = off + row, w_lo = off + r0 + 32 * wave, w_hi = off + min(r0 + 32 * wave + 31, qlen - 1);
+    const KeyTiles kt(off + r0, off + min(r0 + BM, qlen) - 1, a.window, a.sinks, BN);
+    auto issue = [&](int i) {
+      char* t = lds + (i & 1) * 2 * TB;
+      const int k0 = kt.at(i) * BN;
+      Tile::template stage<BN, NW>(t, kb, a.sk.l, k0, klen - 1, cmax, wave, lane);
+      Tile::template stage<BN, NW>(t + TB, vb, a.sv.l, k0, klen - 1, cmax, wave, lane);
+    };
+    if (kt.total > 0) issue(0);
+    for (int i = 0; i < kt.total; ++i) {
+      wait_lgkm0();
+      wait_vm<0>();
+      bar();
+      if (i + 1 < kt.total) issue(i + 1);
+      const char* t = lds + (i & 1) * 2 * TB;
+#pragma unroll
+      for (int sb = 0; sb < BN / 32; ++sb) {
+        const int k0 = kt.at(i) * BN + 32 * sb, k1 = k0 + 31;
+        if (k0 > w_hi || w_lo > w_hi || (k1 <= w_lo - a.window && k0 >= a.sinks)) continue;
+        const bool whole = k1 <= w_lo && (k0 > w_hi - a.window || k1 < a.sinks);
+        f32x16 s = zero16(), dp = zero16();
+#pragma unroll
+        for (int st = 0; st < STEPS; ++st) {
+          s = mma32(row_frag<T, DP>(t, 32 * sb, st, lane), q[st], s);
+          dp = mma32(row_frag<T, DP>(t + TB, 32 * sb, st, lane), g[st], dp);
+        }
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], a.c, -lse2)) * (dp[r] - delta);
+        if (!whole) {
+          const int lo = p - a.window;
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const int key = k0 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+            if (!(key <= p && (key > lo || key < a.sinks))) s[r] = 0.f;
+          }
+        }
+        mma_trans<T, DP, false>(dq, s, t, 32 * sb, lane, !whole);
+      }
+    }
+  }
+  if (row >= qlen) {  // what a clamped row gathered, finite or not, is nothing
+#pragma unroll
+    for (int db = 0; db < DP / 32; ++db) dq[db] = zero16();
+  }
+  if (row < a.Lq) store_rows<T, DP>(dq, a.scale, dqrow, a.d, lane);
+}
+
+// ------------------------------------------------------------------ backward: dk, dv
+// A workgroup owns 128 keys of a key head, a wave 32 of them in registers,
+// and meets every row that sees them, over all query heads of the key head
+// (their sum needs no atomics).  S = Q K^T and dP = dO V^T have the key in
+// the lane; dv^T += dO^T P and dk^T += Q^T dS.
+//
+// Keys below `sinks` are seen by every later row, up to 16 times more than a
+// window's; the rows behind the window of a sink tile's last key are split
+// over further workgroups of `span` rows each, and the fp32 partial sums of a
+// sink tile are added in a fixed order by attn_sink_sum_kernel.
+template <typename T, int DP>
+__global__ __launch_bounds__(256, 1) void attn_dkv_kernel(AttnArgs a) {
+  using Tile = AttnTile<T, DP>;
+  constexpr int NW = 4, BK = 32 * NW, BQ = attn_bn<T, DP>(), TB = BQ * Tile::CPR * 16, STEPS = Tile::STEPS;
+  __shared__ __align__(1024) char lds[4 * TB];
+  __shared__ float stats[2][2][BQ];  // [ring][lse, delta][row]
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 31;
+  int id = xcd_remap(blockIdx.x, gridDim.x);
+  const int jobs = a.tiles + a.sink_tiles * (a.splits - 1);
+  const int job = id % jobs, bk = id / jobs, hk = bk % a.Hk, b = bk / a.Hk;
+  int tile, split = 0;
+  if (job < a.sink_tiles * a.splits) {
+    tile = job / a.splits;
+    split = job % a.splits;
+  } else {
+    tile = job - a.sink_tiles * (a.splits - 1);
+  }
+  const int qlen = seq_len(a.q_lens, b, a.Lq), klen = seq_len(a.k_lens, b, a.Lk), off = klen - qlen;
+  const int k0 = tile * BK, k1 = min(k0 + BK, klen) - 1, cmax = a.d * (int)sizeof(T) / 16 - 1;
+  const int key = k0 + 32 * wave + n;
+  f32x16 dk[DP / 32], dv[DP / 32];
+#pragma unroll
+  for (int db = 0; db < DP / 32; ++db) dk[db] = dv[db] = zero16();
+  // positions of the rows this workgroup meets
+  int p_lo = k0, p_hi = klen - 1;
+  const int reach = (int)min((int64_t)k0 + BK - 1 + a.window, (int64_t)klen) - 1;  // last that sees k0 + BK - 1 by window
+  if (tile < a.sink_tiles && a.splits > 1) {
+    if (split == 0) p_hi = reach;
+    else {
+      p_lo = reach + 1 + (split - 1) * a.span;
+      p_hi = min(klen - 1, p_lo + a.span - 1);
+    }
+  } else if (k0 >= a.sinks) {
+    p_hi = reach;
+  }
+  const int ra = max(0, p_lo - off) / BQ, rz = p_hi - off;  // first row tile, last row
+  const int nt = k0 < klen && rz >= ra * BQ && p_hi >= p_lo ? rz / BQ - ra + 1 : 0;
+  if (nt > 0) {
+    Frag<T> kf[STEPS], vf[STEPS];
+    const int64_t kc = min(key, klen - 1);
+    load_rows(kf, a.k + b * a.sk.b + hk * a.sk.h + kc * a.sk.l, cmax, lane);
+    load_rows(vf, a.v + b * a.sv.b + hk * a.sv.h + kc * a.sv.l, cmax, lane);
+    const int wk0 = k0 + 32 * wave, wk1 = min(wk0 + 31, klen - 1);
+    const int total = nt * a.G;
+    float stat = 0.f;
+    auto issue = [&](int i) {
+      const int h = hk * a.G + i / nt, r = (ra + i % nt) * BQ;
+      char* t = lds + (i & 1) * 2 * TB;
+      Tile::template stage<BQ, NW>(t, a.q + b * a.sq.b + h * a.sq.h, a.sq.l, r, qlen - 1, cmax, wave, lane);
+      Tile::template stage<BQ, NW>(t + TB, a.dO + b * a.sdo.b + h * a.sdo.h, a.sdo.l, r, qlen - 1, cmax, wave, lane);
+      if (threadIdx.x < 2 * BQ) {
+        const int rr = r + (int)threadIdx.x % BQ;
+        const float* src = threadIdx.x < BQ ? a.lse : a.delta;
+        stat = rr < qlen ? src[((int64_t)b * a.H + h) * a.Lq + rr] : 0.f;
+      }
+    };
+    auto put = [&](int i) {
+      if (threadIdx.x < 2 * BQ)
+        stats[i & 1][threadIdx.x / BQ][threadIdx.x % BQ] = threadIdx.x < BQ ? stat * LOG2E : stat;
+    };
+    issue(0);
+    put(0);
+    for (int i = 0; i < total; ++i) {
+      wait_lgkm0();
+      wait_vm<0>();
+      bar();
+      if (i + 1 < total) issue(i + 1);
+      const char* t = lds + (i & 1) * 2 * TB;
+      const int r = (ra + i % nt) * BQ;
+#pragma unroll
+      for (int sb = 0; sb < BQ / 32; ++sb) {
+        const int q0 = off + r + 32 * sb, q1 = q0 + 31;  // positions
+        const int u0 = max(q0, p_lo), u1 = min(q1, p_hi);
+        if (u0 > u1 || wk0 > wk1 || u1 < wk0 || (wk1 <= u0 - a.window && wk0 >= a.sinks)) continue;
+        const bool whole = u0 == q0 && u1 == q1 && wk1 <= q0 && wk0 + 31 == wk1 &&
+                           (wk0 > q1 - a.window || wk1 < a.sinks);
+        f32x16 s = zero16(), dp = zero16();
+#pragma unroll
+        for (int st = 0; st < STEPS; ++st) {
+          s = mma32(row_frag<T, DP>(t, 32 * sb, st, lane), kf[st], s);
+          dp = mma32(row_frag<T, DP>(t + TB, 32 * sb, st, lane), vf[st], dp);
+        }
+        f32x16 ds;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int rr = 32 * sb + 8 * g + 4 * (lane >> 5);
+          const f32x4 ls = *reinterpret_cast<const f32x4*>(&stats[i & 1][0][rr]);
+          const f32x4 de = *reinterpret_cast<const f32x4*>(&stats[i & 1][1][rr]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float pr = __builtin_amdgcn_exp2f(fmaf(s[4 * g + e], a.c, -ls[e]));
+            float d = pr * (dp[4 * g + e] - de[e]);
+            if (!whole) {
+              const int p = q0 + 8 * g + 4 * (lane >> 5) + e;
+              const bool see = p >= u0 && p <= u1 && key <= p && (key > p - a.window || key < a.sinks);
+              pr = see ? pr : 0.f;
+              d = see ? d : 0.f;
+            }
+            s[4 * g + e] = pr;
+            ds[4 * g + e] = d;
+          }
+        }
+        mma_trans<T, DP, false>(dv, s, t + TB, 32 * sb, lane, !whole);
+        mma_trans<T, DP, false>(dk, ds, t, 32 * sb, lane, !whole);
+      }
+      if (i + 1 < total) put(i + 1);
+    }
+  }
+  if (tile < a.sink_tiles && a.splits > 1) {
+    // [batch x key head][sink tile][split][dk, dv][key][d]
+    const int64_t slot = ((int64_t)bk * a.sink_tiles + tile) * a.splits + split;
+    float* pr = a.part + (slot * 2 * BK + 32 * wave + n) * a.d;
+    store_rows<float, DP>(dk, 1.f, reinterpret_cast<char*>(pr), a.d, lane);
+    store_rows<float, DP>(dv, 1.f, reinterpret_cast<char*>(pr + (int64_t)BK * a.d), a.d, lane);
+  } else if (key < a.Lk) {
+    store_rows<T, DP>(dk, key < klen ? a.scale : 0.f, a.dk + b * a.sdk.b + hk * a.sdk.h + (int64_t)key * a.sdk.l, a.d, lane);
+    store_rows<T, DP>(dv, key < klen ? 1.f : 0.f, a.dv + b * a.sdv.b + hk * a.sdv.h + (int64_t)key * a.sdv.l, a.d, lane);
+  }
+}
+
+// dk, dv of the sink tiles: the splits' partial sums, in order
+template <typename T>
+__global__ __launch_bounds__(128) void attn_sink_sum_kernel(AttnArgs a) {
+  const int keys = a.sink_tiles * 128;
+  const int x = blockIdx.x % (2 * keys), bk = blockIdx.x / (2 * keys), what = x / keys, key = x % keys;
+  const int hk = bk % a.Hk, b = bk / a.Hk, c = threadIdx.x;
+  if (key >= a.Lk || c >= a.d) return;
+  const float* pr = a.part + ((((int64_t)bk * a.sink_tiles + key / 128) * a.splits * 2 + what) * 128 + key % 128) * a.d + c;
+  float sum = 0.f;
+  for (int s = 0; s < a.splits; ++s) sum += pr[(int64_t)s * 2 * 128 * a.d];
+  if (key >= seq_len(a.k_lens, b, a.Lk)) sum = 0.f;
+  char* to = what ? a.dv + b * a.sdv.b + hk * a.sdv.h + (int64_t)key * a.sdv.l
+                  : a.dk + b * a.sdk.b + hk * a.sdk.h + (int64_t)key * a.sdk.l;
+  io_traits<T>::store(reinterpret_cast<T*>(to) + c, what ? sum : sum * a.scale);
+}
+
+}  // namespace lact

@@ -35,14 +35,24 @@ CHUNK_APPLY = 2
 NO_RENORM = 1
 QK_PREP = 2
 
-K_UPD, K_APP, K_OUT, K_DW, K_OPT, K_NS, K_SNAP, K_PREP, K_BWD_GEMM, K_BWD_ELEM, K_NSRED = range(11)
+ROTARY_INTERLEAVED = 1
+ROTARY_INVERSE = 2
+ROTARY_SCALING = {"plain": 0, "linear": 1, "ntk": 2, "yarn": 3}
+NORM_GROUP = 128   # LACT_NORM_GROUP: columns that share a scale of the 8-bit output
+
+(K_UPD, K_APP, K_OUT, K_DW, K_OPT, K_NS, K_SNAP, K_PREP, K_BWD_GEMM, K_BWD_ELEM, K_NSRED, K_ATTN, K_ATTN_BWD,
+ K_ROTARY, K_NORM) = range(15)
 K_NAMES = {K_UPD: "update_fwd", K_APP: "apply_fwd", K_OUT: "apply_out", K_DW: "dw", K_OPT: "opt",
            K_NS: "newton_schulz", K_SNAP: "snapshot", K_PREP: "qk_prep", K_BWD_GEMM: "bwd_gemm",
-           K_BWD_ELEM: "bwd_elem", K_NSRED: "ns_reduce"}
+           K_BWD_ELEM: "bwd_elem", K_NSRED: "ns_reduce", K_ATTN: "attention", K_ATTN_BWD: "attention_bwd",
+           K_ROTARY: "rotary", K_NORM: "norm"}
 
 EXPORTS = ["lact_workspace_size", "lact_chunk_update", "lact_apply", "lact_layer_forward",
            "lact_layer_forward_scaled", "lact_layer_forward_noalloc", "lact_backward_workspace_size",
-           "lact_layer_backward", "lact_status_str", "lact_last_error", "lact_timing_enable", "lact_timing_read"]
+           "lact_layer_backward", "lact_window_attention_workspace_size", "lact_window_attention_forward",
+           "lact_window_attention_backward_workspace_size", "lact_window_attention_backward", "lact_rotary",
+           "lact_rotary_frequencies", "lact_add_rmsnorm_forward", "lact_add_rmsnorm_backward_workspace_size",
+           "lact_add_rmsnorm_backward", "lact_status_str", "lact_last_error", "lact_timing_enable", "lact_timing_read"]
 
 NOALLOC_SCRATCH_BYTES = 128 << 20   # LACT_NOALLOC_SCRATCH_BYTES
 
@@ -57,6 +67,29 @@ class Problem(ctypes.Structure):
     _fields_ = [("n_inst", ctypes.c_int32), ("d", ctypes.c_int32), ("dh", ctypes.c_int32),
                 ("io_dtype", ctypes.c_int32), ("opt", ctypes.c_int32), ("ns_iters", ctypes.c_int32),
                 ("rec_planes", ctypes.c_int32), ("flags", ctypes.c_uint32)]
+
+
+class Strides(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("head", ctypes.c_int64), ("token", ctypes.c_int64)]
+
+
+class Attention(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("d", ctypes.c_int32), ("io_dtype", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("q_len", ctypes.c_int64), ("k_len", ctypes.c_int64), ("window", ctypes.c_int64),
+                ("sinks", ctypes.c_int64)]
+
+
+class RotaryProblem(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("d", ctypes.c_int32), ("pairs", ctypes.c_int32), ("io_dtype", ctypes.c_int32),
+                ("flags", ctypes.c_uint32), ("mscale", ctypes.c_float), ("tokens", ctypes.c_int64),
+                ("start", ctypes.c_int64)]
+
+
+class NormProblem(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int32), ("io_dtype", ctypes.c_int32),
+                ("eps", ctypes.c_float)]
 
 
 _lib = None
@@ -102,6 +135,25 @@ def lib() -> ctypes.CDLL:
     L.lact_layer_backward.restype = i32
     L.lact_layer_backward.argtypes = ([P, vp, vp, vp, vp, vp, vp, i64, i64, i32, vp, vp, i32]
                                       + [vp] * 6 + [vp] + [vp] * 6 + [vp] * 6 + [vp] * 6 + [vp, sz, vp])
+    A, R, N, f64 = ctypes.POINTER(Attention), ctypes.POINTER(RotaryProblem), ctypes.POINTER(NormProblem), ctypes.c_double
+    L.lact_window_attention_workspace_size.restype = sz
+    L.lact_window_attention_workspace_size.argtypes = [A]
+    L.lact_window_attention_forward.restype = i32
+    L.lact_window_attention_forward.argtypes = [A] + [vp] * 12 + [sz, vp]
+    L.lact_window_attention_backward_workspace_size.restype = sz
+    L.lact_window_attention_backward_workspace_size.argtypes = [A]
+    L.lact_window_attention_backward.restype = i32
+    L.lact_window_attention_backward.argtypes = [A] + [vp] * 20 + [sz, vp]
+    L.lact_rotary.restype = i32
+    L.lact_rotary.argtypes = [R] + [vp] * 11
+    L.lact_rotary_frequencies.restype = i32
+    L.lact_rotary_frequencies.argtypes = [i32, f64, i32, f64, i64, f64, f64, vp, ctypes.POINTER(ctypes.c_float)]
+    L.lact_add_rmsnorm_forward.restype = i32
+    L.lact_add_rmsnorm_forward.argtypes = [N, vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, i64, vp, vp]
+    L.lact_add_rmsnorm_backward_workspace_size.restype = sz
+    L.lact_add_rmsnorm_backward_workspace_size.argtypes = [N]
+    L.lact_add_rmsnorm_backward.restype = i32
+    L.lact_add_rmsnorm_backward.argtypes = [N, vp, i64, vp, vp, i64, vp, i64, vp, i64, vp, vp, sz, vp]
     L.lact_status_str.restype = ctypes.c_char_p
     L.lact_status_str.argtypes = [i32]
     L.lact_last_error.restype = ctypes.c_char_p
@@ -431,6 +483,301 @@ def layer_backward(q, k, v, lr, beta, W1, W2, W3, M1=None, M2=None, M3=None, *, 
         _ptr(out["dW1"]), _ptr(out["dW2"]), _ptr(out["dW3"]), _ptr(out["dM1"]), _ptr(out["dM2"]), _ptr(out["dM3"]),
         ws.data_ptr(), ws.numel(), _stream(stream)))
     return out
+
+
+# ----------------------------------------------------------------- operators around the layer
+class _Call:
+    """Where a call runs: with the tensors' device current and, if one is
+    given, on `stream` -- what the call allocates then belongs to that stream,
+    and the caching allocator learns that the inputs are in use there."""
+
+    def __init__(self, stream, *tensors):
+        torch = _torch()
+        dev = tensors[0].device
+        if not tensors[0].is_cuda:
+            raise ValueError("tensors must be on the device")
+        for t in tensors:
+            if t is not None and t.device != dev:
+                raise ValueError(f"tensors on {dev} and {t.device}")
+        self.device, self.given = dev, stream
+        self.guards = []
+        if stream is not None:
+            if stream.device != dev:
+                raise ValueError(f"stream of {stream.device} for tensors on {dev}")
+            self.guards.append(torch.cuda.stream(stream))   # makes the device current too
+            self.tensors = tensors
+        elif torch.cuda.current_device() != dev.index:
+            self.guards.append(torch.cuda.device(dev))
+        self.handle = (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
+
+    def __enter__(self):
+        for g in self.guards:
+            g.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        for g in reversed(self.guards):
+            g.__exit__(*exc)
+        if self.given is not None:
+            for t in self.tensors:
+                if t is not None:
+                    t.record_stream(self.given)
+
+
+_STRIDES = {}
+
+
+def _strided(t, name, shape, dtype):
+    """(pointer, strides) of a [batch, heads, tokens, d] tensor with d contiguous."""
+    if t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    b, h, l, e = t.stride()
+    if e != 1 and shape[3] > 1 and t.numel():
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    key = (b, h, l)
+    s = _STRIDES.get(key)
+    if s is None:
+        if len(_STRIDES) >= 256:
+            _STRIDES.clear()
+        s = _STRIDES[key] = Strides(b, h, l)
+    return t.data_ptr(), ctypes.byref(s)
+
+
+def _lens(t, name, batch):
+    if t is None:
+        return None
+    _check_shapes(**{name: (t, (batch,))})
+    return _ptr(t, _torch().int64, name)
+
+
+def _attention(q, k, v, window, sinks, scale):
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q must be [batch, heads, tokens, d] and k [batch, kv_heads, tokens, d]")
+    (b, h, lq, d), (_, hk, lk, _) = q.shape, k.shape
+    return Attention(b, h, hk, d, _io_dtype(q), d ** -0.5 if scale is None else scale, lq, lk, window, sinks)
+
+
+def window_attention(q, k, v, o=None, *, window: int = 0, sinks: int = 0, scale: Optional[float] = None,
+                     q_lens=None, k_lens=None, return_lse: bool = False, lse=None, workspace=None, stream=None):
+    """Causal attention over the last `window` keys (0: all) and the first
+    `sinks` (lact_window_attention_forward).  q [batch, heads, q_len, d], k, v
+    [batch, kv_heads, k_len, d], fp32 or bf16, any strides in multiples of 16
+    bytes with d contiguous: token-major tensors come as transposed views.  Row r
+    stands at position k_len - q_len + r, with q_lens, k_lens (int64 [batch])
+    each sequence's own lengths; scale defaults to d^-1/2.  Returns o in q's
+    layout, and with return_lse also lse [batch, heads, q_len] fp32; what is
+    allocated here has zeros behind q_lens, given tensors keep what they held."""
+    torch = _torch()
+    p = _attention(q, k, v, window, sinks, scale)
+    shape, kshape, dt = tuple(q.shape), (q.shape[0], k.shape[1], k.shape[2], q.shape[3]), q.dtype
+    with _Call(stream, q, k, v, o, q_lens, k_lens, lse, workspace) as call:
+        if o is None:
+            o = torch.empty_like(q) if q_lens is None else torch.zeros_like(q)
+        if lse is None:
+            if return_lse:
+                new = torch.empty if q_lens is None else torch.zeros
+                lse = new(shape[:3], dtype=torch.float32, device=q.device)
+        else:
+            _check_shapes(lse=(lse, shape[:3]))
+        need = lib().lact_window_attention_workspace_size(ctypes.byref(p))
+        ws = _workspace(need, workspace, q.device) if need or workspace is not None else None
+        check(lib().lact_window_attention_forward(
+            ctypes.byref(p), *_strided(q, "q", shape, dt), *_strided(k, "k", kshape, dt),
+            *_strided(v, "v", kshape, dt), _lens(q_lens, "q_lens", shape[0]), _lens(k_lens, "k_lens", shape[0]),
+            *_strided(o, "o", shape, dt), _ptr(lse, torch.float32, "lse"),
+            None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), call.handle))
+    return (o, lse) if return_lse else o
+
+
+def window_attention_backward(q, k, v, o, lse, *, dO, window: int = 0, sinks: int = 0,
+                              scale: Optional[float] = None, q_lens=None, k_lens=None, out=None, workspace=None,
+                              stream=None):
+    """Backward of window_attention (lact_window_attention_backward): o and lse
+    as the forward returned them, dO [batch, heads, q_len, d] in q's dtype.
+    Returns a dict of dq, dk, dv in the inputs' dtype and layout, zero behind
+    the lengths; `out` (such a dict) is filled instead of allocating."""
+    torch = _torch()
+    p = _attention(q, k, v, window, sinks, scale)
+    shape, kshape, dt = tuple(q.shape), (q.shape[0], k.shape[1], k.shape[2], q.shape[3]), q.dtype
+    given = () if out is None else (out["dq"], out["dk"], out["dv"])
+    with _Call(stream, q, k, v, o, lse, dO, q_lens, k_lens, workspace, *given) as call:
+        if out is None:
+            out = {"dq": torch.empty_like(q), "dk": _like(k), "dv": _like(v)}
+        _check_shapes(lse=(lse, shape[:3]))
+        need = lib().lact_window_attention_backward_workspace_size(ctypes.byref(p))
+        ws = _workspace(need, workspace, q.device)
+        check(lib().lact_window_attention_backward(
+            ctypes.byref(p), *_strided(q, "q", shape, dt), *_strided(k, "k", kshape, dt),
+            *_strided(v, "v", kshape, dt), _lens(q_lens, "q_lens", shape[0]), _lens(k_lens, "k_lens", shape[0]),
+            *_strided(o, "o", shape, dt), _ptr(lse, torch.float32, "lse"), *_strided(dO, "dO", shape, dt),
+            *_strided(out["dq"], "out[dq]", shape, dt), *_strided(out["dk"], "out[dk]", kshape, dt),
+            *_strided(out["dv"], "out[dv]", kshape, dt), ws.data_ptr(), ws.numel(), call.handle))
+    return out
+
+
+def _rotary(q, k, freqs, positions, start, interleaved, mscale, q_out, k_out, stream, flags):
+    torch = _torch()
+    if q.dim() != 4 or (k is not None and k.dim() != 4):
+        raise ValueError("q and k must be [batch, heads, tokens, d]")
+    b, h, l, d = shape = tuple(q.shape)
+    kshape = None if k is None else (b, k.shape[1], l, d)
+    if freqs.dim() != 1:
+        raise ValueError("freqs must be [pairs]")
+    if positions is not None:
+        _check_shapes(positions=(positions, (b, l)))
+    p = RotaryProblem(b, h, 0 if k is None else k.shape[1], d, freqs.shape[0], _io_dtype(q),
+                      flags | (ROTARY_INTERLEAVED if interleaved else 0), mscale, l, start)
+    with _Call(stream, q, k, freqs, positions, q_out, k_out) as call:
+        if q_out is None:
+            q_out = _like(q)
+        if k is not None and k_out is None:
+            k_out = _like(k)
+        none = (None, None)
+        check(lib().lact_rotary(
+            ctypes.byref(p), *_strided(q, "q", shape, q.dtype),
+            *(none if k is None else _strided(k, "k", kshape, q.dtype)), _ptr(freqs, torch.float64, "freqs"),
+            _ptr(positions, torch.int64, "positions"), *_strided(q_out, "q_out", shape, q.dtype),
+            *(none if k is None else _strided(k_out, "k_out", kshape, q.dtype)), call.handle))
+    return q_out if k is None else (q_out, k_out)
+
+
+def rotary(q, k=None, *, freqs, positions=None, start: int = 0, interleaved: bool = False, mscale: float = 1.0,
+           q_out=None, k_out=None, stream=None):
+    """Rotary positions of q [batch, heads, tokens, d] and k [batch, kv_heads,
+    tokens, d] in one call (lact_rotary): the first 2 pairs features turn by
+    position * freqs (fp64 [pairs] on the device, see rotary_frequencies) and
+    are scaled by mscale, the others are copied.  positions int64 [batch,
+    tokens], or start + token.  q_out = q and k_out = k work in place.
+    Returns q_out, or (q_out, k_out)."""
+    return _rotary(q, k, freqs, positions, start, interleaved, mscale, q_out, k_out, stream, 0)
+
+
+def rotary_backward(dq, dk=None, *, freqs, positions=None, start: int = 0, interleaved: bool = False,
+                    mscale: float = 1.0, q_out=None, k_out=None, stream=None):
+    """Gradients of rotary's inputs from those of its outputs: the inverse
+    turns with the same scale.  Arguments and results as for rotary."""
+    return _rotary(dq, dk, freqs, positions, start, interleaved, mscale, q_out, k_out, stream, ROTARY_INVERSE)
+
+
+def rotary_frequencies(pairs: int, base: float = 10000.0, *, scaling: str = "plain", factor: float = 1.0,
+                       context: int = 0, slow: float = 1.0, fast: float = 32.0, device=None):
+    """(freqs, mscale) for rotary: base^(-i / pairs), for contexts `factor`
+    times the original one scaled "linear", "ntk" or "yarn"
+    (lact_rotary_frequencies).  Computed once, kept by the caller."""
+    torch = _torch()
+    if scaling not in ROTARY_SCALING:
+        raise ValueError(f"scaling must be one of {sorted(ROTARY_SCALING)}, got {scaling!r}")
+    f = torch.empty(max(pairs, 0), dtype=torch.float64)
+    m = ctypes.c_float(1.0)
+    check(lib().lact_rotary_frequencies(pairs, base, ROTARY_SCALING[scaling], factor, context, slow, fast,
+                                        f.data_ptr(), ctypes.byref(m)))
+    return f.to("cuda" if device is None else device), m.value
+
+
+def _like(t):
+    """An empty tensor of t's shape, in t's order of dimensions where t's rows are distinct."""
+    torch = _torch()
+    if 0 in t.stride():   # an expanded input: its gradient or result has a place for every element
+        return torch.empty(t.shape, dtype=t.dtype, device=t.device)
+    return torch.empty_like(t)
+
+
+def _rows(t, name, shape, dtype):
+    """(pointer, row stride) of a [..., cols] tensor seen as a matrix."""
+    if t is None:
+        return None, 0
+    if t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if t.dim() == 2:
+        ld, e = t.stride()
+        if e != 1 and shape[1] > 1 and t.numel():
+            raise ValueError(f"{name}: columns must be contiguous")
+        return t.data_ptr(), ld
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous (or a matrix with contiguous columns)")
+    return t.data_ptr(), shape[-1]
+
+
+def _norm_problem(x, weight, eps):
+    if x.dim() < 1 or x.shape[-1] == 0:
+        raise ValueError("x must be [..., cols] with cols > 0")
+    cols = x.shape[-1]
+    _check_shapes(weight=(weight, (cols,)))
+    return NormProblem(x.numel() // cols, cols, _io_dtype(x), eps)
+
+
+def add_rmsnorm(x, weight, residual=None, *, eps: float = 1e-6, y=None, h=None, stream=None):
+    """h = x + residual and y = h weight / sqrt(mean(h^2) + eps) over the last
+    dimension (lact_add_rmsnorm_forward).  x, residual [..., cols] fp32 or
+    bf16, weight [cols] fp32.  Returns (y, h); without a residual h is x
+    itself.  h = residual or h = x updates the residual stream in place."""
+    torch = _torch()
+    p = _norm_problem(x, weight, eps)
+    shape, dt = tuple(x.shape), x.dtype
+    with _Call(stream, x, weight, residual, y, h) as call:
+        if y is None:
+            y = torch.empty(shape, dtype=dt, device=x.device)
+        if h is None and residual is not None:
+            h = torch.empty(shape, dtype=dt, device=x.device)
+        check(lib().lact_add_rmsnorm_forward(
+            ctypes.byref(p), *_rows(x, "x", shape, dt), *_rows(residual, "residual", shape, dt),
+            _ptr(weight, torch.float32, "weight"), *_rows(h, "h", shape, dt), *_rows(y, "y", shape, dt),
+            None, 0, None, call.handle))
+    return y, (x if h is None else h)
+
+
+def add_rmsnorm_quantised(x, weight, residual=None, *, eps: float = 1e-6, y8=None, scales=None, h=None, y=None,
+                          stream=None):
+    """As add_rmsnorm, with y in 8-bit floating point: y8 [..., cols]
+    float8_e4m3fn and scales [..., ceil(cols / 128)] fp32, so that y is about
+    y8 * scale of its group of 128 columns.  Returns (y8, scales, h); a given
+    y is filled too."""
+    torch = _torch()
+    p = _norm_problem(x, weight, eps)
+    shape, dt = tuple(x.shape), x.dtype
+    groups = shape[:-1] + ((shape[-1] + NORM_GROUP - 1) // NORM_GROUP,)
+    with _Call(stream, x, weight, residual, y8, scales, h, y) as call:
+        if y8 is None:
+            y8 = torch.empty(shape, dtype=torch.float8_e4m3fn, device=x.device)
+        if scales is None:
+            scales = torch.empty(groups, dtype=torch.float32, device=x.device)
+        else:
+            _check_shapes(scales=(scales, groups))
+        if h is None and residual is not None:
+            h = torch.empty(shape, dtype=dt, device=x.device)
+        check(lib().lact_add_rmsnorm_forward(
+            ctypes.byref(p), *_rows(x, "x", shape, dt), *_rows(residual, "residual", shape, dt),
+            _ptr(weight, torch.float32, "weight"), *_rows(h, "h", shape, dt), *_rows(y, "y", shape, dt),
+            *_rows(y8, "y8", shape, torch.float8_e4m3fn), _ptr(scales, torch.float32, "scales"), call.handle))
+    return y8, scales, (x if h is None else h)
+
+
+def add_rmsnorm_backward(h, weight, *, dy, dh=None, eps: float = 1e-6, dx=None, dw=None, workspace=None,
+                         stream=None):
+    """Backward of add_rmsnorm from the h it returned (lact_add_rmsnorm_backward):
+    dy the gradient of y, dh that of h's other use (or None), in h's dtype.
+    Returns (dx, dw): dx is the gradient of x and of residual alike, dw [cols]
+    fp32 that of the weight."""
+    torch = _torch()
+    p = _norm_problem(h, weight, eps)
+    shape, dt = tuple(h.shape), h.dtype
+    with _Call(stream, h, weight, dy, dh, dx, dw, workspace) as call:
+        if dx is None:
+            dx = torch.empty(shape, dtype=dt, device=h.device)
+        if dw is None:
+            dw = torch.empty(shape[-1], dtype=torch.float32, device=h.device)
+        else:
+            _check_shapes(dw=(dw, shape[-1:]))
+        ws = _workspace(lib().lact_add_rmsnorm_backward_workspace_size(ctypes.byref(p)), workspace, h.device)
+        check(lib().lact_add_rmsnorm_backward(
+            ctypes.byref(p), *_rows(h, "h", shape, dt), _ptr(weight, torch.float32, "weight"),
+            *_rows(dy, "dy", shape, dt), *_rows(dh, "dh", shape, dt), *_rows(dx, "dx", shape, dt),
+            _ptr(dw, torch.float32, "dw"), ws.data_ptr(), ws.numel(), call.handle))
+    return dx, dw
 
 
 lib()  # fail at import time if the library is missing
