@@ -19,8 +19,7 @@
 //
 // Numbers: scores, softmax statistics and all sums are fp32.  For bf16
 // tensors P and dS are rounded to bf16 once, as operands of their products
-// (half a step, 2^-9 of the value, against the same half step of the rounded
-// result); for fp32 tensors every product is an fp32 MFMA and nothing is
+// (half a step, 2^-8 of the value, like the result itself); for fp32 tensors every product is an fp32 MFMA and nothing is
 // rounded.
 #pragma once
 #include "lact_direct.hpp"
@@ -158,112 +157,42 @@ __device__ __forceinline__ float trans_elem(const char* tile, int row0, int r, i
 }
 
 // acc^T[d x lane] += sum over the tile's 32 rows from row0 of row^T p, with p
-// in the layout a 32x32 product leaves.  GUARD: some p are masked (zero), and
-// a NaN or infinity in a row that only they would meet must not get through
-// 0 * NaN.  Such values are taken out of the product and what the others
-// make of them is put back: a row product with their places as ones, > 0
-// where a lane meets one.  FWD: p >= 0 are probabilities, infinities keep
-// their sign; else anything non-finite gives NaN.
-template <typename T, int DP, bool FWD>
+// in the layout a 32x32 product leaves.
+template <int DP>
+__device__ __forceinline__ void mma_trans(f32x16 (&acc)[DP / 32], const bf16x8 (&b)[2], const char* tile, int row0,
+                                          int lane) {
+#pragma unroll
+  for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+    for (int db = 0; db < DP / 32; ++db) acc[db] = mma32(trans_frag<DP>(tile, row0, kb, db, lane), b[kb], acc[db]);
+}
+template <int DP>
 __device__ __forceinline__ void mma_trans(f32x16 (&acc)[DP / 32], const f32x16& p, const char* tile, int row0,
-                                          int lane, bool guard) {
-  constexpr int DB = DP / 32;
-  constexpr float INF = __builtin_huge_valf();
-  if constexpr (sizeof(T) == 2) {
-    bf16x8 b[2];
+                                          int lane) {
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
-      uint4 x = make_uint4(pack_bf16x2(p[8 * kb], p[8 * kb + 1]), pack_bf16x2(p[8 * kb + 2], p[8 * kb + 3]),
-                           pack_bf16x2(p[8 * kb + 4], p[8 * kb + 5]), pack_bf16x2(p[8 * kb + 6], p[8 * kb + 7]));
-      b[kb] = __builtin_bit_cast(bf16x8, x);
-    }
-    if (guard) {
-      bool bad = false;
-#pragma unroll 1
-      for (int i = 0; i < 2 * DB; ++i) {
-        const uint4 a = __builtin_bit_cast(uint4, trans_frag<DP>(tile, row0, i & 1, i >> 1, lane));
-        for (uint32_t w : {a.x, a.y, a.z, a.w})
-          bad |= (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
-      }
-      if (__any(bad)) {
+  for (int r = 0; r < 16; ++r)
 #pragma unroll
-        for (int db = 0; db < DB; ++db) {
-          __builtin_amdgcn_sched_barrier(0);  // one block's registers at a time
-          f32x16 pos = zero16(), neg = zero16();
+    for (int db = 0; db < DP / 32; ++db)
+      acc[db] = __builtin_amdgcn_mfma_f32_32x32x2f32(trans_elem<DP>(tile, row0, r, db, lane), p[r], acc[db], 0, 0, 0);
+}
+
+// p as the operand of mma_trans: rounded to bf16 (registers 8 i .. 8 i + 7 are
+// fragment i), or as it is
+struct Pair {
+  bf16x8 f[2];
+};
+__device__ __forceinline__ Pair round_pair(const f32x16& p) {
+  Pair b;
 #pragma unroll
-          for (int kb = 0; kb < 2; ++kb) {
-            const uint4 a4 = __builtin_bit_cast(uint4, trans_frag<DP>(tile, row0, kb, db, lane));
-            const uint4 b4 = __builtin_bit_cast(uint4, b[kb]);
-            const uint32_t a[4] = {a4.x, a4.y, a4.z, a4.w}, bb[4] = {b4.x, b4.y, b4.z, b4.w};
-            uint32_t fine[4], up[4], dn[4], mag[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              fine[e] = up[e] = dn[e] = 0;
-              mag[e] = bb[e] & 0x7fff7fffu;
-#pragma unroll
-              for (int s = 0; s < 32; s += 16) {
-                const uint32_t x = (a[e] >> s) & 0xffffu;
-                const bool non = (x & 0x7f80u) == 0x7f80u, nan = (x & 0x7fffu) > 0x7f80u;
-                if (!non) fine[e] |= x << s;
-                if (non && (nan || !(x & 0x8000u))) up[e] |= 0x3f80u << s;
-                if (non && (nan || (x & 0x8000u))) dn[e] |= 0x3f80u << s;
-              }
-            }
-            auto frag = [](const uint32_t(&w)[4]) {
-              return __builtin_bit_cast(bf16x8, make_uint4(w[0], w[1], w[2], w[3]));
-            };
-            acc[db] = mma32(frag(fine), b[kb], acc[db]);
-            pos = mma32(frag(up), frag(mag), pos);
-            neg = mma32(frag(dn), frag(mag), neg);
-          }
-#pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const float u = pos[r] > 0.f ? INF : 0.f, w = neg[r] > 0.f ? -INF : 0.f;
-            acc[db][r] += FWD ? u + w : (u - w == 0.f ? 0.f : __builtin_nanf(""));
-          }
-        }
-        return;
-      }
-    }
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-      for (int db = 0; db < DB; ++db) acc[db] = mma32(trans_frag<DP>(tile, row0, kb, db, lane), b[kb], acc[db]);
-  } else {
-    if (guard) {
-      bool bad = false;
-#pragma unroll 1
-      for (int db = 0; db < DB; ++db)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) bad |= !__builtin_isfinite(trans_elem<DP>(tile, row0, r, db, lane));
-      if (__any(bad)) {
-#pragma unroll
-        for (int db = 0; db < DB; ++db) {
-          __builtin_amdgcn_sched_barrier(0);  // one block's registers at a time
-          f32x16 pos = zero16(), neg = zero16();
-#pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const float x = trans_elem<DP>(tile, row0, r, db, lane);
-            const bool non = !__builtin_isfinite(x), nan = x != x;
-            acc[db] = __builtin_amdgcn_mfma_f32_32x32x2f32(non ? 0.f : x, p[r], acc[db], 0, 0, 0);
-            pos = __builtin_amdgcn_mfma_f32_32x32x2f32(nan || x == INF ? 1.f : 0.f, fabsf(p[r]), pos, 0, 0, 0);
-            neg = __builtin_amdgcn_mfma_f32_32x32x2f32(nan || x == -INF ? 1.f : 0.f, fabsf(p[r]), neg, 0, 0, 0);
-          }
-#pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const float u = pos[r] > 0.f ? INF : 0.f, w = neg[r] > 0.f ? -INF : 0.f;
-            acc[db][r] += FWD ? u + w : (u - w == 0.f ? 0.f : __builtin_nanf(""));
-          }
-        }
-        return;
-      }
-    }
-#pragma unroll
-    for (int r = 0; r < 16; ++r)
-#pragma unroll
-      for (int db = 0; db < DB; ++db)
-        acc[db] = __builtin_amdgcn_mfma_f32_32x32x2f32(trans_elem<DP>(tile, row0, r, db, lane), p[r], acc[db], 0, 0, 0);
-  }
+  for (int i = 0; i < 2; ++i)
+    b.f[i] = __builtin_bit_cast(bf16x8, make_uint4(pack_bf16x2(p[8 * i], p[8 * i + 1]), pack_bf16x2(p[8 * i + 2], p[8 * i + 3]),
+                                                   pack_bf16x2(p[8 * i + 4], p[8 * i + 5]), pack_bf16x2(p[8 * i + 6], p[8 * i + 7])));
+  return b;
+}
+template <typename T, int DP>
+__device__ __forceinline__ void acc_trans(f32x16 (&acc)[DP / 32], const f32x16& p, const char* tile, int row0, int lane) {
+  if constexpr (sizeof(T) == 2) mma_trans<DP>(acc, round_pair(p).f, tile, row0, lane);
+  else mma_trans<DP>(acc, p, tile, row0, lane);
 }
 
 // maximum and sum of a lane and its partner 32 away
@@ -296,6 +225,69 @@ struct KeyTiles {
   }
   __device__ int at(int i) const { return i < ns ? i : tl + (i - ns); }
 };
+
+// ------------------------------------------------------------------ non-finite tokens
+// In the matrix products a masked probability is a zero, and a zero times a
+// NaN or infinity of a token that the row does not see is a NaN.  A result
+// that is not finite although its row's statistics are is therefore summed
+// again, one key (or row) after another and only those that it sees, by its
+// wave: lane l holds elements l and l + 64 of a head's row.  Finite inputs
+// cost no more than the test of the results.
+template <typename T>
+struct Lane2 {
+  float x[2];
+  __device__ __forceinline__ Lane2(const char* row, int d, int lane) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int c = lane + 64 * j;
+      x[j] = 0.f;
+      if (c < d) {
+        if constexpr (sizeof(T) == 4) x[j] = reinterpret_cast<const float*>(row)[c];
+        else x[j] = bf2f(reinterpret_cast<const bf16_t*>(row)[c].x);
+      }
+    }
+  }
+  __device__ __forceinline__ float dot(const Lane2& o) const { return wave_sum(x[0] * o.x[0] + x[1] * o.x[1]); }
+};
+template <typename T>
+__device__ __forceinline__ void store_lane2(char* row, const float (&x)[2], int d, int lane) {
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    if (lane + 64 * j < d) io_traits<T>::store(reinterpret_cast<T*>(row) + lane + 64 * j, x[j]);
+}
+__device__ __forceinline__ float of_lane(float x, int lane) { return __shfl(x, lane, WAVE); }
+__device__ __forceinline__ int of_lane(int x, int lane) { return __shfl(x, lane, WAVE); }
+
+// the columns (of 32) with a value that is not finite, as a mask
+template <int DB>
+__device__ __forceinline__ uint32_t not_finite(const f32x16 (&a)[DB]) {
+  bool bad = false;
+#pragma unroll
+  for (int db = 0; db < DB; ++db)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) bad |= !__builtin_isfinite(a[db][r]);
+  const uint64_t b = __ballot(bad);
+  return (uint32_t)(b | (b >> 32));
+}
+
+// sum of exp2(c q.k - m) v over the visible keys of tiles i0, i0 + di .. < i1
+template <typename T>
+__device__ __forceinline__ void slow_o(float (&x)[2], const char* q, const char* kb, int64_t kl, const char* vb,
+                                       int64_t vl, const AttnArgs& a, int p, float m, const KeyTiles& kt, int i0,
+                                       int i1, int di, int bn, int lane) {
+  const Lane2<T> qq(q, a.d, lane);
+  x[0] = x[1] = 0.f;
+#pragma unroll 1
+  for (int i = i0; i < i1; i += di)
+#pragma unroll 1
+    for (int j = kt.at(i) * bn; j < kt.at(i) * bn + bn && j <= p; ++j) {
+      if (j <= p - a.window && j >= a.sinks) continue;
+      const float pr = __builtin_amdgcn_exp2f(fmaf(qq.dot(Lane2<T>(kb + j * kl, a.d, lane)), a.c, -m));
+      const Lane2<T> v(vb + j * vl, a.d, lane);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) x[e] = fmaf(pr, v.x[e], x[e]);
+    }
+}
 
 // ------------------------------------------------------------------ forward
 // A wave's 32 rows: running maximum and sum, and O^T.
@@ -367,7 +359,7 @@ struct AttnRows {
       }
     }
 #pragma unroll
-    for (int i = 0; i < SB; ++i) mma_trans<T, DP, true>(o, s[i], vt, 32 * i, lane, !whole);
+    for (int i = 0; i < SB; ++i) acc_trans<T, DP>(o, s[i], vt, 32 * i, lane);
   }
 };
 
@@ -451,12 +443,21 @@ __global__ __launch_bounds__(256, (attn_waves<T, DP>())) void attn_fwd_kernel(At
       w.template step<BN / 32>(t, t + TB, kt.at(i) * BN, a.window, a.sinks, a.c, lane);
     }
   }
-  const float l = pair_sum(w.l);
+  const float l = pair_sum(w.l), inv = l > 0.f || l != l ? 1.f / l : 0.f;
+  char* out = a.out + at.b * a.so.b + at.h * a.so.h;
   if (row < qlen) {
-    store_rows<T, DP>(w.o, l > 0.f || l != l ? 1.f / l : 0.f, a.out + at.b * a.so.b + at.h * a.so.h + row * a.so.l,
-                      a.d, lane);
+    store_rows<T, DP>(w.o, inv, out + row * a.so.l, a.d, lane);
     if (a.lse && lane < 32)
       a.lse[((int64_t)at.b * a.H + at.h) * a.Lq + row] = l == 0.f ? -__builtin_huge_valf() : w.m * LN2 + logf(l);
+  }
+  for (uint32_t bad = not_finite(w.o) & (uint32_t)__ballot(row < qlen && l == l); bad; bad &= bad - 1) {
+    const int n = __builtin_ctz(bad), r = r0 + 32 * wave + n;
+    const float f = of_lane(inv, n);
+    float x[2];
+    slow_o<T>(x, a.q + at.b * a.sq.b + at.h * a.sq.h + r * a.sq.l, kb, a.sk.l, vb, a.sv.l, a, off + r, of_lane(w.m, n),
+              kt, 0, kt.total, 1, BN, lane);
+    x[0] *= f, x[1] *= f;
+    store_lane2<T>(out + r * a.so.l, x, a.d, lane);
   }
 }
 
@@ -516,6 +517,14 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(AttnArgs a) {
 #pragma unroll
     for (int r = 0; r < 16; ++r) mine[(32 * db + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) * 32 + n] = w.o[db][r];
   const float lsum = pair_sum(w.l);
+  for (uint32_t bad = not_finite(w.o) & (uint32_t)__ballot(lsum == lsum); bad; bad &= bad - 1) {
+    const int i = __builtin_ctz(bad), r = of_lane(row, i), t = min(r % a.Lq, qlen - 1);
+    float x[2];
+    slow_o<T>(x, a.q + b * a.sq.b + (int64_t)(hk * a.G + r / a.Lq) * a.sq.h + t * a.sq.l, kb, a.sk.l, vb, a.sv.l, a,
+              off + t, of_lane(w.m, i), kt, i0 + wave, i1, NW, 32, lane);
+    mine[lane * 32 + i] = x[0];
+    if (lane + 64 < DP) mine[(lane + 64) * 32 + i] = x[1];
+  }
   if (lane < 32) {
     mine[DP * 32 + n] = w.m;
     mine[DP * 32 + 32 + n] = lsum;
@@ -598,12 +607,24 @@ __global__ __launch_bounds__(64) void attn_join_kernel(AttnArgs a) {
 
 // ------------------------------------------------------------------ backward: dq
 // As the forward, with dP^T = V dO^T beside S^T and dq^T += K^T dS^T.  Lane n
-// holds half of its row's dO and o: D = dO.o costs no launch of its own and
-// is left in `delta` for the dk, dv kernel.
+// holds half of its row's dO and o: D = dO.o costs no launch of its own.
+//
+// bf16: a row's dS sum to zero, sum_j P (dO.v - D) = 0, so that any vector may
+// be taken off all keys.  With the rounded dS, and D from a rounded o, they
+// do not, and what is left meets the keys' common part, which is larger than
+// their spread where a few keys take much of every row.  The kernel takes off
+// the row's mean key: with R the sum of the rounded dS,
+//   dq = scale (sum_j dS_j k_j - R sum_j P_j k_j),
+// for one more product that reads no operand anew; and D + sum_j dS_j, the
+// unrounded sum, is the exact D, which is left in `delta` for the dk, dv
+// kernel.  Relative error of dq against fp64 where first tokens draw
+// attention: 2.2e-3 for 2.8e-3 to 3.8e-3 without (1.7e-3 is the result's own
+// rounding).
 template <typename T, int DP>
 __global__ __launch_bounds__(256, (attn_waves<T, DP>())) void attn_dq_kernel(AttnArgs a) {
   using Tile = AttnTile<T, DP>;
   constexpr int NW = 4, BM = 32 * NW, BN = attn_bn<T, DP>(), TB = BN * Tile::CPR * 16, STEPS = Tile::STEPS;
+  constexpr bool CENTRE = sizeof(T) == 2;
   __shared__ __align__(1024) char lds[4 * TB];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const AttnPlace at(xcd_remap(blockIdx.x, gridDim.x), a);
@@ -611,20 +632,22 @@ __global__ __launch_bounds__(256, (attn_waves<T, DP>())) void attn_dq_kernel(Att
   const int r0 = at.tile * BM, off = klen - qlen, n = lane & 31;
   const int row = r0 + 32 * wave + n, cmax = a.d * (int)sizeof(T) / 16 - 1;
   const int64_t stat = ((int64_t)at.b * a.H + at.h) * a.Lq + row;
-  char* dqrow = a.dq + at.b * a.sdq.b + at.h * a.sdq.h + (int64_t)row * a.sdq.l;
   f32x16 dq[DP / 32];
 #pragma unroll
   for (int db = 0; db < DP / 32; ++db) dq[db] = zero16();
+  const char* kb = a.k + at.b * a.sk.b + at.hk * a.sk.h;
+  const char* vb = a.v + at.b * a.sv.b + at.hk * a.sv.h;
+  const char* qb = a.q + at.b * a.sq.b + at.h * a.sq.h;
+  const char* gb = a.dO + at.b * a.sdo.b + at.h * a.sdo.h;
+  float delta = 0.f, lse2 = 0.f;
+  const KeyTiles kt(off + r0, off + min(r0 + BM, qlen) - 1, a.window, a.sinks, BN);
   if (r0 < qlen) {
-    const char* kb = a.k + at.b * a.sk.b + at.hk * a.sk.h;
-    const char* vb = a.v + at.b * a.sv.b + at.hk * a.sv.h;
     const int64_t rc = min(row, qlen - 1);
     Frag<T> q[STEPS], g[STEPS];
-    float delta = 0.f;
     {
       Frag<T> o[STEPS];
-      load_rows(q, a.q + at.b * a.sq.b + at.h * a.sq.h + rc * a.sq.l, cmax, lane);
-      load_rows(g, a.dO + at.b * a.sdo.b + at.h * a.sdo.h + rc * a.sdo.l, cmax, lane);
+      load_rows(q, qb + rc * a.sq.l, cmax, lane);
+      load_rows(g, gb + rc * a.sdo.l, cmax, lane);
       load_rows(o, a.o + at.b * a.so.b + at.h * a.so.h + rc * a.so.l, cmax, lane);
 #pragma unroll
       for (int s = 0; s < STEPS; ++s)
@@ -632,10 +655,12 @@ __global__ __launch_bounds__(256, (attn_waves<T, DP>())) void attn_dq_kernel(Att
         for (int e = 0; e < 16 / (int)sizeof(T); ++e) delta = fmaf((float)g[s][e], (float)o[s][e], delta);
     }
     delta = pair_sum(delta);
-    if (row < qlen && lane < 32) a.delta[stat] = delta;
-    const float lse2 = (row < qlen ? a.lse[stat] : 0.f) * LOG2E;
+    float sum = 0.f, rsum = 0.f;
+    f32x16 kbar[CENTRE ? DP / 32 : 1];
+#pragma unroll
+    for (auto& x : kbar) x = zero16();
+    lse2 = (row < qlen ? a.lse[stat] : 0.f) * LOG2E;
     const int p = off + row, w_lo = off + r0 + 32 * wave, w_hi = off + min(r0 + 32 * wave + 31, qlen - 1);
-    const KeyTiles kt(off + r0, off + min(r0 + BM, qlen) - 1, a.window, a.sinks, BN);
     auto issue = [&](int i) {
       char* t = lds + (i & 1) * 2 * TB;
       const int k0 = kt.at(i) * BN;
@@ -660,26 +685,81 @@ __global__ __launch_bounds__(256, (attn_waves<T, DP>())) void attn_dq_kernel(Att
           s = mma32(row_frag<T, DP>(t, 32 * sb, st, lane), q[st], s);
           dp = mma32(row_frag<T, DP>(t + TB, 32 * sb, st, lane), g[st], dp);
         }
+        f32x16 ds;
 #pragma unroll
-        for (int r = 0; r < 16; ++r)
-          s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], a.c, -lse2)) * (dp[r] - delta);
+        for (int r = 0; r < 16; ++r) {
+          s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], a.c, -lse2));
+          ds[r] = s[r] * (dp[r] - delta);
+        }
         if (!whole) {
           const int lo = p - a.window;
 #pragma unroll
           for (int r = 0; r < 16; ++r) {
             const int key = k0 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
-            if (!(key <= p && (key > lo || key < a.sinks))) s[r] = 0.f;
+            const bool see = key <= p && (key > lo || key < a.sinks);
+            s[r] = see ? s[r] : 0.f;
+            ds[r] = see ? ds[r] : 0.f;
           }
         }
-        mma_trans<T, DP, false>(dq, s, t, 32 * sb, lane, !whole);
+        if constexpr (CENTRE) {
+          const Pair x = round_pair(ds), y = round_pair(s);
+#pragma unroll
+          for (int r = 0; r < 16; ++r) sum += ds[r];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+            const bf16x2 one = {(__bf16)1.f, (__bf16)1.f};
+#pragma unroll
+            for (int r = 0; r < 8; r += 2)
+              rsum = __builtin_amdgcn_fdot2_f32_bf16(bf16x2{x.f[e][r], x.f[e][r + 1]}, one, rsum, false);
+          }
+#pragma unroll
+          for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int db = 0; db < DP / 32; ++db) {
+              const bf16x8 k = trans_frag<DP>(t, 32 * sb, kb, db, lane);
+              dq[db] = mma32(k, x.f[kb], dq[db]);
+              kbar[db] = mma32(k, y.f[kb], kbar[db]);
+            }
+        } else {
+          mma_trans<DP>(dq, ds, t, 32 * sb, lane);
+        }
       }
     }
+    if constexpr (CENTRE) {
+      rsum = pair_sum(rsum);
+      delta += pair_sum(sum);
+#pragma unroll
+      for (int db = 0; db < DP / 32; ++db)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) dq[db][r] = fmaf(-rsum, kbar[db][r], dq[db][r]);
+    }
+    if (row < qlen && lane < 32) a.delta[stat] = delta;
   }
   if (row >= qlen) {  // what a clamped row gathered, finite or not, is nothing
 #pragma unroll
     for (int db = 0; db < DP / 32; ++db) dq[db] = zero16();
   }
-  if (row < a.Lq) store_rows<T, DP>(dq, a.scale, dqrow, a.d, lane);
+  char* out = a.dq + at.b * a.sdq.b + at.h * a.sdq.h;
+  if (row < a.Lq) store_rows<T, DP>(dq, a.scale, out + (int64_t)row * a.sdq.l, a.d, lane);
+  for (uint32_t bad = not_finite(dq) & (uint32_t)__ballot(lse2 == lse2 && delta == delta); bad; bad &= bad - 1) {
+    const int i = __builtin_ctz(bad), r = r0 + 32 * wave + i;
+    const float ls = of_lane(lse2, i), de = of_lane(delta, i);
+    const Lane2<T> q(qb + r * a.sq.l, a.d, lane), g(gb + r * a.sdo.l, a.d, lane);
+    float x[2] = {0.f, 0.f};
+#pragma unroll 1
+    for (int t = 0; t < kt.total; ++t)
+#pragma unroll 1
+      for (int j = kt.at(t) * BN; j < kt.at(t) * BN + BN && j <= off + r; ++j) {
+        if (j <= off + r - a.window && j >= a.sinks) continue;
+        const Lane2<T> k(kb + j * a.sk.l, a.d, lane), v(vb + j * a.sv.l, a.d, lane);
+        const float ds = __builtin_amdgcn_exp2f(fmaf(q.dot(k), a.c, -ls)) * (g.dot(v) - de);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) x[e] = fmaf(ds, k.x[e], x[e]);
+      }
+    x[0] *= a.scale, x[1] *= a.scale;
+    store_lane2<T>(out + r * a.sdq.l, x, a.d, lane);
+  }
 }
 
 // ------------------------------------------------------------------ backward: dk, dv
@@ -794,21 +874,56 @@ __global__ __launch_bounds__(256, 1) void attn_dkv_kernel(AttnArgs a) {
             ds[4 * g + e] = d;
           }
         }
-        mma_trans<T, DP, false>(dv, s, t + TB, 32 * sb, lane, !whole);
-        mma_trans<T, DP, false>(dk, ds, t, 32 * sb, lane, !whole);
+        acc_trans<T, DP>(dv, s, t + TB, 32 * sb, lane);
+        acc_trans<T, DP>(dk, ds, t, 32 * sb, lane);
       }
       if (i + 1 < total) put(i + 1);
     }
   }
-  if (tile < a.sink_tiles && a.splits > 1) {
-    // [batch x key head][sink tile][split][dk, dv][key][d]
-    const int64_t slot = ((int64_t)bk * a.sink_tiles + tile) * a.splits + split;
-    float* pr = a.part + (slot * 2 * BK + 32 * wave + n) * a.d;
-    store_rows<float, DP>(dk, 1.f, reinterpret_cast<char*>(pr), a.d, lane);
-    store_rows<float, DP>(dv, 1.f, reinterpret_cast<char*>(pr + (int64_t)BK * a.d), a.d, lane);
+  const bool parts = tile < a.sink_tiles && a.splits > 1;
+  // [batch x key head][sink tile][split][dk, dv][key][d]
+  float* pk = a.part + (((int64_t)bk * a.sink_tiles + tile) * a.splits + split) * 2 * BK * a.d;
+  char* ok = a.dk + b * a.sdk.b + hk * a.sdk.h;
+  char* ov = a.dv + b * a.sdv.b + hk * a.sdv.h;
+  if (parts) {
+    float* to = pk + (32 * wave + n) * a.d;
+    store_rows<float, DP>(dk, 1.f, reinterpret_cast<char*>(to), a.d, lane);
+    store_rows<float, DP>(dv, 1.f, reinterpret_cast<char*>(to + BK * a.d), a.d, lane);
   } else if (key < a.Lk) {
-    store_rows<T, DP>(dk, key < klen ? a.scale : 0.f, a.dk + b * a.sdk.b + hk * a.sdk.h + (int64_t)key * a.sdk.l, a.d, lane);
-    store_rows<T, DP>(dv, key < klen ? 1.f : 0.f, a.dv + b * a.sdv.b + hk * a.sdv.h + (int64_t)key * a.sdv.l, a.d, lane);
+    store_rows<T, DP>(dk, a.scale, ok + (int64_t)key * a.sdk.l, a.d, lane);
+    store_rows<T, DP>(dv, 1.f, ov + (int64_t)key * a.sdv.l, a.d, lane);
+  }
+  for (uint32_t bad = (not_finite(dk) | not_finite(dv)) & (uint32_t)__ballot(key < klen); bad; bad &= bad - 1) {
+    const int i = __builtin_ctz(bad), j = k0 + 32 * wave + i;
+    const Lane2<T> k(a.k + b * a.sk.b + hk * a.sk.h + j * a.sk.l, a.d, lane);
+    const Lane2<T> v(a.v + b * a.sv.b + hk * a.sv.h + j * a.sv.l, a.d, lane);
+    float x[2] = {0.f, 0.f}, y[2] = {0.f, 0.f};
+#pragma unroll 1
+    for (int h = hk * a.G; h < (hk + 1) * a.G; ++h)
+#pragma unroll 1
+      for (int p = max(max(p_lo, j), off); p <= p_hi; ++p) {
+        if (j <= p - a.window && j >= a.sinks) break;
+        const int r = p - off;
+        const int64_t st = ((int64_t)b * a.H + h) * a.Lq + r;
+        const Lane2<T> q(a.q + b * a.sq.b + h * a.sq.h + r * a.sq.l, a.d, lane);
+        const Lane2<T> g(a.dO + b * a.sdo.b + h * a.sdo.h + r * a.sdo.l, a.d, lane);
+        const float pr = __builtin_amdgcn_exp2f(fmaf(q.dot(k), a.c, -a.lse[st] * LOG2E));
+        const float ds = pr * (g.dot(v) - a.delta[st]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          x[e] = fmaf(ds, q.x[e], x[e]);
+          y[e] = fmaf(pr, g.x[e], y[e]);
+        }
+      }
+    if (parts) {
+      float* to = pk + (32 * wave + i) * a.d;
+      store_lane2<float>(reinterpret_cast<char*>(to), x, a.d, lane);
+      store_lane2<float>(reinterpret_cast<char*>(to + BK * a.d), y, a.d, lane);
+    } else {
+      x[0] *= a.scale, x[1] *= a.scale;
+      store_lane2<T>(ok + j * a.sdk.l, x, a.d, lane);
+      store_lane2<T>(ov + j * a.sdv.l, y, a.d, lane);
+    }
   }
 }
 
