@@ -28,6 +28,9 @@ namespace lact {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
+// instruction kinds of __builtin_amdgcn_sched_group_barrier
+constexpr int SG_VALU = 0x2, SG_MFMA = 0x8, SG_LDS = 0x100;
+
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 
@@ -88,6 +91,46 @@ struct AttnTile {
       const int row = s / CPR, c = min((s % CPR) ^ f(row), cmax);
       const int gr = max(0, min(row0 + row, rmax));
       dma16(base + (int64_t)gr * stride + c * 16, m0 + (uint32_t)(i * NW * WAVE * 16));
+    }
+  }
+};
+
+// One direct load of 16 bytes a lane from a uniform base and a lane's offset.
+__device__ __forceinline__ void dma16_at(uint32_t off, const char* base, uint32_t m0) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+               :
+               : "v"(off), "s"(base), "s"(m0)
+               : "memory", "m0");
+}
+
+// AttnTile::stage with the lanes' offsets kept: a tile inside the matrix then
+// costs no vector arithmetic (forward of a 32K prompt: 40 of 143 vector
+// instructions per 32 x 32 scores were addresses).
+template <typename T, int DP, int R, int NW>
+struct Stager {
+  using Tile = AttnTile<T, DP>;
+  static constexpr int N = R * Tile::CPR / (WAVE * NW);
+  static constexpr int64_t FAR = (INT64_C(1) << 31) / R;  // row strides whose offsets need more than 32 bits
+  const char* base;
+  int64_t stride;
+  int rmax, cmax, wave, lane;
+  uint32_t off[N];
+  __device__ __forceinline__ Stager(const char* base_, int64_t stride_, int rmax_, int cmax_, int wave_, int lane_)
+      : base(base_), stride(stride_), rmax(rmax_), cmax(cmax_), wave(wave_), lane(lane_) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int s = (i * NW + wave) * WAVE + lane, row = s / Tile::CPR;
+      off[i] = (uint32_t)row * (uint32_t)stride + (uint32_t)min((s % Tile::CPR) ^ Tile::f(row), cmax) * 16u;
+    }
+  }
+  __device__ __forceinline__ void issue(char* tile, int row0) const {
+    if (row0 >= 0 && row0 + R - 1 <= rmax && stride < FAR) {
+      const char* b = base + (int64_t)row0 * stride;
+      const uint32_t m0 = __builtin_amdgcn_readfirstlane(lds_off(tile) + (uint32_t)(wave * WAVE * 16));
+#pragma unroll
+      for (int i = 0; i < N; ++i) dma16_at(off[i], b, m0 + (uint32_t)(i * NW * WAVE * 16));
+    } else {
+      Tile::template stage<R, NW>(tile, base, stride, row0, rmax, cmax, wave, lane);
     }
   }
 };
@@ -156,6 +199,39 @@ __device__ __forceinline__ float trans_elem(const char* tile, int row0, int r, i
   return *reinterpret_cast<const float*>(tile + AttnTile<float, DP>::at(row, col >> 2) + (col & 3) * 4);
 }
 
+// A lane's offsets into a bf16 tile, formed once: with the tile's place and a
+// block's first row as constants, every read's address is one of these
+// registers and an immediate.
+typedef const __attribute__((address_space(3))) char* lds_ptr;
+template <int DP>
+struct AttnAddr {
+  using Tile = AttnTile<bf16_t, DP>;
+  static constexpr int STEPS = Tile::STEPS, DB = DP / 32, ROW = Tile::CPR * 16;
+  int r[STEPS], t[DB][2];
+  __device__ __forceinline__ explicit AttnAddr(int lane) {
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) r[s] = Tile::at(lane & 31, 2 * s + (lane >> 5));
+    const int j = lane & 15, row = 4 * (lane >> 5) + (j >> 2);
+#pragma unroll
+    for (int db = 0; db < DB; ++db)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        t[db][i] = Tile::at(row + 8 * i, 4 * db + 2 * ((lane >> 4) & 1) + ((j & 3) >> 1)) + (j & 1) * 8;
+  }
+  // operand of a row product: rows row0 .. row0 + 31 (row0 a multiple of 32), step s
+  __device__ __forceinline__ bf16x8 rows(lds_ptr tile, int row0, int s) const {
+    return *reinterpret_cast<const __attribute__((address_space(3))) bf16x8*>(tile + r[s] + row0 * ROW);
+  }
+  // transposed operand: rows row0 .. row0 + 15 (row0 a multiple of 16), columns 32 db .. 32 db + 31
+  __device__ __forceinline__ bf16x8 cols(lds_ptr tile, int row0, int db) const {
+    const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(tile + t[db][0] + row0 * ROW));
+    const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(tile + t[db][1] + row0 * ROW));
+    typedef short v8s __attribute__((ext_vector_type(8)));
+    const v8s v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    return __builtin_bit_cast(bf16x8, v);
+  }
+};
+
 // acc^T[d x lane] += sum over the tile's 32 rows from row0 of row^T p, with p
 // in the layout a 32x32 product leaves.
 template <int DP>
@@ -212,6 +288,14 @@ __device__ __forceinline__ int seq_len(const int64_t* lens, int b, int most) {
   const int64_t n = lens[b];
   return (int)(n < 0 ? 0 : n > most ? most : n);
 }
+
+// Whether the row at position p sees key k + o, for a run of offsets o
+struct Seen {
+  int hi, lo, first;
+  __device__ __forceinline__ Seen(int p, int k, int window, int sinks)
+      : hi(p - k), lo(p - window - k), first(sinks - k) {}
+  __device__ __forceinline__ bool operator()(int o) const { return (o <= hi) & ((o > lo) | (o < first)); }
+};
 
 // The key tiles of BN keys that rows at positions p_lo .. p_hi can see: the
 // `ns` first ones for the sinks, then those from `tl` on for the window.
@@ -307,38 +391,26 @@ struct AttnRows {
     l = 0.f;
   }
 
-  // keys k0 .. k0 + 32 SB - 1, in LDS tiles of as many rows
-  template <int SB>
-  __device__ __forceinline__ void step(const char* kt, const char* vt, int k0, int window, int sinks, float c,
-                                       int lane) {
-    const int k1 = k0 + 32 * SB - 1;
-    if (k0 > w_hi || (k1 <= w_lo - window && k0 >= sinks)) return;  // no row sees any of it
-    const bool whole = k1 <= w_lo && (k0 > w_hi - window || k1 < sinks);
-    f32x16 s[SB];
+  // scores of the 32 keys from row `at` of a tile
+  __device__ __forceinline__ f32x16 scores(const char* kt, int at, int lane) const {
+    f32x16 s = zero16();
 #pragma unroll
-    for (int i = 0; i < SB; ++i) s[i] = zero16();
+    for (int t = 0; t < STEPS; ++t) s = mma32(row_frag<T, DP>(kt, at, t, lane), q[t], s);
+    return s;
+  }
+  __device__ __forceinline__ void mask(f32x16& s, int k0, int window, int sinks, int lane) const {
+    const Seen seen(p, k0 + 4 * (lane >> 5), window, sinks);
 #pragma unroll
-    for (int t = 0; t < STEPS; ++t)
+    for (int r = 0; r < 16; ++r) s[r] = seen(8 * (r >> 2) + (r & 3)) ? s[r] : -__builtin_huge_valf();
+  }
+  // The sums are taken relative to m, which may lag behind the largest score:
+  // exp2 of up to 8 loses nothing in fp32, and most tiles then rescale
+  // nothing.  `held`: probabilities that are not in o yet.
+  __device__ __forceinline__ void follow(const f32x16& s, float c, f32x16* held) {
+    float top = s[0];
 #pragma unroll
-      for (int i = 0; i < SB; ++i) s[i] = mma32(row_frag<T, DP>(kt, 32 * i, t, lane), q[t], s[i]);
-    if (!whole) {
-      const int h4 = 4 * (lane >> 5), lo = p - window;
-#pragma unroll
-      for (int i = 0; i < SB; ++i)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int key = k0 + 32 * i + 8 * (r >> 2) + (r & 3) + h4;
-          if (!(key <= p && (key > lo || key < sinks))) s[i][r] = -__builtin_huge_valf();
-        }
-    }
-    float top = s[0][0];
-#pragma unroll
-    for (int i = 0; i < SB; ++i)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) top = fmaxf(top, s[i][r]);
+    for (int r = 1; r < 16; ++r) top = fmaxf(top, s[r]);
     top = pair_max(top) * c;
-    // The sums are taken relative to m, which may lag: exp2 of up to 8 loses
-    // nothing in fp32, and most tiles then rescale nothing.
     if (__any(top > m + 8.f)) {
       const float to = fmaxf(m, top);
       const float a = to == m ? 1.f : __builtin_amdgcn_exp2f(m - to);
@@ -348,18 +420,107 @@ struct AttnRows {
       for (int db = 0; db < DB; ++db)
 #pragma unroll
         for (int r = 0; r < 16; ++r) o[db][r] *= a;
-    }
-    const float ref = m == -__builtin_huge_valf() ? 0.f : m;  // nothing seen yet: every term is exp2(-inf)
+      if (held) {
 #pragma unroll
-    for (int i = 0; i < SB; ++i) {
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        s[i][r] = __builtin_amdgcn_exp2f(fmaf(s[i][r], c, -ref));
-        l += s[i][r];
+        for (int r = 0; r < 16; ++r) (*held)[r] *= a;
       }
     }
+  }
+  __device__ __forceinline__ void exps(f32x16& s, float c) {
+    const float ref = m == -__builtin_huge_valf() ? 0.f : m;  // nothing seen yet: every term is exp2(-inf)
 #pragma unroll
-    for (int i = 0; i < SB; ++i) acc_trans<T, DP>(o, s[i], vt, 32 * i, lane);
+    for (int r = 0; r < 16; ++r) {
+      s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, -ref));
+      l += s[r];
+    }
+  }
+  // whether some row sees some of the keys k0 .. k1; whether all see all
+  __device__ __forceinline__ bool some(int k0, int k1, int window, int sinks) const {
+    return !(k0 > w_hi || (k1 <= w_lo - window && k0 >= sinks));
+  }
+  __device__ __forceinline__ bool whole(int k0, int k1, int window, int sinks) const {
+    return k1 <= w_lo && (k0 > w_hi - window || k1 < sinks);
+  }
+  // 32 keys, in LDS tiles of as many rows
+  __device__ __forceinline__ void step(const char* kt, const char* vt, int k0, int window, int sinks, float c,
+                                       int lane) {
+    f32x16 s = scores(kt, 0, lane);
+    if (!whole(k0, k0 + 31, window, sinks)) mask(s, k0, window, sinks, lane);
+    follow(s, c, nullptr);
+    exps(s, c);
+    acc_trans<T, DP>(o, s, vt, 0, lane);
+  }
+  // 64 keys that every row sees: the matrix products of one half run beside the exponentials of
+  // the other, and the operands of a product are read while the one before it
+  // runs, so that one wave keeps matrix pipe, vector pipe and LDS busy.  The
+  // scheduling groups spell that order out; left to itself the compiler reads
+  // an operand just before its product and waits.
+  __device__ __forceinline__ void step2(const AttnAddr<DP>& at, lds_ptr kt, lds_ptr vt, float c) {
+    static_assert(sizeof(T) == 2, "bf16");
+    constexpr int NV = 2 * DB;  // V fragments of 32 keys
+    Frag<T> ka[STEPS], kb[STEPS];
+    bf16x8 va[NV], vb[NV];
+    auto load_k = [&](Frag<T>(&f)[STEPS], int row) {
+#pragma unroll
+      for (int t = 0; t < STEPS; ++t) f[t] = at.rows(kt, row, t);
+    };
+    auto load_v = [&](bf16x8(&f)[NV], int row) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) f[i] = at.cols(vt, row + 16 * (i / DB), i % DB);
+    };
+    auto product = [&](const Frag<T>(&f)[STEPS]) {
+      f32x16 s = zero16();
+#pragma unroll
+      for (int t = 0; t < STEPS; ++t) s = mma32(f[t], q[t], s);
+      return s;
+    };
+    auto add = [&](const bf16x8(&f)[NV], const Pair& b) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) o[i % DB] = mma32(f[i], b.f[i / DB], o[i % DB]);
+    };
+    load_k(ka, 0);
+    f32x16 s0 = product(ka);
+    __builtin_amdgcn_sched_group_barrier(SG_LDS, STEPS, 0);
+    __builtin_amdgcn_sched_group_barrier(SG_MFMA, STEPS, 0);
+    follow(s0, c, nullptr);
+
+    load_k(kb, 32);
+    f32x16 s1 = product(kb);
+    exps(s0, c);
+    __builtin_amdgcn_sched_group_barrier(SG_LDS, 4, 1);
+    __builtin_amdgcn_sched_group_barrier(SG_VALU, 8, 1);
+#pragma unroll
+    for (int t = 0; t < STEPS; ++t) {
+      __builtin_amdgcn_sched_group_barrier(SG_MFMA, 1, 1);
+      if (t + 4 < STEPS) __builtin_amdgcn_sched_group_barrier(SG_LDS, 1, 1);
+      __builtin_amdgcn_sched_group_barrier(SG_VALU, 40 / STEPS, 1);
+    }
+    asm volatile("" : "+v"(s0));  // the exponentials stay on this side of the branch
+    follow(s1, c, &s0);
+
+    load_v(va, 0);
+    add(va, round_pair(s0));
+    exps(s1, c);
+    __builtin_amdgcn_sched_group_barrier(SG_LDS, 4, 2);
+    __builtin_amdgcn_sched_group_barrier(SG_VALU, 12, 2);
+#pragma unroll
+    for (int t = 0; t < NV; ++t) {
+      __builtin_amdgcn_sched_group_barrier(SG_MFMA, 1, 2);
+      if (t + 2 < NV) __builtin_amdgcn_sched_group_barrier(SG_LDS, 2, 2);
+      __builtin_amdgcn_sched_group_barrier(SG_VALU, 48 / NV, 2);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    load_v(vb, 32);
+    add(vb, round_pair(s1));
+  }
+  // BN keys of which a row may see some or none
+  template <int BN>
+  __device__ __forceinline__ void tile(const char* kt, const char* vt, int k0, int window, int sinks, float c,
+                                       int lane) {
+#pragma unroll 1
+    for (int i = 0; i < BN; i += 32)
+      if (some(k0 + i, k0 + i + 31, window, sinks))
+        step(kt + i * AttnTile<T, DP>::CPR * 16, vt + i * AttnTile<T, DP>::CPR * 16, k0 + i, window, sinks, c, lane);
   }
 };
 
@@ -411,7 +572,7 @@ __global__ __launch_bounds__(256, (attn_waves<T, DP>())) void attn_fwd_kernel(At
   using Tile = AttnTile<T, DP>;
   constexpr int NW = 4, BM = 32 * NW, BN = attn_bn<T, DP>(), TB = BN * Tile::CPR * 16;
   __shared__ __align__(1024) char lds[4 * TB];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const AttnPlace at(xcd_remap(blockIdx.x, gridDim.x), a);
   const int qlen = seq_len(a.q_lens, at.b, a.Lq), klen = seq_len(a.k_lens, at.b, a.Lk);
   const int r0 = at.tile * BM, off = klen - qlen;
@@ -426,23 +587,49 @@ __global__ __launch_bounds__(256, (attn_waves<T, DP>())) void attn_fwd_kernel(At
   w.w_lo = off + r0 + 32 * wave;
   w.w_hi = off + min(r0 + 32 * wave + 31, qlen - 1);
   const KeyTiles kt(off + r0, off + min(r0 + BM, qlen) - 1, a.window, a.sinks, BN);
-  auto issue = [&](int i) {
-    char* t = lds + (i & 1) * 2 * TB;
-    const int k0 = kt.at(i) * BN;
-    Tile::template stage<BN, NW>(t, kb, a.sk.l, k0, klen - 1, cmax, wave, lane);
-    Tile::template stage<BN, NW>(t + TB, vb, a.sv.l, k0, klen - 1, cmax, wave, lane);
-  };
-  if (kt.total > 0) issue(0);
-  for (int i = 0; i < kt.total; ++i) {
+  const Stager<T, DP, BN, NW> sk(kb, a.sk.l, klen - 1, cmax, wave, lane), sv(vb, a.sv.l, klen - 1, cmax, wave, lane);
+  const AttnAddr<DP> addr(lane);
+  // ring of two: tile i + 1 is copied while tile i is computed
+  auto arrive = [&](int i, char* other) {
     wait_lgkm0();
     wait_vm<0>();
     bar();
-    if (i + 1 < kt.total) issue(i + 1);
-    if (w.w_lo <= w.w_hi) {
-      const char* t = lds + (i & 1) * 2 * TB;
-      w.template step<BN / 32>(t, t + TB, kt.at(i) * BN, a.window, a.sinks, a.c, lane);
+    if (i + 1 < kt.total) {
+      sk.issue(other, kt.at(i + 1) * BN);
+      sv.issue(other + TB, kt.at(i + 1) * BN);
+    }
+  };
+  auto edge = [&](int i) {
+    char* t = lds + (i & 1) * 2 * TB;
+    arrive(i, lds + (2 - 2 * (i & 1)) * TB);
+    if (w.w_lo <= w.w_hi) w.template tile<BN>(t, t + TB, kt.at(i) * BN, a.window, a.sinks, a.c, lane);
+  };
+  if (kt.total > 0) {
+    sk.issue(lds, kt.at(0) * BN);
+    sv.issue(lds + TB, kt.at(0) * BN);
+  }
+  // Tiles that all rows of the workgroup see whole run in a loop of their own,
+  // two a round: with nothing but straight code in it the sums stay in their
+  // registers (with the edges' branches inside the loop the compiler copied
+  // all 64 twice a tile).
+  int i = 0;
+  if constexpr (sizeof(T) == 2) {
+    const int p_lo = off + r0, p_hi = off + min(r0 + BM, qlen) - 1;
+    int lo = kt.ns, hi = kt.total;  // of the tiles behind the sinks'
+    while (lo < hi && kt.at(lo) * BN <= p_hi - a.window) ++lo;
+    lo += lo & 1;
+    while (hi > lo && kt.at(hi - 1) * BN + BN - 1 > p_lo) --hi;
+    if (r0 + BM > qlen) hi = lo;  // some wave has no rows
+    for (; i < lo && i < kt.total; ++i) edge(i);
+    for (; i + 1 < hi; i += 2) {
+      arrive(i, lds + 2 * TB);
+      w.step2(addr, (lds_ptr)lds, (lds_ptr)lds + TB, a.c);
+      arrive(i + 1, lds);
+      w.step2(addr, (lds_ptr)lds + 2 * TB, (lds_ptr)lds + 3 * TB, a.c);
     }
   }
+#pragma unroll 1
+  for (; i < kt.total; ++i) edge(i);
   const float l = pair_sum(w.l), inv = l > 0.f || l != l ? 1.f / l : 0.f;
   char* out = a.out + at.b * a.so.b + at.h * a.so.h;
   if (row < qlen) {
@@ -471,7 +658,7 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(AttnArgs a) {
   using Tile = AttnTile<T, DP>;
   constexpr int TB = 32 * Tile::CPR * 16, WB = 4 * TB > 32 * DP * 4 + 256 ? 4 * TB : 32 * DP * 4 + 256;
   __shared__ __align__(1024) char lds[NW * WB];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int split = blockIdx.x % a.splits, bk = blockIdx.x / a.splits;
   const int hk = bk % a.Hk, b = bk / a.Hk;
   const int qlen = seq_len(a.q_lens, b, a.Lq), klen = seq_len(a.k_lens, b, a.Lk);
@@ -507,7 +694,7 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(AttnArgs a) {
     }
     asm volatile("" ::: "memory");
     const char* t = ring + buf * 2 * TB;
-    w.template step<1>(t, t + TB, kt.at(i) * 32, a.window, a.sinks, a.c, lane);
+    w.template tile<32>(t, t + TB, kt.at(i) * 32, a.window, a.sinks, a.c, lane);
   }
   // join the waves: O as [d][row] and the statistics behind it
   wait_lgkm0();
@@ -626,7 +813,7 @@ __global__ __launch_bounds__(256, (attn_waves<T, DP>())) void attn_dq_kernel(Att
   constexpr int NW = 4, BM = 32 * NW, BN = attn_bn<T, DP>(), TB = BN * Tile::CPR * 16, STEPS = Tile::STEPS;
   constexpr bool CENTRE = sizeof(T) == 2;
   __shared__ __align__(1024) char lds[4 * TB];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const AttnPlace at(xcd_remap(blockIdx.x, gridDim.x), a);
   const int qlen = seq_len(a.q_lens, at.b, a.Lq), klen = seq_len(a.k_lens, at.b, a.Lk);
   const int r0 = at.tile * BM, off = klen - qlen, n = lane & 31;
@@ -692,11 +879,10 @@ __global__ __launch_bounds__(256, (attn_waves<T, DP>())) void attn_dq_kernel(Att
           ds[r] = s[r] * (dp[r] - delta);
         }
         if (!whole) {
-          const int lo = p - a.window;
+          const Seen seen(p, k0 + 4 * (lane >> 5), a.window, a.sinks);
 #pragma unroll
           for (int r = 0; r < 16; ++r) {
-            const int key = k0 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
-            const bool see = key <= p && (key > lo || key < a.sinks);
+            const bool see = seen(8 * (r >> 2) + (r & 3));
             s[r] = see ? s[r] : 0.f;
             ds[r] = see ? ds[r] : 0.f;
           }
@@ -773,12 +959,12 @@ __global__ __launch_bounds__(256, (attn_waves<T, DP>())) void attn_dq_kernel(Att
 // over further workgroups of `span` rows each, and the fp32 partial sums of a
 // sink tile are added in a fixed order by attn_sink_sum_kernel.
 template <typename T, int DP>
-__global__ __launch_bounds__(256, 1) void attn_dkv_kernel(AttnArgs a) {
+__global__ __launch_bounds__(256, (attn_waves<T, DP>())) void attn_dkv_kernel(AttnArgs a) {
   using Tile = AttnTile<T, DP>;
   constexpr int NW = 4, BK = 32 * NW, BQ = attn_bn<T, DP>(), TB = BQ * Tile::CPR * 16, STEPS = Tile::STEPS;
   __shared__ __align__(1024) char lds[4 * TB];
   __shared__ float stats[2][2][BQ];  // [ring][lse, delta][row]
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 31;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 31;
   int id = xcd_remap(blockIdx.x, gridDim.x);
   const int jobs = a.tiles + a.sink_tiles * (a.splits - 1);
   const int job = id % jobs, bk = id / jobs, hk = bk % a.Hk, b = bk / a.Hk;
@@ -855,6 +1041,8 @@ __global__ __launch_bounds__(256, 1) void attn_dkv_kernel(AttnArgs a) {
           dp = mma32(row_frag<T, DP>(t + TB, 32 * sb, st, lane), vf[st], dp);
         }
         f32x16 ds;
+        const int base = q0 + 4 * (lane >> 5), lo = max(u0, key) - base,
+                  hi = (key < a.sinks ? u1 : min(u1, key + a.window - 1)) - base;
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           const int rr = 32 * sb + 8 * g + 4 * (lane >> 5);
@@ -865,8 +1053,9 @@ __global__ __launch_bounds__(256, 1) void attn_dkv_kernel(AttnArgs a) {
             float pr = __builtin_amdgcn_exp2f(fmaf(s[4 * g + e], a.c, -ls[e]));
             float d = pr * (dp[4 * g + e] - de[e]);
             if (!whole) {
-              const int p = q0 + 8 * g + 4 * (lane >> 5) + e;
-              const bool see = p >= u0 && p <= u1 && key <= p && (key > p - a.window || key < a.sinks);
+              // the row's position p = q0 + 8 g + 4 h + e, against the key's own bounds
+              const int o = 8 * g + e;
+              const bool see = (o >= lo) & (o <= hi);
               pr = see ? pr : 0.f;
               d = see ? d : 0.f;
             }
