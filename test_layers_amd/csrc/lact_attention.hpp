@@ -45,7 +45,7 @@ struct AttnArgs {
   AttnStride sq, sk, sv, so, sdo, sdq, sdk, sdv;
   const int64_t *q_lens, *k_lens;  // device, or null: Lq, Lk
   float* lse;                      // [B, H, Lq], or null (forward)
-  float* delta;                    // [B, H, Lq]: D = dO.o
+  float* stats;                    // [2][B, H, Lq]: -lse / scale and -D, D = dO.o
   float* part;                     // partial sums (few-row forward: O; backward: dK, dV of sink tiles)
   float* part_ml;                  // few-row forward: running maximum and sum of each split
   int32_t B, H, Hk, G;             // G = H / Hk query heads share a key head
@@ -308,6 +308,27 @@ struct KeyTiles {
     total = ns + max(0, p_hi / BN - tl + 1);
   }
   __device__ int at(int i) const { return i < ns ? i : tl + (i - ns); }
+  // Indices lo .. hi - 1 of the tiles that all rows at p_lo .. p_hi see whole
+  // (lo even: the ring's first place), none where `full` is not set
+  __device__ void whole(int p_lo, int p_hi, int window, int BN, bool full, int& lo, int& hi) const {
+    lo = min(ns, total), hi = full ? total : 0;
+    while (lo < hi && at(lo) * BN <= p_hi - window) ++lo;
+    lo += lo & 1;
+    while (hi > lo && at(hi - 1) * BN + BN - 1 > p_lo) --hi;
+    lo = min(lo, total);
+  }
+};
+
+// the lowest and highest position of a wave's rows
+struct AttnWave {
+  int lo, hi;
+  // some row sees some of the keys k0 .. k1; every row sees all of them
+  __device__ __forceinline__ bool some(int k0, int k1, int window, int sinks) const {
+    return !(k0 > hi || (k1 <= lo - window && k0 >= sinks));
+  }
+  __device__ __forceinline__ bool whole(int k0, int k1, int window, int sinks) const {
+    return k1 <= lo && (k0 > hi - window || k1 < sinks);
+  }
 };
 
 // ------------------------------------------------------------------ non-finite tokens
@@ -382,7 +403,7 @@ struct AttnRows {
   f32x16 o[DB];
   float m, l;   // maximum (in units of log2, at most 8 behind), this lane's half of the sum
   int p;        // position of lane l % 32's row
-  int w_lo, w_hi;  // lowest and highest position of the wave's rows
+  AttnWave w;
 
   __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -434,18 +455,11 @@ struct AttnRows {
       l += s[r];
     }
   }
-  // whether some row sees some of the keys k0 .. k1; whether all see all
-  __device__ __forceinline__ bool some(int k0, int k1, int window, int sinks) const {
-    return !(k0 > w_hi || (k1 <= w_lo - window && k0 >= sinks));
-  }
-  __device__ __forceinline__ bool whole(int k0, int k1, int window, int sinks) const {
-    return k1 <= w_lo && (k0 > w_hi - window || k1 < sinks);
-  }
   // 32 keys, in LDS tiles of as many rows
   __device__ __forceinline__ void step(const char* kt, const char* vt, int k0, int window, int sinks, float c,
                                        int lane) {
     f32x16 s = scores(kt, 0, lane);
-    if (!whole(k0, k0 + 31, window, sinks)) mask(s, k0, window, sinks, lane);
+    if (!w.whole(k0, k0 + 31, window, sinks)) mask(s, k0, window, sinks, lane);
     follow(s, c, nullptr);
     exps(s, c);
     acc_trans<T, DP>(o, s, vt, 0, lane);
@@ -519,7 +533,7 @@ struct AttnRows {
                                        int lane) {
 #pragma unroll 1
     for (int i = 0; i < BN; i += 32)
-      if (some(k0 + i, k0 + i + 31, window, sinks))
+      if (w.some(k0 + i, k0 + i + 31, window, sinks))
         step(kt + i * AttnTile<T, DP>::CPR * 16, vt + i * AttnTile<T, DP>::CPR * 16, k0 + i, window, sinks, c, lane);
   }
 };
@@ -545,6 +559,10 @@ __device__ __forceinline__ void store_rows(const f32x16 (&o)[DP / 32], float f, 
 // waves a SIMD: two where 256 registers hold a wave's 32 rows
 template <typename T, int DP>
 constexpr int attn_waves() { return DP * (int)sizeof(T) > 256 ? 1 : 2; }
+
+// the backward keeps two operands and two sums of 32 rows or keys
+template <typename T, int DP>
+constexpr int attn_back_waves() { return DP * (int)sizeof(T) >= 256 ? 1 : 2; }
 
 // keys of a tile: 16 KB of K and of V, or 64 keys
 template <typename T, int DP>
@@ -584,8 +602,7 @@ __global__ __launch_bounds__(256, (attn_waves<T, DP>())) void attn_fwd_kernel(At
   w.clear();
   load_rows(w.q, a.q + at.b * a.sq.b + at.h * a.sq.h + (int64_t)min(row, qlen - 1) * a.sq.l, cmax, lane);
   w.p = off + row;
-  w.w_lo = off + r0 + 32 * wave;
-  w.w_hi = off + min(r0 + 32 * wave + 31, qlen - 1);
+  w.w = {off + r0 + 32 * wave, off + min(r0 + 32 * wave + 31, qlen - 1)};
   const KeyTiles kt(off + r0, off + min(r0 + BM, qlen) - 1, a.window, a.sinks, BN);
   const Stager<T, DP, BN, NW> sk(kb, a.sk.l, klen - 1, cmax, wave, lane), sv(vb, a.sv.l, klen - 1, cmax, wave, lane);
   const AttnAddr<DP> addr(lane);
@@ -602,7 +619,7 @@ __global__ __launch_bounds__(256, (attn_waves<T, DP>())) void attn_fwd_kernel(At
   auto edge = [&](int i) {
     char* t = lds + (i & 1) * 2 * TB;
     arrive(i, lds + (2 - 2 * (i & 1)) * TB);
-    if (w.w_lo <= w.w_hi) w.template tile<BN>(t, t + TB, kt.at(i) * BN, a.window, a.sinks, a.c, lane);
+    if (w.w.lo <= w.w.hi) w.template tile<BN>(t, t + TB, kt.at(i) * BN, a.window, a.sinks, a.c, lane);
   };
   if (kt.total > 0) {
     sk.issue(lds, kt.at(0) * BN);
@@ -614,13 +631,9 @@ __global__ __launch_bounds__(256, (attn_waves<T, DP>())) void attn_fwd_kernel(At
   // all 64 twice a tile).
   int i = 0;
   if constexpr (sizeof(T) == 2) {
-    const int p_lo = off + r0, p_hi = off + min(r0 + BM, qlen) - 1;
-    int lo = kt.ns, hi = kt.total;  // of the tiles behind the sinks'
-    while (lo < hi && kt.at(lo) * BN <= p_hi - a.window) ++lo;
-    lo += lo & 1;
-    while (hi > lo && kt.at(hi - 1) * BN + BN - 1 > p_lo) --hi;
-    if (r0 + BM > qlen) hi = lo;  // some wave has no rows
-    for (; i < lo && i < kt.total; ++i) edge(i);
+    int lo, hi;
+    kt.whole(off + r0, off + min(r0 + BM, qlen) - 1, a.window, BN, r0 + BM <= qlen, lo, hi);
+    for (; i < lo; ++i) edge(i);
     for (; i + 1 < hi; i += 2) {
       arrive(i, lds + 2 * TB);
       w.step2(addr, (lds_ptr)lds, (lds_ptr)lds + TB, a.c);
@@ -672,9 +685,8 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(AttnArgs a) {
   load_rows(w.q, a.q + b * a.sq.b + (int64_t)(hk * a.G + row / a.Lq) * a.sq.h +
                             (int64_t)min(tok, qlen - 1) * a.sq.l, cmax, lane);
   w.p = off + min(tok, qlen - 1);
-  w.w_lo = off;
-  w.w_hi = klen - 1;
-  const KeyTiles kt(w.w_lo, w.w_hi, a.window, a.sinks, 32);
+  w.w = {off, klen - 1};
+  const KeyTiles kt(off, klen - 1, a.window, a.sinks, 32);
   const int i0 = (int)((int64_t)kt.total * split / a.splits), i1 = (int)((int64_t)kt.total * (split + 1) / a.splits);
   char* ring = lds + wave * WB;
   auto issue = [&](int i, int buf) {
@@ -808,9 +820,9 @@ __global__ __launch_bounds__(64) void attn_join_kernel(AttnArgs a) {
 // attention: 2.2e-3 for 2.8e-3 to 3.8e-3 without (1.7e-3 is the result's own
 // rounding).
 template <typename T, int DP>
-__global__ __launch_bounds__(256, (attn_waves<T, DP>())) void attn_dq_kernel(AttnArgs a) {
+__global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dq_kernel(AttnArgs a) {
   using Tile = AttnTile<T, DP>;
-  constexpr int NW = 4, BM = 32 * NW, BN = attn_bn<T, DP>(), TB = BN * Tile::CPR * 16, STEPS = Tile::STEPS;
+  constexpr int NW = 4, BM = 32 * NW, BN = attn_bn<T, DP>(), TB = BN * Tile::CPR * 16, STEPS = Tile::STEPS, DB = DP / 32;
   constexpr bool CENTRE = sizeof(T) == 2;
   __shared__ __align__(1024) char lds[4 * TB];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -819,9 +831,9 @@ __global__ __launch_bounds__(256, (attn_waves<T, DP>())) void attn_dq_kernel(Att
   const int r0 = at.tile * BM, off = klen - qlen, n = lane & 31;
   const int row = r0 + 32 * wave + n, cmax = a.d * (int)sizeof(T) / 16 - 1;
   const int64_t stat = ((int64_t)at.b * a.H + at.h) * a.Lq + row;
-  f32x16 dq[DP / 32];
+  f32x16 dq[DB];
 #pragma unroll
-  for (int db = 0; db < DP / 32; ++db) dq[db] = zero16();
+  for (int db = 0; db < DB; ++db) dq[db] = zero16();
   const char* kb = a.k + at.b * a.sk.b + at.hk * a.sk.h;
   const char* vb = a.v + at.b * a.sv.b + at.hk * a.sv.h;
   const char* qb = a.q + at.b * a.sq.b + at.h * a.sq.h;
@@ -842,43 +854,61 @@ __global__ __launch_bounds__(256, (attn_waves<T, DP>())) void attn_dq_kernel(Att
         for (int e = 0; e < 16 / (int)sizeof(T); ++e) delta = fmaf((float)g[s][e], (float)o[s][e], delta);
     }
     delta = pair_sum(delta);
-    float sum = 0.f, rsum = 0.f;
-    f32x16 kbar[CENTRE ? DP / 32 : 1];
+    const float lse = row < qlen ? a.lse[stat] : 0.f;
+    lse2 = lse * LOG2E;
+    f32x16 less;  // -D: what dP's product starts from
+#pragma unroll
+    for (int r = 0; r < 16; ++r) less[r] = -delta;
+    float sum = 0.f, rsum = 0.f;  // of dS, exact and rounded
+    f32x16 kbar[CENTRE ? DB : 1];
 #pragma unroll
     for (auto& x : kbar) x = zero16();
-    lse2 = (row < qlen ? a.lse[stat] : 0.f) * LOG2E;
-    const int p = off + row, w_lo = off + r0 + 32 * wave, w_hi = off + min(r0 + 32 * wave + 31, qlen - 1);
-    auto issue = [&](int i) {
-      char* t = lds + (i & 1) * 2 * TB;
-      const int k0 = kt.at(i) * BN;
-      Tile::template stage<BN, NW>(t, kb, a.sk.l, k0, klen - 1, cmax, wave, lane);
-      Tile::template stage<BN, NW>(t + TB, vb, a.sv.l, k0, klen - 1, cmax, wave, lane);
-    };
-    if (kt.total > 0) issue(0);
-    for (int i = 0; i < kt.total; ++i) {
+    const int p = off + row;
+    const AttnWave w{off + r0 + 32 * wave, off + min(r0 + 32 * wave + 31, qlen - 1)};
+    const Stager<T, DP, BN, NW> sk(kb, a.sk.l, klen - 1, cmax, wave, lane), sv(vb, a.sv.l, klen - 1, cmax, wave, lane);
+    auto arrive = [&](int i, char* other) {
       wait_lgkm0();
       wait_vm<0>();
       bar();
-      if (i + 1 < kt.total) issue(i + 1);
-      const char* t = lds + (i & 1) * 2 * TB;
+      if (i + 1 < kt.total) {
+        sk.issue(other, kt.at(i + 1) * BN);
+        sv.issue(other + TB, kt.at(i + 1) * BN);
+      }
+    };
+    auto gradients = [&](f32x16& s, f32x16& ds) {  // scores and dP - D to P and dS
 #pragma unroll
-      for (int sb = 0; sb < BN / 32; ++sb) {
-        const int k0 = kt.at(i) * BN + 32 * sb, k1 = k0 + 31;
-        if (k0 > w_hi || w_lo > w_hi || (k1 <= w_lo - a.window && k0 >= a.sinks)) continue;
-        const bool whole = k1 <= w_lo && (k0 > w_hi - a.window || k1 < a.sinks);
-        f32x16 s = zero16(), dp = zero16();
+      for (int r = 0; r < 16; ++r) {
+        s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], a.c, -lse2));
+        ds[r] *= s[r];
+      }
+    };
+    auto count = [&](const f32x16& ds, const Pair& x) {
+      typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+      const bf16x2 one = {(__bf16)1.f, (__bf16)1.f};
+#pragma unroll
+      for (int r = 0; r < 16; ++r) sum += ds[r];
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int r = 0; r < 8; r += 2)
+          rsum = __builtin_amdgcn_fdot2_f32_bf16(bf16x2{x.f[e][r], x.f[e][r + 1]}, one, rsum, false);
+    };
+    // a tile of which rows may see a part, 32 keys after another
+    auto edge = [&](int i) {
+      const char* t = lds + (i & 1) * 2 * TB;
+      arrive(i, lds + (2 - 2 * (i & 1)) * TB);
+#pragma unroll 1
+      for (int sb = 0; sb < BN; sb += 32) {
+        const int k0 = kt.at(i) * BN + sb;
+        if (w.lo > w.hi || !w.some(k0, k0 + 31, a.window, a.sinks)) continue;
+        f32x16 s = zero16(), ds = less;
 #pragma unroll
         for (int st = 0; st < STEPS; ++st) {
-          s = mma32(row_frag<T, DP>(t, 32 * sb, st, lane), q[st], s);
-          dp = mma32(row_frag<T, DP>(t + TB, 32 * sb, st, lane), g[st], dp);
+          s = mma32(row_frag<T, DP>(t, sb, st, lane), q[st], s);
+          ds = mma32(row_frag<T, DP>(t + TB, sb, st, lane), g[st], ds);
         }
-        f32x16 ds;
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], a.c, -lse2));
-          ds[r] = s[r] * (dp[r] - delta);
-        }
-        if (!whole) {
+        gradients(s, ds);
+        if (!w.whole(k0, k0 + 31, a.window, a.sinks)) {
           const Seen seen(p, k0 + 4 * (lane >> 5), a.window, a.sinks);
 #pragma unroll
           for (int r = 0; r < 16; ++r) {
@@ -888,43 +918,108 @@ __global__ __launch_bounds__(256, (attn_waves<T, DP>())) void attn_dq_kernel(Att
           }
         }
         if constexpr (CENTRE) {
-          const Pair x = round_pair(ds), y = round_pair(s);
-#pragma unroll
-          for (int r = 0; r < 16; ++r) sum += ds[r];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-            const bf16x2 one = {(__bf16)1.f, (__bf16)1.f};
-#pragma unroll
-            for (int r = 0; r < 8; r += 2)
-              rsum = __builtin_amdgcn_fdot2_f32_bf16(bf16x2{x.f[e][r], x.f[e][r + 1]}, one, rsum, false);
-          }
-#pragma unroll
-          for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-            for (int db = 0; db < DP / 32; ++db) {
-              const bf16x8 k = trans_frag<DP>(t, 32 * sb, kb, db, lane);
-              dq[db] = mma32(k, x.f[kb], dq[db]);
-              kbar[db] = mma32(k, y.f[kb], kbar[db]);
-            }
+          const Pair x = round_pair(ds);
+          count(ds, x);
+          mma_trans<DP>(dq, x.f, t, sb, lane);
+          mma_trans<DP>(kbar, round_pair(s).f, t, sb, lane);
         } else {
-          mma_trans<DP>(dq, ds, t, 32 * sb, lane);
+          mma_trans<DP>(dq, ds, t, sb, lane);
         }
       }
+    };
+    if (kt.total > 0) {
+      sk.issue(lds, kt.at(0) * BN);
+      sv.issue(lds + TB, kt.at(0) * BN);
     }
+    int i = 0;
+    if constexpr (CENTRE && BN == 64) {
+      const AttnAddr<DP> addr(lane);
+      constexpr int NV = 2 * DB;
+      // 64 keys that every row sees: scores and dP of one half beside the
+      // exponentials of the other, then each half's sums (see AttnRows::step2)
+      auto whole = [&](lds_ptr kp, lds_ptr vp) {
+        auto products = [&](int row0, f32x16& s, f32x16& ds) {
+          s = zero16(), ds = less;
+#pragma unroll
+          for (int t = 0; t < STEPS; ++t) {
+            s = mma32(addr.rows(kp, row0, t), q[t], s);
+            ds = mma32(addr.rows(vp, row0, t), g[t], ds);
+          }
+        };
+        auto sums = [&](int row0, const Pair& x, const Pair& y) {
+#pragma unroll
+          for (int v = 0; v < NV; ++v) {
+            const bf16x8 k = addr.cols(kp, row0 + 16 * (v / DB), v % DB);
+            dq[v % DB] = mma32(k, x.f[v / DB], dq[v % DB]);
+            kbar[v % DB] = mma32(k, y.f[v / DB], kbar[v % DB]);
+          }
+        };
+        f32x16 s0, ds0, s1, ds1;
+        products(0, s0, ds0);
+        __builtin_amdgcn_sched_group_barrier(SG_LDS, 4, 0);
+#pragma unroll
+        for (int t = 0; t < 2 * STEPS; ++t) {
+          __builtin_amdgcn_sched_group_barrier(SG_MFMA, 1, 0);
+          if (t + 4 < 2 * STEPS) __builtin_amdgcn_sched_group_barrier(SG_LDS, 1, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        products(32, s1, ds1);
+        gradients(s0, ds0);
+        const Pair x0 = round_pair(ds0), y0 = round_pair(s0);
+        count(ds0, x0);
+        __builtin_amdgcn_sched_group_barrier(SG_LDS, 4, 1);
+        __builtin_amdgcn_sched_group_barrier(SG_VALU, 8, 1);
+#pragma unroll
+        for (int t = 0; t < 2 * STEPS; ++t) {
+          __builtin_amdgcn_sched_group_barrier(SG_MFMA, 1, 1);
+          if (t + 4 < 2 * STEPS) __builtin_amdgcn_sched_group_barrier(SG_LDS, 1, 1);
+          __builtin_amdgcn_sched_group_barrier(SG_VALU, 88 / (2 * STEPS), 1);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        sums(0, x0, y0);
+        gradients(s1, ds1);
+        const Pair x1 = round_pair(ds1), y1 = round_pair(s1);
+        count(ds1, x1);
+        __builtin_amdgcn_sched_group_barrier(SG_LDS, 4, 2);
+        __builtin_amdgcn_sched_group_barrier(SG_VALU, 8, 2);
+#pragma unroll
+        for (int t = 0; t < NV; ++t) {
+          __builtin_amdgcn_sched_group_barrier(SG_MFMA, 2, 2);
+          if (t + 2 < NV) __builtin_amdgcn_sched_group_barrier(SG_LDS, 2, 2);
+          __builtin_amdgcn_sched_group_barrier(SG_VALU, 88 / NV, 2);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        sums(32, x1, y1);
+      };
+      int lo, hi;
+      kt.whole(off + r0, off + min(r0 + BM, qlen) - 1, a.window, BN, r0 + BM <= qlen, lo, hi);
+      for (; i < lo; ++i) edge(i);
+      for (; i + 1 < hi; i += 2) {
+        arrive(i, lds + 2 * TB);
+        whole((lds_ptr)lds, (lds_ptr)lds + TB);
+        arrive(i + 1, lds);
+        whole((lds_ptr)lds + 2 * TB, (lds_ptr)lds + 3 * TB);
+      }
+    }
+#pragma unroll 1
+    for (; i < kt.total; ++i) edge(i);
     if constexpr (CENTRE) {
       rsum = pair_sum(rsum);
       delta += pair_sum(sum);
 #pragma unroll
-      for (int db = 0; db < DP / 32; ++db)
+      for (int db = 0; db < DB; ++db)
 #pragma unroll
         for (int r = 0; r < 16; ++r) dq[db][r] = fmaf(-rsum, kbar[db][r], dq[db][r]);
     }
-    if (row < qlen && lane < 32) a.delta[stat] = delta;
+    // what the dk, dv kernel's products start from: exp2(c (q.k - lse / scale)), dO.v - D
+    if (row < qlen && lane < 32) {
+      a.stats[stat] = -lse / a.scale;
+      a.stats[(int64_t)a.B * a.H * a.Lq + stat] = -delta;
+    }
   }
   if (row >= qlen) {  // what a clamped row gathered, finite or not, is nothing
 #pragma unroll
-    for (int db = 0; db < DP / 32; ++db) dq[db] = zero16();
+    for (int db = 0; db < DB; ++db) dq[db] = zero16();
   }
   char* out = a.dq + at.b * a.sdq.b + at.h * a.sdq.h;
   if (row < a.Lq) store_rows<T, DP>(dq, a.scale, out + (int64_t)row * a.sdq.l, a.d, lane);
@@ -952,18 +1047,19 @@ __global__ __launch_bounds__(256, (attn_waves<T, DP>())) void attn_dq_kernel(Att
 // A workgroup owns 128 keys of a key head, a wave 32 of them in registers,
 // and meets every row that sees them, over all query heads of the key head
 // (their sum needs no atomics).  S = Q K^T and dP = dO V^T have the key in
-// the lane; dv^T += dO^T P and dk^T += Q^T dS.
+// the lane and start from the rows' -lse / scale and -D, so that neither is
+// subtracted element by element; dv^T += dO^T P and dk^T += Q^T dS.
 //
 // Keys below `sinks` are seen by every later row, up to 16 times more than a
 // window's; the rows behind the window of a sink tile's last key are split
 // over further workgroups of `span` rows each, and the fp32 partial sums of a
 // sink tile are added in a fixed order by attn_sink_sum_kernel.
 template <typename T, int DP>
-__global__ __launch_bounds__(256, (attn_waves<T, DP>())) void attn_dkv_kernel(AttnArgs a) {
+__global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dkv_kernel(AttnArgs a) {
   using Tile = AttnTile<T, DP>;
-  constexpr int NW = 4, BK = 32 * NW, BQ = attn_bn<T, DP>(), TB = BQ * Tile::CPR * 16, STEPS = Tile::STEPS;
+  constexpr int NW = 4, BK = 32 * NW, BQ = attn_bn<T, DP>(), TB = BQ * Tile::CPR * 16, STEPS = Tile::STEPS, DB = DP / 32;
   __shared__ __align__(1024) char lds[4 * TB];
-  __shared__ float stats[2][2][BQ];  // [ring][lse, delta][row]
+  __shared__ __align__(1024) float stats[2][2][64];  // [ring][-lse / scale, -D][row]
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 31;
   int id = xcd_remap(blockIdx.x, gridDim.x);
   const int jobs = a.tiles + a.sink_tiles * (a.splits - 1);
@@ -976,11 +1072,14 @@ __global__ __launch_bounds__(256, (attn_waves<T, DP>())) void attn_dkv_kernel(At
     tile = job - a.sink_tiles * (a.splits - 1);
   }
   const int qlen = seq_len(a.q_lens, b, a.Lq), klen = seq_len(a.k_lens, b, a.Lk), off = klen - qlen;
-  const int k0 = tile * BK, k1 = min(k0 + BK, klen) - 1, cmax = a.d * (int)sizeof(T) / 16 - 1;
+  const int k0 = tile * BK, cmax = a.d * (int)sizeof(T) / 16 - 1;
   const int key = k0 + 32 * wave + n;
-  f32x16 dk[DP / 32], dv[DP / 32];
+  const char* qh = a.q + b * a.sq.b + (int64_t)hk * a.G * a.sq.h;
+  const char* gh = a.dO + b * a.sdo.b + (int64_t)hk * a.G * a.sdo.h;
+  const int64_t sh = ((int64_t)b * a.H + hk * a.G) * a.Lq, sn = (int64_t)a.B * a.H * a.Lq;
+  f32x16 dk[DB], dv[DB];
 #pragma unroll
-  for (int db = 0; db < DP / 32; ++db) dk[db] = dv[db] = zero16();
+  for (int db = 0; db < DB; ++db) dk[db] = dv[db] = zero16();
   // positions of the rows this workgroup meets
   int p_lo = k0, p_hi = klen - 1;
   const int reach = (int)min((int64_t)k0 + BK - 1 + a.window, (int64_t)klen) - 1;  // last that sees k0 + BK - 1 by window
@@ -994,79 +1093,155 @@ __global__ __launch_bounds__(256, (attn_waves<T, DP>())) void attn_dkv_kernel(At
     p_hi = reach;
   }
   const int ra = max(0, p_lo - off) / BQ, rz = p_hi - off;  // first row tile, last row
-  const int nt = k0 < klen && rz >= ra * BQ && p_hi >= p_lo ? rz / BQ - ra + 1 : 0;
-  if (nt > 0) {
+  if (k0 < klen && rz >= ra * BQ && p_hi >= p_lo) {
+    const int rend = rz / BQ + 1;  // behind the last row tile
     Frag<T> kf[STEPS], vf[STEPS];
     const int64_t kc = min(key, klen - 1);
     load_rows(kf, a.k + b * a.sk.b + hk * a.sk.h + kc * a.sk.l, cmax, lane);
     load_rows(vf, a.v + b * a.sv.b + hk * a.sv.h + kc * a.sv.l, cmax, lane);
     const int wk0 = k0 + 32 * wave, wk1 = min(wk0 + 31, klen - 1);
-    const int total = nt * a.G;
-    float stat = 0.f;
-    auto issue = [&](int i) {
-      const int h = hk * a.G + i / nt, r = (ra + i % nt) * BQ;
-      char* t = lds + (i & 1) * 2 * TB;
-      Tile::template stage<BQ, NW>(t, a.q + b * a.sq.b + h * a.sq.h, a.sq.l, r, qlen - 1, cmax, wave, lane);
-      Tile::template stage<BQ, NW>(t + TB, a.dO + b * a.sdo.b + h * a.sdo.h, a.sdo.l, r, qlen - 1, cmax, wave, lane);
-      if (threadIdx.x < 2 * BQ) {
-        const int rr = r + (int)threadIdx.x % BQ;
-        const float* src = threadIdx.x < BQ ? a.lse : a.delta;
-        stat = rr < qlen ? src[((int64_t)b * a.H + h) * a.Lq + rr] : 0.f;
-      }
+    Stager<T, DP, BQ, NW> sq(qh, a.sq.l, qlen - 1, cmax, wave, lane), sg(gh, a.sdo.l, qlen - 1, cmax, wave, lane);
+    auto issue = [&](int h, int rt, char* t, float* st) {
+      sq.base = qh + h * a.sq.h;
+      sg.base = gh + h * a.sdo.h;
+      sq.issue(t, rt * BQ);
+      sg.issue(t + TB, rt * BQ);
+      if (wave < 2)
+        dma4(a.stats + wave * sn + sh + (int64_t)h * a.Lq + min(rt * BQ + lane, qlen - 1),
+             __builtin_amdgcn_readfirstlane(lds_off(st) + (uint32_t)wave * 256u));
     };
-    auto put = [&](int i) {
-      if (threadIdx.x < 2 * BQ)
-        stats[i & 1][threadIdx.x / BQ][threadIdx.x % BQ] = threadIdx.x < BQ ? stat * LOG2E : stat;
-    };
-    issue(0);
-    put(0);
-    for (int i = 0; i < total; ++i) {
+    auto arrive = [&](int h, int rt, char* other, float* st) {
       wait_lgkm0();
       wait_vm<0>();
       bar();
-      if (i + 1 < total) issue(i + 1);
-      const char* t = lds + (i & 1) * 2 * TB;
-      const int r = (ra + i % nt) * BQ;
+      if (rt + 1 < rend) issue(h, rt + 1, other, st);
+      else if (h + 1 < a.G) issue(h + 1, ra, other, st);
+    };
+    // -lse / scale or -D of 32 rows, as a product leaves them
+    auto start = [&](const float* st, int row0) {
+      f32x16 x;
 #pragma unroll
-      for (int sb = 0; sb < BQ / 32; ++sb) {
-        const int q0 = off + r + 32 * sb, q1 = q0 + 31;  // positions
+      for (int g = 0; g < 4; ++g) {
+        const f32x4 v = *reinterpret_cast<const f32x4*>(st + row0 + 8 * g + 4 * (lane >> 5));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[4 * g + e] = v[e];
+      }
+      return x;
+    };
+    auto gradients = [&](f32x16& s, f32x16& ds) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        s[r] = __builtin_amdgcn_exp2f(s[r] * a.c);
+        ds[r] *= s[r];
+      }
+    };
+    // a tile of which rows may see a part, 32 rows after another
+    auto edge = [&](int h, int rt, int ring) {
+      const char* t = lds + ring * 2 * TB;
+      arrive(h, rt, lds + (2 - 2 * ring) * TB, stats[1 - ring][0]);
+#pragma unroll 1
+      for (int sb = 0; sb < BQ; sb += 32) {
+        const int q0 = off + rt * BQ + sb, q1 = q0 + 31;  // positions
         const int u0 = max(q0, p_lo), u1 = min(q1, p_hi);
         if (u0 > u1 || wk0 > wk1 || u1 < wk0 || (wk1 <= u0 - a.window && wk0 >= a.sinks)) continue;
         const bool whole = u0 == q0 && u1 == q1 && wk1 <= q0 && wk0 + 31 == wk1 &&
                            (wk0 > q1 - a.window || wk1 < a.sinks);
-        f32x16 s = zero16(), dp = zero16();
+        f32x16 s = start(stats[ring][0], sb), ds = start(stats[ring][1], sb);
 #pragma unroll
         for (int st = 0; st < STEPS; ++st) {
-          s = mma32(row_frag<T, DP>(t, 32 * sb, st, lane), kf[st], s);
-          dp = mma32(row_frag<T, DP>(t + TB, 32 * sb, st, lane), vf[st], dp);
+          s = mma32(row_frag<T, DP>(t, sb, st, lane), kf[st], s);
+          ds = mma32(row_frag<T, DP>(t + TB, sb, st, lane), vf[st], ds);
         }
-        f32x16 ds;
-        const int base = q0 + 4 * (lane >> 5), lo = max(u0, key) - base,
-                  hi = (key < a.sinks ? u1 : min(u1, key + a.window - 1)) - base;
+        gradients(s, ds);
+        if (!whole) {
+          // a row's position p = q0 + 4 (lane / 32) + o, against the key's own bounds
+          const int base = q0 + 4 * (lane >> 5), lo = max(u0, key) - base,
+                    hi = (key < a.sinks ? u1 : min(u1, key + a.window - 1)) - base;
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int rr = 32 * sb + 8 * g + 4 * (lane >> 5);
-          const f32x4 ls = *reinterpret_cast<const f32x4*>(&stats[i & 1][0][rr]);
-          const f32x4 de = *reinterpret_cast<const f32x4*>(&stats[i & 1][1][rr]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float pr = __builtin_amdgcn_exp2f(fmaf(s[4 * g + e], a.c, -ls[e]));
-            float d = pr * (dp[4 * g + e] - de[e]);
-            if (!whole) {
-              // the row's position p = q0 + 8 g + 4 h + e, against the key's own bounds
-              const int o = 8 * g + e;
-              const bool see = (o >= lo) & (o <= hi);
-              pr = see ? pr : 0.f;
-              d = see ? d : 0.f;
-            }
-            s[4 * g + e] = pr;
-            ds[4 * g + e] = d;
+          for (int r = 0; r < 16; ++r) {
+            const int o = 8 * (r >> 2) + (r & 3);
+            const bool see = (o >= lo) & (o <= hi);
+            s[r] = see ? s[r] : 0.f;
+            ds[r] = see ? ds[r] : 0.f;
           }
         }
-        acc_trans<T, DP>(dv, s, t + TB, 32 * sb, lane);
-        acc_trans<T, DP>(dk, ds, t, 32 * sb, lane);
+        acc_trans<T, DP>(dv, s, t + TB, sb, lane);
+        acc_trans<T, DP>(dk, ds, t, sb, lane);
       }
-      if (i + 1 < total) put(i + 1);
+    };
+    issue(0, ra, lds, stats[0][0]);
+    int i = 0;  // tiles done: the ring's place
+#pragma unroll 1
+    for (int h = 0; h < a.G; ++h) {
+      int rt = ra;
+      if constexpr (sizeof(T) == 2 && BQ == 64) {
+        // row tiles that see all keys of the workgroup
+        const int last = k0 + BK - 1 < a.sinks ? p_hi : min(p_hi, k0 + a.window - 1);
+        const int wa = max(ra, (max(max(k0 + BK - 1, p_lo) - off, 0) + BQ - 1) / BQ);
+        const int wz = k0 + BK <= klen && last >= off ? min(rend, (last - off + 1) / BQ) : 0;
+        const AttnAddr<DP> addr(lane);
+        constexpr int NV = 2 * DB;
+        auto all = [&](lds_ptr qp, lds_ptr gp, const float* st) {
+          auto products = [&](int row0, f32x16& s, f32x16& ds) {
+            s = start(st, row0), ds = start(st + 64, row0);
+#pragma unroll
+            for (int t = 0; t < STEPS; ++t) {
+              s = mma32(addr.rows(qp, row0, t), kf[t], s);
+              ds = mma32(addr.rows(gp, row0, t), vf[t], ds);
+            }
+          };
+          auto sums = [&](int row0, const Pair& x, const Pair& y) {
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+              dv[v % DB] = mma32(addr.cols(gp, row0 + 16 * (v / DB), v % DB), y.f[v / DB], dv[v % DB]);
+              dk[v % DB] = mma32(addr.cols(qp, row0 + 16 * (v / DB), v % DB), x.f[v / DB], dk[v % DB]);
+            }
+          };
+          f32x16 s0, ds0, s1, ds1;
+          products(0, s0, ds0);
+          __builtin_amdgcn_sched_group_barrier(SG_LDS, 12, 0);
+#pragma unroll
+          for (int t = 0; t < 2 * STEPS; ++t) {
+            __builtin_amdgcn_sched_group_barrier(SG_MFMA, 1, 0);
+            if (t + 4 < 2 * STEPS) __builtin_amdgcn_sched_group_barrier(SG_LDS, 1, 0);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+          products(32, s1, ds1);
+          gradients(s0, ds0);
+          const Pair x0 = round_pair(ds0), y0 = round_pair(s0);
+          __builtin_amdgcn_sched_group_barrier(SG_LDS, 12, 1);
+          __builtin_amdgcn_sched_group_barrier(SG_VALU, 8, 1);
+#pragma unroll
+          for (int t = 0; t < 2 * STEPS; ++t) {
+            __builtin_amdgcn_sched_group_barrier(SG_MFMA, 1, 1);
+            if (t + 4 < 2 * STEPS) __builtin_amdgcn_sched_group_barrier(SG_LDS, 1, 1);
+            __builtin_amdgcn_sched_group_barrier(SG_VALU, 56 / (2 * STEPS), 1);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+          sums(0, x0, y0);
+          gradients(s1, ds1);
+          const Pair x1 = round_pair(ds1), y1 = round_pair(s1);
+          __builtin_amdgcn_sched_group_barrier(SG_LDS, 4, 2);
+          __builtin_amdgcn_sched_group_barrier(SG_VALU, 8, 2);
+#pragma unroll
+          for (int t = 0; t < 2 * NV; ++t) {
+            __builtin_amdgcn_sched_group_barrier(SG_MFMA, 1, 2);
+            if (t + 2 < 2 * NV) __builtin_amdgcn_sched_group_barrier(SG_LDS, 2, 2);
+            __builtin_amdgcn_sched_group_barrier(SG_VALU, 56 / (2 * NV), 2);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+          sums(32, x1, y1);
+        };
+        for (; rt < rend && (rt < wa || (rt < wz && (i & 1))); ++rt, ++i) edge(h, rt, i & 1);
+        for (; rt + 1 < wz; rt += 2, i += 2) {
+          arrive(h, rt, lds + 2 * TB, stats[1][0]);
+          all((lds_ptr)lds, (lds_ptr)lds + TB, stats[0][0]);
+          arrive(h, rt + 1, lds, stats[0][0]);
+          all((lds_ptr)lds + 2 * TB, (lds_ptr)lds + 3 * TB, stats[1][0]);
+        }
+      }
+#pragma unroll 1
+      for (; rt < rend; ++rt, ++i) edge(h, rt, i & 1);
     }
   }
   const bool parts = tile < a.sink_tiles && a.splits > 1;
@@ -1088,16 +1263,14 @@ __global__ __launch_bounds__(256, (attn_waves<T, DP>())) void attn_dkv_kernel(At
     const Lane2<T> v(a.v + b * a.sv.b + hk * a.sv.h + j * a.sv.l, a.d, lane);
     float x[2] = {0.f, 0.f}, y[2] = {0.f, 0.f};
 #pragma unroll 1
-    for (int h = hk * a.G; h < (hk + 1) * a.G; ++h)
+    for (int h = 0; h < a.G; ++h)
 #pragma unroll 1
       for (int p = max(max(p_lo, j), off); p <= p_hi; ++p) {
         if (j <= p - a.window && j >= a.sinks) break;
-        const int r = p - off;
-        const int64_t st = ((int64_t)b * a.H + h) * a.Lq + r;
-        const Lane2<T> q(a.q + b * a.sq.b + h * a.sq.h + r * a.sq.l, a.d, lane);
-        const Lane2<T> g(a.dO + b * a.sdo.b + h * a.sdo.h + r * a.sdo.l, a.d, lane);
-        const float pr = __builtin_amdgcn_exp2f(fmaf(q.dot(k), a.c, -a.lse[st] * LOG2E));
-        const float ds = pr * (g.dot(v) - a.delta[st]);
+        const int64_t r = p - off, st = sh + (int64_t)h * a.Lq + r;
+        const Lane2<T> q(qh + h * a.sq.h + r * a.sq.l, a.d, lane), g(gh + h * a.sdo.h + r * a.sdo.l, a.d, lane);
+        const float pr = __builtin_amdgcn_exp2f(a.c * (q.dot(k) + a.stats[st]));
+        const float ds = pr * (g.dot(v) + a.stats[sn + st]);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           x[e] = fmaf(ds, q.x[e], x[e]);

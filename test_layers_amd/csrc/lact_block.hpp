@@ -123,7 +123,7 @@ void sink_plan(const lact_attention& p, AttnArgs& a) {
 }
 
 struct AttnWs {
-  size_t part = 0, ml = 0, delta = 0, total = 0;
+  size_t part = 0, ml = 0, total = 0;
 };
 AttnWs attn_ws(const lact_attention& p) {
   AttnWs w;
@@ -139,7 +139,7 @@ AttnWs attn_back_ws(const lact_attention& p) {
   AttnWs w;
   AttnArgs a = attn_args(p);
   sink_plan(p, a);
-  w.part = align256((size_t)p.batch * p.heads * p.q_len * 4);
+  w.part = align256((size_t)p.batch * p.heads * p.q_len * 2 * 4);
   w.total = w.part;
   if (a.splits > 1) w.total += align256((size_t)p.batch * p.kv_heads * a.sink_tiles * a.splits * 2 * 128 * p.d * 4);
   return w;
@@ -284,7 +284,7 @@ lact_status lact_window_attention_backward(const lact_attention* p, const void* 
   a.q_lens = q_lens;
   a.k_lens = k_lens;
   a.lse = const_cast<float*>(lse);
-  a.delta = static_cast<float*>(ws);
+  a.stats = static_cast<float*>(ws);
   a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + w.part);
   AttnArgs kv = a;
   sink_plan(*p, kv);
