@@ -375,6 +375,11 @@ __device__ __forceinline__ uint32_t not_finite(const f32x16 (&a)[DB]) {
   return (uint32_t)(b | (b >> 32));
 }
 
+// a sum that is NaN in every column stays so
+__device__ __forceinline__ bool settled(const float (&x)[2], int d, int lane) {
+  return __all((lane >= d || x[0] != x[0]) && (lane + 64 >= d || x[1] != x[1]));
+}
+
 // sum of exp2(c q.k - m) v over the visible keys of tiles i0, i0 + di .. < i1
 template <typename T>
 __device__ __forceinline__ void slow_o(float (&x)[2], const char* q, const char* kb, int64_t kl, const char* vb,
@@ -391,6 +396,7 @@ __device__ __forceinline__ void slow_o(float (&x)[2], const char* q, const char*
       const Lane2<T> v(vb + j * vl, a.d, lane);
 #pragma unroll
       for (int e = 0; e < 2; ++e) x[e] = fmaf(pr, v.x[e], x[e]);
+      if (settled(x, a.d, lane)) return;
     }
 }
 
@@ -774,34 +780,50 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(AttnArgs a) {
   }
 }
 
-// One wave a row: the splits' sums, rescaled to their common maximum.
-template <typename T>
-__global__ __launch_bounds__(64) void attn_join_kernel(AttnArgs a) {
-  const int rows = a.G * a.Lq, n = blockIdx.x % rows, bk = blockIdx.x / rows;
+// One workgroup a row: the splits' sums, rescaled to their common maximum.
+// All loads of a thread are independent: the kernel is as long as two trips
+// to memory.
+template <typename T, int DP>
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
+  constexpr int PARTS = 256 / DP;  // threads that share a column
+  __shared__ float f[256], red[4], out[PARTS][DP];
+  const int rows = a.G * a.Lq, n = blockIdx.x % rows, bk = blockIdx.x / rows, t = threadIdx.x;
   const int hk = bk % a.Hk, b = bk / a.Hk, tok = n % a.Lq, h = hk * a.G + n / a.Lq;
-  const int qlen = seq_len(a.q_lens, b, a.Lq), lane = threadIdx.x;
-  if (tok >= qlen) return;
+  if (tok >= seq_len(a.q_lens, b, a.Lq)) return;
   const float* ml = a.part_ml + ((int64_t)bk * rows + n) * a.splits * 2;
   const float* pr = a.part + ((int64_t)bk * rows + n) * a.splits * a.d;
-  float m = -__builtin_huge_valf(), l = 0.f;
-  for (int s = 0; s < a.splits; ++s) m = fmaxf(m, ml[2 * s]);
-  float x[2] = {0.f, 0.f};
-  for (int s = 0; s < a.splits; ++s) {
-    const float ms = ml[2 * s], ls = ml[2 * s + 1];
-    if (ls == 0.f) continue;
-    const float f = ms == -__builtin_huge_valf() ? 1.f : __builtin_amdgcn_exp2f(ms - m);
-    l += ls * f;
+  constexpr float NONE = -__builtin_huge_valf();
+  const float ms = t < a.splits ? ml[2 * t] : NONE, ls = t < a.splits ? ml[2 * t + 1] : 0.f;
+  float m = ms;
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-      if (lane + 64 * j < a.d) x[j] += f * pr[(int64_t)s * a.d + lane + 64 * j];
+  for (int o = 32; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, WAVE));
+  if (t % WAVE == 0) red[t / WAVE] = m;
+  __syncthreads();
+  m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  // a split without keys counts for nothing; one whose scores are all NaN has no maximum but a sum
+  const float w = ls == 0.f ? 0.f : ms == NONE ? 1.f : __builtin_amdgcn_exp2f(ms - m);
+  f[t] = w;
+  const float s = wave_sum(ls == 0.f ? 0.f : ls * w);
+  __syncthreads();
+  if (t % WAVE == 0) red[t / WAVE] = s;
+  __syncthreads();
+  const float l = (red[0] + red[1]) + (red[2] + red[3]), inv = l > 0.f || l != l ? 1.f / l : 0.f;
+  const int c = t % DP, part = t / DP;
+  float x = 0.f;
+  if (c < a.d)
+#pragma unroll 8
+    for (int i = part; i < a.splits; i += PARTS) {
+      const float v = pr[(int64_t)i * a.d + c];
+      x += f[i] == 0.f ? 0.f : f[i] * v;
+    }
+  out[part][c] = x;
+  __syncthreads();
+  if (part == 0 && c < a.d) {
+#pragma unroll
+    for (int i = 1; i < PARTS; ++i) x += out[i][c];
+    io_traits<T>::store(reinterpret_cast<T*>(a.out + b * a.so.b + (int64_t)h * a.so.h + (int64_t)tok * a.so.l) + c, x * inv);
   }
-  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-  T* orow = reinterpret_cast<T*>(a.out + b * a.so.b + (int64_t)h * a.so.h + (int64_t)tok * a.so.l);
-#pragma unroll
-  for (int j = 0; j < 2; ++j)
-    if (lane + 64 * j < a.d) io_traits<T>::store(orow + lane + 64 * j, x[j] * inv);
-  if (a.lse && lane == 0)
-    a.lse[((int64_t)b * a.H + h) * a.Lq + tok] = l == 0.f ? -__builtin_huge_valf() : m * LN2 + logf(l);
+  if (a.lse && t == 0) a.lse[((int64_t)b * a.H + h) * a.Lq + tok] = l == 0.f ? NONE : m * LN2 + logf(l);
 }
 
 // ------------------------------------------------------------------ backward: dq
@@ -1037,6 +1059,7 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dq_kerne
         const float ds = __builtin_amdgcn_exp2f(fmaf(q.dot(k), a.c, -ls)) * (g.dot(v) - de);
 #pragma unroll
         for (int e = 0; e < 2; ++e) x[e] = fmaf(ds, k.x[e], x[e]);
+        if (settled(x, a.d, lane)) t = kt.total, j = off + r;
       }
     x[0] *= a.scale, x[1] *= a.scale;
     store_lane2<T>(out + r * a.sdq.l, x, a.d, lane);
@@ -1275,6 +1298,10 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dkv_kern
         for (int e = 0; e < 2; ++e) {
           x[e] = fmaf(ds, q.x[e], x[e]);
           y[e] = fmaf(pr, g.x[e], y[e]);
+        }
+        if (settled(x, a.d, lane) && settled(y, a.d, lane)) {
+          h = a.G;
+          break;
         }
       }
     if (parts) {

@@ -169,6 +169,17 @@ lact_status by_tile(const lact_attention& p, F&& fn) {
   return p.d <= 64 ? fn(bf16_t{}, IC<64>{}) : fn(bf16_t{}, IC<128>{});
 }
 
+// check_device for calls that come every few microseconds: the device that
+// this thread checked last needs no second look
+lact_status check_device_again() {
+  static thread_local int last = -1;
+  int dev = -1;
+  if (last >= 0 && hipGetDevice(&dev) == hipSuccess && dev == last) return LACT_OK;
+  TRY(check_device());
+  if (hipGetDevice(&dev) == hipSuccess) last = dev;
+  return LACT_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -212,7 +223,7 @@ lact_status lact_window_attention_forward(const lact_attention* p, const void* q
     a.splits = few_splits(*p);
     const int64_t grid = (int64_t)p->batch * p->kv_heads * a.splits;
     TRY(check_grid(std::max(grid, rows)));
-    TRY(check_device());
+    TRY(check_device_again());
     if (a.splits > 1) {
       a.part = static_cast<float*>(ws);
       a.part_ml = reinterpret_cast<float*>(static_cast<char*>(ws) + w.ml);
@@ -222,7 +233,7 @@ lact_status lact_window_attention_forward(const lact_attention* p, const void* q
       using T = decltype(t);
       constexpr int DP = decltype(dp)::value, NW = DP * sizeof(T) > 256 ? 2 : 4;
       LACT_LAUNCH((attn_few_kernel<T, DP, NW>), dim3((unsigned)grid), dim3(64 * NW), s, a);
-      if (a.splits > 1) LACT_LAUNCH((attn_join_kernel<T>), dim3((unsigned)rows), dim3(64), s, a);
+      if (a.splits > 1) LACT_LAUNCH((attn_join_kernel<T, DP>), dim3((unsigned)rows), dim3(256), s, a);
       HIP_TRY(hipGetLastError());
       return LACT_OK;
     });
@@ -230,7 +241,7 @@ lact_status lact_window_attention_forward(const lact_attention* p, const void* q
   a.tiles = (int32_t)ceil_div(p->q_len, 128);
   const int64_t grid = (int64_t)p->batch * p->heads * a.tiles;
   TRY(check_grid(grid));
-  TRY(check_device());
+  TRY(check_device_again());
   KernelTimer kt(LACT_K_ATTN, s);
   return by_tile(*p, [&](auto t, auto dp) -> lact_status {
     LACT_LAUNCH((attn_fwd_kernel<decltype(t), decltype(dp)::value>), dim3((unsigned)grid), dim3(256), s, a);
@@ -293,7 +304,7 @@ lact_status lact_window_attention_backward(const lact_attention* p, const void* 
                 gk = heads * (kv.tiles + (int64_t)kv.sink_tiles * (kv.splits - 1)),
                 gs = kv.splits > 1 ? heads * kv.sink_tiles * 2 * 128 : 0;
   TRY(check_grid(std::max(std::max(gq, gk), gs)));
-  TRY(check_device());
+  TRY(check_device_again());
   const hipStream_t s = static_cast<hipStream_t>(stream);
   return by_tile(*p, [&](auto t, auto dp) -> lact_status {
     using T = decltype(t);
@@ -374,14 +385,20 @@ lact_status lact_rotary(const lact_rotary_problem* p, const void* q, const lact_
   while (a.tok > 1 && p->batch * ceil_div(p->tokens, a.tok) < 4 * NCU) a.tok = (a.tok + 1) / 2;
   int64_t groups = p->batch * ceil_div(p->tokens, a.tok);
   a.head_groups = (int32_t)std::max<int64_t>(1, std::min<int64_t>(heads, 2 * NCU / std::max<int64_t>(1, groups)));
+  a.group = (int32_t)ceil_div(heads, a.head_groups);
+  a.head_groups = (int32_t)ceil_div(heads, a.group);
   TRY(check_grid(groups * a.head_groups));
-  TRY(check_device());
+  TRY(check_device_again());
   const unsigned grid = (unsigned)(groups * a.head_groups);
   const hipStream_t s = static_cast<hipStream_t>(stream);
   KernelTimer kt(LACT_K_ROTARY, s);
+  a.by_pairs = FastDiv((uint32_t)std::max(1, p->pairs));
+  a.heads_inner = a.t[0].ih < a.t[0].il;
+  a.by_inner = FastDiv((uint32_t)(a.heads_inner ? a.group : a.tok));
   auto launch = [&](auto t, auto ve) -> lact_status {
     using T = decltype(t);
     constexpr int VE = decltype(ve)::value;
+    a.by_per = FastDiv((uint32_t)(p->pairs / (il ? (VE > 1 ? VE / 2 : 1) : VE) + (p->d - 2 * p->pairs) / VE));
     if (il) LACT_LAUNCH((rotary_kernel<T, VE, true>), dim3(grid), dim3(256), s, a);
     else LACT_LAUNCH((rotary_kernel<T, VE, false>), dim3(grid), dim3(256), s, a);
     HIP_TRY(hipGetLastError());
@@ -464,19 +481,22 @@ NormPlan norm_plan(const lact_norm_problem& p) {
   const int64_t n = ceil_div(p.cols, 16 / size_of(p.io_dtype));
   const int gs = n <= 64 || (n <= 256 && p.rows >= 4 * NCU) ? 64 : n <= 1024 ? 256 : 1024;
   const int64_t nv = ceil_div(n, gs);
-  return {gs, nv <= 1 && gs < 1024 ? 1 : nv <= 2 ? 2 : nv <= 4 ? 4 : 8};
+  return {gs, nv <= 1 && gs < 1024 ? 1 : nv <= 2 ? 2 : nv <= 3 ? 3 : nv <= 4 ? 4 : 8};
 }
+// workgroups of the backward, 512 threads or one row's 1024 each: as many as
+// run at once, so that few partial sums of dw remain
 int64_t norm_back_grid(const lact_norm_problem& p, const NormPlan& c) {
-  return std::min<int64_t>(p.rows, (c.gs == 64 ? 8 : c.gs == 256 ? 4 : 1) * NCU);
+  return std::min<int64_t>(ceil_div(p.rows, c.gs < 512 ? 512 / c.gs : 1), (c.gs == 1024 ? 1 : 2) * NCU);
 }
 
 // calls fn with the element type, vectors and threads of the plan, and whether rows are vector-aligned
 template <class F>
 lact_status by_plan(const lact_norm_problem& p, const NormPlan& c, bool vec, F&& fn) {
   auto with = [&](auto t, auto v) -> lact_status {
-    if (c.gs == 64) return c.nv == 1 ? fn(t, IC<1>{}, IC<64>{}, v) : c.nv == 2 ? fn(t, IC<2>{}, IC<64>{}, v) : fn(t, IC<4>{}, IC<64>{}, v);
-    if (c.gs == 256) return c.nv == 1 ? fn(t, IC<1>{}, IC<256>{}, v) : c.nv == 2 ? fn(t, IC<2>{}, IC<256>{}, v) : fn(t, IC<4>{}, IC<256>{}, v);
+    if (c.gs == 64) return c.nv == 1 ? fn(t, IC<1>{}, IC<64>{}, v) : c.nv == 2 ? fn(t, IC<2>{}, IC<64>{}, v) : c.nv == 3 ? fn(t, IC<3>{}, IC<64>{}, v) : fn(t, IC<4>{}, IC<64>{}, v);
+    if (c.gs == 256) return c.nv == 1 ? fn(t, IC<1>{}, IC<256>{}, v) : c.nv == 2 ? fn(t, IC<2>{}, IC<256>{}, v) : c.nv == 3 ? fn(t, IC<3>{}, IC<256>{}, v) : fn(t, IC<4>{}, IC<256>{}, v);
     if (c.nv == 2) return fn(t, IC<2>{}, IC<1024>{}, v);
+    if (c.nv == 3) return fn(t, IC<3>{}, IC<1024>{}, v);
     if (c.nv == 4) return fn(t, IC<4>{}, IC<1024>{}, v);
     if constexpr (sizeof(t) == 4) return fn(t, IC<8>{}, IC<1024>{}, v);
     return fail(LACT_ERR_UNSUPPORTED, "internal: %d columns", p.cols);
@@ -516,7 +536,7 @@ lact_status lact_add_rmsnorm_forward(const lact_norm_problem* p, const void* x, 
     TRY(check_in_place("y", y, ldy, residual, ldr));
   }
   if (y && y == h) return fail(LACT_ERR_INVALID_ARG, "y is h");
-  TRY(check_device());
+  TRY(check_device_again());
   a.x = static_cast<const char*>(x);
   a.res = static_cast<const char*>(residual);
   a.w = weight;
@@ -577,7 +597,7 @@ lact_status lact_add_rmsnorm_backward(const lact_norm_problem* p, const void* h,
     NEED(dw, 4);
     TRY(check_ws(ws, ws_bytes, align256((size_t)grid * p->cols * 4)));
   }
-  TRY(check_device());
+  TRY(check_device_again());
   a.x = static_cast<const char*>(h);
   a.w = weight;
   a.dy = static_cast<const char*>(dy);
@@ -593,14 +613,14 @@ lact_status lact_add_rmsnorm_backward(const lact_norm_problem* p, const void* h,
     TRY(by_plan(*p, c, vec, [&](auto t, auto nv, auto gs, auto v) -> lact_status {
       constexpr int NV = decltype(nv)::value, GS = decltype(gs)::value;
       constexpr bool VEC = decltype(v)::value;
-      LACT_LAUNCH((norm_back_kernel<decltype(t), NV, GS, VEC>), dim3((unsigned)grid), dim3(GS), s, a);
+      LACT_LAUNCH((norm_back_kernel<decltype(t), NV, GS, VEC>), dim3((unsigned)grid), dim3(GS < 512 ? 512 : GS), s, a);
       HIP_TRY(hipGetLastError());
       return LACT_OK;
     }));
   }
   if (dw) {
     KernelTimer kt(LACT_K_NORM, s);
-    LACT_LAUNCH(norm_dw_kernel, dim3((unsigned)ceil_div(p->cols, 64)), dim3(1024), s, a.part, dw, (int)grid, p->cols);
+    LACT_LAUNCH(norm_dw_kernel, dim3((unsigned)ceil_div(p->cols, 32)), dim3(1024), s, a.part, dw, (int)grid, p->cols);
     HIP_TRY(hipGetLastError());
   }
   return LACT_OK;

@@ -43,13 +43,27 @@ struct RotaryTensor {
   int64_t ib, ih, il, ob, oh, ol;  // byte strides
   int32_t heads;
 };
+// n / d for 0 <= n < 2^31 and a divisor that the host knows: a multiplication
+// and a shift (four divisions of every 8-byte item took as long as its memory)
+struct FastDiv {
+  uint32_t d, m, s;
+  FastDiv() = default;
+  explicit FastDiv(uint32_t d_) : d(d_), m(0), s(0) {
+    while ((uint64_t(1) << s) < d) ++s;
+    m = (uint32_t)(((uint64_t(1) << 32) * ((uint64_t(1) << s) - d)) / d + 1);
+  }
+  __device__ __forceinline__ uint32_t div(uint32_t n) const { return (__umulhi(n, m) + n) >> s; }
+};
+
 struct RotaryArgs {
   RotaryTensor t[2];         // q and k (k.heads 0: none)
   const double* freqs;       // [pairs] radians a position
   const int64_t* positions;  // [B, L], or null: start + token
   int64_t start;
   int32_t B, L, d, pairs;
-  int32_t tok, head_groups;  // tokens and head groups of a workgroup
+  int32_t tok, group, head_groups;  // tokens and heads of a workgroup, groups of heads
+  int32_t heads_inner;              // heads are closer in memory than tokens
+  FastDiv by_pairs, by_per, by_inner;  // pairs; items of a head's row; group or tok
   float mscale;
   int32_t inverse;
 };
@@ -71,9 +85,9 @@ __global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a) {
   const int t0 = (id % groups) * a.tok, b = id / groups;
   const int nt = min(a.tok, a.L - t0), n = a.pairs;
   for (int i = threadIdx.x; i < nt * n; i += 256) {
-    const int t = t0 + i / n;
+    const int k = (int)a.by_pairs.div(i), t = t0 + k;
     const double pos = (double)(a.positions ? a.positions[(int64_t)b * a.L + t] : a.start + t);
-    double turn = pos * (a.freqs[i % n] * 0.15915494309189533577);  // / (2 pi)
+    double turn = pos * (a.freqs[i - k * n] * 0.15915494309189533577);  // / (2 pi)
     turn -= rint(turn);
     float s, c;
     if constexpr (sizeof(T) == 4) {
@@ -87,53 +101,65 @@ __global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a) {
     sn[i] = (a.inverse ? -s : s) * a.mscale;
   }
   __syncthreads();
-  // items of a row: pairs by VE (half layout) or VE / 2, then the copied rest
+  // items of a head's row: pairs by VE (half layout) or VE / 2, then the copied rest
   constexpr int PV = INTERLEAVED ? (VE > 1 ? VE / 2 : 1) : VE;
-  const int turned = n / PV, rest = (a.d - 2 * n) / VE, per = turned + rest;
+  // interleaved vectors hold whole pairs, so an item is one vector; else two
+  constexpr bool ONE = INTERLEAVED && VE > 1;
+  const int turned = n / PV, per = (int)a.by_per.d;
   const int heads = a.t[0].heads + a.t[1].heads;
-  const int h0 = (int)((int64_t)heads * hg / a.head_groups), h1 = (int)((int64_t)heads * (hg + 1) / a.head_groups);
-  const int items = nt * (h1 - h0) * per;
-  const bool heads_inner = a.t[0].ih < a.t[0].il;  // neighbours in memory go to neighbouring lanes
-  for (int i = threadIdx.x; i < items; i += 256) {
-    const int c = i % per, r = i / per;
-    const int t = heads_inner ? r / (h1 - h0) : r % nt;
-    int h = h0 + (heads_inner ? r % (h1 - h0) : r / nt);
-    const RotaryTensor& x = h < a.t[0].heads ? a.t[0] : a.t[1];
-    if (h >= a.t[0].heads) h -= a.t[0].heads;
-    const T* in = reinterpret_cast<const T*>(x.in + b * x.ib + h * x.ih + (int64_t)(t0 + t) * x.il);
-    T* out = reinterpret_cast<T*>(x.out + b * x.ob + h * x.oh + (int64_t)(t0 + t) * x.ol);
-    if (c >= turned) {
-      if (in != out) {
-        float v[VE];
-        const int e = 2 * n + (c - turned) * VE;
-        load_n<T, VE>(in + e, v);
-        store_n<T, VE>(out + e, v);
-      }
-    } else if constexpr (INTERLEAVED && VE > 1) {
-      float v[VE];
-      load_n<T, VE>(in + c * VE, v);
+  const int h0 = hg * a.group;
+  // neighbours in memory go to neighbouring lanes: heads run inside tokens or
+  // tokens inside heads; what the last groups lack is skipped
+  const int items = a.tok * a.group * per;
+  constexpr int U = VE * (int)sizeof(T) >= 16 ? 2 : 4;  // items in flight: all loads of a round before its stores
+  for (int i0 = threadIdx.x; i0 < items; i0 += 256 * U) {
+    float u[U][VE], v[U][VE];
+    T* out[U];
+    int c[U], tab[U];  // c: -1 nothing to do
 #pragma unroll
-      for (int j = 0; j < VE; j += 2) {
-        const float co = cs[t * n + c * PV + j / 2], si = sn[t * n + c * PV + j / 2];
-        const float x0 = v[j], x1 = v[j + 1];
-        v[j] = x0 * co - x1 * si;
-        v[j + 1] = x0 * si + x1 * co;
-      }
-      store_n<T, VE>(out + c * VE, v);
-    } else {
-      const int e0 = INTERLEAVED ? 2 * c : c * VE, e1 = INTERLEAVED ? e0 + 1 : e0 + n;
-      float u[VE], v[VE];
-      load_n<T, VE>(in + e0, u);
-      load_n<T, VE>(in + e1, v);
+    for (int k = 0; k < U; ++k) {
+      const int i = i0 + 256 * k;
+      c[k] = -1;
+      if (i >= items) continue;
+      const int r = (int)a.by_per.div(i), outer = (int)a.by_inner.div(r), inner = r - outer * (int)a.by_inner.d;
+      const int t = a.heads_inner ? outer : inner;
+      int h = h0 + (a.heads_inner ? inner : outer);
+      if (t >= nt || h >= heads) continue;
+      const RotaryTensor& x = h < a.t[0].heads ? a.t[0] : a.t[1];
+      if (h >= a.t[0].heads) h -= a.t[0].heads;
+      const T* in = reinterpret_cast<const T*>(x.in + b * x.ib + h * x.ih + (int64_t)(t0 + t) * x.il);
+      out[k] = reinterpret_cast<T*>(x.out + b * x.ob + h * x.oh + (int64_t)(t0 + t) * x.ol);
+      const int cc = i - r * per;
+      if (cc >= turned && in == out[k]) continue;  // in place, the rest is there
+      c[k] = cc;
+      tab[k] = t * n + cc * PV;
+      const int e0 = cc >= turned ? 2 * n + (cc - turned) * VE : ONE ? cc * VE : INTERLEAVED ? 2 * cc : cc * VE;
+      load_n<T, VE>(in + e0, u[k]);
+      if (!ONE && cc < turned) load_n<T, VE>(in + e0 + (INTERLEAVED ? 1 : n), v[k]);
+      out[k] += e0;
+    }
 #pragma unroll
-      for (int j = 0; j < VE; ++j) {
-        const float co = cs[t * n + c * PV + j], si = sn[t * n + c * PV + j];
-        const float x0 = u[j], x1 = v[j];
-        u[j] = x0 * co - x1 * si;
-        v[j] = x0 * si + x1 * co;
+    for (int k = 0; k < U; ++k) {
+      if (c[k] < 0) continue;
+      if (c[k] < turned) {
+        if constexpr (ONE) {
+#pragma unroll
+          for (int j = 0; j < VE; j += 2) {
+            const float co = cs[tab[k] + j / 2], si = sn[tab[k] + j / 2], x0 = u[k][j], x1 = u[k][j + 1];
+            u[k][j] = x0 * co - x1 * si;
+            u[k][j + 1] = x0 * si + x1 * co;
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < VE; ++j) {
+            const float co = cs[tab[k] + j], si = sn[tab[k] + j], x0 = u[k][j], x1 = v[k][j];
+            u[k][j] = x0 * co - x1 * si;
+            v[k][j] = x0 * si + x1 * co;
+          }
+          store_n<T, VE>(out[k] + (INTERLEAVED ? 1 : n), v[k]);
+        }
       }
-      store_n<T, VE>(out + e0, u);
-      store_n<T, VE>(out + e1, v);
+      store_n<T, VE>(out[k], u[k]);
     }
   }
 }
@@ -296,24 +322,32 @@ __global__ __launch_bounds__(GS < 256 ? 256 : GS) void norm_kernel(NormArgs a) {
 
 // From the stored h, with g = w dy and f = 1 / sqrt(mean h^2 + eps):
 //   dx = f g - h f^3 mean(g h) + dh,  dw = sum over rows of dy h f.
-// A workgroup takes every gridDim-th row and keeps its dw in registers; the
+// A workgroup takes NT / GS rows at a time, gridDim of them apart, and keeps
+// its dw in registers; its threads of a column add up in LDS, and the
 // workgroups' partial sums are added in a fixed order by norm_dw_kernel.
 template <typename T, int NV, int GS, bool VEC>
-__global__ __launch_bounds__(GS) void norm_back_kernel(NormArgs a) {
+__global__ __launch_bounds__(GS < 512 ? 512 : GS) void norm_back_kernel(NormArgs a) {
   using R = NormRow<T, NV, GS, VEC>;
-  constexpr int VE = R::VE;
-  __shared__ float2 lds[GS / WAVE];
-  const int t = threadIdx.x;
+  constexpr int VE = R::VE, NT = GS < 512 ? 512 : GS, RPB = NT / GS;
+  __shared__ float2 lds[NT / WAVE];
+  __shared__ float sums[RPB > 1 ? NV * VE * GS : 1];
+  const int t = threadIdx.x % GS, group = threadIdx.x / GS;
+  float2* mine = lds + group * (GS / WAVE);
   float w[NV][VE], dw[NV][VE];
   R::weights(a.w, a.cols, t, w);
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
     for (int e = 0; e < VE; ++e) dw[j][e] = 0.f;
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    float h[NV][VE], g[NV][VE];
-    R::load(a.x + row * a.ldx, a.cols, t, h);
-    R::load(a.dy + row * a.ldg, a.cols, t, g);
+  // every group runs the same number of rounds (a row's sum has barriers where GS > 64)
+  for (int64_t row0 = (int64_t)blockIdx.x * RPB; row0 < a.rows; row0 += (int64_t)gridDim.x * RPB) {
+    const int64_t row = row0 + group;
+    const bool some = row < a.rows;
+    float h[NV][VE], g[NV][VE], o[NV][VE];
+    const int cols = some ? a.cols : 0;
+    R::load(a.x + row * a.ldx, cols, t, h);
+    R::load(a.dy + row * a.ldg, cols, t, g);
+    if (a.dh) R::load(a.dh + row * a.lddh, cols, t, o);
     float ss = 0.f, sg = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
@@ -322,25 +356,38 @@ __global__ __launch_bounds__(GS) void norm_back_kernel(NormArgs a) {
         ss = fmaf(h[j][e], h[j][e], ss);
         sg = fmaf(g[j][e] * w[j][e], h[j][e], sg);
       }
-    const float2 s = row_sum2<GS>(ss, sg, lds, t);
+    const float2 s = row_sum2<GS>(ss, sg, mine, t);
     const float f = rsqrtf(s.x / (float)a.cols + a.eps), k = f * f * (s.y / (float)a.cols);
+    if (!some) continue;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int e = 0; e < VE; ++e) {
         dw[j][e] = fmaf(g[j][e], h[j][e] * f, dw[j][e]);
-        h[j][e] = f * (g[j][e] * w[j][e] - h[j][e] * k);
+        h[j][e] = f * (g[j][e] * w[j][e] - h[j][e] * k) + (a.dh ? o[j][e] : 0.f);
       }
-    if (a.dh) {
-      R::load(a.dh + row * a.lddh, a.cols, t, g);
-#pragma unroll
-      for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int e = 0; e < VE; ++e) h[j][e] += g[j][e];
-    }
     R::store(a.dx + row * a.lddx, a.cols, t, h);
   }
   if (!a.part) return;
+  if constexpr (RPB > 1) {
+    for (int q = 1; q < RPB; ++q) {
+      __syncthreads();
+      if (group == q) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+          for (int e = 0; e < VE; ++e) sums[(j * VE + e) * GS + t] = dw[j][e];
+      }
+      __syncthreads();
+      if (group == 0) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+          for (int e = 0; e < VE; ++e) dw[j][e] += sums[(j * VE + e) * GS + t];
+      }
+    }
+    if (group != 0) return;
+  }
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
@@ -348,20 +395,21 @@ __global__ __launch_bounds__(GS) void norm_back_kernel(NormArgs a) {
       if (R::col(j, t) + e < a.cols) a.part[(int64_t)blockIdx.x * a.cols + R::col(j, t) + e] = dw[j][e];
 }
 
-// dw[c] = the sum of part[0 .. n - 1][c]: 16 threads a column, a fixed order
+// dw[c] = the sum of part[0 .. n - 1][c]: 32 threads a column, a fixed order
 __global__ __launch_bounds__(1024) void norm_dw_kernel(const float* part, float* dw, int n, int cols) {
-  __shared__ float lds[16][64];
-  const int c = blockIdx.x * 64 + threadIdx.x % 64, r = threadIdx.x / 64;
+  __shared__ float lds[32][33];
+  const int x = threadIdx.x % 32, r = threadIdx.x / 32, c = blockIdx.x * 32 + x;
   float s = 0.f;
   if (c < cols)
-    for (int i = r; i < n; i += 16) s += part[(int64_t)i * cols + c];
-  lds[r][threadIdx.x % 64] = s;
+#pragma unroll 8
+    for (int i = r; i < n; i += 32) s += part[(int64_t)i * cols + c];
+  lds[r][x] = s;
   __syncthreads();
   if (r == 0 && c < cols) {
-    float x = 0.f;
+    float y = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) x += lds[i][threadIdx.x];
-    dw[c] = x;
+    for (int i = 0; i < 32; ++i) y += lds[i][x];
+    dw[c] = y;
   }
 }
 

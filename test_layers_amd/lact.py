@@ -486,49 +486,95 @@ def layer_backward(q, k, v, lr, beta, W1, W2, W3, M1=None, M2=None, M3=None, *, 
 
 
 # ----------------------------------------------------------------- operators around the layer
-class _Call:
+# A call's checks depend on its tensors' shapes, strides, types and devices
+# and on its parameters alone.  What they yield -- the C structs, the layout
+# of results, the workspace size -- is kept for recent combinations, so that a
+# serving loop's repeated call costs little beyond its launch.  Nothing of a
+# tensor's contents, address or identity is kept.
+_PLANS = {}
+
+
+class _Plan:
+    pass
+
+
+def _meta(t):
+    return None if t is None else (t.dtype, t.device, t.shape, t.stride())
+
+
+def _plan(key, build):
+    plan = _PLANS.get(key)
+    if plan is None:
+        plan = build()
+        if len(_PLANS) >= 512:
+            _PLANS.clear()
+        _PLANS[key] = plan
+    return plan
+
+
+def _one_device(*tensors):
+    """The CUDA device that all given tensors share."""
+    dev = tensors[0].device
+    if dev.type != "cuda":
+        raise ValueError("tensors must be on the device")
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}")
+    return dev
+
+
+def _here(index):
+    """The raw current stream of the current device, or None if that is not
+    device `index`: the short way of a call that names no stream."""
+    torch = _torch()
+    if torch.cuda.current_device() != index:
+        return None
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return torch.cuda.current_stream().cuda_stream if raw is None else raw(index)
+
+
+def _on(device, stream, tensors, run):
+    """run(handle of the stream) where the call belongs (see _Stream)."""
+    if stream is None:
+        handle = _here(device.index)
+        if handle is not None:
+            return run(handle)
+    with _Stream(device, stream, tensors) as handle:
+        return run(handle)
+
+
+class _Stream:
     """Where a call runs: with the tensors' device current and, if one is
     given, on `stream` -- what the call allocates then belongs to that stream,
     and the caching allocator learns that the inputs are in use there."""
 
-    def __init__(self, stream, *tensors):
+    def __init__(self, device, stream, tensors):
         torch = _torch()
-        dev = tensors[0].device
-        if not tensors[0].is_cuda:
-            raise ValueError("tensors must be on the device")
-        for t in tensors:
-            if t is not None and t.device != dev:
-                raise ValueError(f"tensors on {dev} and {t.device}")
-        self.device, self.given = dev, stream
-        self.guards = []
+        self.tensors, self.given, self.guard = tensors, stream, None
         if stream is not None:
-            if stream.device != dev:
-                raise ValueError(f"stream of {stream.device} for tensors on {dev}")
-            self.guards.append(torch.cuda.stream(stream))   # makes the device current too
-            self.tensors = tensors
-        elif torch.cuda.current_device() != dev.index:
-            self.guards.append(torch.cuda.device(dev))
-        self.handle = (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
+            if stream.device != device:
+                raise ValueError(f"stream of {stream.device} for tensors on {device}")
+            self.guard = torch.cuda.stream(stream)   # makes its device current too
+        elif torch.cuda.current_device() != device.index:
+            self.guard = torch.cuda.device(device)
+        self.handle = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
 
     def __enter__(self):
-        for g in self.guards:
-            g.__enter__()
-        return self
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self.handle
 
     def __exit__(self, *exc):
-        for g in reversed(self.guards):
-            g.__exit__(*exc)
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
         if self.given is not None:
             for t in self.tensors:
                 if t is not None:
                     t.record_stream(self.given)
 
 
-_STRIDES = {}
-
-
 def _strided(t, name, shape, dtype):
-    """(pointer, strides) of a [batch, heads, tokens, d] tensor with d contiguous."""
+    """Strides of a [batch, heads, tokens, d] tensor with d contiguous."""
     if t.dtype != dtype:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if tuple(t.shape) != shape:
@@ -536,27 +582,65 @@ def _strided(t, name, shape, dtype):
     b, h, l, e = t.stride()
     if e != 1 and shape[3] > 1 and t.numel():
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    key = (b, h, l)
-    s = _STRIDES.get(key)
-    if s is None:
-        if len(_STRIDES) >= 256:
-            _STRIDES.clear()
-        s = _STRIDES[key] = Strides(b, h, l)
-    return t.data_ptr(), ctypes.byref(s)
+    return Strides(b, h, l)
 
 
 def _lens(t, name, batch):
-    if t is None:
-        return None
-    _check_shapes(**{name: (t, (batch,))})
-    return _ptr(t, _torch().int64, name)
+    if t is not None:
+        _check_shapes(**{name: (t, (batch,))})
+        _ptr(t, _torch().int64, name)
 
 
-def _attention(q, k, v, window, sinks, scale):
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _like(t):
+    """An empty tensor of t's shape, in t's order of dimensions where t's rows are distinct."""
+    torch = _torch()
+    if 0 in t.stride():   # an expanded input: its gradient or result has a place for every element
+        return torch.empty(t.shape, dtype=t.dtype, device=t.device)
+    return torch.empty_like(t)
+
+
+def _new(t, meta):
+    """An empty tensor with the shape, strides and type that `meta` recorded, beside t."""
+    dtype, _, shape, stride = meta
+    if stride == t.stride() and shape == t.shape and dtype == t.dtype:
+        return _torch().empty_like(t)   # dense: the recorded strides are what this gives
+    return _torch().empty_strided(shape, stride, dtype=dtype, device=t.device)
+
+
+def _attention_plan(q, k, v, window, sinks, scale, q_lens, k_lens, back):
+    torch = _torch()
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q must be [batch, heads, tokens, d] and k [batch, kv_heads, tokens, d]")
     (b, h, lq, d), (_, hk, lk, _) = q.shape, k.shape
-    return Attention(b, h, hk, d, _io_dtype(q), d ** -0.5 if scale is None else scale, lq, lk, window, sinks)
+    plan = _Plan()
+    plan.device = _one_device(q, k, v, q_lens, k_lens)
+    plan.shape, plan.kshape, plan.dtype = (b, h, lq, d), (b, hk, lk, d), q.dtype
+    plan.problem = Attention(b, h, hk, d, _io_dtype(q), d ** -0.5 if scale is None else scale, lq, lk, window, sinks)
+    plan.p = ctypes.byref(plan.problem)
+    plan.strides = [_strided(q, "q", plan.shape, q.dtype), _strided(k, "k", plan.kshape, q.dtype),
+                    _strided(v, "v", plan.kshape, q.dtype)]
+    plan.sq, plan.sk, plan.sv = (ctypes.byref(x) for x in plan.strides)
+    _lens(q_lens, "q_lens", b)
+    _lens(k_lens, "k_lens", b)
+    plan.need = (lib().lact_window_attention_backward_workspace_size if back
+                 else lib().lact_window_attention_workspace_size)(plan.p)
+    plan.results = [_meta(_like(t)) for t in (q, k, v)]
+    plan.rstrides = [Strides(*m[3][:3]) for m in plan.results]
+    plan.rq, plan.rk, plan.rv = (ctypes.byref(x) for x in plan.rstrides)
+    plan.lse = (torch.float32, None, (b, h, lq), (h * lq, lq, 1))
+    return plan
+
+
+def _scratch(need, workspace, device):
+    """(address, bytes) of the workspace, and the tensor that holds it."""
+    if workspace is None and need == 0:
+        return None, 0, None
+    ws = _workspace(need, workspace, device)
+    return ws.data_ptr(), ws.numel(), ws
 
 
 def window_attention(q, k, v, o=None, *, window: int = 0, sinks: int = 0, scale: Optional[float] = None,
@@ -569,26 +653,32 @@ def window_attention(q, k, v, o=None, *, window: int = 0, sinks: int = 0, scale:
     each sequence's own lengths; scale defaults to d^-1/2.  Returns o in q's
     layout, and with return_lse also lse [batch, heads, q_len] fp32; what is
     allocated here has zeros behind q_lens, given tensors keep what they held."""
-    torch = _torch()
-    p = _attention(q, k, v, window, sinks, scale)
-    shape, kshape, dt = tuple(q.shape), (q.shape[0], k.shape[1], k.shape[2], q.shape[3]), q.dtype
-    with _Call(stream, q, k, v, o, q_lens, k_lens, lse, workspace) as call:
+    plan = _plan(("attention", window, sinks, scale, _meta(q), _meta(k), _meta(v), _meta(q_lens), _meta(k_lens)),
+                 lambda: _attention_plan(q, k, v, window, sinks, scale, q_lens, k_lens, False))
+    so = plan.rq
+    if o is not None or lse is not None or workspace is not None:
+        _one_device(q, o, lse, workspace)
+        if o is not None:
+            so = ctypes.byref(_strided(o, "o", plan.shape, plan.dtype))
+        _check_shapes(lse=(lse, plan.shape[:3]))
+        _ptr(lse, _torch().float32, "lse")
+    def run(handle, o=o, lse=lse):
         if o is None:
-            o = torch.empty_like(q) if q_lens is None else torch.zeros_like(q)
-        if lse is None:
-            if return_lse:
-                new = torch.empty if q_lens is None else torch.zeros
-                lse = new(shape[:3], dtype=torch.float32, device=q.device)
-        else:
-            _check_shapes(lse=(lse, shape[:3]))
-        need = lib().lact_window_attention_workspace_size(ctypes.byref(p))
-        ws = _workspace(need, workspace, q.device) if need or workspace is not None else None
-        check(lib().lact_window_attention_forward(
-            ctypes.byref(p), *_strided(q, "q", shape, dt), *_strided(k, "k", kshape, dt),
-            *_strided(v, "v", kshape, dt), _lens(q_lens, "q_lens", shape[0]), _lens(k_lens, "k_lens", shape[0]),
-            *_strided(o, "o", shape, dt), _ptr(lse, torch.float32, "lse"),
-            None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), call.handle))
-    return (o, lse) if return_lse else o
+            o = _new(q, plan.results[0])
+            if q_lens is not None:
+                o.zero_()
+        if lse is None and return_lse:
+            lse = _new(q, plan.lse)
+            if q_lens is not None:
+                lse.zero_()
+        ws, ws_bytes, _held = _scratch(plan.need, workspace, q.device)
+        st = lib().lact_window_attention_forward(
+            plan.p, q.data_ptr(), plan.sq, k.data_ptr(), plan.sk, v.data_ptr(), plan.sv, _addr(q_lens), _addr(k_lens),
+            o.data_ptr(), so, _addr(lse), ws, ws_bytes, handle)
+        check(st)
+        return (o, lse) if return_lse else o
+
+    return _on(plan.device, stream, (q, k, v, o, q_lens, k_lens, lse, workspace), run)
 
 
 def window_attention_backward(q, k, v, o, lse, *, dO, window: int = 0, sinks: int = 0,
@@ -598,49 +688,80 @@ def window_attention_backward(q, k, v, o, lse, *, dO, window: int = 0, sinks: in
     as the forward returned them, dO [batch, heads, q_len, d] in q's dtype.
     Returns a dict of dq, dk, dv in the inputs' dtype and layout, zero behind
     the lengths; `out` (such a dict) is filled instead of allocating."""
-    torch = _torch()
-    p = _attention(q, k, v, window, sinks, scale)
-    shape, kshape, dt = tuple(q.shape), (q.shape[0], k.shape[1], k.shape[2], q.shape[3]), q.dtype
+    plan = _plan(("attention back", window, sinks, scale, _meta(q), _meta(k), _meta(v), _meta(q_lens), _meta(k_lens)),
+                 lambda: _attention_plan(q, k, v, window, sinks, scale, q_lens, k_lens, True))
     given = () if out is None else (out["dq"], out["dk"], out["dv"])
-    with _Call(stream, q, k, v, o, lse, dO, q_lens, k_lens, workspace, *given) as call:
+    _one_device(q, o, lse, dO, workspace, *given)
+    so = ctypes.byref(_strided(o, "o", plan.shape, plan.dtype))
+    sg = ctypes.byref(_strided(dO, "dO", plan.shape, plan.dtype))
+    _check_shapes(lse=(lse, plan.shape[:3]))
+    rq, rk, rv = plan.rq, plan.rk, plan.rv
+    if out is not None:
+        rq, rk, rv = (ctypes.byref(_strided(t, f"out[{n}]", s, plan.dtype))
+                      for t, n, s in zip(given, ("dq", "dk", "dv"), (plan.shape, plan.kshape, plan.kshape)))
+    def run(handle, out=out):
         if out is None:
-            out = {"dq": torch.empty_like(q), "dk": _like(k), "dv": _like(v)}
-        _check_shapes(lse=(lse, shape[:3]))
-        need = lib().lact_window_attention_backward_workspace_size(ctypes.byref(p))
-        ws = _workspace(need, workspace, q.device)
-        check(lib().lact_window_attention_backward(
-            ctypes.byref(p), *_strided(q, "q", shape, dt), *_strided(k, "k", kshape, dt),
-            *_strided(v, "v", kshape, dt), _lens(q_lens, "q_lens", shape[0]), _lens(k_lens, "k_lens", shape[0]),
-            *_strided(o, "o", shape, dt), _ptr(lse, torch.float32, "lse"), *_strided(dO, "dO", shape, dt),
-            *_strided(out["dq"], "out[dq]", shape, dt), *_strided(out["dk"], "out[dk]", kshape, dt),
-            *_strided(out["dv"], "out[dv]", kshape, dt), ws.data_ptr(), ws.numel(), call.handle))
-    return out
+            out = {n: _new(q, m) for n, m in zip(("dq", "dk", "dv"), plan.results)}
+        ws, ws_bytes, _held = _scratch(plan.need, workspace, q.device)
+        st = lib().lact_window_attention_backward(
+            plan.p, q.data_ptr(), plan.sq, k.data_ptr(), plan.sk, v.data_ptr(), plan.sv, _addr(q_lens), _addr(k_lens),
+            o.data_ptr(), so, _ptr(lse, _torch().float32, "lse"), dO.data_ptr(), sg, out["dq"].data_ptr(), rq,
+            out["dk"].data_ptr(), rk, out["dv"].data_ptr(), rv, ws, ws_bytes, handle)
+        check(st)
+        return out
+
+    return _on(plan.device, stream, (q, k, v, o, lse, dO, q_lens, k_lens, workspace) + given, run)
 
 
-def _rotary(q, k, freqs, positions, start, interleaved, mscale, q_out, k_out, stream, flags):
+def _rotary_plan(q, k, freqs, positions, start, mscale, flags):
     torch = _torch()
     if q.dim() != 4 or (k is not None and k.dim() != 4):
         raise ValueError("q and k must be [batch, heads, tokens, d]")
-    b, h, l, d = shape = tuple(q.shape)
-    kshape = None if k is None else (b, k.shape[1], l, d)
+    b, h, l, d = q.shape
     if freqs.dim() != 1:
         raise ValueError("freqs must be [pairs]")
-    if positions is not None:
-        _check_shapes(positions=(positions, (b, l)))
-    p = RotaryProblem(b, h, 0 if k is None else k.shape[1], d, freqs.shape[0], _io_dtype(q),
-                      flags | (ROTARY_INTERLEAVED if interleaved else 0), mscale, l, start)
-    with _Call(stream, q, k, freqs, positions, q_out, k_out) as call:
+    _check_shapes(positions=(positions, (b, l)))
+    plan = _Plan()
+    plan.device = _one_device(q, k, freqs, positions)
+    _ptr(freqs, torch.float64, "freqs")
+    _ptr(positions, torch.int64, "positions")
+    plan.problem = RotaryProblem(b, h, 0 if k is None else k.shape[1], d, freqs.shape[0], _io_dtype(q), flags, mscale, l,
+                                 start)
+    plan.p = ctypes.byref(plan.problem)
+    plan.dtype, plan.shape, plan.kshape = q.dtype, (b, h, l, d), None if k is None else (b, k.shape[1], l, d)
+    given = [_strided(q, "q", plan.shape, q.dtype)] + ([] if k is None else [_strided(k, "k", plan.kshape, q.dtype)])
+    plan.results = [_meta(_like(t)) for t in ((q,) if k is None else (q, k))]
+    plan.strides = given + [Strides(*m[3][:3]) for m in plan.results]
+    refs = [ctypes.byref(x) for x in plan.strides]
+    plan.sq, plan.sk, plan.rq, plan.rk = refs if k is not None else (refs[0], None, refs[1], None)
+    return plan
+
+
+def _rotary(q, k, freqs, positions, start, interleaved, mscale, q_out, k_out, stream, flags):
+    if interleaved:
+        flags |= ROTARY_INTERLEAVED
+    plan = _plan(("rotary", _meta(q), _meta(k), _meta(freqs), _meta(positions), start, mscale, flags),
+                 lambda: _rotary_plan(q, k, freqs, positions, start, mscale, flags))
+    rq, rk = plan.rq, plan.rk
+    if q_out is not None or k_out is not None:
+        _one_device(q, q_out, k_out)
+        if q_out is not None:
+            rq = ctypes.byref(_strided(q_out, "q_out", plan.shape, plan.dtype))
+        if k_out is not None:
+            if k is None:
+                raise ValueError("k_out is given without k")
+            rk = ctypes.byref(_strided(k_out, "k_out", plan.kshape, plan.dtype))
+    def run(handle, q_out=q_out, k_out=k_out):
         if q_out is None:
-            q_out = _like(q)
+            q_out = _new(q, plan.results[0])
         if k is not None and k_out is None:
-            k_out = _like(k)
-        none = (None, None)
-        check(lib().lact_rotary(
-            ctypes.byref(p), *_strided(q, "q", shape, q.dtype),
-            *(none if k is None else _strided(k, "k", kshape, q.dtype)), _ptr(freqs, torch.float64, "freqs"),
-            _ptr(positions, torch.int64, "positions"), *_strided(q_out, "q_out", shape, q.dtype),
-            *(none if k is None else _strided(k_out, "k_out", kshape, q.dtype)), call.handle))
-    return q_out if k is None else (q_out, k_out)
+            k_out = _new(k, plan.results[1])
+        st = lib().lact_rotary(plan.p, q.data_ptr(), plan.sq, _addr(k), plan.sk, freqs.data_ptr(), _addr(positions),
+                               q_out.data_ptr(), rq, _addr(k_out), rk, handle)
+        check(st)
+        return q_out if k is None else (q_out, k_out)
+
+    return _on(plan.device, stream, (q, k, freqs, positions, q_out, k_out), run)
 
 
 def rotary(q, k=None, *, freqs, positions=None, start: int = 0, interleaved: bool = False, mscale: float = 1.0,
@@ -676,18 +797,10 @@ def rotary_frequencies(pairs: int, base: float = 10000.0, *, scaling: str = "pla
     return f.to("cuda" if device is None else device), m.value
 
 
-def _like(t):
-    """An empty tensor of t's shape, in t's order of dimensions where t's rows are distinct."""
-    torch = _torch()
-    if 0 in t.stride():   # an expanded input: its gradient or result has a place for every element
-        return torch.empty(t.shape, dtype=t.dtype, device=t.device)
-    return torch.empty_like(t)
-
-
 def _rows(t, name, shape, dtype):
-    """(pointer, row stride) of a [..., cols] tensor seen as a matrix."""
+    """Row stride of a [..., cols] tensor seen as a matrix."""
     if t is None:
-        return None, 0
+        return 0
     if t.dtype != dtype:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if tuple(t.shape) != shape:
@@ -696,18 +809,31 @@ def _rows(t, name, shape, dtype):
         ld, e = t.stride()
         if e != 1 and shape[1] > 1 and t.numel():
             raise ValueError(f"{name}: columns must be contiguous")
-        return t.data_ptr(), ld
+        return ld
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous (or a matrix with contiguous columns)")
-    return t.data_ptr(), shape[-1]
+    return shape[-1]
 
 
-def _norm_problem(x, weight, eps):
+def _norm_plan(x, weight, eps, *others):
+    """others: (name, tensor, whether it is in 8 bits)"""
+    torch = _torch()
     if x.dim() < 1 or x.shape[-1] == 0:
         raise ValueError("x must be [..., cols] with cols > 0")
     cols = x.shape[-1]
+    plan = _Plan()
+    plan.device = _one_device(x, weight, *[t for _, t, _ in others])
     _check_shapes(weight=(weight, (cols,)))
-    return NormProblem(x.numel() // cols, cols, _io_dtype(x), eps)
+    _ptr(weight, torch.float32, "weight")
+    plan.problem = NormProblem(x.numel() // cols, cols, _io_dtype(x), eps)
+    plan.p = ctypes.byref(plan.problem)
+    plan.shape, plan.cols = tuple(x.shape), cols
+    plan.groups = plan.shape[:-1] + ((cols + NORM_GROUP - 1) // NORM_GROUP,)
+    plan.ld = [_rows(x, "x", plan.shape, x.dtype)]
+    plan.ld += [_rows(t, n, plan.shape, torch.float8_e4m3fn if byte else x.dtype) if t is not None else cols
+                for n, t, byte in others]
+    plan.need = lib().lact_add_rmsnorm_backward_workspace_size(plan.p)
+    return plan
 
 
 def add_rmsnorm(x, weight, residual=None, *, eps: float = 1e-6, y=None, h=None, stream=None):
@@ -715,19 +841,20 @@ def add_rmsnorm(x, weight, residual=None, *, eps: float = 1e-6, y=None, h=None, 
     dimension (lact_add_rmsnorm_forward).  x, residual [..., cols] fp32 or
     bf16, weight [cols] fp32.  Returns (y, h); without a residual h is x
     itself.  h = residual or h = x updates the residual stream in place."""
-    torch = _torch()
-    p = _norm_problem(x, weight, eps)
-    shape, dt = tuple(x.shape), x.dtype
-    with _Call(stream, x, weight, residual, y, h) as call:
+    plan = _plan(("norm", eps, _meta(x), _meta(weight), _meta(residual), _meta(y), _meta(h)),
+                 lambda: _norm_plan(x, weight, eps, ("residual", residual, False), ("h", h, False), ("y", y, False)))
+    ldx, ldr, ldh, ldy = plan.ld
+    def run(handle, y=y, h=h):
         if y is None:
-            y = torch.empty(shape, dtype=dt, device=x.device)
+            y = x.new_empty(plan.shape)
         if h is None and residual is not None:
-            h = torch.empty(shape, dtype=dt, device=x.device)
-        check(lib().lact_add_rmsnorm_forward(
-            ctypes.byref(p), *_rows(x, "x", shape, dt), *_rows(residual, "residual", shape, dt),
-            _ptr(weight, torch.float32, "weight"), *_rows(h, "h", shape, dt), *_rows(y, "y", shape, dt),
-            None, 0, None, call.handle))
-    return y, (x if h is None else h)
+            h = x.new_empty(plan.shape)
+        st = lib().lact_add_rmsnorm_forward(plan.p, x.data_ptr(), ldx, _addr(residual), ldr, weight.data_ptr(), _addr(h),
+                                            ldh, y.data_ptr(), ldy, None, 0, None, handle)
+        check(st)
+        return y, (x if h is None else h)
+
+    return _on(plan.device, stream, (x, weight, residual, y, h), run)
 
 
 def add_rmsnorm_quantised(x, weight, residual=None, *, eps: float = 1e-6, y8=None, scales=None, h=None, y=None,
@@ -737,23 +864,27 @@ def add_rmsnorm_quantised(x, weight, residual=None, *, eps: float = 1e-6, y8=Non
     y8 * scale of its group of 128 columns.  Returns (y8, scales, h); a given
     y is filled too."""
     torch = _torch()
-    p = _norm_problem(x, weight, eps)
-    shape, dt = tuple(x.shape), x.dtype
-    groups = shape[:-1] + ((shape[-1] + NORM_GROUP - 1) // NORM_GROUP,)
-    with _Call(stream, x, weight, residual, y8, scales, h, y) as call:
+    plan = _plan(("norm 8", eps, _meta(x), _meta(weight), _meta(residual), _meta(y8), _meta(h), _meta(y)),
+                 lambda: _norm_plan(x, weight, eps, ("residual", residual, False), ("h", h, False), ("y", y, False),
+                                    ("y8", y8, True)))
+    ldx, ldr, ldh, ldy, ld8 = plan.ld
+    if scales is not None:
+        _one_device(x, scales)
+        _check_shapes(scales=(scales, plan.groups))
+        _ptr(scales, torch.float32, "scales")
+    def run(handle, h=h, y8=y8, scales=scales):
         if y8 is None:
-            y8 = torch.empty(shape, dtype=torch.float8_e4m3fn, device=x.device)
+            y8 = x.new_empty(plan.shape, dtype=torch.float8_e4m3fn)
         if scales is None:
-            scales = torch.empty(groups, dtype=torch.float32, device=x.device)
-        else:
-            _check_shapes(scales=(scales, groups))
+            scales = x.new_empty(plan.groups, dtype=torch.float32)
         if h is None and residual is not None:
-            h = torch.empty(shape, dtype=dt, device=x.device)
-        check(lib().lact_add_rmsnorm_forward(
-            ctypes.byref(p), *_rows(x, "x", shape, dt), *_rows(residual, "residual", shape, dt),
-            _ptr(weight, torch.float32, "weight"), *_rows(h, "h", shape, dt), *_rows(y, "y", shape, dt),
-            *_rows(y8, "y8", shape, torch.float8_e4m3fn), _ptr(scales, torch.float32, "scales"), call.handle))
-    return y8, scales, (x if h is None else h)
+            h = x.new_empty(plan.shape)
+        st = lib().lact_add_rmsnorm_forward(plan.p, x.data_ptr(), ldx, _addr(residual), ldr, weight.data_ptr(), _addr(h),
+                                            ldh, _addr(y), ldy, y8.data_ptr(), ld8, scales.data_ptr(), handle)
+        check(st)
+        return y8, scales, (x if h is None else h)
+
+    return _on(plan.device, stream, (x, weight, residual, y8, scales, h, y), run)
 
 
 def add_rmsnorm_backward(h, weight, *, dy, dh=None, eps: float = 1e-6, dx=None, dw=None, workspace=None,
@@ -763,21 +894,25 @@ def add_rmsnorm_backward(h, weight, *, dy, dh=None, eps: float = 1e-6, dx=None, 
     Returns (dx, dw): dx is the gradient of x and of residual alike, dw [cols]
     fp32 that of the weight."""
     torch = _torch()
-    p = _norm_problem(h, weight, eps)
-    shape, dt = tuple(h.shape), h.dtype
-    with _Call(stream, h, weight, dy, dh, dx, dw, workspace) as call:
+    plan = _plan(("norm back", eps, _meta(h), _meta(weight), _meta(dy), _meta(dh), _meta(dx)),
+                 lambda: _norm_plan(h, weight, eps, ("dy", dy, False), ("dh", dh, False), ("dx", dx, False)))
+    ldh, ldy, lddh, lddx = plan.ld
+    _one_device(h, dw, workspace)
+    if dw is not None:
+        _check_shapes(dw=(dw, plan.shape[-1:]))
+        _ptr(dw, torch.float32, "dw")
+    def run(handle, dx=dx, dw=dw):
         if dx is None:
-            dx = torch.empty(shape, dtype=dt, device=h.device)
+            dx = h.new_empty(plan.shape)
         if dw is None:
-            dw = torch.empty(shape[-1], dtype=torch.float32, device=h.device)
-        else:
-            _check_shapes(dw=(dw, shape[-1:]))
-        ws = _workspace(lib().lact_add_rmsnorm_backward_workspace_size(ctypes.byref(p)), workspace, h.device)
-        check(lib().lact_add_rmsnorm_backward(
-            ctypes.byref(p), *_rows(h, "h", shape, dt), _ptr(weight, torch.float32, "weight"),
-            *_rows(dy, "dy", shape, dt), *_rows(dh, "dh", shape, dt), *_rows(dx, "dx", shape, dt),
-            _ptr(dw, torch.float32, "dw"), ws.data_ptr(), ws.numel(), call.handle))
-    return dx, dw
+            dw = h.new_empty(plan.cols, dtype=torch.float32)
+        ws, ws_bytes, _held = _scratch(plan.need, workspace, h.device)
+        st = lib().lact_add_rmsnorm_backward(plan.p, h.data_ptr(), ldh, weight.data_ptr(), dy.data_ptr(), ldy, _addr(dh),
+                                             lddh, dx.data_ptr(), lddx, dw.data_ptr(), ws, ws_bytes, handle)
+        check(st)
+        return dx, dw
+
+    return _on(plan.device, stream, (h, weight, dy, dh, dx, dw, workspace), run)
 
 
 lib()  # fail at import time if the library is missing
