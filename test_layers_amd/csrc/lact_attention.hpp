@@ -28,8 +28,7 @@ namespace lact {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-// instruction kinds of __builtin_amdgcn_sched_group_barrier
-constexpr int SG_VALU = 0x2, SG_MFMA = 0x8, SG_LDS = 0x100;
+constexpr int AHEAD = 4;  // products by which an operand's read from LDS comes before its own
 
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
@@ -265,6 +264,29 @@ __device__ __forceinline__ Pair round_pair(const f32x16& p) {
                                                    pack_bf16x2(p[8 * i + 4], p[8 * i + 5]), pack_bf16x2(p[8 * i + 6], p[8 * i + 7])));
   return b;
 }
+// the sum of a packed pair of bf16 and c
+__device__ __forceinline__ float pair_add(uint32_t x, float c) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, x), bf16x2{(__bf16)1.f, (__bf16)1.f}, c, false);
+}
+
+// half a tile of the backward: scores then P, dP - D then dS, and both rounded
+// pair by pair
+struct Half {
+  f32x16 s, ds;
+  uint32_t x[8], y[8];
+  __device__ __forceinline__ void round(int i) {
+    x[i] = pack_bf16x2(ds[2 * i], ds[2 * i + 1]);
+    y[i] = pack_bf16x2(s[2 * i], s[2 * i + 1]);
+  }
+  __device__ __forceinline__ bf16x8 frag_ds(int i) const {
+    return __builtin_bit_cast(bf16x8, make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]));
+  }
+  __device__ __forceinline__ bf16x8 frag_s(int i) const {
+    return __builtin_bit_cast(bf16x8, make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]));
+  }
+};
+
 template <typename T, int DP>
 __device__ __forceinline__ void acc_trans(f32x16 (&acc)[DP / 32], const f32x16& p, const char* tile, int row0, int lane) {
   if constexpr (sizeof(T) == 2) mma_trans<DP>(acc, round_pair(p).f, tile, row0, lane);
@@ -470,68 +492,69 @@ struct AttnRows {
     exps(s, c);
     acc_trans<T, DP>(o, s, vt, 0, lane);
   }
-  // 64 keys that every row sees: the matrix products of one half run beside the exponentials of
-  // the other, and the operands of a product are read while the one before it
-  // runs, so that one wave keeps matrix pipe, vector pipe and LDS busy.  The
-  // scheduling groups spell that order out; left to itself the compiler reads
-  // an operand just before its product and waits.
+  // 64 keys that every row sees.  Four runs of products: the scores of one
+  // half and of the other, then each half's sums.  The exponentials of a half
+  // go between the products of the run behind its own, a few after each, so
+  // that one wave keeps matrix and vector pipe busy, and an operand is read
+  // from LDS AHEAD products before its own.  The order is spelled out by the
+  // scheduling barriers: left to itself the compiler reads an operand just
+  // before its product, which then waits for LDS (dk, dv of the 32K step:
+  // 614 us that way).
   __device__ __forceinline__ void step2(const AttnAddr<DP>& at, lds_ptr kt, lds_ptr vt, float c) {
     static_assert(sizeof(T) == 2, "bf16");
-    constexpr int NV = 2 * DB;  // V fragments of 32 keys
-    Frag<T> ka[STEPS], kb[STEPS];
-    bf16x8 va[NV], vb[NV];
-    auto load_k = [&](Frag<T>(&f)[STEPS], int row) {
-#pragma unroll
-      for (int t = 0; t < STEPS; ++t) f[t] = at.rows(kt, row, t);
+    constexpr int NM = STEPS, E = 16 / NM;  // products of a run; scores behind each
+    auto frag = [&](int m) {
+      const int run = m / NM, i = m % NM;
+      return run < 2 ? at.rows(kt, 32 * run, i) : at.cols(vt, 32 * (run - 2) + 16 * (i / DB), i % DB);
     };
-    auto load_v = [&](bf16x8(&f)[NV], int row) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) f[i] = at.cols(vt, row + 16 * (i / DB), i % DB);
+    bf16x8 f[AHEAD];
+    auto next = [&](int m) {
+      if (m + AHEAD < 4 * NM) f[m % AHEAD] = frag(m + AHEAD);
     };
-    auto product = [&](const Frag<T>(&f)[STEPS]) {
-      f32x16 s = zero16();
 #pragma unroll
-      for (int t = 0; t < STEPS; ++t) s = mma32(f[t], q[t], s);
-      return s;
-    };
-    auto add = [&](const bf16x8(&f)[NV], const Pair& b) {
+    for (int m = 0; m < AHEAD; ++m) f[m] = frag(m);
+    __builtin_amdgcn_sched_barrier(0);
+    f32x16 s0 = zero16(), s1 = zero16();
 #pragma unroll
-      for (int i = 0; i < NV; ++i) o[i % DB] = mma32(f[i], b.f[i / DB], o[i % DB]);
-    };
-    load_k(ka, 0);
-    f32x16 s0 = product(ka);
-    __builtin_amdgcn_sched_group_barrier(SG_LDS, STEPS, 0);
-    __builtin_amdgcn_sched_group_barrier(SG_MFMA, STEPS, 0);
+    for (int i = 0; i < NM; ++i) {
+      s0 = mma32(f[i % AHEAD], q[i], s0);
+      next(i);
+      __builtin_amdgcn_sched_barrier(0);
+    }
     follow(s0, c, nullptr);
-
-    load_k(kb, 32);
-    f32x16 s1 = product(kb);
-    exps(s0, c);
-    __builtin_amdgcn_sched_group_barrier(SG_LDS, 4, 1);
-    __builtin_amdgcn_sched_group_barrier(SG_VALU, 8, 1);
+    float ref = m == -__builtin_huge_valf() ? 0.f : m;
+    auto some = [&](f32x16& s, int i) {
 #pragma unroll
-    for (int t = 0; t < STEPS; ++t) {
-      __builtin_amdgcn_sched_group_barrier(SG_MFMA, 1, 1);
-      if (t + 4 < STEPS) __builtin_amdgcn_sched_group_barrier(SG_LDS, 1, 1);
-      __builtin_amdgcn_sched_group_barrier(SG_VALU, 40 / STEPS, 1);
+      for (int r = i * E; r < i * E + E; ++r) {
+        s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, -ref));
+        l += s[r];
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < NM; ++i) {
+      s1 = mma32(f[(NM + i) % AHEAD], q[i], s1);
+      next(NM + i);
+      some(s0, i);
+      __builtin_amdgcn_sched_barrier(0);
     }
     asm volatile("" : "+v"(s0));  // the exponentials stay on this side of the branch
     follow(s1, c, &s0);
-
-    load_v(va, 0);
-    add(va, round_pair(s0));
-    exps(s1, c);
-    __builtin_amdgcn_sched_group_barrier(SG_LDS, 4, 2);
-    __builtin_amdgcn_sched_group_barrier(SG_VALU, 12, 2);
+    ref = m == -__builtin_huge_valf() ? 0.f : m;
+    const Pair p0 = round_pair(s0);
 #pragma unroll
-    for (int t = 0; t < NV; ++t) {
-      __builtin_amdgcn_sched_group_barrier(SG_MFMA, 1, 2);
-      if (t + 2 < NV) __builtin_amdgcn_sched_group_barrier(SG_LDS, 2, 2);
-      __builtin_amdgcn_sched_group_barrier(SG_VALU, 48 / NV, 2);
+    for (int i = 0; i < NM; ++i) {
+      o[i % DB] = mma32(f[(2 * NM + i) % AHEAD], p0.f[i / DB], o[i % DB]);
+      next(2 * NM + i);
+      some(s1, i);
+      __builtin_amdgcn_sched_barrier(0);
     }
-    __builtin_amdgcn_sched_barrier(0);
-    load_v(vb, 32);
-    add(vb, round_pair(s1));
+    const Pair p1 = round_pair(s1);
+#pragma unroll
+    for (int i = 0; i < NM; ++i) {
+      o[i % DB] = mma32(f[(3 * NM + i) % AHEAD], p1.f[i / DB], o[i % DB]);
+      next(3 * NM + i);
+      __builtin_amdgcn_sched_barrier(0);
+    }
   }
   // BN keys of which a row may see some or none
   template <int BN>
@@ -905,15 +928,13 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dq_kerne
       }
     };
     auto count = [&](const f32x16& ds, const Pair& x) {
-      typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-      const bf16x2 one = {(__bf16)1.f, (__bf16)1.f};
 #pragma unroll
       for (int r = 0; r < 16; ++r) sum += ds[r];
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int r = 0; r < 8; r += 2)
-          rsum = __builtin_amdgcn_fdot2_f32_bf16(bf16x2{x.f[e][r], x.f[e][r + 1]}, one, rsum, false);
+      for (int e = 0; e < 2; ++e) {
+        const uint4 w = __builtin_bit_cast(uint4, x.f[e]);
+        rsum = pair_add(w.x, pair_add(w.y, pair_add(w.z, pair_add(w.w, rsum))));
+      }
     };
     // a tile of which rows may see a part, 32 keys after another
     auto edge = [&](int i) {
@@ -956,62 +977,77 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dq_kerne
     int i = 0;
     if constexpr (CENTRE && BN == 64) {
       const AttnAddr<DP> addr(lane);
-      constexpr int NV = 2 * DB;
-      // 64 keys that every row sees: scores and dP of one half beside the
-      // exponentials of the other, then each half's sums (see AttnRows::step2)
+      // 64 keys that every row sees, as in AttnRows::step2: runs of scores and
+      // dP of one half and the other, then of each half's sums, each of whose
+      // operands serves two products
       auto whole = [&](lds_ptr kp, lds_ptr vp) {
-        auto products = [&](int row0, f32x16& s, f32x16& ds) {
-          s = zero16(), ds = less;
+        constexpr int NM = 2 * STEPS, E = 16 / NM, NF = 3 * NM;
+        auto frag = [&](int m) {
+          const int run = m / NM, i = m % NM;
+          if (run < 2) return addr.rows(i & 1 ? vp : kp, 32 * run, i / 2);
+          const int v = m - 2 * NM;  // of the sums: half v / STEPS
+          return addr.cols(kp, 32 * (v / STEPS) + 16 * (v % STEPS / DB), v % DB);
+        };
+        bf16x8 f[AHEAD];
+        auto next = [&](int m) {
+          if (m + AHEAD < NF) f[m % AHEAD] = frag(m + AHEAD);
+        };
+        Half h0, h1;
+        h0.s = h1.s = zero16();
+        h0.ds = h1.ds = less;
+        auto some = [&](Half& h, int i) {
 #pragma unroll
-          for (int t = 0; t < STEPS; ++t) {
-            s = mma32(addr.rows(kp, row0, t), q[t], s);
-            ds = mma32(addr.rows(vp, row0, t), g[t], ds);
+          for (int r = i * E; r < i * E + E; ++r) {
+            h.s[r] = __builtin_amdgcn_exp2f(fmaf(h.s[r], a.c, -lse2));
+            h.ds[r] *= h.s[r];
+            sum += h.ds[r];
+            if (r & 1) {
+              h.round(r / 2);
+              rsum = pair_add(h.x[r / 2], rsum);
+            }
           }
         };
-        auto sums = [&](int row0, const Pair& x, const Pair& y) {
 #pragma unroll
-          for (int v = 0; v < NV; ++v) {
-            const bf16x8 k = addr.cols(kp, row0 + 16 * (v / DB), v % DB);
-            dq[v % DB] = mma32(k, x.f[v / DB], dq[v % DB]);
-            kbar[v % DB] = mma32(k, y.f[v / DB], kbar[v % DB]);
+        for (int m = 0; m < AHEAD; ++m) f[m] = frag(m);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < NM; ++i) {
+          if (i & 1) h0.ds = mma32(f[i % AHEAD], g[i / 2], h0.ds);
+          else h0.s = mma32(f[i % AHEAD], q[i / 2], h0.s);
+          next(i);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int i = 0; i < NM; ++i) {
+          if (i & 1) h1.ds = mma32(f[(NM + i) % AHEAD], g[i / 2], h1.ds);
+          else h1.s = mma32(f[(NM + i) % AHEAD], q[i / 2], h1.s);
+          next(NM + i);
+          some(h0, i);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int i = 0; i < NM; ++i) {
+          const int m = 2 * NM + i / 2, v = i / 2;
+          if (i & 1) {
+            kbar[v % DB] = mma32(f[m % AHEAD], h0.frag_s(v / DB), kbar[v % DB]);
+            next(m);
+          } else {
+            dq[v % DB] = mma32(f[m % AHEAD], h0.frag_ds(v / DB), dq[v % DB]);
           }
-        };
-        f32x16 s0, ds0, s1, ds1;
-        products(0, s0, ds0);
-        __builtin_amdgcn_sched_group_barrier(SG_LDS, 4, 0);
-#pragma unroll
-        for (int t = 0; t < 2 * STEPS; ++t) {
-          __builtin_amdgcn_sched_group_barrier(SG_MFMA, 1, 0);
-          if (t + 4 < 2 * STEPS) __builtin_amdgcn_sched_group_barrier(SG_LDS, 1, 0);
+          some(h1, i);
+          __builtin_amdgcn_sched_barrier(0);
         }
-        __builtin_amdgcn_sched_barrier(0);
-        products(32, s1, ds1);
-        gradients(s0, ds0);
-        const Pair x0 = round_pair(ds0), y0 = round_pair(s0);
-        count(ds0, x0);
-        __builtin_amdgcn_sched_group_barrier(SG_LDS, 4, 1);
-        __builtin_amdgcn_sched_group_barrier(SG_VALU, 8, 1);
 #pragma unroll
-        for (int t = 0; t < 2 * STEPS; ++t) {
-          __builtin_amdgcn_sched_group_barrier(SG_MFMA, 1, 1);
-          if (t + 4 < 2 * STEPS) __builtin_amdgcn_sched_group_barrier(SG_LDS, 1, 1);
-          __builtin_amdgcn_sched_group_barrier(SG_VALU, 88 / (2 * STEPS), 1);
+        for (int i = 0; i < NM; ++i) {
+          const int m = 2 * NM + STEPS + i / 2, v = i / 2;
+          if (i & 1) {
+            kbar[v % DB] = mma32(f[m % AHEAD], h1.frag_s(v / DB), kbar[v % DB]);
+            next(m);
+          } else {
+            dq[v % DB] = mma32(f[m % AHEAD], h1.frag_ds(v / DB), dq[v % DB]);
+          }
+          __builtin_amdgcn_sched_barrier(0);
         }
-        __builtin_amdgcn_sched_barrier(0);
-        sums(0, x0, y0);
-        gradients(s1, ds1);
-        const Pair x1 = round_pair(ds1), y1 = round_pair(s1);
-        count(ds1, x1);
-        __builtin_amdgcn_sched_group_barrier(SG_LDS, 4, 2);
-        __builtin_amdgcn_sched_group_barrier(SG_VALU, 8, 2);
-#pragma unroll
-        for (int t = 0; t < NV; ++t) {
-          __builtin_amdgcn_sched_group_barrier(SG_MFMA, 2, 2);
-          if (t + 2 < NV) __builtin_amdgcn_sched_group_barrier(SG_LDS, 2, 2);
-          __builtin_amdgcn_sched_group_barrier(SG_VALU, 88 / NV, 2);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        sums(32, x1, y1);
       };
       int lo, hi;
       kt.whole(off + r0, off + min(r0 + BM, qlen) - 1, a.window, BN, r0 + BM <= qlen, lo, hi);
@@ -1203,57 +1239,65 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dkv_kern
         const int wa = max(ra, (max(max(k0 + BK - 1, p_lo) - off, 0) + BQ - 1) / BQ);
         const int wz = k0 + BK <= klen && last >= off ? min(rend, (last - off + 1) / BQ) : 0;
         const AttnAddr<DP> addr(lane);
-        constexpr int NV = 2 * DB;
+        // 64 rows that see every key (see AttnRows::step2)
         auto all = [&](lds_ptr qp, lds_ptr gp, const float* st) {
-          auto products = [&](int row0, f32x16& s, f32x16& ds) {
-            s = start(st, row0), ds = start(st + 64, row0);
+          constexpr int NM = 2 * STEPS, E = 16 / NM;
+          auto frag = [&](int m) {
+            const int run = m / NM, i = m % NM;
+            return run < 2 ? addr.rows(i & 1 ? gp : qp, 32 * run, i / 2)
+                           : addr.cols(i & 1 ? qp : gp, 32 * (run - 2) + 16 * (i / 2 / DB), i / 2 % DB);
+          };
+          bf16x8 f[AHEAD];
+          auto next = [&](int m) {
+            if (m + AHEAD < 4 * NM) f[m % AHEAD] = frag(m + AHEAD);
+          };
+          Half h0, h1;
+          auto some = [&](Half& h, int i) {
 #pragma unroll
-            for (int t = 0; t < STEPS; ++t) {
-              s = mma32(addr.rows(qp, row0, t), kf[t], s);
-              ds = mma32(addr.rows(gp, row0, t), vf[t], ds);
+            for (int r = i * E; r < i * E + E; ++r) {
+              h.s[r] = __builtin_amdgcn_exp2f(h.s[r] * a.c);
+              h.ds[r] *= h.s[r];
+              if (r & 1) h.round(r / 2);
             }
           };
-          auto sums = [&](int row0, const Pair& x, const Pair& y) {
-#pragma unroll
-            for (int v = 0; v < NV; ++v) {
-              dv[v % DB] = mma32(addr.cols(gp, row0 + 16 * (v / DB), v % DB), y.f[v / DB], dv[v % DB]);
-              dk[v % DB] = mma32(addr.cols(qp, row0 + 16 * (v / DB), v % DB), x.f[v / DB], dk[v % DB]);
-            }
+          auto add = [&](const Half& h, int run, int i) {
+            const bf16x8 x = f[(run * NM + i) % AHEAD];
+            const int v = i / 2;
+            if (i & 1) dk[v % DB] = mma32(x, h.frag_ds(v / DB), dk[v % DB]);
+            else dv[v % DB] = mma32(x, h.frag_s(v / DB), dv[v % DB]);
+            next(run * NM + i);
           };
-          f32x16 s0, ds0, s1, ds1;
-          products(0, s0, ds0);
-          __builtin_amdgcn_sched_group_barrier(SG_LDS, 12, 0);
+          h0.s = start(st, 0), h0.ds = start(st + 64, 0);
 #pragma unroll
-          for (int t = 0; t < 2 * STEPS; ++t) {
-            __builtin_amdgcn_sched_group_barrier(SG_MFMA, 1, 0);
-            if (t + 4 < 2 * STEPS) __builtin_amdgcn_sched_group_barrier(SG_LDS, 1, 0);
-          }
+          for (int m = 0; m < AHEAD; ++m) f[m] = frag(m);
           __builtin_amdgcn_sched_barrier(0);
-          products(32, s1, ds1);
-          gradients(s0, ds0);
-          const Pair x0 = round_pair(ds0), y0 = round_pair(s0);
-          __builtin_amdgcn_sched_group_barrier(SG_LDS, 12, 1);
-          __builtin_amdgcn_sched_group_barrier(SG_VALU, 8, 1);
 #pragma unroll
-          for (int t = 0; t < 2 * STEPS; ++t) {
-            __builtin_amdgcn_sched_group_barrier(SG_MFMA, 1, 1);
-            if (t + 4 < 2 * STEPS) __builtin_amdgcn_sched_group_barrier(SG_LDS, 1, 1);
-            __builtin_amdgcn_sched_group_barrier(SG_VALU, 56 / (2 * STEPS), 1);
+          for (int i = 0; i < NM; ++i) {
+            if (i & 1) h0.ds = mma32(f[i % AHEAD], vf[i / 2], h0.ds);
+            else h0.s = mma32(f[i % AHEAD], kf[i / 2], h0.s);
+            next(i);
+            if (i == NM / 2) h1.s = start(st, 32), h1.ds = start(st + 64, 32);
+            __builtin_amdgcn_sched_barrier(0);
           }
-          __builtin_amdgcn_sched_barrier(0);
-          sums(0, x0, y0);
-          gradients(s1, ds1);
-          const Pair x1 = round_pair(ds1), y1 = round_pair(s1);
-          __builtin_amdgcn_sched_group_barrier(SG_LDS, 4, 2);
-          __builtin_amdgcn_sched_group_barrier(SG_VALU, 8, 2);
 #pragma unroll
-          for (int t = 0; t < 2 * NV; ++t) {
-            __builtin_amdgcn_sched_group_barrier(SG_MFMA, 1, 2);
-            if (t + 2 < 2 * NV) __builtin_amdgcn_sched_group_barrier(SG_LDS, 2, 2);
-            __builtin_amdgcn_sched_group_barrier(SG_VALU, 56 / (2 * NV), 2);
+          for (int i = 0; i < NM; ++i) {
+            if (i & 1) h1.ds = mma32(f[(NM + i) % AHEAD], vf[i / 2], h1.ds);
+            else h1.s = mma32(f[(NM + i) % AHEAD], kf[i / 2], h1.s);
+            next(NM + i);
+            some(h0, i);
+            __builtin_amdgcn_sched_barrier(0);
           }
-          __builtin_amdgcn_sched_barrier(0);
-          sums(32, x1, y1);
+#pragma unroll
+          for (int i = 0; i < NM; ++i) {
+            add(h0, 2, i);
+            some(h1, i);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+#pragma unroll
+          for (int i = 0; i < NM; ++i) {
+            add(h1, 3, i);
+            __builtin_amdgcn_sched_barrier(0);
+          }
         };
         for (; rt < rend && (rt < wa || (rt < wz && (i & 1))); ++rt, ++i) edge(h, rt, i & 1);
         for (; rt + 1 < wz; rt += 2, i += 2) {
