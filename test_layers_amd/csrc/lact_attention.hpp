@@ -936,40 +936,6 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dq_kerne
         rsum = pair_add(w.x, pair_add(w.y, pair_add(w.z, pair_add(w.w, rsum))));
       }
     };
-    // a tile of which rows may see a part, 32 keys after another
-    auto edge = [&](int i) {
-      const char* t = lds + (i & 1) * 2 * TB;
-      arrive(i, lds + (2 - 2 * (i & 1)) * TB);
-#pragma unroll 1
-      for (int sb = 0; sb < BN; sb += 32) {
-        const int k0 = kt.at(i) * BN + sb;
-        if (w.lo > w.hi || !w.some(k0, k0 + 31, a.window, a.sinks)) continue;
-        f32x16 s = zero16(), ds = less;
-#pragma unroll
-        for (int st = 0; st < STEPS; ++st) {
-          s = mma32(row_frag<T, DP>(t, sb, st, lane), q[st], s);
-          ds = mma32(row_frag<T, DP>(t + TB, sb, st, lane), g[st], ds);
-        }
-        gradients(s, ds);
-        if (!w.whole(k0, k0 + 31, a.window, a.sinks)) {
-          const Seen seen(p, k0 + 4 * (lane >> 5), a.window, a.sinks);
-#pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const bool see = seen(8 * (r >> 2) + (r & 3));
-            s[r] = see ? s[r] : 0.f;
-            ds[r] = see ? ds[r] : 0.f;
-          }
-        }
-        if constexpr (CENTRE) {
-          const Pair x = round_pair(ds);
-          count(ds, x);
-          mma_trans<DP>(dq, x.f, t, sb, lane);
-          mma_trans<DP>(kbar, round_pair(s).f, t, sb, lane);
-        } else {
-          mma_trans<DP>(dq, ds, t, sb, lane);
-        }
-      }
-    };
     if (kt.total > 0) {
       sk.issue(lds, kt.at(0) * BN);
       sv.issue(lds + TB, kt.at(0) * BN);
@@ -980,8 +946,9 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dq_kerne
       // 64 keys that every row sees, as in AttnRows::step2: runs of scores and
       // dP of one half and the other, then of each half's sums, each of whose
       // operands serves two products
-      auto whole = [&](lds_ptr kp, lds_ptr vp) {
+      auto pair = [&](lds_ptr kp, lds_ptr vp, auto masked, int k0) {
         constexpr int NM = 2 * STEPS, E = 16 / NM, NF = 3 * NM;
+        const Seen seen(p, k0 + 4 * (lane >> 5), a.window, a.sinks);
         auto frag = [&](int m) {
           const int run = m / NM, i = m % NM;
           if (run < 2) return addr.rows(i & 1 ? vp : kp, 32 * run, i / 2);
@@ -1000,6 +967,11 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dq_kerne
           for (int r = i * E; r < i * E + E; ++r) {
             h.s[r] = __builtin_amdgcn_exp2f(fmaf(h.s[r], a.c, -lse2));
             h.ds[r] *= h.s[r];
+            if constexpr (masked.value) {
+              const bool see = seen((&h == &h0 ? 0 : 32) + 8 * (r >> 2) + (r & 3));
+              h.s[r] = see ? h.s[r] : 0.f;
+              h.ds[r] = see ? h.ds[r] : 0.f;
+            }
             sum += h.ds[r];
             if (r & 1) {
               h.round(r / 2);
@@ -1051,16 +1023,62 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dq_kerne
       };
       int lo, hi;
       kt.whole(off + r0, off + min(r0 + BM, qlen) - 1, a.window, BN, r0 + BM <= qlen, lo, hi);
+      // a tile of which rows may see a part
+      auto edge = [&](int i) {
+        lds_ptr t = (lds_ptr)lds + (i & 1) * 2 * TB;
+        arrive(i, lds + (2 - 2 * (i & 1)) * TB);
+        const int k0 = kt.at(i) * BN;
+        if (w.lo > w.hi || !w.some(k0, k0 + BN - 1, a.window, a.sinks)) return;
+        pair(t, t + TB, std::true_type{}, k0);
+      };
+#pragma unroll 1
       for (; i < lo; ++i) edge(i);
       for (; i + 1 < hi; i += 2) {
         arrive(i, lds + 2 * TB);
-        whole((lds_ptr)lds, (lds_ptr)lds + TB);
+        pair((lds_ptr)lds, (lds_ptr)lds + TB, std::false_type{}, 0);
         arrive(i + 1, lds);
-        whole((lds_ptr)lds + 2 * TB, (lds_ptr)lds + 3 * TB);
+        pair((lds_ptr)lds + 2 * TB, (lds_ptr)lds + 3 * TB, std::false_type{}, 0);
       }
-    }
 #pragma unroll 1
-    for (; i < kt.total; ++i) edge(i);
+      for (; i < kt.total; ++i) edge(i);
+    } else {
+      // a tile of which rows may see a part, 32 keys after another
+      auto edge = [&](int i) {
+        const char* t = lds + (i & 1) * 2 * TB;
+        arrive(i, lds + (2 - 2 * (i & 1)) * TB);
+#pragma unroll 1
+        for (int sb = 0; sb < BN; sb += 32) {
+          const int k0 = kt.at(i) * BN + sb;
+          if (w.lo > w.hi || !w.some(k0, k0 + 31, a.window, a.sinks)) continue;
+          f32x16 s = zero16(), ds = less;
+#pragma unroll
+          for (int st = 0; st < STEPS; ++st) {
+            s = mma32(row_frag<T, DP>(t, sb, st, lane), q[st], s);
+            ds = mma32(row_frag<T, DP>(t + TB, sb, st, lane), g[st], ds);
+          }
+          gradients(s, ds);
+          if (!w.whole(k0, k0 + 31, a.window, a.sinks)) {
+            const Seen seen(p, k0 + 4 * (lane >> 5), a.window, a.sinks);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+              const bool see = seen(8 * (r >> 2) + (r & 3));
+              s[r] = see ? s[r] : 0.f;
+              ds[r] = see ? ds[r] : 0.f;
+            }
+          }
+          if constexpr (CENTRE) {
+            const Pair x = round_pair(ds);
+            count(ds, x);
+            mma_trans<DP>(dq, x.f, t, sb, lane);
+            mma_trans<DP>(kbar, round_pair(s).f, t, sb, lane);
+          } else {
+            mma_trans<DP>(dq, ds, t, sb, lane);
+          }
+        }
+      };
+#pragma unroll 1
+      for (; i < kt.total; ++i) edge(i);
+    }
     if constexpr (CENTRE) {
       rsum = pair_sum(rsum);
       delta += pair_sum(sum);
@@ -1194,40 +1212,6 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dkv_kern
         ds[r] *= s[r];
       }
     };
-    // a tile of which rows may see a part, 32 rows after another
-    auto edge = [&](int h, int rt, int ring) {
-      const char* t = lds + ring * 2 * TB;
-      arrive(h, rt, lds + (2 - 2 * ring) * TB, stats[1 - ring][0]);
-#pragma unroll 1
-      for (int sb = 0; sb < BQ; sb += 32) {
-        const int q0 = off + rt * BQ + sb, q1 = q0 + 31;  // positions
-        const int u0 = max(q0, p_lo), u1 = min(q1, p_hi);
-        if (u0 > u1 || wk0 > wk1 || u1 < wk0 || (wk1 <= u0 - a.window && wk0 >= a.sinks)) continue;
-        const bool whole = u0 == q0 && u1 == q1 && wk1 <= q0 && wk0 + 31 == wk1 &&
-                           (wk0 > q1 - a.window || wk1 < a.sinks);
-        f32x16 s = start(stats[ring][0], sb), ds = start(stats[ring][1], sb);
-#pragma unroll
-        for (int st = 0; st < STEPS; ++st) {
-          s = mma32(row_frag<T, DP>(t, sb, st, lane), kf[st], s);
-          ds = mma32(row_frag<T, DP>(t + TB, sb, st, lane), vf[st], ds);
-        }
-        gradients(s, ds);
-        if (!whole) {
-          // a row's position p = q0 + 4 (lane / 32) + o, against the key's own bounds
-          const int base = q0 + 4 * (lane >> 5), lo = max(u0, key) - base,
-                    hi = (key < a.sinks ? u1 : min(u1, key + a.window - 1)) - base;
-#pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const int o = 8 * (r >> 2) + (r & 3);
-            const bool see = (o >= lo) & (o <= hi);
-            s[r] = see ? s[r] : 0.f;
-            ds[r] = see ? ds[r] : 0.f;
-          }
-        }
-        acc_trans<T, DP>(dv, s, t + TB, sb, lane);
-        acc_trans<T, DP>(dk, ds, t, sb, lane);
-      }
-    };
     issue(0, ra, lds, stats[0][0]);
     int i = 0;  // tiles done: the ring's place
 #pragma unroll 1
@@ -1240,7 +1224,7 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dkv_kern
         const int wz = k0 + BK <= klen && last >= off ? min(rend, (last - off + 1) / BQ) : 0;
         const AttnAddr<DP> addr(lane);
         // 64 rows that see every key (see AttnRows::step2)
-        auto all = [&](lds_ptr qp, lds_ptr gp, const float* st) {
+        auto pair = [&](lds_ptr qp, lds_ptr gp, const float* st, auto masked, int lo, int hi) {
           constexpr int NM = 2 * STEPS, E = 16 / NM;
           auto frag = [&](int m) {
             const int run = m / NM, i = m % NM;
@@ -1257,6 +1241,12 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dkv_kern
             for (int r = i * E; r < i * E + E; ++r) {
               h.s[r] = __builtin_amdgcn_exp2f(h.s[r] * a.c);
               h.ds[r] *= h.s[r];
+              if constexpr (masked.value) {
+                const int o = (&h == &h0 ? 0 : 32) + 8 * (r >> 2) + (r & 3);
+                const bool see = (o >= lo) & (o <= hi);
+                h.s[r] = see ? h.s[r] : 0.f;
+                h.ds[r] = see ? h.ds[r] : 0.f;
+              }
               if (r & 1) h.round(r / 2);
             }
           };
@@ -1299,16 +1289,65 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dkv_kern
             __builtin_amdgcn_sched_barrier(0);
           }
         };
+        // a tile of which a key may be seen by a part of the rows: those at
+        // positions q0 + 4 (lane / 32) + lo .. hi
+        auto edge = [&](int h, int rt, int ring) {
+          lds_ptr t = (lds_ptr)lds + ring * 2 * TB;
+          arrive(h, rt, lds + (2 - 2 * ring) * TB, stats[1 - ring][0]);
+          const int q0 = off + rt * BQ, u0 = max(q0, p_lo), u1 = min(q0 + BQ - 1, p_hi);
+          if (u0 > u1 || wk0 > wk1 || u1 < wk0 || (wk1 <= u0 - a.window && wk0 >= a.sinks)) return;
+          const int base = q0 + 4 * (lane >> 5), lo = max(u0, key) - base,
+                    hi = (key < a.sinks ? u1 : min(u1, key + a.window - 1)) - base;
+          pair(t, t + TB, stats[ring][0], std::true_type{}, lo, hi);
+        };
+#pragma unroll 1
         for (; rt < rend && (rt < wa || (rt < wz && (i & 1))); ++rt, ++i) edge(h, rt, i & 1);
         for (; rt + 1 < wz; rt += 2, i += 2) {
           arrive(h, rt, lds + 2 * TB, stats[1][0]);
-          all((lds_ptr)lds, (lds_ptr)lds + TB, stats[0][0]);
+          pair((lds_ptr)lds, (lds_ptr)lds + TB, stats[0][0], std::false_type{}, 0, 0);
           arrive(h, rt + 1, lds, stats[0][0]);
-          all((lds_ptr)lds + 2 * TB, (lds_ptr)lds + 3 * TB, stats[1][0]);
+          pair((lds_ptr)lds + 2 * TB, (lds_ptr)lds + 3 * TB, stats[1][0], std::false_type{}, 0, 0);
         }
-      }
 #pragma unroll 1
-      for (; rt < rend; ++rt, ++i) edge(h, rt, i & 1);
+        for (; rt < rend; ++rt, ++i) edge(h, rt, i & 1);
+      } else {
+        // a tile of which rows may see a part, 32 rows after another
+        auto edge = [&](int h, int rt, int ring) {
+          const char* t = lds + ring * 2 * TB;
+          arrive(h, rt, lds + (2 - 2 * ring) * TB, stats[1 - ring][0]);
+#pragma unroll 1
+          for (int sb = 0; sb < BQ; sb += 32) {
+            const int q0 = off + rt * BQ + sb, q1 = q0 + 31;  // positions
+            const int u0 = max(q0, p_lo), u1 = min(q1, p_hi);
+            if (u0 > u1 || wk0 > wk1 || u1 < wk0 || (wk1 <= u0 - a.window && wk0 >= a.sinks)) continue;
+            const bool whole = u0 == q0 && u1 == q1 && wk1 <= q0 && wk0 + 31 == wk1 &&
+                               (wk0 > q1 - a.window || wk1 < a.sinks);
+            f32x16 s = start(stats[ring][0], sb), ds = start(stats[ring][1], sb);
+#pragma unroll
+            for (int st = 0; st < STEPS; ++st) {
+              s = mma32(row_frag<T, DP>(t, sb, st, lane), kf[st], s);
+              ds = mma32(row_frag<T, DP>(t + TB, sb, st, lane), vf[st], ds);
+            }
+            gradients(s, ds);
+            if (!whole) {
+              // a row's position p = q0 + 4 (lane / 32) + o, against the key's own bounds
+              const int base = q0 + 4 * (lane >> 5), lo = max(u0, key) - base,
+                        hi = (key < a.sinks ? u1 : min(u1, key + a.window - 1)) - base;
+#pragma unroll
+              for (int r = 0; r < 16; ++r) {
+                const int o = 8 * (r >> 2) + (r & 3);
+                const bool see = (o >= lo) & (o <= hi);
+                s[r] = see ? s[r] : 0.f;
+                ds[r] = see ? ds[r] : 0.f;
+              }
+            }
+            acc_trans<T, DP>(dv, s, t + TB, sb, lane);
+            acc_trans<T, DP>(dk, ds, t, sb, lane);
+          }
+        };
+#pragma unroll 1
+        for (; rt < rend; ++rt, ++i) edge(h, rt, i & 1);
+      }
     }
   }
   const bool parts = tile < a.sink_tiles && a.splits > 1;

@@ -84,23 +84,6 @@ __global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a) {
   id /= a.head_groups;
   const int t0 = (id % groups) * a.tok, b = id / groups;
   const int nt = min(a.tok, a.L - t0), n = a.pairs;
-  for (int i = threadIdx.x; i < nt * n; i += 256) {
-    const int k = (int)a.by_pairs.div(i), t = t0 + k;
-    const double pos = (double)(a.positions ? a.positions[(int64_t)b * a.L + t] : a.start + t);
-    double turn = pos * (a.freqs[i - k * n] * 0.15915494309189533577);  // / (2 pi)
-    turn -= rint(turn);
-    float s, c;
-    if constexpr (sizeof(T) == 4) {
-      sincospif(2.f * (float)turn, &s, &c);
-    } else {
-      // the hardware's sine of turns: off by less than 2^-16, far below a bf16 step
-      s = __builtin_amdgcn_sinf((float)turn);
-      c = __builtin_amdgcn_cosf((float)turn);
-    }
-    cs[i] = c * a.mscale;
-    sn[i] = (a.inverse ? -s : s) * a.mscale;
-  }
-  __syncthreads();
   // items of a head's row: pairs by VE (half layout) or VE / 2, then the copied rest
   constexpr int PV = INTERLEAVED ? (VE > 1 ? VE / 2 : 1) : VE;
   // interleaved vectors hold whole pairs, so an item is one vector; else two
@@ -112,10 +95,10 @@ __global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a) {
   // tokens inside heads; what the last groups lack is skipped
   const int items = a.tok * a.group * per;
   constexpr int U = VE * (int)sizeof(T) >= 16 ? 2 : 4;  // items in flight: all loads of a round before its stores
-  for (int i0 = threadIdx.x; i0 < items; i0 += 256 * U) {
-    float u[U][VE], v[U][VE];
-    T* out[U];
-    int c[U], tab[U];  // c: -1 nothing to do
+  float u[U][VE], v[U][VE];
+  T* out[U];
+  int c[U], tab[U];  // c: -1 nothing to do
+  auto fetch = [&](int i0) {
 #pragma unroll
     for (int k = 0; k < U; ++k) {
       const int i = i0 + 256 * k;
@@ -138,6 +121,27 @@ __global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a) {
       if (!ONE && cc < turned) load_n<T, VE>(in + e0 + (INTERLEAVED ? 1 : n), v[k]);
       out[k] += e0;
     }
+  };
+  fetch(threadIdx.x);  // on its way while the table is made
+  for (int i = threadIdx.x; i < nt * n; i += 256) {
+    const int k = (int)a.by_pairs.div(i), t = t0 + k;
+    const double pos = (double)(a.positions ? a.positions[(int64_t)b * a.L + t] : a.start + t);
+    double turn = pos * (a.freqs[i - k * n] * 0.15915494309189533577);  // / (2 pi)
+    turn -= rint(turn);
+    float s, co;
+    if constexpr (sizeof(T) == 4) {
+      sincospif(2.f * (float)turn, &s, &co);
+    } else {
+      // the hardware's sine of turns: off by less than 2^-16, far below a bf16 step
+      s = __builtin_amdgcn_sinf((float)turn);
+      co = __builtin_amdgcn_cosf((float)turn);
+    }
+    cs[i] = co * a.mscale;
+    sn[i] = (a.inverse ? -s : s) * a.mscale;
+  }
+  __syncthreads();
+  for (int i0 = threadIdx.x; i0 < items; i0 += 256 * U) {
+    if (i0 >= 256 * U) fetch(i0);
 #pragma unroll
     for (int k = 0; k < U; ++k) {
       if (c[k] < 0) continue;
@@ -203,6 +207,33 @@ struct NormRow {
           }
       }
     }
+  }
+  // the same vectors as they lie in memory
+  __device__ static __forceinline__ void load_raw(const char* row, int cols, int t, uint4 (&v)[NV]) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = col(j, t);
+      const T* p = reinterpret_cast<const T*>(row) + c;
+      v[j] = zero4();
+      if constexpr (VEC) {
+        if (c < cols) v[j] = *reinterpret_cast<const uint4*>(p);
+      } else {
+        uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int e = 0; e < VE; ++e)
+          if (c + e < cols) {
+            if constexpr (sizeof(T) == 4) w[e] = __float_as_uint(p[e]);
+            else w[e / 2] |= (uint32_t)p[e].x << (16 * (e % 2));
+          }
+        v[j] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+  }
+  // value e of a vector
+  __device__ static __forceinline__ float value(const uint4& v, int e) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[e]);
+    else return e % 2 ? __uint_as_float(w[e / 2] & 0xffff0000u) : __uint_as_float(w[e / 2] << 16);
   }
   __device__ static __forceinline__ void store(char* row, int cols, int t, const float (&v)[NV][VE]) {
 #pragma unroll
@@ -339,34 +370,47 @@ __global__ __launch_bounds__(GS < 512 ? 512 : GS) void norm_back_kernel(NormArgs
   for (int j = 0; j < NV; ++j)
 #pragma unroll
     for (int e = 0; e < VE; ++e) dw[j][e] = 0.f;
-  // every group runs the same number of rounds (a row's sum has barriers where GS > 64)
-  for (int64_t row0 = (int64_t)blockIdx.x * RPB; row0 < a.rows; row0 += (int64_t)gridDim.x * RPB) {
+  // Rows come as they lie in memory, and the next one's before this one is
+  // used: the loads of a row then have a row's arithmetic to arrive.  Every
+  // group runs the same number of rounds (a row's sum has barriers where GS > 64).
+  uint4 h[NV], g[NV], o[NV];
+  auto fetch = [&](int64_t row) {
+    const int cols = row < a.rows ? a.cols : 0;
+    R::load_raw(a.x + row * a.ldx, cols, t, h);
+    R::load_raw(a.dy + row * a.ldg, cols, t, g);
+    if (a.dh) R::load_raw(a.dh + row * a.lddh, cols, t, o);
+  };
+  const int64_t step = (int64_t)gridDim.x * RPB;
+  int64_t row0 = (int64_t)blockIdx.x * RPB;
+  if (row0 < a.rows) fetch(row0 + group);
+  for (; row0 < a.rows; row0 += step) {
     const int64_t row = row0 + group;
-    const bool some = row < a.rows;
-    float h[NV][VE], g[NV][VE], o[NV][VE];
-    const int cols = some ? a.cols : 0;
-    R::load(a.x + row * a.ldx, cols, t, h);
-    R::load(a.dy + row * a.ldg, cols, t, g);
-    if (a.dh) R::load(a.dh + row * a.lddh, cols, t, o);
+    uint4 hc[NV], gc[NV], oc[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) hc[j] = h[j], gc[j] = g[j], oc[j] = a.dh ? o[j] : zero4();
+    if (row0 + step < a.rows) fetch(row + step);
     float ss = 0.f, sg = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int e = 0; e < VE; ++e) {
-        ss = fmaf(h[j][e], h[j][e], ss);
-        sg = fmaf(g[j][e] * w[j][e], h[j][e], sg);
+        const float x = R::value(hc[j], e);
+        ss = fmaf(x, x, ss);
+        sg = fmaf(R::value(gc[j], e) * w[j][e], x, sg);
       }
     const float2 s = row_sum2<GS>(ss, sg, mine, t);
     const float f = rsqrtf(s.x / (float)a.cols + a.eps), k = f * f * (s.y / (float)a.cols);
-    if (!some) continue;
+    if (row >= a.rows) continue;
+    float dx[NV][VE];
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int e = 0; e < VE; ++e) {
-        dw[j][e] = fmaf(g[j][e], h[j][e] * f, dw[j][e]);
-        h[j][e] = f * (g[j][e] * w[j][e] - h[j][e] * k) + (a.dh ? o[j][e] : 0.f);
+        const float x = R::value(hc[j], e), y = R::value(gc[j], e);
+        dw[j][e] = fmaf(y, x * f, dw[j][e]);
+        dx[j][e] = f * (y * w[j][e] - x * k) + R::value(oc[j], e);
       }
-    R::store(a.dx + row * a.lddx, a.cols, t, h);
+    R::store(a.dx + row * a.lddx, a.cols, t, dx);
   }
   if (!a.part) return;
   if constexpr (RPB > 1) {
