@@ -319,6 +319,34 @@ struct Seen {
   __device__ __forceinline__ bool operator()(int o) const { return (o <= hi) & ((o > lo) | (o < first)); }
 };
 
+// Two waves' parts of a sum, added into part 0's by way of LDS that the whole
+// workgroup has done with
+template <int RG>
+__device__ __forceinline__ float add_parts(float* lds, int rg, int ks, int lane, float x) {
+  __syncthreads();
+  if (ks == 1) lds[rg * WAVE + lane] = x;
+  __syncthreads();
+  return ks == 0 ? x + lds[rg * WAVE + lane] : x;
+}
+template <int RG, int DB>
+__device__ __forceinline__ void add_parts(float* lds, int rg, int ks, int lane, f32x16 (&x)[DB]) {
+  float* to = lds + rg * DB * 16 * WAVE + lane;
+  __syncthreads();
+  if (ks == 1) {
+#pragma unroll
+    for (int db = 0; db < DB; ++db)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) to[(db * 16 + r) * WAVE] = x[db][r];
+  }
+  __syncthreads();
+  if (ks == 0) {
+#pragma unroll
+    for (int db = 0; db < DB; ++db)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) x[db][r] += to[(db * 16 + r) * WAVE];
+  }
+}
+
 // The key tiles of BN keys that rows at positions p_lo .. p_hi can see: the
 // `ns` first ones for the sinks, then those from `tl` on for the window.
 struct KeyTiles {
@@ -556,12 +584,12 @@ struct AttnRows {
       __builtin_amdgcn_sched_barrier(0);
     }
   }
-  // BN keys of which a row may see some or none
-  template <int BN>
-  __device__ __forceinline__ void tile(const char* kt, const char* vt, int k0, int window, int sinks, float c,
+  // BN keys of which a row may see some or none; of KS waves' parts, part ks
+  template <int BN, int KS>
+  __device__ __forceinline__ void tile(const char* kt, const char* vt, int ks, int k0, int window, int sinks, float c,
                                        int lane) {
 #pragma unroll 1
-    for (int i = 0; i < BN; i += 32)
+    for (int i = 32 * ks; i < BN; i += 32 * KS)
       if (w.some(k0 + i, k0 + i + 31, window, sinks))
         step(kt + i * AttnTile<T, DP>::CPR * 16, vt + i * AttnTile<T, DP>::CPR * 16, k0 + i, window, sinks, c, lane);
   }
@@ -614,24 +642,28 @@ struct AttnPlace {
 };
 
 // Four waves x 32 rows; K and V tiles in a two-deep ring of direct loads.
-template <typename T, int DP>
+// KS = 2: two waves share 32 rows, each taking one half of every tile, and
+// join at the end: for few rows, which 128 a workgroup would leave on half
+// the chip or less.
+template <typename T, int DP, int KS>
 __global__ __launch_bounds__(256, (attn_waves<T, DP>())) void attn_fwd_kernel(AttnArgs a) {
   using Tile = AttnTile<T, DP>;
-  constexpr int NW = 4, BM = 32 * NW, BN = attn_bn<T, DP>(), TB = BN * Tile::CPR * 16;
+  constexpr int NW = 4, RG = NW / KS, BM = 32 * RG, BN = attn_bn<T, DP>(), TB = BN * Tile::CPR * 16;
   __shared__ __align__(1024) char lds[4 * TB];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const AttnPlace at(xcd_remap(blockIdx.x, gridDim.x), a);
   const int qlen = seq_len(a.q_lens, at.b, a.Lq), klen = seq_len(a.k_lens, at.b, a.Lk);
   const int r0 = at.tile * BM, off = klen - qlen;
   if (r0 >= qlen) return;
-  const int row = r0 + 32 * wave + (lane & 31), cmax = a.d * (int)sizeof(T) / 16 - 1;
+  const int rg = wave % RG, ks = wave / RG;  // rows of the wave; its part of a tile
+  const int row = r0 + 32 * rg + (lane & 31), cmax = a.d * (int)sizeof(T) / 16 - 1;
   const char* kb = a.k + at.b * a.sk.b + at.hk * a.sk.h;
   const char* vb = a.v + at.b * a.sv.b + at.hk * a.sv.h;
   AttnRows<T, DP> w;
   w.clear();
   load_rows(w.q, a.q + at.b * a.sq.b + at.h * a.sq.h + (int64_t)min(row, qlen - 1) * a.sq.l, cmax, lane);
   w.p = off + row;
-  w.w = {off + r0 + 32 * wave, off + min(r0 + 32 * wave + 31, qlen - 1)};
+  w.w = {off + r0 + 32 * rg, off + min(r0 + 32 * rg + 31, qlen - 1)};
   const KeyTiles kt(off + r0, off + min(r0 + BM, qlen) - 1, a.window, a.sinks, BN);
   const Stager<T, DP, BN, NW> sk(kb, a.sk.l, klen - 1, cmax, wave, lane), sv(vb, a.sv.l, klen - 1, cmax, wave, lane);
   const AttnAddr<DP> addr(lane);
@@ -648,7 +680,7 @@ __global__ __launch_bounds__(256, (attn_waves<T, DP>())) void attn_fwd_kernel(At
   auto edge = [&](int i) {
     char* t = lds + (i & 1) * 2 * TB;
     arrive(i, lds + (2 - 2 * (i & 1)) * TB);
-    if (w.w.lo <= w.w.hi) w.template tile<BN>(t, t + TB, kt.at(i) * BN, a.window, a.sinks, a.c, lane);
+    if (w.w.lo <= w.w.hi) w.template tile<BN, KS>(t, t + TB, ks, kt.at(i) * BN, a.window, a.sinks, a.c, lane);
   };
   if (kt.total > 0) {
     sk.issue(lds, kt.at(0) * BN);
@@ -659,7 +691,7 @@ __global__ __launch_bounds__(256, (attn_waves<T, DP>())) void attn_fwd_kernel(At
   // registers (with the edges' branches inside the loop the compiler copied
   // all 64 twice a tile).
   int i = 0;
-  if constexpr (sizeof(T) == 2) {
+  if constexpr (sizeof(T) == 2 && KS == 1) {
     int lo, hi;
     kt.whole(off + r0, off + min(r0 + BM, qlen) - 1, a.window, BN, r0 + BM <= qlen, lo, hi);
     for (; i < lo; ++i) edge(i);
@@ -672,7 +704,40 @@ __global__ __launch_bounds__(256, (attn_waves<T, DP>())) void attn_fwd_kernel(At
   }
 #pragma unroll 1
   for (; i < kt.total; ++i) edge(i);
-  const float l = pair_sum(w.l), inv = l > 0.f || l != l ? 1.f / l : 0.f;
+  float l = pair_sum(w.l);
+  if constexpr (KS == 2) {
+    static_assert(RG * (32 * DP + 64) * 4 <= 4 * TB, "the join's place");
+    float* theirs = reinterpret_cast<float*>(lds) + rg * (32 * DP + 64);  // [d][row], maximum, sum
+    __syncthreads();
+    if (ks == 1) {
+#pragma unroll
+      for (int db = 0; db < DP / 32; ++db)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) theirs[(16 * db + r) * 64 + lane] = w.o[db][r];
+      if (lane < 32) {
+        theirs[32 * DP + lane] = w.m;
+        theirs[32 * DP + 32 + lane] = l;
+      }
+    }
+    __syncthreads();
+    if (ks == 1) return;
+    const float m1 = theirs[32 * DP + (lane & 31)], l1 = theirs[32 * DP + 32 + (lane & 31)], m = fmaxf(w.m, m1);
+    // a part that saw nothing adds nothing; one whose scores are all NaN has no maximum but a sum
+    auto weight = [&](float x, float sum) {
+      return sum == 0.f ? 0.f : x == -__builtin_huge_valf() ? 1.f : __builtin_amdgcn_exp2f(x - m);
+    };
+    const float f0 = weight(w.m, l), f1 = weight(m1, l1);
+    l = (l == 0.f ? 0.f : l * f0) + (l1 == 0.f ? 0.f : l1 * f1);
+    w.m = m;
+#pragma unroll
+    for (int db = 0; db < DP / 32; ++db)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const float x = theirs[(16 * db + r) * 64 + lane];
+        w.o[db][r] = (f0 == 0.f ? 0.f : f0 * w.o[db][r]) + (f1 == 0.f ? 0.f : f1 * x);
+      }
+  }
+  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
   char* out = a.out + at.b * a.so.b + at.h * a.so.h;
   if (row < qlen) {
     store_rows<T, DP>(w.o, inv, out + row * a.so.l, a.d, lane);
@@ -680,7 +745,7 @@ __global__ __launch_bounds__(256, (attn_waves<T, DP>())) void attn_fwd_kernel(At
       a.lse[((int64_t)at.b * a.H + at.h) * a.Lq + row] = l == 0.f ? -__builtin_huge_valf() : w.m * LN2 + logf(l);
   }
   for (uint32_t bad = not_finite(w.o) & (uint32_t)__ballot(row < qlen && l == l); bad; bad &= bad - 1) {
-    const int n = __builtin_ctz(bad), r = r0 + 32 * wave + n;
+    const int n = __builtin_ctz(bad), r = r0 + 32 * rg + n;
     const float f = of_lane(inv, n);
     float x[2];
     slow_o<T>(x, a.q + at.b * a.sq.b + at.h * a.sq.h + r * a.sq.l, kb, a.sk.l, vb, a.sv.l, a, off + r, of_lane(w.m, n),
@@ -735,7 +800,7 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(AttnArgs a) {
     }
     asm volatile("" ::: "memory");
     const char* t = ring + buf * 2 * TB;
-    w.template tile<32>(t, t + TB, kt.at(i) * 32, a.window, a.sinks, a.c, lane);
+    w.template tile<32, 1>(t, t + TB, 0, kt.at(i) * 32, a.window, a.sinks, a.c, lane);
   }
   // join the waves: O as [d][row] and the statistics behind it
   wait_lgkm0();
@@ -864,17 +929,18 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
 // kernel.  Relative error of dq against fp64 where first tokens draw
 // attention: 2.2e-3 for 2.8e-3 to 3.8e-3 without (1.7e-3 is the result's own
 // rounding).
-template <typename T, int DP>
+template <typename T, int DP, int KS>
 __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dq_kernel(AttnArgs a) {
   using Tile = AttnTile<T, DP>;
-  constexpr int NW = 4, BM = 32 * NW, BN = attn_bn<T, DP>(), TB = BN * Tile::CPR * 16, STEPS = Tile::STEPS, DB = DP / 32;
+  constexpr int NW = 4, RG = NW / KS, BM = 32 * RG, BN = attn_bn<T, DP>(), TB = BN * Tile::CPR * 16, STEPS = Tile::STEPS, DB = DP / 32;
   constexpr bool CENTRE = sizeof(T) == 2;
   __shared__ __align__(1024) char lds[4 * TB];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const AttnPlace at(xcd_remap(blockIdx.x, gridDim.x), a);
   const int qlen = seq_len(a.q_lens, at.b, a.Lq), klen = seq_len(a.k_lens, at.b, a.Lk);
   const int r0 = at.tile * BM, off = klen - qlen, n = lane & 31;
-  const int row = r0 + 32 * wave + n, cmax = a.d * (int)sizeof(T) / 16 - 1;
+  const int rg = wave % RG, ks = wave / RG;  // rows of the wave; its part of a tile (see the forward)
+  const int row = r0 + 32 * rg + n, cmax = a.d * (int)sizeof(T) / 16 - 1;
   const int64_t stat = ((int64_t)at.b * a.H + at.h) * a.Lq + row;
   f32x16 dq[DB];
 #pragma unroll
@@ -909,7 +975,7 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dq_kerne
 #pragma unroll
     for (auto& x : kbar) x = zero16();
     const int p = off + row;
-    const AttnWave w{off + r0 + 32 * wave, off + min(r0 + 32 * wave + 31, qlen - 1)};
+    const AttnWave w{off + r0 + 32 * rg, off + min(r0 + 32 * rg + 31, qlen - 1)};
     const Stager<T, DP, BN, NW> sk(kb, a.sk.l, klen - 1, cmax, wave, lane), sv(vb, a.sv.l, klen - 1, cmax, wave, lane);
     auto arrive = [&](int i, char* other) {
       wait_lgkm0();
@@ -941,7 +1007,7 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dq_kerne
       sv.issue(lds + TB, kt.at(0) * BN);
     }
     int i = 0;
-    if constexpr (CENTRE && BN == 64) {
+    if constexpr (CENTRE && BN == 64 && KS == 1) {
       const AttnAddr<DP> addr(lane);
       // 64 keys that every row sees, as in AttnRows::step2: runs of scores and
       // dP of one half and the other, then of each half's sums, each of whose
@@ -1047,7 +1113,7 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dq_kerne
         const char* t = lds + (i & 1) * 2 * TB;
         arrive(i, lds + (2 - 2 * (i & 1)) * TB);
 #pragma unroll 1
-        for (int sb = 0; sb < BN; sb += 32) {
+        for (int sb = 32 * ks; sb < BN; sb += 32 * KS) {
           const int k0 = kt.at(i) * BN + sb;
           if (w.lo > w.hi || !w.some(k0, k0 + 31, a.window, a.sinks)) continue;
           f32x16 s = zero16(), ds = less;
@@ -1079,6 +1145,14 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dq_kerne
 #pragma unroll 1
       for (; i < kt.total; ++i) edge(i);
     }
+    if constexpr (KS == 2) {
+      sum = add_parts<RG>(reinterpret_cast<float*>(lds), rg, ks, lane, sum);
+      if constexpr (CENTRE) {
+        rsum = add_parts<RG>(reinterpret_cast<float*>(lds), rg, ks, lane, rsum);
+        add_parts<RG, DB>(reinterpret_cast<float*>(lds), rg, ks, lane, kbar);
+      }
+      add_parts<RG, DB>(reinterpret_cast<float*>(lds), rg, ks, lane, dq);
+    }
     if constexpr (CENTRE) {
       rsum = pair_sum(rsum);
       delta += pair_sum(sum);
@@ -1088,11 +1162,12 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dq_kerne
         for (int r = 0; r < 16; ++r) dq[db][r] = fmaf(-rsum, kbar[db][r], dq[db][r]);
     }
     // what the dk, dv kernel's products start from: exp2(c (q.k - lse / scale)), dO.v - D
-    if (row < qlen && lane < 32) {
+    if (ks == 0 && row < qlen && lane < 32) {
       a.stats[stat] = -lse / a.scale;
       a.stats[(int64_t)a.B * a.H * a.Lq + stat] = -delta;
     }
   }
+  if (ks != 0) return;
   if (row >= qlen) {  // what a clamped row gathered, finite or not, is nothing
 #pragma unroll
     for (int db = 0; db < DB; ++db) dq[db] = zero16();
@@ -1100,7 +1175,7 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dq_kerne
   char* out = a.dq + at.b * a.sdq.b + at.h * a.sdq.h;
   if (row < a.Lq) store_rows<T, DP>(dq, a.scale, out + (int64_t)row * a.sdq.l, a.d, lane);
   for (uint32_t bad = not_finite(dq) & (uint32_t)__ballot(lse2 == lse2 && delta == delta); bad; bad &= bad - 1) {
-    const int i = __builtin_ctz(bad), r = r0 + 32 * wave + i;
+    const int i = __builtin_ctz(bad), r = r0 + 32 * rg + i;
     const float ls = of_lane(lse2, i), de = of_lane(delta, i);
     const Lane2<T> q(qb + r * a.sq.l, a.d, lane), g(gb + r * a.sdo.l, a.d, lane);
     float x[2] = {0.f, 0.f};
@@ -1121,7 +1196,7 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dq_kerne
 }
 
 // ------------------------------------------------------------------ backward: dk, dv
-// A workgroup owns 128 keys of a key head, a wave 32 of them in registers,
+// A workgroup owns 128 keys of a key head (64 with KS = 2), a wave 32 of them in registers,
 // and meets every row that sees them, over all query heads of the key head
 // (their sum needs no atomics).  S = Q K^T and dP = dO V^T have the key in
 // the lane and start from the rows' -lse / scale and -D, so that neither is
@@ -1131,10 +1206,10 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dq_kerne
 // window's; the rows behind the window of a sink tile's last key are split
 // over further workgroups of `span` rows each, and the fp32 partial sums of a
 // sink tile are added in a fixed order by attn_sink_sum_kernel.
-template <typename T, int DP>
+template <typename T, int DP, int KS>
 __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dkv_kernel(AttnArgs a) {
   using Tile = AttnTile<T, DP>;
-  constexpr int NW = 4, BK = 32 * NW, BQ = attn_bn<T, DP>(), TB = BQ * Tile::CPR * 16, STEPS = Tile::STEPS, DB = DP / 32;
+  constexpr int NW = 4, RG = NW / KS, BK = 32 * RG, BQ = attn_bn<T, DP>(), TB = BQ * Tile::CPR * 16, STEPS = Tile::STEPS, DB = DP / 32;
   __shared__ __align__(1024) char lds[4 * TB];
   __shared__ __align__(1024) float stats[2][2][64];  // [ring][-lse / scale, -D][row]
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 31;
@@ -1150,7 +1225,8 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dkv_kern
   }
   const int qlen = seq_len(a.q_lens, b, a.Lq), klen = seq_len(a.k_lens, b, a.Lk), off = klen - qlen;
   const int k0 = tile * BK, cmax = a.d * (int)sizeof(T) / 16 - 1;
-  const int key = k0 + 32 * wave + n;
+  const int rg = wave % RG, ks = wave / RG;  // keys of the wave; its part of a row tile (see the forward)
+  const int key = k0 + 32 * rg + n;
   const char* qh = a.q + b * a.sq.b + (int64_t)hk * a.G * a.sq.h;
   const char* gh = a.dO + b * a.sdo.b + (int64_t)hk * a.G * a.sdo.h;
   const int64_t sh = ((int64_t)b * a.H + hk * a.G) * a.Lq, sn = (int64_t)a.B * a.H * a.Lq;
@@ -1176,7 +1252,7 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dkv_kern
     const int64_t kc = min(key, klen - 1);
     load_rows(kf, a.k + b * a.sk.b + hk * a.sk.h + kc * a.sk.l, cmax, lane);
     load_rows(vf, a.v + b * a.sv.b + hk * a.sv.h + kc * a.sv.l, cmax, lane);
-    const int wk0 = k0 + 32 * wave, wk1 = min(wk0 + 31, klen - 1);
+    const int wk0 = k0 + 32 * rg, wk1 = min(wk0 + 31, klen - 1);
     Stager<T, DP, BQ, NW> sq(qh, a.sq.l, qlen - 1, cmax, wave, lane), sg(gh, a.sdo.l, qlen - 1, cmax, wave, lane);
     auto issue = [&](int h, int rt, char* t, float* st) {
       sq.base = qh + h * a.sq.h;
@@ -1217,7 +1293,7 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dkv_kern
 #pragma unroll 1
     for (int h = 0; h < a.G; ++h) {
       int rt = ra;
-      if constexpr (sizeof(T) == 2 && BQ == 64) {
+      if constexpr (sizeof(T) == 2 && BQ == 64 && KS == 1) {
         // row tiles that see all keys of the workgroup
         const int last = k0 + BK - 1 < a.sinks ? p_hi : min(p_hi, k0 + a.window - 1);
         const int wa = max(ra, (max(max(k0 + BK - 1, p_lo) - off, 0) + BQ - 1) / BQ);
@@ -1316,7 +1392,7 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dkv_kern
           const char* t = lds + ring * 2 * TB;
           arrive(h, rt, lds + (2 - 2 * ring) * TB, stats[1 - ring][0]);
 #pragma unroll 1
-          for (int sb = 0; sb < BQ; sb += 32) {
+          for (int sb = 32 * ks; sb < BQ; sb += 32 * KS) {
             const int q0 = off + rt * BQ + sb, q1 = q0 + 31;  // positions
             const int u0 = max(q0, p_lo), u1 = min(q1, p_hi);
             if (u0 > u1 || wk0 > wk1 || u1 < wk0 || (wk1 <= u0 - a.window && wk0 >= a.sinks)) continue;
@@ -1350,13 +1426,18 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dkv_kern
       }
     }
   }
+  if constexpr (KS == 2) {
+    add_parts<RG, DB>(reinterpret_cast<float*>(lds), rg, ks, lane, dk);
+    add_parts<RG, DB>(reinterpret_cast<float*>(lds), rg, ks, lane, dv);
+    if (ks != 0) return;
+  }
   const bool parts = tile < a.sink_tiles && a.splits > 1;
   // [batch x key head][sink tile][split][dk, dv][key][d]
   float* pk = a.part + (((int64_t)bk * a.sink_tiles + tile) * a.splits + split) * 2 * BK * a.d;
   char* ok = a.dk + b * a.sdk.b + hk * a.sdk.h;
   char* ov = a.dv + b * a.sdv.b + hk * a.sdv.h;
   if (parts) {
-    float* to = pk + (32 * wave + n) * a.d;
+    float* to = pk + (32 * rg + n) * a.d;
     store_rows<float, DP>(dk, 1.f, reinterpret_cast<char*>(to), a.d, lane);
     store_rows<float, DP>(dv, 1.f, reinterpret_cast<char*>(to + BK * a.d), a.d, lane);
   } else if (key < a.Lk) {
@@ -1364,7 +1445,7 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dkv_kern
     store_rows<T, DP>(dv, 1.f, ov + (int64_t)key * a.sdv.l, a.d, lane);
   }
   for (uint32_t bad = (not_finite(dk) | not_finite(dv)) & (uint32_t)__ballot(key < klen); bad; bad &= bad - 1) {
-    const int i = __builtin_ctz(bad), j = k0 + 32 * wave + i;
+    const int i = __builtin_ctz(bad), j = k0 + 32 * rg + i;
     const Lane2<T> k(a.k + b * a.sk.b + hk * a.sk.h + j * a.sk.l, a.d, lane);
     const Lane2<T> v(a.v + b * a.sv.b + hk * a.sv.h + j * a.sv.l, a.d, lane);
     float x[2] = {0.f, 0.f}, y[2] = {0.f, 0.f};
@@ -1388,7 +1469,7 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dkv_kern
         }
       }
     if (parts) {
-      float* to = pk + (32 * wave + i) * a.d;
+      float* to = pk + (32 * rg + i) * a.d;
       store_lane2<float>(reinterpret_cast<char*>(to), x, a.d, lane);
       store_lane2<float>(reinterpret_cast<char*>(to + BK * a.d), y, a.d, lane);
     } else {
@@ -1399,16 +1480,16 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dkv_kern
   }
 }
 
-// dk, dv of the sink tiles: the splits' partial sums, in order
-template <typename T>
+// dk, dv of the sink tiles, BK keys each: the splits' partial sums, in order
+template <typename T, int BK>
 __global__ __launch_bounds__(128) void attn_sink_sum_kernel(AttnArgs a) {
-  const int keys = a.sink_tiles * 128;
+  const int keys = a.sink_tiles * BK;
   const int x = blockIdx.x % (2 * keys), bk = blockIdx.x / (2 * keys), what = x / keys, key = x % keys;
   const int hk = bk % a.Hk, b = bk / a.Hk, c = threadIdx.x;
   if (key >= a.Lk || c >= a.d) return;
-  const float* pr = a.part + ((((int64_t)bk * a.sink_tiles + key / 128) * a.splits * 2 + what) * 128 + key % 128) * a.d + c;
+  const float* pr = a.part + ((((int64_t)bk * a.sink_tiles + key / BK) * a.splits * 2 + what) * BK + key % BK) * a.d + c;
   float sum = 0.f;
-  for (int s = 0; s < a.splits; ++s) sum += pr[(int64_t)s * 2 * 128 * a.d];
+  for (int s = 0; s < a.splits; ++s) sum += pr[(int64_t)s * 2 * BK * a.d];
   if (key >= seq_len(a.k_lens, b, a.Lk)) sum = 0.f;
   char* to = what ? a.dv + b * a.sdv.b + hk * a.sdv.h + (int64_t)key * a.sdv.l
                   : a.dk + b * a.sdk.b + hk * a.sdk.h + (int64_t)key * a.sdk.l;

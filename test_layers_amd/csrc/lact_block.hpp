@@ -84,7 +84,9 @@ bool few_rows(const lact_attention& p) { return p.heads / p.kv_heads * p.q_len <
 int few_splits(const lact_attention& p) {
   const int64_t keys = p.window ? std::min(p.k_len, p.window + p.q_len - 1 + std::min(p.sinks, p.k_len)) : p.k_len;
   const int64_t most = std::max<int64_t>(1, ceil_div(keys, 256));
-  const int64_t want = std::max<int64_t>(1, 2 * NCU / std::max<int64_t>(1, (int64_t)p.batch * p.kv_heads));
+  // workgroups that run at once: their rings take 64 KB of a compute unit's LDS, or 128
+  const int64_t room = (p.d * size_of(p.io_dtype) > 128 ? 1 : 2) * NCU;
+  const int64_t want = std::max<int64_t>(1, room / std::max<int64_t>(1, (int64_t)p.batch * p.kv_heads));
   return (int)std::min<int64_t>(std::min(most, want), 256);
 }
 
@@ -106,9 +108,19 @@ AttnArgs attn_args(const lact_attention& p) {
   return a;
 }
 
-// sink tiles of the dk, dv kernel and the splits of the rows behind their window
+// Waves that share the rows (keys) of a tile: two where `tiles` of 128 are no
+// more than the compute units.  fp32 heads wider than 64 have tiles of 32 keys,
+// which do not divide.
+int parts(const lact_attention& p, int64_t tiles) {
+  return tiles <= NCU && !(p.io_dtype == LACT_DTYPE_F32 && p.d > 64) ? 2 : 1;
+}
+int parts_q(const lact_attention& p) { return parts(p, (int64_t)p.batch * p.heads * ceil_div(p.q_len, 128)); }
+int parts_k(const lact_attention& p) { return parts(p, (int64_t)p.batch * p.kv_heads * ceil_div(p.k_len, 128)); }
+
+// key tiles of the dk, dv kernel, those of them with sinks, and the splits of
+// the rows behind a sink tile's window
 void sink_plan(const lact_attention& p, AttnArgs& a) {
-  constexpr int64_t BK = 128;
+  const int64_t BK = 128 / parts_k(p);
   a.tiles = (int32_t)ceil_div(p.k_len, BK);
   a.splits = 1;
   a.sink_tiles = 0;
@@ -141,7 +153,7 @@ AttnWs attn_back_ws(const lact_attention& p) {
   sink_plan(p, a);
   w.part = align256((size_t)p.batch * p.heads * p.q_len * 2 * 4);
   w.total = w.part;
-  if (a.splits > 1) w.total += align256((size_t)p.batch * p.kv_heads * a.sink_tiles * a.splits * 2 * 128 * p.d * 4);
+  if (a.splits > 1) w.total += align256((size_t)p.batch * p.kv_heads * a.sink_tiles * a.splits * 2 * (128 / parts_k(p)) * p.d * 4);
   return w;
 }
 
@@ -167,6 +179,14 @@ template <class F>
 lact_status by_tile(const lact_attention& p, F&& fn) {
   if (p.io_dtype == LACT_DTYPE_F32) return p.d <= 64 ? fn(float{}, IC<64>{}) : fn(float{}, IC<128>{});
   return p.d <= 64 ? fn(bf16_t{}, IC<64>{}) : fn(bf16_t{}, IC<128>{});
+}
+
+// calls fn with the number of waves that share a tile
+template <typename T, class DP, class F>
+void by_parts(T, DP, int ks, F&& fn) {
+  if constexpr (sizeof(T) == 4 && DP::value > 64) fn(IC<1>{});
+  else if (ks == 2) fn(IC<2>{});
+  else fn(IC<1>{});
 }
 
 // check_device for calls that come every few microseconds: the device that
@@ -238,13 +258,16 @@ lact_status lact_window_attention_forward(const lact_attention* p, const void* q
       return LACT_OK;
     });
   }
-  a.tiles = (int32_t)ceil_div(p->q_len, 128);
+  const int ks = parts_q(*p);
+  a.tiles = (int32_t)ceil_div(p->q_len, 128 / ks);
   const int64_t grid = (int64_t)p->batch * p->heads * a.tiles;
   TRY(check_grid(grid));
   TRY(check_device_again());
   KernelTimer kt(LACT_K_ATTN, s);
   return by_tile(*p, [&](auto t, auto dp) -> lact_status {
-    LACT_LAUNCH((attn_fwd_kernel<decltype(t), decltype(dp)::value>), dim3((unsigned)grid), dim3(256), s, a);
+    by_parts(t, dp, ks, [&](auto n) {
+      LACT_LAUNCH((attn_fwd_kernel<decltype(t), decltype(dp)::value, decltype(n)::value>), dim3((unsigned)grid), dim3(256), s, a);
+    });
     HIP_TRY(hipGetLastError());
     return LACT_OK;
   });
@@ -299,10 +322,11 @@ lact_status lact_window_attention_backward(const lact_attention* p, const void* 
   a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + w.part);
   AttnArgs kv = a;
   sink_plan(*p, kv);
-  a.tiles = (int32_t)ceil_div(p->q_len, 128);
+  const int ksq = parts_q(*p), ksk = parts_k(*p);
+  a.tiles = (int32_t)ceil_div(p->q_len, 128 / ksq);
   const int64_t heads = (int64_t)p->batch * p->kv_heads, gq = (int64_t)p->batch * p->heads * a.tiles,
                 gk = heads * (kv.tiles + (int64_t)kv.sink_tiles * (kv.splits - 1)),
-                gs = kv.splits > 1 ? heads * kv.sink_tiles * 2 * 128 : 0;
+                gs = kv.splits > 1 ? heads * kv.sink_tiles * 2 * (128 / ksk) : 0;
   TRY(check_grid(std::max(std::max(gq, gk), gs)));
   TRY(check_device_again());
   const hipStream_t s = static_cast<hipStream_t>(stream);
@@ -311,15 +335,20 @@ lact_status lact_window_attention_backward(const lact_attention* p, const void* 
     constexpr int DP = decltype(dp)::value;
     if (gq > 0) {
       KernelTimer kt(LACT_K_ATTN_BWD, s);
-      LACT_LAUNCH((attn_dq_kernel<T, DP>), dim3((unsigned)gq), dim3(256), s, a);
+      by_parts(t, dp, ksq, [&](auto n) {
+        LACT_LAUNCH((attn_dq_kernel<T, DP, decltype(n)::value>), dim3((unsigned)gq), dim3(256), s, a);
+      });
     }
     if (gk > 0) {
       KernelTimer kt(LACT_K_ATTN_BWD, s);
-      LACT_LAUNCH((attn_dkv_kernel<T, DP>), dim3((unsigned)gk), dim3(256), s, kv);
+      by_parts(t, dp, ksk, [&](auto n) {
+        LACT_LAUNCH((attn_dkv_kernel<T, DP, decltype(n)::value>), dim3((unsigned)gk), dim3(256), s, kv);
+      });
     }
     if (gs > 0) {
       KernelTimer kt(LACT_K_ATTN_BWD, s);
-      LACT_LAUNCH((attn_sink_sum_kernel<T>), dim3((unsigned)gs), dim3(128), s, kv);
+      if (ksk == 2) LACT_LAUNCH((attn_sink_sum_kernel<T, 64>), dim3((unsigned)gs), dim3(128), s, kv);
+      else LACT_LAUNCH((attn_sink_sum_kernel<T, 128>), dim3((unsigned)gs), dim3(128), s, kv);
     }
     HIP_TRY(hipGetLastError());
     return LACT_OK;
@@ -378,11 +407,11 @@ lact_status lact_rotary(const lact_rotary_problem* p, const void* q, const lact_
   a.pairs = p->pairs;
   a.mscale = p->mscale;
   a.inverse = (p->flags & LACT_ROTARY_INVERSE) != 0;
-  // a workgroup's tokens: a table of at most 2048 angles, and at most 16
+  // a workgroup's tokens: a table of at most 2048 angles, and at most 8
   // tokens; fewer, and the heads split, where that fills the chip no better
   const int heads = p->heads + p->kv_heads;
-  a.tok = (int32_t)std::min<int64_t>(std::min<int64_t>(16, std::max(1, ROT_TABLE / std::max(1, p->pairs))), p->tokens);
-  while (a.tok > 1 && p->batch * ceil_div(p->tokens, a.tok) < 4 * NCU) a.tok = (a.tok + 1) / 2;
+  a.tok = (int32_t)std::min<int64_t>(std::min<int64_t>(8, std::max(1, ROT_TABLE / std::max(1, p->pairs))), p->tokens);
+  while (a.tok > 1 && p->batch * ceil_div(p->tokens, a.tok) < 8 * NCU) a.tok = (a.tok + 1) / 2;
   int64_t groups = p->batch * ceil_div(p->tokens, a.tok);
   a.head_groups = (int32_t)std::max<int64_t>(1, std::min<int64_t>(heads, 2 * NCU / std::max<int64_t>(1, groups)));
   a.group = (int32_t)ceil_div(heads, a.head_groups);

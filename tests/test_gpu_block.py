@@ -106,6 +106,14 @@ ATTENTION = [
     (1, 8, 8, 128, 1, 3000, 2048, 4, None, None),          # split keys
     (3, 8, 2, 64, 8, 400, 50, 2, [8, 3, 0], [400, 399, 7]),
     (2, 6, 2, 104, 33, 65, 31, 3, None, None),             # one row more than the few-row kernel takes
+    # more than 256 tiles of 128 rows (keys): a wave for every 32 of them, and
+    # tiles that all of a workgroup's rows see whole
+    (4, 24, 24, 64, 700, 700, 400, 5, None, None),
+    (3, 32, 16, 128, 600, 600, 330, 4, [600, 513, 100], [600, 513, 100]),
+    (5, 24, 24, 40, 500, 640, 0, 0, None, None),
+    (6, 26, 26, 72, 270, 270, 50, 130, None, None),
+    (2, 64, 64, 64, 515, 515, 129, 64, [515, 300], [515, 400]),
+    (40, 8, 4, 128, 130, 130, 1000, 0, None, None),
 ]
 
 
@@ -203,10 +211,12 @@ def test_lengths_beyond_the_arrays_are_clamped(lact):
 @pytest.mark.parametrize("L,d", [(150, 64), (300, 128), (3, 64)])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
 def test_a_non_finite_token_reaches_only_rows_that_see_it(lact, t, L, d, bad):
+    L_ = lact
     """Masked places hold anything: with one key and value spoilt, the rows
     that do not see it are right (those that met it only as a masked place may
     be summed in another order), and those that do see the value are not
-    finite where it is."""
+    finite where it is.  Once for a few heads and once for the same repeated
+    (stride 0) over a batch that fills the chip: other kernels."""
     dt = DT[t]
     gen = torch.Generator("cuda").manual_seed(5)
     Lk = 300
@@ -214,6 +224,14 @@ def test_a_non_finite_token_reaches_only_rows_that_see_it(lact, t, L, d, bad):
     kw = dict(window=37, sinks=2)
     ref = OB.window_attention(f64(q), f64(k), f64(v), 37, 2, d ** -0.5)
     see = OB.visible(L, Lk, 37, 2)
+    class lact:   # noqa: N801  the binding, both ways
+        @staticmethod
+        def window_attention(*x, **kw):
+            one = L_.window_attention(*x, **kw)
+            many = L_.window_attention(*[t.expand((90,) + t.shape[1:]) for t in x], **kw)
+            unseen_are_right(many[-1:], s)
+            assert torch.equal(many[:1].isfinite(), many[-1:].isfinite())
+            return one
 
     def unseen_are_right(o, s):
         part = {n: ref[n][:, :, ~s] for n in ("o", "o_abs")}
@@ -223,8 +241,8 @@ def test_a_non_finite_token_reaches_only_rows_that_see_it(lact, t, L, d, bad):
     for j in (0, 5, Lk - L, Lk - 40, Lk - 2, Lk - 1):
         v2, k2 = v.clone(), k.clone()
         v2[0, 0, j, 3] = bad
-        o = lact.window_attention(q, k, v2, **kw)
         s = see[:, j]
+        o = lact.window_attention(q, k, v2, **kw)
         unseen_are_right(o, s)
         others = [c for c in range(d) if c != 3]
         assert torch.isfinite(o[..., others]).all()
@@ -239,12 +257,23 @@ def test_a_non_finite_token_reaches_only_rows_that_see_it(lact, t, L, d, bad):
 
 
 @pytest.mark.parametrize("t", ["bf16", "fp32"])
-def test_non_finite_gradients_stay_with_what_they_reach(lact, t):
+@pytest.mark.parametrize("batch", [1, 80])
+def test_non_finite_gradients_stay_with_what_they_reach(lact, t, batch):
     dt = DT[t]
     gen = torch.Generator("cuda").manual_seed(6)
     L, d, j = 500, 64, 150
     q, k, v, g = (randn(gen, (1, 1, L, d), dt) for _ in range(4))
     kw = dict(window=20, sinks=2)
+    L_ = lact
+    class lact:   # noqa: N801  the same repeated over a batch (stride 0); its last sequence is looked at
+        window_attention = staticmethod(L_.window_attention)
+
+        @staticmethod
+        def window_attention_backward(*x, dO, **kw):
+            r = lambda t: t.expand((batch,) + t.shape[1:])
+            y = [r(t) for t in x]
+            y[4] = y[4].contiguous()
+            return {n: t[-1:] for n, t in L_.window_attention_backward(*y, dO=r(dO), **kw).items()}
     o, lse = lact.window_attention(q, k, v, return_lse=True, **kw)
     ref = OB.window_attention(f64(q), f64(k), f64(v), 20, 2, 0.125, dO=f64(g))
     see = OB.visible(L, L, 20, 2)
