@@ -326,7 +326,7 @@ typedef struct {
     int32_t kv_heads;   /* >= 1 */
     int32_t d;          /* width of a head: a multiple of 8 in [8, 128] */
     int32_t io_dtype;   /* lact_dtype of q, k, v, o and their gradients */
-    float scale;        /* finite, > 0 */
+    float scale;        /* 2^-100 .. 2^100 */
     int64_t q_len;      /* rows of q and o, 0 <= q_len < 2^30 */
     int64_t k_len;      /* rows of k and v, 0 <= k_len < 2^30 */
     int64_t window;     /* >= 0; 0: no limit */
@@ -451,7 +451,7 @@ lact_status lact_add_rmsnorm_forward(const lact_norm_problem* p, const void* x, 
  * dx is the gradient of x and of residual alike; dh (NULL: none) is what
  * reaches h from its other use; dx may be dy or dh itself (same row stride).
  * dw [cols] float32, or NULL.  ws: lact_add_rmsnorm_backward_workspace_size
- * bytes, 256-B aligned.
+ * bytes, 256-B aligned (may be NULL where that is 0, or without dw).
  */
 size_t lact_add_rmsnorm_backward_workspace_size(const lact_norm_problem* p);
 lact_status lact_add_rmsnorm_backward(const lact_norm_problem* p, const void* h, int64_t ldh, const float* weight,

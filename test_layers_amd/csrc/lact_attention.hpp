@@ -44,7 +44,7 @@ struct AttnArgs {
   AttnStride sq, sk, sv, so, sdo, sdq, sdk, sdv;
   const int64_t *q_lens, *k_lens;  // device, or null: Lq, Lk
   float* lse;                      // [B, H, Lq], or null (forward)
-  float* stats;                    // [2][B, H, Lq]: -lse / scale and -D, D = dO.o
+  float* stats;                    // [2][B, H, Lq]: -lse / scale (fp32: -lse) and -D, D = dO.o
   float* part;                     // partial sums (few-row forward: O; backward: dK, dV of sink tiles)
   float* part_ml;                  // few-row forward: running maximum and sum of each split
   int32_t B, H, Hk, G;             // G = H / Hk query heads share a key head
@@ -949,7 +949,7 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dq_kerne
   const char* vb = a.v + at.b * a.sv.b + at.hk * a.sv.h;
   const char* qb = a.q + at.b * a.sq.b + at.h * a.sq.h;
   const char* gb = a.dO + at.b * a.sdo.b + at.h * a.sdo.h;
-  float delta = 0.f, lse2 = 0.f;
+  float delta = 0.f, lse = 0.f, lse2 = 0.f;
   const KeyTiles kt(off + r0, off + min(r0 + BM, qlen) - 1, a.window, a.sinks, BN);
   if (r0 < qlen) {
     const int64_t rc = min(row, qlen - 1);
@@ -965,11 +965,11 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dq_kerne
         for (int e = 0; e < 16 / (int)sizeof(T); ++e) delta = fmaf((float)g[s][e], (float)o[s][e], delta);
     }
     delta = pair_sum(delta);
-    const float lse = row < qlen ? a.lse[stat] : 0.f;
+    lse = row < qlen ? a.lse[stat] : 0.f;
     lse2 = lse * LOG2E;
-    f32x16 less;  // -D: what dP's product starts from
+    f32x16 less;  // -D: what dP's product starts from (bf16)
 #pragma unroll
-    for (int r = 0; r < 16; ++r) less[r] = -delta;
+    for (int r = 0; r < 16; ++r) less[r] = sizeof(T) == 4 ? 0.f : -delta;
     float sum = 0.f, rsum = 0.f;  // of dS, exact and rounded
     f32x16 kbar[CENTRE ? DB : 1];
 #pragma unroll
@@ -986,11 +986,19 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dq_kerne
         sv.issue(other + TB, kt.at(i + 1) * BN);
       }
     };
-    auto gradients = [&](f32x16& s, f32x16& ds) {  // scores and dP - D to P and dS
+    // Scores and dP - D to P and dS.  fp32: the exponent is formed in one
+    // rounding, log2(e) multiplied last, and D subtracted last: scale log2(e)
+    // and lse log2(e) rounded beforehand are a tenth of dk's error budget each.
+    auto gradients = [&](f32x16& s, f32x16& ds) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], a.c, -lse2));
-        ds[r] *= s[r];
+        if constexpr (sizeof(T) == 4) {
+          s[r] = __builtin_amdgcn_exp2f(LOG2E * fmaf(s[r], a.scale, -lse));
+          ds[r] = (ds[r] - delta) * s[r];
+        } else {
+          s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], a.c, -lse2));
+          ds[r] *= s[r];
+        }
       }
     };
     auto count = [&](const f32x16& ds, const Pair& x) {
@@ -1163,7 +1171,7 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dq_kerne
     }
     // what the dk, dv kernel's products start from: exp2(c (q.k - lse / scale)), dO.v - D
     if (ks == 0 && row < qlen && lane < 32) {
-      a.stats[stat] = -lse / a.scale;
+      a.stats[stat] = sizeof(T) == 4 ? -lse : -lse / a.scale;
       a.stats[(int64_t)a.B * a.H * a.Lq + stat] = -delta;
     }
   }
@@ -1281,11 +1289,18 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dkv_kern
       }
       return x;
     };
-    auto gradients = [&](f32x16& s, f32x16& ds) {
+    // products of a row tile, from the rows' statistics (bf16) or with them
+    // added last (fp32, see the dq kernel)
+    auto gradients = [&](f32x16& s, f32x16& ds, const f32x16& less_s, const f32x16& less_ds) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        s[r] = __builtin_amdgcn_exp2f(s[r] * a.c);
-        ds[r] *= s[r];
+        if constexpr (sizeof(T) == 4) {
+          s[r] = __builtin_amdgcn_exp2f(LOG2E * fmaf(s[r], a.scale, less_s[r]));
+          ds[r] = (ds[r] + less_ds[r]) * s[r];
+        } else {
+          s[r] = __builtin_amdgcn_exp2f(s[r] * a.c);
+          ds[r] *= s[r];
+        }
       }
     };
     issue(0, ra, lds, stats[0][0]);
@@ -1398,13 +1413,14 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dkv_kern
             if (u0 > u1 || wk0 > wk1 || u1 < wk0 || (wk1 <= u0 - a.window && wk0 >= a.sinks)) continue;
             const bool whole = u0 == q0 && u1 == q1 && wk1 <= q0 && wk0 + 31 == wk1 &&
                                (wk0 > q1 - a.window || wk1 < a.sinks);
-            f32x16 s = start(stats[ring][0], sb), ds = start(stats[ring][1], sb);
+            const f32x16 less_s = start(stats[ring][0], sb), less_ds = start(stats[ring][1], sb);
+            f32x16 s = sizeof(T) == 4 ? zero16() : less_s, ds = sizeof(T) == 4 ? zero16() : less_ds;
 #pragma unroll
             for (int st = 0; st < STEPS; ++st) {
               s = mma32(row_frag<T, DP>(t, sb, st, lane), kf[st], s);
               ds = mma32(row_frag<T, DP>(t + TB, sb, st, lane), vf[st], ds);
             }
-            gradients(s, ds);
+            gradients(s, ds, less_s, less_ds);
             if (!whole) {
               // a row's position p = q0 + 4 (lane / 32) + o, against the key's own bounds
               const int base = q0 + 4 * (lane >> 5), lo = max(u0, key) - base,
@@ -1456,7 +1472,8 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dkv_kern
         if (j <= p - a.window && j >= a.sinks) break;
         const int64_t r = p - off, st = sh + (int64_t)h * a.Lq + r;
         const Lane2<T> q(qh + h * a.sq.h + r * a.sq.l, a.d, lane), g(gh + h * a.sdo.h + r * a.sdo.l, a.d, lane);
-        const float pr = __builtin_amdgcn_exp2f(a.c * (q.dot(k) + a.stats[st]));
+        const float pr = sizeof(T) == 4 ? __builtin_amdgcn_exp2f(LOG2E * fmaf(q.dot(k), a.scale, a.stats[st]))
+                                        : __builtin_amdgcn_exp2f(a.c * (q.dot(k) + a.stats[st]));
         const float ds = pr * (g.dot(v) + a.stats[sn + st]);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {

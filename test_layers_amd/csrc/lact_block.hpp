@@ -67,8 +67,8 @@ lact_status validate(const lact_attention* p) {
     return fail(LACT_ERR_UNSUPPORTED, "d = %d: need a multiple of 8 in [8, 128]", p->d);
   lact_status r = check_dtype(p->io_dtype);
   if (r) return r;
-  if (!(p->scale > 0.f) || !std::isfinite(p->scale * LOG2E))
-    return fail(LACT_ERR_INVALID_ARG, "scale = %g: need a finite value > 0", (double)p->scale);
+  if (!(p->scale >= 0x1p-100f) || !(p->scale <= 0x1p100f))
+    return fail(LACT_ERR_INVALID_ARG, "scale = %g: need 2^-100 .. 2^100", (double)p->scale);
   if (p->q_len < 0 || p->q_len >= MOST_TOKENS) return fail(LACT_ERR_INVALID_ARG, "q_len = %lld", (long long)p->q_len);
   if (p->k_len < 0 || p->k_len >= MOST_TOKENS) return fail(LACT_ERR_INVALID_ARG, "k_len = %lld", (long long)p->k_len);
   if (p->window < 0) return fail(LACT_ERR_INVALID_ARG, "window = %lld < 0", (long long)p->window);
@@ -514,7 +514,11 @@ NormPlan norm_plan(const lact_norm_problem& p) {
 }
 // workgroups of the backward, 512 threads or one row's 1024 each: as many as
 // run at once, so that few partial sums of dw remain
+// One workgroup's rows need no second launch to add them up; that takes as
+// long as three more rounds of it.
 int64_t norm_back_grid(const lact_norm_problem& p, const NormPlan& c) {
+  const int64_t at_once = c.gs < 512 ? 512 / c.gs : 1;
+  if (p.rows <= 4 * at_once) return std::min<int64_t>(p.rows, 1);
   return std::min<int64_t>(ceil_div(p.rows, c.gs < 512 ? 512 / c.gs : 1), (c.gs == 1024 ? 1 : 2) * NCU);
 }
 
@@ -595,7 +599,8 @@ lact_status lact_add_rmsnorm_forward(const lact_norm_problem* p, const void* x, 
 size_t lact_add_rmsnorm_backward_workspace_size(const lact_norm_problem* p) {
   g_err.clear();
   if (validate(p)) return 0;
-  return align256((size_t)norm_back_grid(*p, norm_plan(*p)) * p->cols * 4);
+  const int64_t grid = norm_back_grid(*p, norm_plan(*p));
+  return grid > 1 ? align256((size_t)grid * p->cols * 4) : 0;
 }
 
 lact_status lact_add_rmsnorm_backward(const lact_norm_problem* p, const void* h, int64_t ldh, const float* weight,
@@ -624,7 +629,7 @@ lact_status lact_add_rmsnorm_backward(const lact_norm_problem* p, const void* h,
   }
   if (dw) {
     NEED(dw, 4);
-    TRY(check_ws(ws, ws_bytes, align256((size_t)grid * p->cols * 4)));
+    if (grid > 1) TRY(check_ws(ws, ws_bytes, align256((size_t)grid * p->cols * 4)));
   }
   TRY(check_device_again());
   a.x = static_cast<const char*>(h);
@@ -632,7 +637,7 @@ lact_status lact_add_rmsnorm_backward(const lact_norm_problem* p, const void* h,
   a.dy = static_cast<const char*>(dy);
   a.dh = static_cast<const char*>(dh);
   a.dx = static_cast<char*>(dx);
-  a.part = dw ? static_cast<float*>(ws) : nullptr;
+  a.part = !dw ? nullptr : grid == 1 ? dw : static_cast<float*>(ws);
   a.rows = p->rows;
   a.cols = p->cols;
   a.eps = p->eps;
@@ -647,7 +652,7 @@ lact_status lact_add_rmsnorm_backward(const lact_norm_problem* p, const void* h,
       return LACT_OK;
     }));
   }
-  if (dw) {
+  if (dw && grid != 1) {
     KernelTimer kt(LACT_K_NORM, s);
     LACT_LAUNCH(norm_dw_kernel, dim3((unsigned)ceil_div(p->cols, 32)), dim3(1024), s, a.part, dw, (int)grid, p->cols);
     HIP_TRY(hipGetLastError());

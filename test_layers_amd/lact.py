@@ -635,10 +635,30 @@ def _attention_plan(q, k, v, window, sinks, scale, q_lens, k_lens, back):
     return plan
 
 
+def _attention_back_plan(q, k, v, window, sinks, scale, q_lens, k_lens, o, lse, dO, given):
+    plan = _attention_plan(q, k, v, window, sinks, scale, q_lens, k_lens, True)
+    _one_device(q, o, lse, dO, *given)
+    _check_shapes(lse=(lse, plan.shape[:3]))
+    _ptr(lse, _torch().float32, "lse")
+    more = [_strided(o, "o", plan.shape, plan.dtype), _strided(dO, "dO", plan.shape, plan.dtype)]
+    plan.so, plan.sg = (ctypes.byref(x) for x in more)
+    if given[0] is not None:
+        more += [_strided(t, f"out[{n}]", s, plan.dtype)
+                 for t, n, s in zip(given, ("dq", "dk", "dv"), (plan.shape, plan.kshape, plan.kshape))]
+        plan.rq, plan.rk, plan.rv = (ctypes.byref(x) for x in more[2:])
+    plan.strides += more
+    return plan
+
+
 def _scratch(need, workspace, device):
     """(address, bytes) of the workspace, and the tensor that holds it."""
-    if workspace is None and need == 0:
-        return None, 0, None
+    if workspace is None:
+        if need == 0:
+            return None, 0, None
+        ws = _torch().empty(need, dtype=_torch().uint8, device=device)
+        return ws.data_ptr(), need, ws
+    if workspace.device != device:
+        raise ValueError(f"workspace on {workspace.device} for tensors on {device}")
     ws = _workspace(need, workspace, device)
     return ws.data_ptr(), ws.numel(), ws
 
@@ -656,12 +676,13 @@ def window_attention(q, k, v, o=None, *, window: int = 0, sinks: int = 0, scale:
     plan = _plan(("attention", window, sinks, scale, _meta(q), _meta(k), _meta(v), _meta(q_lens), _meta(k_lens)),
                  lambda: _attention_plan(q, k, v, window, sinks, scale, q_lens, k_lens, False))
     so = plan.rq
-    if o is not None or lse is not None or workspace is not None:
-        _one_device(q, o, lse, workspace)
+    if o is not None or lse is not None:
+        _one_device(q, o, lse)
         if o is not None:
             so = ctypes.byref(_strided(o, "o", plan.shape, plan.dtype))
         _check_shapes(lse=(lse, plan.shape[:3]))
         _ptr(lse, _torch().float32, "lse")
+
     def run(handle, o=o, lse=lse):
         if o is None:
             o = _new(q, plan.results[0])
@@ -688,25 +709,20 @@ def window_attention_backward(q, k, v, o, lse, *, dO, window: int = 0, sinks: in
     as the forward returned them, dO [batch, heads, q_len, d] in q's dtype.
     Returns a dict of dq, dk, dv in the inputs' dtype and layout, zero behind
     the lengths; `out` (such a dict) is filled instead of allocating."""
-    plan = _plan(("attention back", window, sinks, scale, _meta(q), _meta(k), _meta(v), _meta(q_lens), _meta(k_lens)),
-                 lambda: _attention_plan(q, k, v, window, sinks, scale, q_lens, k_lens, True))
-    given = () if out is None else (out["dq"], out["dk"], out["dv"])
-    _one_device(q, o, lse, dO, workspace, *given)
-    so = ctypes.byref(_strided(o, "o", plan.shape, plan.dtype))
-    sg = ctypes.byref(_strided(dO, "dO", plan.shape, plan.dtype))
-    _check_shapes(lse=(lse, plan.shape[:3]))
-    rq, rk, rv = plan.rq, plan.rk, plan.rv
-    if out is not None:
-        rq, rk, rv = (ctypes.byref(_strided(t, f"out[{n}]", s, plan.dtype))
-                      for t, n, s in zip(given, ("dq", "dk", "dv"), (plan.shape, plan.kshape, plan.kshape)))
+    given = (None,) * 3 if out is None else (out["dq"], out["dk"], out["dv"])
+    plan = _plan(("attention back", window, sinks, scale, _meta(q), _meta(k), _meta(v), _meta(q_lens), _meta(k_lens),
+                  _meta(o), _meta(lse), _meta(dO), _meta(given[0]), _meta(given[1]), _meta(given[2])),
+                 lambda: _attention_back_plan(q, k, v, window, sinks, scale, q_lens, k_lens, o, lse, dO, given))
+
     def run(handle, out=out):
         if out is None:
-            out = {n: _new(q, m) for n, m in zip(("dq", "dk", "dv"), plan.results)}
+            m = plan.results
+            out = {"dq": _new(q, m[0]), "dk": _new(k, m[1]), "dv": _new(v, m[2])}
         ws, ws_bytes, _held = _scratch(plan.need, workspace, q.device)
         st = lib().lact_window_attention_backward(
             plan.p, q.data_ptr(), plan.sq, k.data_ptr(), plan.sk, v.data_ptr(), plan.sv, _addr(q_lens), _addr(k_lens),
-            o.data_ptr(), so, _ptr(lse, _torch().float32, "lse"), dO.data_ptr(), sg, out["dq"].data_ptr(), rq,
-            out["dk"].data_ptr(), rk, out["dv"].data_ptr(), rv, ws, ws_bytes, handle)
+            o.data_ptr(), plan.so, lse.data_ptr(), dO.data_ptr(), plan.sg, out["dq"].data_ptr(), plan.rq,
+            out["dk"].data_ptr(), plan.rk, out["dv"].data_ptr(), plan.rv, ws, ws_bytes, handle)
         check(st)
         return out
 
@@ -751,6 +767,7 @@ def _rotary(q, k, freqs, positions, start, interleaved, mscale, q_out, k_out, st
             if k is None:
                 raise ValueError("k_out is given without k")
             rk = ctypes.byref(_strided(k_out, "k_out", plan.kshape, plan.dtype))
+
     def run(handle, q_out=q_out, k_out=k_out):
         if q_out is None:
             q_out = _new(q, plan.results[0])
@@ -844,6 +861,7 @@ def add_rmsnorm(x, weight, residual=None, *, eps: float = 1e-6, y=None, h=None, 
     plan = _plan(("norm", eps, _meta(x), _meta(weight), _meta(residual), _meta(y), _meta(h)),
                  lambda: _norm_plan(x, weight, eps, ("residual", residual, False), ("h", h, False), ("y", y, False)))
     ldx, ldr, ldh, ldy = plan.ld
+
     def run(handle, y=y, h=h):
         if y is None:
             y = x.new_empty(plan.shape)
@@ -872,6 +890,7 @@ def add_rmsnorm_quantised(x, weight, residual=None, *, eps: float = 1e-6, y8=Non
         _one_device(x, scales)
         _check_shapes(scales=(scales, plan.groups))
         _ptr(scales, torch.float32, "scales")
+
     def run(handle, h=h, y8=y8, scales=scales):
         if y8 is None:
             y8 = x.new_empty(plan.shape, dtype=torch.float8_e4m3fn)
@@ -897,10 +916,11 @@ def add_rmsnorm_backward(h, weight, *, dy, dh=None, eps: float = 1e-6, dx=None, 
     plan = _plan(("norm back", eps, _meta(h), _meta(weight), _meta(dy), _meta(dh), _meta(dx)),
                  lambda: _norm_plan(h, weight, eps, ("dy", dy, False), ("dh", dh, False), ("dx", dx, False)))
     ldh, ldy, lddh, lddx = plan.ld
-    _one_device(h, dw, workspace)
     if dw is not None:
+        _one_device(h, dw)
         _check_shapes(dw=(dw, plan.shape[-1:]))
         _ptr(dw, torch.float32, "dw")
+
     def run(handle, dx=dx, dw=dw):
         if dx is None:
             dx = h.new_empty(plan.shape)

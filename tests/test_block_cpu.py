@@ -143,7 +143,7 @@ BAD_ATTENTION = [
     (dict(d=0), lact.ERR_UNSUPPORTED), (dict(d=12), lact.ERR_UNSUPPORTED), (dict(d=136), lact.ERR_UNSUPPORTED),
     (dict(io_dtype=2), lact.ERR_INVALID_ARG), (dict(scale=0.0), lact.ERR_INVALID_ARG),
     (dict(scale=-1.0), lact.ERR_INVALID_ARG), (dict(scale=float("nan")), lact.ERR_INVALID_ARG),
-    (dict(scale=float("inf")), lact.ERR_INVALID_ARG), (dict(q_len=-1), lact.ERR_INVALID_ARG),
+    (dict(scale=float("inf")), lact.ERR_INVALID_ARG), (dict(scale=1e-37), lact.ERR_INVALID_ARG), (dict(q_len=-1), lact.ERR_INVALID_ARG),
     (dict(k_len=1 << 30), lact.ERR_INVALID_ARG), (dict(window=-1), lact.ERR_INVALID_ARG),
     (dict(sinks=-1), lact.ERR_INVALID_ARG),
 ]
@@ -272,7 +272,7 @@ def test_norm_refuses_bad_tensors():
                dict(y=(None, 0)), dict(y8=(FAKE, 256)), dict(y8=(FAKE, 8), scales=FAKE),
                dict(h=(FAKE, 512)), dict(y=(FAKE, 512)), dict(y=(FAKE * 2, 256))):
         assert _norm(_np(), **kw) == I, kw
-    p = _np()
+    p = _np(rows=800)
     back = lambda dx=(FAKE, 256), dw=FAKE, ws=FAKE, n=1 << 40, dy=(FAKE, 256): lact.lib().lact_add_rmsnorm_backward(
         ctypes.byref(p), FAKE * 2, 256, FAKE, *dy, None, 0, *dx, dw, ws, n, None)
     need = lact.lib().lact_add_rmsnorm_backward_workspace_size(ctypes.byref(p))
