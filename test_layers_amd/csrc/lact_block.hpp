@@ -4,13 +4,14 @@
 // one translation unit, after lact.hip.
 #pragma once
 #include <cmath>
+#include <initializer_list>
 
 #include "lact_attention.hpp"
 #include "lact_rows.hpp"
 
 namespace {
 
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t ceil_div(int64_t a, int64_t b) { return a / b + (a % b != 0); }
 
 lact_status check_dtype(int32_t t) {
   if (t != LACT_DTYPE_F32 && t != LACT_DTYPE_BF16) return fail(LACT_ERR_INVALID_ARG, "io_dtype = %d", t);
@@ -65,6 +66,8 @@ lact_status validate(const lact_attention* p) {
     return fail(LACT_ERR_INVALID_ARG, "heads = %d, kv_heads = %d: need a positive multiple", p->heads, p->kv_heads);
   if (p->d < 8 || p->d > 128 || p->d % 8)
     return fail(LACT_ERR_UNSUPPORTED, "d = %d: need a multiple of 8 in [8, 128]", p->d);
+  if ((int64_t)p->batch * p->heads > MOST_GRID)
+    return fail(LACT_ERR_UNSUPPORTED, "batch * heads = %lld: more than a launch takes", (long long)p->batch * p->heads);
   lact_status r = check_dtype(p->io_dtype);
   if (r) return r;
   if (!(p->scale >= 0x1p-100f) || !(p->scale <= 0x1p100f))
@@ -157,6 +160,19 @@ AttnWs attn_back_ws(const lact_attention& p) {
   return w;
 }
 
+// Outputs that are an input or each other.  Only whole tensors can be told
+// here; that parts do not overlap is the caller's to keep.
+lact_status check_apart(std::initializer_list<const void*> outputs, std::initializer_list<const void*> inputs) {
+  for (auto o = outputs.begin(); o != outputs.end(); ++o) {
+    if (!*o) continue;
+    for (const void* i : inputs)
+      if (i == *o) return fail(LACT_ERR_INVALID_ARG, "an output is an input");
+    for (auto p = outputs.begin(); p != o; ++p)
+      if (*p == *o) return fail(LACT_ERR_INVALID_ARG, "two outputs are the same");
+  }
+  return LACT_OK;
+}
+
 #define TRY(expr)                      \
   do {                                 \
     const lact_status s_ = (expr);     \
@@ -228,6 +244,7 @@ lact_status lact_window_attention_forward(const lact_attention* p, const void* q
   TRY(check_tensor("o", o, so, p->batch, p->heads, p->q_len, p->d, es, 16, true, &a.so));
   if (!aligned(q_lens, 8) || !aligned(k_lens, 8)) return fail(LACT_ERR_INVALID_ARG, "lengths are not 8-byte aligned");
   if (!aligned(lse, 4)) return fail(LACT_ERR_INVALID_ARG, "lse is not 4-byte aligned");
+  TRY(check_apart({o, lse}, {q, k, v}));
   const AttnWs w = attn_ws(*p);
   TRY(check_ws(ws, ws_bytes, w.total));
   a.q = static_cast<const char*>(q);
@@ -248,11 +265,14 @@ lact_status lact_window_attention_forward(const lact_attention* p, const void* q
       a.part = static_cast<float*>(ws);
       a.part_ml = reinterpret_cast<float*>(static_cast<char*>(ws) + w.ml);
     }
-    KernelTimer kt(LACT_K_ATTN, s);
     return by_tile(*p, [&](auto t, auto dp) -> lact_status {
       using T = decltype(t);
       constexpr int DP = decltype(dp)::value, NW = DP * sizeof(T) > 256 ? 2 : 4;
-      LACT_LAUNCH((attn_few_kernel<T, DP, NW>), dim3((unsigned)grid), dim3(64 * NW), s, a);
+      {
+        KernelTimer kt(LACT_K_ATTN, s);
+        LACT_LAUNCH((attn_few_kernel<T, DP, NW>), dim3((unsigned)grid), dim3(64 * NW), s, a);
+      }
+      KernelTimer kt(LACT_K_ATTN, s);
       if (a.splits > 1) LACT_LAUNCH((attn_join_kernel<T, DP>), dim3((unsigned)rows), dim3(256), s, a);
       HIP_TRY(hipGetLastError());
       return LACT_OK;
@@ -305,6 +325,7 @@ lact_status lact_window_attention_backward(const lact_attention* p, const void* 
     TRY(check_tensor("dv", dv, sdv, p->batch, p->kv_heads, p->k_len, p->d, es, 16, true, &a.sdv));
   }
   if (!aligned(q_lens, 8) || !aligned(k_lens, 8)) return fail(LACT_ERR_INVALID_ARG, "lengths are not 8-byte aligned");
+  TRY(check_apart({p->q_len ? dq : nullptr, p->k_len ? dk : nullptr, p->k_len ? dv : nullptr}, {q, k, v, o, dO, lse}));
   const AttnWs w = attn_back_ws(*p);
   TRY(check_ws(ws, ws_bytes, w.total));
   a.q = static_cast<const char*>(q);
@@ -390,7 +411,13 @@ lact_status lact_rotary(const lact_rotary_problem* p, const void* q, const lact_
     return LACT_OK;
   };
   TRY(tensor(0, "q", q, sq, q_out, sqo, p->heads));
-  if (p->kv_heads > 0) TRY(tensor(1, "k", k, sk, k_out, sko, p->kv_heads));
+  if (p->kv_heads > 0) {
+    TRY(tensor(1, "k", k, sk, k_out, sko, p->kv_heads));
+    // each may be turned in place, not into the other
+    TRY(check_apart({q_out, k_out}, {}));
+    TRY(check_apart({q_out}, {k}));
+    TRY(check_apart({k_out}, {q}));
+  }
   if (p->pairs > 0) NEED(freqs, 8);
   if (!aligned(positions, 8)) return fail(LACT_ERR_INVALID_ARG, "positions is not 8-byte aligned");
   const bool il = p->flags & LACT_ROTARY_INTERLEAVED;
@@ -414,6 +441,8 @@ lact_status lact_rotary(const lact_rotary_problem* p, const void* q, const lact_
   while (a.tok > 1 && p->batch * ceil_div(p->tokens, a.tok) < 8 * NCU) a.tok = (a.tok + 1) / 2;
   int64_t groups = p->batch * ceil_div(p->tokens, a.tok);
   a.head_groups = (int32_t)std::max<int64_t>(1, std::min<int64_t>(heads, 2 * NCU / std::max<int64_t>(1, groups)));
+  // and a workgroup's items stay far below 2^31
+  a.head_groups = (int32_t)std::max<int64_t>(a.head_groups, ceil_div((int64_t)a.tok * heads * p->d, 1 << 24));
   a.group = (int32_t)ceil_div(heads, a.head_groups);
   a.head_groups = (int32_t)ceil_div(heads, a.group);
   TRY(check_grid(groups * a.head_groups));

@@ -123,14 +123,16 @@ def _st(b=4 * 64 * 64, h=64 * 64, l=64):
 
 
 def _fwd(p=None, ws=FAKE, ws_bytes=1 << 40, lse=None, q_lens=None, k_lens=None, **over):
-    a = {n: (FAKE, _st()) for n in "qkvo"}
+    a = {n: (FAKE, _st()) for n in "qkv"}
+    a["o"] = (FAKE * 8, _st())
     a.update(over)
     return lact.lib().lact_window_attention_forward(None if p is None else ctypes.byref(p), *a["q"], *a["k"],
                                                     *a["v"], q_lens, k_lens, *a["o"], lse, ws, ws_bytes, None)
 
 
 def _bwd(p=None, ws=FAKE, ws_bytes=1 << 40, lse=FAKE, **over):
-    a = {n: (FAKE, _st()) for n in ("q", "k", "v", "o", "dO", "dq", "dk", "dv")}
+    a = {n: (FAKE, _st()) for n in ("q", "k", "v", "o", "dO")}
+    a.update({n: (FAKE * (8 + i), _st()) for i, n in enumerate(("dq", "dk", "dv"))})
     a.update(over)
     return lact.lib().lact_window_attention_backward(
         None if p is None else ctypes.byref(p), *a["q"], *a["k"], *a["v"], None, None, *a["o"], lse, *a["dO"],
@@ -180,6 +182,20 @@ def test_attention_refuses_bad_tensors():
         assert _bwd(_attn(), dk=(FAKE, st)) == I
 
 
+def test_outputs_that_are_inputs_are_refused():
+    I = lact.ERR_INVALID_ARG
+    two, three, four = FAKE * 2, FAKE * 3, FAKE * 4
+    for n in ("q", "k", "v"):
+        assert _fwd(_attn(), **{n: (two, _st()), "o": (two, _st())}) == I and "output" in lact.last_error()
+    apart = dict(dq=(two, _st()), dk=(three, _st()), dv=(four, _st()))
+    for n in ("q", "k", "v", "o", "dO"):
+        assert _bwd(_attn(), **apart, **{n: (three, _st())}) == I and "output" in lact.last_error()
+    assert _bwd(_attn(), **dict(apart, dv=(two, _st()))) == I and "same" in lact.last_error()
+    assert _rot(_rp(), qo=(two, _st()), ko=(two, _st())) == I
+    assert _rot(_rp(), k=(two, _st()), qo=(two, _st()), ko=(three, _st())) == I
+    assert _rot(_rp(), q=(two, _st()), qo=(three, _st()), ko=(two, _st())) == I
+
+
 def test_attention_workspace_checks():
     p = _attn(heads=2, kv_heads=2, q_len=1, k_len=5000, window=0, batch=1)   # few rows, keys split
     need = lact.lib().lact_window_attention_workspace_size(ctypes.byref(p))
@@ -196,7 +212,7 @@ def test_attention_workspace_checks():
 def test_attention_refuses_grids_beyond_a_launch():
     p = _attn(batch=1 << 20, heads=1 << 12, kv_heads=1 << 12, q_len=64, k_len=64)
     big = _st(b=64 * 64, h=64 * 64 << 20, l=64)
-    assert _fwd(p, q=(FAKE, big), k=(FAKE, big), v=(FAKE, big), o=(FAKE, big)) == lact.ERR_UNSUPPORTED
+    assert _fwd(p, q=(FAKE, big), k=(FAKE, big), v=(FAKE, big), o=(FAKE * 8, big)) == lact.ERR_UNSUPPORTED
 
 
 def test_nothing_to_do_is_accepted():
@@ -207,7 +223,7 @@ def test_nothing_to_do_is_accepted():
 
 def _rot(p=None, freqs=FAKE, positions=None, **over):
     a = {n: (FAKE, _st()) for n in ("q", "k", "qo", "ko")}
-    a.update(qo=(FAKE * 2, _st()), ko=(FAKE * 2, _st()))
+    a.update(qo=(FAKE * 8, _st()), ko=(FAKE * 9, _st()))
     a.update(over)
     return lact.lib().lact_rotary(None if p is None else ctypes.byref(p), *a["q"], *a["k"], freqs, positions,
                                   *a["qo"], *a["ko"], None)
@@ -238,7 +254,7 @@ def test_rotary_refuses_bad_tensors():
         assert _rot(_rp(), **{n: (FAKE, _st(b=-8))}) == I
     assert _rot(_rp(), freqs=None) == I and _rot(_rp(), freqs=FAKE + 4) == I
     assert _rot(_rp(), positions=FAKE + 4) == I
-    assert _rot(_rp(), qo=(FAKE * 2, _st(l=60))) == I and "overlap" in lact.last_error()
+    assert _rot(_rp(), qo=(FAKE * 8, _st(l=60))) == I and "overlap" in lact.last_error()
     assert _rot(_rp(), qo=(FAKE, _st(b=5 * 64 * 64))) == I and "in place" in lact.last_error()
 
 
