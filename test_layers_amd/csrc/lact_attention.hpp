@@ -50,6 +50,7 @@ struct AttnArgs {
   int32_t B, H, Hk, G;             // G = H / Hk query heads share a key head
   int32_t d, Lq, Lk;
   int32_t window, sinks;           // window: 1 << 30 where there is none
+  int32_t hg;                      // query heads of a workgroup (forward, dq): its waves share their keys
   int32_t tiles;                   // row tiles (forward, dq), key tiles (dk, dv), per head
   int32_t splits;                  // few-row forward: key splits; backward: row splits of a sink tile
   int32_t sink_tiles, span;        // backward: key tiles with sinks; rows of one of their splits
@@ -457,14 +458,15 @@ struct AttnRows {
   static constexpr int STEPS = AttnTile<T, DP>::STEPS, DB = DP / 32;
   Frag<T> q[STEPS];
   f32x16 o[DB];
-  float m, l;   // maximum (in units of log2, at most 8 behind), this lane's half of the sum
+  float m, l;   // maximum (in units of log2, at most 24 behind), this lane's half of the sum
+  float limit;  // the score at which m is 24 behind
   int p;        // position of lane l % 32's row
   AttnWave w;
 
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int db = 0; db < DB; ++db) o[db] = zero16();
-    m = -__builtin_huge_valf();
+    m = limit = -__builtin_huge_valf();
     l = 0.f;
   }
 
@@ -481,17 +483,19 @@ struct AttnRows {
     for (int r = 0; r < 16; ++r) s[r] = seen(8 * (r >> 2) + (r & 3)) ? s[r] : -__builtin_huge_valf();
   }
   // The sums are taken relative to m, which may lag behind the largest score:
-  // exp2 of up to 8 loses nothing in fp32, and most tiles then rescale
-  // nothing.  `held`: probabilities that are not in o yet.
+  // exp2 of up to 24 loses nothing in floating point.  A lane then looks only
+  // whether one of its own scores is past `limit`; the row's maximum over both
+  // of its lanes is formed, and everything rescaled, in the rare block where
+  // one is.  `held`: probabilities that are not in o yet.
   __device__ __forceinline__ void follow(const f32x16& s, float c, f32x16* held) {
     float top = s[0];
 #pragma unroll
     for (int r = 1; r < 16; ++r) top = fmaxf(top, s[r]);
-    top = pair_max(top) * c;
-    if (__any(top > m + 8.f)) {
-      const float to = fmaxf(m, top);
+    if (__any(top > limit)) {
+      const float to = fmaxf(m, pair_max(top) * c);
       const float a = to == m ? 1.f : __builtin_amdgcn_exp2f(m - to);
       m = to;
+      limit = (m + 24.f) / c;
       l *= a;
 #pragma unroll
       for (int db = 0; db < DB; ++db)
@@ -631,8 +635,9 @@ constexpr int attn_bn() { return DP * (int)sizeof(T) > 256 ? 32 : 64; }
 struct AttnPlace {
   int b, hk, h, tile;
   __device__ AttnPlace(int id, const AttnArgs& a) {
-    h = id % a.G;
-    id /= a.G;
+    const int groups = a.G / a.hg;
+    h = id % groups * a.hg;
+    id /= groups;
     tile = a.tiles - 1 - id % a.tiles;  // where rows have unequal work the long ones go first
     id /= a.tiles;
     hk = id % a.Hk;
@@ -648,22 +653,24 @@ struct AttnPlace {
 template <typename T, int DP, int KS>
 __global__ __launch_bounds__(256, (attn_waves<T, DP>())) void attn_fwd_kernel(AttnArgs a) {
   using Tile = AttnTile<T, DP>;
-  constexpr int NW = 4, RG = NW / KS, BM = 32 * RG, BN = attn_bn<T, DP>(), TB = BN * Tile::CPR * 16;
+  constexpr int NW = 4, RG = NW / KS, BN = attn_bn<T, DP>(), TB = BN * Tile::CPR * 16;
   __shared__ __align__(1024) char lds[4 * TB];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const AttnPlace at(xcd_remap(blockIdx.x, gridDim.x), a);
+  AttnPlace at(xcd_remap(blockIdx.x, gridDim.x), a);
   const int qlen = seq_len(a.q_lens, at.b, a.Lq), klen = seq_len(a.k_lens, at.b, a.Lk);
-  const int r0 = at.tile * BM, off = klen - qlen;
+  const int rg = wave % RG, ks = wave / RG;  // head and rows of the wave; its part of a tile
+  const int BM = 32 * RG / a.hg;             // rows of the workgroup
+  at.h += rg % a.hg;
+  const int r0 = at.tile * BM, rw = r0 + 32 * (rg / a.hg), off = klen - qlen;
   if (r0 >= qlen) return;
-  const int rg = wave % RG, ks = wave / RG;  // rows of the wave; its part of a tile
-  const int row = r0 + 32 * rg + (lane & 31), cmax = a.d * (int)sizeof(T) / 16 - 1;
+  const int row = rw + (lane & 31), cmax = a.d * (int)sizeof(T) / 16 - 1;
   const char* kb = a.k + at.b * a.sk.b + at.hk * a.sk.h;
   const char* vb = a.v + at.b * a.sv.b + at.hk * a.sv.h;
   AttnRows<T, DP> w;
   w.clear();
   load_rows(w.q, a.q + at.b * a.sq.b + at.h * a.sq.h + (int64_t)min(row, qlen - 1) * a.sq.l, cmax, lane);
   w.p = off + row;
-  w.w = {off + r0 + 32 * rg, off + min(r0 + 32 * rg + 31, qlen - 1)};
+  w.w = {off + rw, off + min(rw + 31, qlen - 1)};
   const KeyTiles kt(off + r0, off + min(r0 + BM, qlen) - 1, a.window, a.sinks, BN);
   const Stager<T, DP, BN, NW> sk(kb, a.sk.l, klen - 1, cmax, wave, lane), sv(vb, a.sv.l, klen - 1, cmax, wave, lane);
   const AttnAddr<DP> addr(lane);
@@ -745,7 +752,7 @@ __global__ __launch_bounds__(256, (attn_waves<T, DP>())) void attn_fwd_kernel(At
       a.lse[((int64_t)at.b * a.H + at.h) * a.Lq + row] = l == 0.f ? -__builtin_huge_valf() : w.m * LN2 + logf(l);
   }
   for (uint32_t bad = not_finite(w.o) & (uint32_t)__ballot(row < qlen && l == l); bad; bad &= bad - 1) {
-    const int n = __builtin_ctz(bad), r = r0 + 32 * rg + n;
+    const int n = __builtin_ctz(bad), r = rw + n;
     const float f = of_lane(inv, n);
     float x[2];
     slow_o<T>(x, a.q + at.b * a.sq.b + at.h * a.sq.h + r * a.sq.l, kb, a.sk.l, vb, a.sv.l, a, off + r, of_lane(w.m, n),
@@ -932,15 +939,17 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
 template <typename T, int DP, int KS>
 __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dq_kernel(AttnArgs a) {
   using Tile = AttnTile<T, DP>;
-  constexpr int NW = 4, RG = NW / KS, BM = 32 * RG, BN = attn_bn<T, DP>(), TB = BN * Tile::CPR * 16, STEPS = Tile::STEPS, DB = DP / 32;
+  constexpr int NW = 4, RG = NW / KS, BN = attn_bn<T, DP>(), TB = BN * Tile::CPR * 16, STEPS = Tile::STEPS, DB = DP / 32;
   constexpr bool CENTRE = sizeof(T) == 2;
   __shared__ __align__(1024) char lds[4 * TB];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const AttnPlace at(xcd_remap(blockIdx.x, gridDim.x), a);
+  AttnPlace at(xcd_remap(blockIdx.x, gridDim.x), a);
   const int qlen = seq_len(a.q_lens, at.b, a.Lq), klen = seq_len(a.k_lens, at.b, a.Lk);
-  const int r0 = at.tile * BM, off = klen - qlen, n = lane & 31;
-  const int rg = wave % RG, ks = wave / RG;  // rows of the wave; its part of a tile (see the forward)
-  const int row = r0 + 32 * rg + n, cmax = a.d * (int)sizeof(T) / 16 - 1;
+  const int rg = wave % RG, ks = wave / RG;  // head and rows of the wave; its part of a tile
+  const int BM = 32 * RG / a.hg;             // rows of the workgroup
+  at.h += rg % a.hg;
+  const int r0 = at.tile * BM, rw = r0 + 32 * (rg / a.hg), off = klen - qlen, n = lane & 31;
+  const int row = rw + n, cmax = a.d * (int)sizeof(T) / 16 - 1;
   const int64_t stat = ((int64_t)at.b * a.H + at.h) * a.Lq + row;
   f32x16 dq[DB];
 #pragma unroll
@@ -975,7 +984,7 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dq_kerne
 #pragma unroll
     for (auto& x : kbar) x = zero16();
     const int p = off + row;
-    const AttnWave w{off + r0 + 32 * rg, off + min(r0 + 32 * rg + 31, qlen - 1)};
+    const AttnWave w{off + rw, off + min(rw + 31, qlen - 1)};
     const Stager<T, DP, BN, NW> sk(kb, a.sk.l, klen - 1, cmax, wave, lane), sv(vb, a.sv.l, klen - 1, cmax, wave, lane);
     auto arrive = [&](int i, char* other) {
       wait_lgkm0();
@@ -1183,7 +1192,7 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dq_kerne
   char* out = a.dq + at.b * a.sdq.b + at.h * a.sdq.h;
   if (row < a.Lq) store_rows<T, DP>(dq, a.scale, out + (int64_t)row * a.sdq.l, a.d, lane);
   for (uint32_t bad = not_finite(dq) & (uint32_t)__ballot(lse2 == lse2 && delta == delta); bad; bad &= bad - 1) {
-    const int i = __builtin_ctz(bad), r = r0 + 32 * rg + i;
+    const int i = __builtin_ctz(bad), r = rw + i;
     const float ls = of_lane(lse2, i), de = of_lane(delta, i);
     const Lane2<T> q(qb + r * a.sq.l, a.d, lane), g(gb + r * a.sdo.l, a.d, lane);
     float x[2] = {0.f, 0.f};
