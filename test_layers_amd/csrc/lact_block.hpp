@@ -123,19 +123,27 @@ void row_tiles(const lact_attention& p, int rows, AttnArgs& a) {
   a.tiles = (int32_t)ceil_div(p.q_len, rows / a.hg);
 }
 
-// Waves that share the rows (keys) of a tile: two where `tiles` of 128 are no
-// more than the compute units.  fp32 heads wider than 64 have tiles of 32 keys,
-// which do not divide.
-int parts(const lact_attention& p, int64_t tiles) {
-  return tiles <= NCU && !(p.io_dtype == LACT_DTYPE_F32 && p.d > 64) ? 2 : 1;
+// Waves that share the rows (keys) of a tile.  One wave a 32-row group has the
+// pipelined order, two fill the chip where there are few tiles of 128: bf16, as
+// many as compute units (2 x 8 heads x 1024 tokens, d = 64: 52 us with one, 41
+// with two; 16 heads x 4096, 512 tiles: 126 and 133).  Of a padded batch's
+// tiles some are empty; 5/8 are counted (5 texts of up to 1777 tokens, 280 key
+// tiles: 218 and 209 us).  fp32 has no pipelined order to lose (16 heads x 4096:
+// 528 and 471 us), but beyond d = 64 its tiles of 32 keys do not divide.
+int parts(const lact_attention& p, int64_t tiles, bool padded) {
+  if (p.io_dtype == LACT_DTYPE_F32) return p.d <= 64 && tiles <= 4 * NCU ? 2 : 1;
+  return (padded ? tiles * 5 / 8 : tiles) <= NCU ? 2 : 1;
 }
-int parts_q(const lact_attention& p) { return parts(p, (int64_t)p.batch * p.heads * ceil_div(p.q_len, 128)); }
-int parts_k(const lact_attention& p) { return parts(p, (int64_t)p.batch * p.kv_heads * ceil_div(p.k_len, 128)); }
+int parts_q(const lact_attention& p, bool padded) {
+  return parts(p, (int64_t)p.batch * p.heads * ceil_div(p.q_len, 128), padded);
+}
+int parts_k(const lact_attention& p, bool padded) {
+  return parts(p, (int64_t)p.batch * p.kv_heads * ceil_div(p.k_len, 128), padded);
+}
 
 // key tiles of the dk, dv kernel, those of them with sinks, and the splits of
 // the rows behind a sink tile's window
-void sink_plan(const lact_attention& p, AttnArgs& a) {
-  const int64_t BK = 128 / parts_k(p);
+void sink_plan(const lact_attention& p, int64_t BK, AttnArgs& a) {
   a.tiles = (int32_t)ceil_div(p.k_len, BK);
   a.splits = 1;
   a.sink_tiles = 0;
@@ -164,11 +172,14 @@ AttnWs attn_ws(const lact_attention& p) {
 }
 AttnWs attn_back_ws(const lact_attention& p) {
   AttnWs w;
-  AttnArgs a = attn_args(p);
-  sink_plan(p, a);
   w.part = align256((size_t)p.batch * p.heads * p.q_len * 2 * 4);
   w.total = w.part;
-  if (a.splits > 1) w.total += align256((size_t)p.batch * p.kv_heads * a.sink_tiles * a.splits * 2 * (128 / parts_k(p)) * p.d * 4);
+  for (int64_t BK : {64, 128}) {  // the query does not know whether the batch is padded
+    AttnArgs a = attn_args(p);
+    sink_plan(p, BK, a);
+    if (a.splits > 1)
+      w.total = std::max(w.total, w.part + align256((size_t)p.batch * p.kv_heads * a.sink_tiles * a.splits * 2 * BK * p.d * 4));
+  }
   return w;
 }
 
@@ -290,7 +301,7 @@ lact_status lact_window_attention_forward(const lact_attention* p, const void* q
       return LACT_OK;
     });
   }
-  const int ks = parts_q(*p);
+  const int ks = parts_q(*p, q_lens != nullptr);
   row_tiles(*p, 128 / ks, a);
   const int64_t grid = (int64_t)p->batch * (p->heads / a.hg) * a.tiles;
   TRY(check_grid(grid));
@@ -353,9 +364,9 @@ lact_status lact_window_attention_backward(const lact_attention* p, const void* 
   a.lse = const_cast<float*>(lse);
   a.stats = static_cast<float*>(ws);
   a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + w.part);
+  const int ksq = parts_q(*p, q_lens != nullptr), ksk = parts_k(*p, k_lens != nullptr);
   AttnArgs kv = a;
-  sink_plan(*p, kv);
-  const int ksq = parts_q(*p), ksk = parts_k(*p);
+  sink_plan(*p, 128 / ksk, kv);
   row_tiles(*p, 128 / ksq, a);
   const int64_t heads = (int64_t)p->batch * p->kv_heads, gq = (int64_t)p->batch * (p->heads / a.hg) * a.tiles,
                 gk = heads * (kv.tiles + (int64_t)kv.sink_tiles * (kv.splits - 1)),

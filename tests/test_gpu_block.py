@@ -114,6 +114,7 @@ ATTENTION = [
     (6, 26, 26, 72, 270, 270, 50, 130, None, None),
     (2, 64, 64, 64, 515, 515, 129, 64, [515, 300], [515, 400]),
     (40, 8, 4, 128, 130, 130, 1000, 0, None, None),
+    (9, 64, 64, 40, 140, 140, 60, 3, None, None),          # more than 1024: the same in fp32
 ]
 
 
