@@ -51,7 +51,7 @@ struct AttnArgs {
   int32_t d, Lq, Lk;
   int32_t window, sinks;           // window: 1 << 30 where there is none
   int32_t hg;                      // query heads of a workgroup (forward, dq): its waves share their keys
-  int32_t tiles;                   // row tiles (forward, dq), key tiles (dk, dv), per head
+  int32_t tiles;                   // row tiles (forward, dq; few-row forward: of 32), key tiles (dk, dv), per head
   int32_t splits;                  // few-row forward: key splits; backward: row splits of a sink tile
   int32_t sink_tiles, span;        // backward: key tiles with sinks; rows of one of their splits
   float c;                         // scale * log2(e): exp(scale s) = exp2(c s)
@@ -763,7 +763,8 @@ __global__ __launch_bounds__(256, (attn_waves<T, DP>())) void attn_fwd_kernel(At
 }
 
 // ------------------------------------------------------------------ forward, few rows
-// At most 32 rows a key head (its query heads x tokens): the work is reading
+// Few rows a key head, 32 to a workgroup (row r is token r / G's query head r
+// % G, so that a workgroup's rows see the same keys): the work is reading
 // keys, so the keys are split, over workgroups and again over a workgroup's
 // waves.  Each wave runs its own ring of 32-key tiles with no barrier; the
 // waves join in LDS, the workgroups through `part` in attn_join_kernel.
@@ -773,21 +774,22 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(AttnArgs a) {
   constexpr int TB = 32 * Tile::CPR * 16, WB = 4 * TB > 32 * DP * 4 + 256 ? 4 * TB : 32 * DP * 4 + 256;
   __shared__ __align__(1024) char lds[NW * WB];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int split = blockIdx.x % a.splits, bk = blockIdx.x / a.splits;
+  const int split = blockIdx.x % a.splits, tile = blockIdx.x / a.splits % a.tiles, bk = blockIdx.x / a.splits / a.tiles;
   const int hk = bk % a.Hk, b = bk / a.Hk;
   const int qlen = seq_len(a.q_lens, b, a.Lq), klen = seq_len(a.k_lens, b, a.Lk);
-  if (qlen == 0) return;
-  const int off = klen - qlen, rows = a.G * a.Lq, n = lane & 31;
-  const int row = n < rows ? n : 0, tok = row % a.Lq, cmax = a.d * (int)sizeof(T) / 16 - 1;
+  const int t0 = 32 * tile / a.G;  // the first row's token
+  if (t0 >= qlen) return;
+  const int off = klen - qlen, rows = a.G * a.Lq, n = lane & 31, at = 32 * tile + n;
+  const int row = min(at, rows - 1), tok = row / a.G, cmax = a.d * (int)sizeof(T) / 16 - 1;
   const char* kb = a.k + b * a.sk.b + hk * a.sk.h;
   const char* vb = a.v + b * a.sv.b + hk * a.sv.h;
   AttnRows<T, DP> w;
   w.clear();
-  load_rows(w.q, a.q + b * a.sq.b + (int64_t)(hk * a.G + row / a.Lq) * a.sq.h +
+  load_rows(w.q, a.q + b * a.sq.b + (int64_t)(hk * a.G + row % a.G) * a.sq.h +
                             (int64_t)min(tok, qlen - 1) * a.sq.l, cmax, lane);
   w.p = off + min(tok, qlen - 1);
-  w.w = {off, klen - 1};
-  const KeyTiles kt(off, klen - 1, a.window, a.sinks, 32);
+  w.w = {off + t0, off + min((32 * tile + 31) / a.G, qlen - 1)};
+  const KeyTiles kt(w.w.lo, w.w.hi, a.window, a.sinks, 32);
   const int i0 = (int)((int64_t)kt.total * split / a.splits), i1 = (int)((int64_t)kt.total * (split + 1) / a.splits);
   char* ring = lds + wave * WB;
   auto issue = [&](int i, int buf) {
@@ -818,9 +820,9 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(AttnArgs a) {
     for (int r = 0; r < 16; ++r) mine[(32 * db + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) * 32 + n] = w.o[db][r];
   const float lsum = pair_sum(w.l);
   for (uint32_t bad = not_finite(w.o) & (uint32_t)__ballot(lsum == lsum); bad; bad &= bad - 1) {
-    const int i = __builtin_ctz(bad), r = of_lane(row, i), t = min(r % a.Lq, qlen - 1);
+    const int i = __builtin_ctz(bad), r = of_lane(row, i), t = min(r / a.G, qlen - 1);
     float x[2];
-    slow_o<T>(x, a.q + b * a.sq.b + (int64_t)(hk * a.G + r / a.Lq) * a.sq.h + t * a.sq.l, kb, a.sk.l, vb, a.sv.l, a,
+    slow_o<T>(x, a.q + b * a.sq.b + (int64_t)(hk * a.G + r % a.G) * a.sq.h + t * a.sq.l, kb, a.sk.l, vb, a.sv.l, a,
               off + t, of_lane(w.m, i), kt, i0 + wave, i1, NW, 32, lane);
     mine[lane * 32 + i] = x[0];
     if (lane + 64 < DP) mine[(lane + 64) * 32 + i] = x[1];
@@ -841,11 +843,11 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(AttnArgs a) {
     // a wave that met a NaN has a NaN sum whatever its maximum
     l += other(v)[DP * 32 + 32 + n] == 0.f ? 0.f : other(v)[DP * 32 + 32 + n] * (f[v] == 0.f && x == -__builtin_huge_valf() ? 1.f : f[v]);
   }
-  if (n >= rows || tok >= qlen) return;
+  if (at >= rows || tok >= qlen) return;
   constexpr int PER = DP / (2 * NW);  // columns of a thread
   const int c0 = (int)(threadIdx.x >> 5) * PER;
-  float* pr = a.part + (((int64_t)bk * rows + n) * a.splits + split) * a.d;
-  char* orow = a.out + b * a.so.b + (int64_t)(hk * a.G + row / a.Lq) * a.so.h + (int64_t)tok * a.so.l;
+  float* pr = a.part + (((int64_t)bk * rows + at) * a.splits + split) * a.d;
+  char* orow = a.out + b * a.so.b + (int64_t)(hk * a.G + row % a.G) * a.so.h + (int64_t)tok * a.so.l;
   const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
 #pragma unroll
   for (int j = 0; j < PER; j += 4) {
@@ -865,11 +867,11 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(AttnArgs a) {
   }
   if (threadIdx.x < 32) {
     if (a.splits > 1) {
-      float* ml = a.part_ml + (((int64_t)bk * rows + n) * a.splits + split) * 2;
+      float* ml = a.part_ml + (((int64_t)bk * rows + at) * a.splits + split) * 2;
       ml[0] = m;
       ml[1] = l;
     } else if (a.lse) {
-      a.lse[((int64_t)b * a.H + hk * a.G + row / a.Lq) * a.Lq + tok] =
+      a.lse[((int64_t)b * a.H + hk * a.G + row % a.G) * a.Lq + tok] =
           l == 0.f ? -__builtin_huge_valf() : m * LN2 + logf(l);
     }
   }
@@ -883,7 +885,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
   constexpr int PARTS = 256 / DP;  // threads that share a column
   __shared__ float f[256], red[4], out[PARTS][DP];
   const int rows = a.G * a.Lq, n = blockIdx.x % rows, bk = blockIdx.x / rows, t = threadIdx.x;
-  const int hk = bk % a.Hk, b = bk / a.Hk, tok = n % a.Lq, h = hk * a.G + n / a.Lq;
+  const int hk = bk % a.Hk, b = bk / a.Hk, tok = n / a.G, h = hk * a.G + n % a.G;
   if (tok >= seq_len(a.q_lens, b, a.Lq)) return;
   const float* ml = a.part_ml + ((int64_t)bk * rows + n) * a.splits * 2;
   const float* pr = a.part + ((int64_t)bk * rows + n) * a.splits * a.d;

@@ -79,18 +79,39 @@ lact_status validate(const lact_attention* p) {
   return LACT_OK;
 }
 
-// Rows of a key head in the few-row kernel: one 32-row tile.
-bool few_rows(const lact_attention& p) { return p.heads / p.kv_heads * p.q_len <= 32; }
+// keys that the 32 rows of a tile of the few-row kernel can see
+int64_t few_keys(const lact_attention& p) {
+  const int64_t tokens = std::min(p.q_len, ceil_div(31, p.heads / p.kv_heads) + 1);
+  return p.window ? std::min(p.k_len, std::min(p.window, MOST_TOKENS) + tokens - 1 + std::min(p.sinks, p.k_len)) : p.k_len;
+}
+
+// workgroups of the few-row kernel that run at once: their rings take 64 KB
+// of a compute unit's LDS, or 128
+int64_t few_room(const lact_attention& p) { return (p.d * size_of(p.io_dtype) > 128 ? 1 : 2) * NCU; }
+
+// Row tiles of the few-row kernel, 0 where the other kernel takes the problem.
+// A key head's rows in one tile: always.  More of them:
+// - where the keys are long and split at least in two, or a few workgroups
+//   walk along them while the chip waits (8 heads, 512 tokens over 8192 keys:
+//   128 tiles, 81 us in the other kernel and 35 here; 2048 keys: 24 and 20;
+//   1024 keys: 16.3 and 18.0; 256 tiles, unsplit at d = 128: 191 and 205);
+// - where the other kernel's tiles, rows of one head each, would be empty for
+//   the most part (64 heads to a key head, next tokens of a batch of 256, 1024
+//   keys: 255 and 52 us; 8 to a key head, 8 tokens: 170 and 164; 16 tokens,
+//   half the tiles rather than a quarter: 172 and 310).
+int few_tiles(const lact_attention& p) {
+  const int64_t G = p.heads / p.kv_heads, tiles = ceil_div(G * p.q_len, 32);
+  if (tiles <= 1) return 1;
+  const bool split = 2 * tiles * p.batch * p.kv_heads <= few_room(p) && few_keys(p) >= 1536;
+  return split || (4 * tiles <= G * ceil_div(p.q_len, 32) && tiles < 65536) ? (int)tiles : 0;
+}
 
 // Key splits of the few-row kernel: enough workgroups to fill the chip, none
 // with fewer keys than a round of its waves.
 int few_splits(const lact_attention& p) {
-  const int64_t keys = p.window ? std::min(p.k_len, p.window + p.q_len - 1 + std::min(p.sinks, p.k_len)) : p.k_len;
-  const int64_t most = std::max<int64_t>(1, ceil_div(keys, 256));
-  // workgroups that run at once: their rings take 64 KB of a compute unit's LDS, or 128
-  const int64_t room = (p.d * size_of(p.io_dtype) > 128 ? 1 : 2) * NCU;
-  const int64_t want = std::max<int64_t>(1, room / std::max<int64_t>(1, (int64_t)p.batch * p.kv_heads));
-  return (int)std::min<int64_t>(std::min(most, want), 256);
+  const int64_t most = std::max<int64_t>(1, ceil_div(few_keys(p), 256));
+  const int64_t want = few_room(p) / std::max<int64_t>(1, (int64_t)p.batch * p.kv_heads * few_tiles(p));
+  return (int)std::min<int64_t>(std::min(most, std::max<int64_t>(1, want)), 256);
 }
 
 AttnArgs attn_args(const lact_attention& p) {
@@ -162,7 +183,7 @@ struct AttnWs {
 };
 AttnWs attn_ws(const lact_attention& p) {
   AttnWs w;
-  if (!few_rows(p)) return w;
+  if (!few_tiles(p)) return w;
   const int s = few_splits(p);
   if (s == 1) return w;
   const size_t rows = (size_t)p.batch * p.heads * p.q_len;
@@ -279,9 +300,9 @@ lact_status lact_window_attention_forward(const lact_attention* p, const void* q
   a.lse = lse;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const int64_t rows = (int64_t)p->batch * p->heads * p->q_len;
-  if (few_rows(*p)) {
+  if ((a.tiles = few_tiles(*p)) > 0) {
     a.splits = few_splits(*p);
-    const int64_t grid = (int64_t)p->batch * p->kv_heads * a.splits;
+    const int64_t grid = (int64_t)p->batch * p->kv_heads * a.tiles * a.splits;
     TRY(check_grid(std::max(grid, rows)));
     TRY(check_device_again());
     if (a.splits > 1) {

@@ -106,6 +106,13 @@ ATTENTION = [
     (1, 8, 8, 128, 1, 3000, 2048, 4, None, None),          # split keys
     (3, 8, 2, 64, 8, 400, 50, 2, [8, 3, 0], [400, 399, 7]),
     (2, 6, 2, 104, 33, 65, 31, 3, None, None),             # one row more than the few-row kernel takes
+    # several tiles of 32 rows over split keys; many query heads to a key head
+    (1, 2, 2, 64, 100, 1700, 0, 0, None, None),
+    (2, 6, 2, 72, 45, 2100, 1600, 5, [45, 20], [2100, 900]),
+    (3, 4, 2, 128, 40, 1601, 1580, 40, [0, 40, 33], [1601, 30, 1600]),
+    (2, 5, 1, 40, 67, 1900, 1700, 0, [67, 9], [1900, 4]),
+    (3, 72, 2, 64, 1, 200, 77, 3, None, [200, 0, 5]),
+    (1, 40, 1, 128, 7, 90, 50, 2, [6], [90]),
     # more than 256 tiles of 128 rows (keys): a wave for every 32 of them, and
     # tiles that all of a workgroup's rows see whole
     (4, 24, 24, 64, 700, 700, 400, 5, None, None),
