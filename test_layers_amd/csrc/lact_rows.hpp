@@ -183,7 +183,13 @@ struct NormArgs {
   float eps;
 };
 
-// one thread's NV vectors of a row: vector j holds columns (j GS + t) VE ..
+// One thread's NV vectors of a row: vector j holds columns (j GS + t) VE ..
+// Rows that are not vector-aligned take the same 16-byte accesses, which need
+// no more than an element's alignment, and single ones in a row's last vector
+// (16384 rows of 2047 bf16: 169 us with single ones throughout, 70 so).  The
+// weight is read the same way: loaded value by value it took longer than the
+// few rows that a workgroup has (the same rows: 70 and 49 us; 8192 of 1000,
+// aligned: 21 and 12).
 template <typename T, int NV, int GS, bool VEC>
 struct NormRow {
   static constexpr int VE = io_traits<T>::VE;
@@ -195,9 +201,16 @@ struct NormRow {
       const T* p = reinterpret_cast<const T*>(row) + c;
 #pragma unroll
       for (int e = 0; e < VE; ++e) v[j][e] = 0.f;
-      if constexpr (VEC) {
-        if (c < cols) load_n<T, VE>(p, v[j]);
-      } else {
+      if (VEC ? c < cols : c + VE <= cols) {
+        if constexpr (VEC) {
+          load_n<T, VE>(p, v[j]);
+        } else {
+          uint4 u;
+          __builtin_memcpy(&u, p, 16);
+#pragma unroll
+          for (int e = 0; e < VE; ++e) v[j][e] = value(u, e);
+        }
+      } else if constexpr (!VEC) {
 #pragma unroll
         for (int e = 0; e < VE; ++e)
           if (c + e < cols) {
@@ -215,9 +228,10 @@ struct NormRow {
       const int c = col(j, t);
       const T* p = reinterpret_cast<const T*>(row) + c;
       v[j] = zero4();
-      if constexpr (VEC) {
-        if (c < cols) v[j] = *reinterpret_cast<const uint4*>(p);
-      } else {
+      if (VEC ? c < cols : c + VE <= cols) {
+        if constexpr (VEC) v[j] = *reinterpret_cast<const uint4*>(p);
+        else __builtin_memcpy(&v[j], p, 16);
+      } else if constexpr (!VEC) {
         uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int e = 0; e < VE; ++e)
@@ -240,9 +254,19 @@ struct NormRow {
     for (int j = 0; j < NV; ++j) {
       const int c = col(j, t);
       T* p = reinterpret_cast<T*>(row) + c;
-      if constexpr (VEC) {
-        if (c < cols) store_n<T, VE>(p, v[j]);
-      } else {
+      if (VEC ? c < cols : c + VE <= cols) {
+        if constexpr (VEC) {
+          store_n<T, VE>(p, v[j]);
+        } else {
+          T u[VE];
+#pragma unroll
+          for (int e = 0; e < VE; ++e) {
+            const float x[1] = {v[j][e]};
+            store_n<T, 1>(u + e, x);
+          }
+          __builtin_memcpy(p, u, 16);
+        }
+      } else if constexpr (!VEC) {
 #pragma unroll
         for (int e = 0; e < VE; ++e)
           if (c + e < cols) {
@@ -254,9 +278,15 @@ struct NormRow {
   }
   __device__ static __forceinline__ void weights(const float* w, int cols, int t, float (&v)[NV][VE]) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+    for (int j = 0; j < NV; ++j) {
+      const int c = col(j, t);
+      if (c + VE <= cols) {
+        __builtin_memcpy(v[j], w + c, VE * 4);
+      } else {
 #pragma unroll
-      for (int e = 0; e < VE; ++e) v[j][e] = col(j, t) + e < cols ? w[col(j, t) + e] : 0.f;
+        for (int e = 0; e < VE; ++e) v[j][e] = !VEC && c + e < cols ? w[c + e] : 0.f;
+      }
+    }
   }
 };
 
@@ -341,6 +371,8 @@ __global__ __launch_bounds__(GS < 256 ? 256 : GS) void norm_kernel(NormArgs a) {
         if constexpr (VEC) {
           if constexpr (VE == 8) *reinterpret_cast<uint2*>(to) = make_uint2(q[0], q[1]);
           else *reinterpret_cast<uint32_t*>(to) = q[0];
+        } else if (c + VE <= a.cols) {
+          __builtin_memcpy(to, q, VE);
         } else {
 #pragma unroll
           for (int e = 0; e < VE; ++e)
