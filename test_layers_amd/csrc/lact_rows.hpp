@@ -75,6 +75,11 @@ constexpr int ROT_TABLE = 2048;  // pairs of one workgroup's table
 // angles of its tokens, in fp64 turns: a far position times a frequency needs
 // all of a double's bits before whole turns are dropped.  All heads of q and
 // k then use the table.
+//
+// Bound by memory: 32768 tokens of 32 + 8 heads of 128, bf16: 131 us, 5.1 TB/s
+// of the 671 MB read and written; the table is 1 / 40 of the work.  Short
+// calls are bound by the table: two dependent trips to memory around fp64
+// sines, 3.4 us for the next tokens of 64 sequences.
 template <typename T, int VE, bool INTERLEAVED>
 __global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a) {
   __shared__ float cs[ROT_TABLE], sn[ROT_TABLE];
@@ -314,6 +319,9 @@ __device__ __forceinline__ float2 row_sum2(float a, float b, float2* lds, int t)
 // workgroup's rows.  The 8-bit output: a 128-column group is 16 (bf16) or 32
 // (fp32) neighbouring lanes, so its largest magnitude costs a few lane
 // exchanges; y is divided by it before it is rounded, once.
+//
+// Bound by memory: 32768 rows of 4096 bf16 with a residual to h and 8 bits:
+// 181 us, 5.2 TB/s of 943 MB; of 1536 to h and y: 72 us, 5.6 TB/s.
 template <typename T, int NV, int GS, bool VEC, bool QUANT>
 __global__ __launch_bounds__(GS < 256 ? 256 : GS) void norm_kernel(NormArgs a) {
   using R = NormRow<T, NV, GS, VEC>;
@@ -388,6 +396,8 @@ __global__ __launch_bounds__(GS < 256 ? 256 : GS) void norm_kernel(NormArgs a) {
 // A workgroup takes NT / GS rows at a time, gridDim of them apart, and keeps
 // its dw in registers; its threads of a column add up in LDS, and the
 // workgroups' partial sums are added in a fixed order by norm_dw_kernel.
+// Bound by memory: 32768 rows of 1536 bf16: 77 us, 5.2 TB/s of 403 MB, and
+// 4.5 us for the partial sums.
 template <typename T, int NV, int GS, bool VEC>
 __global__ __launch_bounds__(GS < 512 ? 512 : GS) void norm_back_kernel(NormArgs a) {
   using R = NormRow<T, NV, GS, VEC>;
