@@ -439,7 +439,8 @@ typedef struct {
  * (NULL: none) [rows, cols], each with its row stride in elements (>= cols;
  * inputs also 0: one row for all), aligned to their elements; weight [cols]
  * float32; scales [rows, ceil(cols / 128)] float32, with y8.  h and y may be
- * x or residual themselves (same row stride), not partly overlap them.
+ * x or residual themselves (same row stride), not partly overlap them; y8 and
+ * scales overlap nothing.
  */
 lact_status lact_add_rmsnorm_forward(const lact_norm_problem* p, const void* x, int64_t ldx, const void* residual,
                                      int64_t ldr, const float* weight, void* h, int64_t ldh, void* y,

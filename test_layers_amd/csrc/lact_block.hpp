@@ -643,6 +643,8 @@ lact_status lact_add_rmsnorm_forward(const lact_norm_problem* p, const void* x, 
     TRY(check_in_place("y", y, ldy, residual, ldr));
   }
   if (y && y == h) return fail(LACT_ERR_INVALID_ARG, "y is h");
+  TRY(check_apart({h, y, y8, scales}, {weight}));
+  TRY(check_apart({y8, scales}, {x, residual}));
   TRY(check_device_again());
   a.x = static_cast<const char*>(x);
   a.res = static_cast<const char*>(residual);
@@ -704,6 +706,10 @@ lact_status lact_add_rmsnorm_backward(const lact_norm_problem* p, const void* h,
   if (dw) {
     NEED(dw, 4);
     if (grid > 1) TRY(check_ws(ws, ws_bytes, align256((size_t)grid * p->cols * 4)));
+  }
+  if (p->rows > 0) {
+    TRY(check_apart({dx, dw}, {weight}));
+    TRY(check_apart({dw}, {h, dy, dh}));
   }
   TRY(check_device_again());
   a.x = static_cast<const char*>(h);

@@ -321,7 +321,7 @@ __device__ __forceinline__ float2 row_sum2(float a, float b, float2* lds, int t)
 // exchanges; y is divided by it before it is rounded, once.
 //
 // Bound by memory: 32768 rows of 4096 bf16 with a residual to h and 8 bits:
-// 181 us, 5.2 TB/s of 943 MB; of 1536 to h and y: 72 us, 5.6 TB/s.
+// 181 us, 5.2 TB/s of 943 MB; of 1536 to h and y: 64 us, 6.3 TB/s.
 template <typename T, int NV, int GS, bool VEC, bool QUANT>
 __global__ __launch_bounds__(GS < 256 ? 256 : GS) void norm_kernel(NormArgs a) {
   using R = NormRow<T, NV, GS, VEC>;
@@ -396,7 +396,7 @@ __global__ __launch_bounds__(GS < 256 ? 256 : GS) void norm_kernel(NormArgs a) {
 // A workgroup takes NT / GS rows at a time, gridDim of them apart, and keeps
 // its dw in registers; its threads of a column add up in LDS, and the
 // workgroups' partial sums are added in a fixed order by norm_dw_kernel.
-// Bound by memory: 32768 rows of 1536 bf16: 77 us, 5.2 TB/s of 403 MB, and
+// Bound by memory: 32768 rows of 1536 bf16: 82 us, 4.9 TB/s of 403 MB, and
 // 4.5 us for the partial sums.
 template <typename T, int NV, int GS, bool VEC>
 __global__ __launch_bounds__(GS < 512 ? 512 : GS) void norm_back_kernel(NormArgs a) {

@@ -297,6 +297,21 @@ def test_norm_refuses_bad_tensors():
     assert back(ws=None) == I and back(dw=FAKE + 1) == I and back(dx=(FAKE, 300)) == I
 
 
+def test_norm_outputs_that_are_inputs_are_refused():
+    I = lact.ERR_INVALID_ARG
+    five = FAKE * 5
+    for kw in (dict(x=(five, 256)), dict(r=(five, 256)), dict(h=(five, 256)), dict(y=(five, 256)), dict(w=five)):
+        assert _norm(_np(), y8=(five, 256), scales=FAKE * 6, **kw) == I, kw
+        assert _norm(_np(), y8=(FAKE * 6, 256), scales=five, **kw) == I, kw
+    assert _norm(_np(), y8=(five, 256), scales=five) == I
+    assert _norm(_np(), w=FAKE * 2) == I and _norm(_np(), w=FAKE * 3) == I
+    p = _np(rows=800)
+    back = lambda dx, dw: lact.lib().lact_add_rmsnorm_backward(
+        ctypes.byref(p), FAKE * 2, 256, FAKE * 3, FAKE * 4, 256, FAKE * 5, 256, dx, 256, dw, FAKE * 6, 1 << 40, None)
+    assert back(FAKE * 3, FAKE) == I and back(FAKE, FAKE) == I
+    assert all(back(FAKE, FAKE * n) == I for n in (2, 3, 4, 5))
+
+
 # ------------------------------------------------------------------ refusals of the binding
 def test_binding_refuses_host_tensors_and_shapes():
     q = torch.zeros(1, 2, 4, 64)

@@ -265,6 +265,46 @@ def test_a_non_finite_token_reaches_only_rows_that_see_it(lact, t, L, d, bad):
 
 
 @pytest.mark.parametrize("t", ["bf16", "fp32"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_non_finite_token_among_split_keys(lact, t, d):
+    """As above where several tiles of 32 rows share the work on long keys."""
+    dt = DT[t]
+    gen = torch.Generator("cuda").manual_seed(8)
+    L, Lk = 70, 2000
+    q, k, v = randn(gen, (1, 2, L, d), dt), randn(gen, (1, 1, Lk, d), dt), randn(gen, (1, 1, Lk, d), dt)
+    kw = dict(window=1600, sinks=2)
+    ref = OB.window_attention(f64(q), f64(k), f64(v), 1600, 2, d ** -0.5)
+    see = OB.visible(L, Lk, 1600, 2)
+    for j in (0, 5, Lk - L - 1600, Lk - 1630, Lk - L, Lk - 33, Lk - 1):
+        for bad in (float("nan"), float("inf")):
+            v2, k2 = v.clone(), k.clone()
+            v2[0, 0, j, 3] = bad
+            s = see[:, j]
+            o = lact.window_attention(q, k, v2, **kw)
+            k2[0, 0, j] = float("nan")
+            o2 = lact.window_attention(q, k2, v2, **kw)
+            for x in (o, o2):
+                part = {n: ref[n][:, :, ~s] for n in ("o", "o_abs")}
+                part["score_abs"] = ref["score_abs"]
+                check_attention(part, {"o": x[:, :, torch.from_numpy(~s).cuda()]}, dt, d, Lk, False)
+            assert torch.isfinite(o[..., [c for c in range(d) if c != 3]]).all()
+            assert not torch.isfinite(o[:, :, torch.from_numpy(s).cuda(), 3]).any()
+
+
+def test_no_rows_and_no_keys(lact):
+    """Gradients over nothing are zeros, and nothing is written elsewhere."""
+    for lq, lk in ((0, 50), (50, 0), (0, 0)):
+        q, k = torch.randn(2, 4, lq, 64, device="cuda"), torch.randn(2, 2, lk, 64, device="cuda")
+        o, lse = lact.window_attention(q, k, k, window=9, sinks=1, return_lse=True)
+        assert o.shape == q.shape and (o == 0).all() and (lse == -float("inf")).all()
+        g = lact.window_attention_backward(q, k, k, o, lse, dO=torch.randn_like(q), window=9, sinks=1)
+        assert all((x == 0).all() for x in g.values()) and g["dk"].shape == k.shape and g["dq"].shape == q.shape
+    e = torch.empty(0, 4, 10, 64, device="cuda")
+    o, lse = lact.window_attention(e, e, e, return_lse=True)
+    assert o.shape == e.shape and lact.window_attention_backward(e, e, e, o, lse, dO=e)["dq"].shape == e.shape
+
+
+@pytest.mark.parametrize("t", ["bf16", "fp32"])
 @pytest.mark.parametrize("batch", [1, 80])
 def test_non_finite_gradients_stay_with_what_they_reach(lact, t, batch):
     dt = DT[t]
