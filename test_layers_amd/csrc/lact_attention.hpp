@@ -1320,20 +1320,6 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dkv_kern
       }
       return x;
     };
-    // products of a row tile, from the rows' statistics (bf16) or with them
-    // added last (fp32, see the dq kernel)
-    auto gradients = [&](f32x16& s, f32x16& ds, const f32x16& less_s, const f32x16& less_ds) {
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        if constexpr (sizeof(T) == 4) {
-          s[r] = __builtin_amdgcn_exp2f(LOG2E * fmaf(s[r], a.scale, less_s[r]));
-          ds[r] = (ds[r] + less_ds[r]) * s[r];
-        } else {
-          s[r] = __builtin_amdgcn_exp2f(s[r] * a.c);
-          ds[r] *= s[r];
-        }
-      }
-    };
     issue(0, ra, lds, stats[0][0]);
     int i = 0;  // tiles done: the ring's place
 #pragma unroll 1
@@ -1432,6 +1418,76 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dkv_kern
         }
 #pragma unroll 1
         for (; rt < rend; ++rt, ++i) edge(h, rt, i & 1);
+      } else if constexpr (sizeof(T) == 2) {
+        // the wave's 32 rows of a tile in four runs of products, S, dP, dv and
+        // dk, with P formed between those of dP and dS between those of dv (5
+        // texts of up to 1777 tokens, 12 (4) heads of 96: 100 us one after
+        // another, 85 so)
+        const AttnAddr<DP> addr(lane);
+        auto edge = [&](int h, int rt, int ring) {
+          constexpr int NM = STEPS, E = 16 / NM;
+          arrive(h, rt, lds + (2 - 2 * ring) * TB, stats[1 - ring][0]);
+          const int q0 = off + rt * BQ + 32 * ks, u0 = max(q0, p_lo), u1 = min(q0 + 31, p_hi);
+          if (u0 > u1 || wk0 > wk1 || u1 < wk0 || (wk1 <= u0 - a.window && wk0 >= a.sinks)) return;
+          const int base = q0 + 4 * (lane >> 5), lo = max(u0, key) - base,
+                    hi = (key < a.sinks ? u1 : min(u1, key + a.window - 1)) - base;
+          const lds_ptr qp = (lds_ptr)lds + ring * 2 * TB + 32 * ks * AttnAddr<DP>::ROW, gp = qp + TB;
+          const float* st = stats[ring][0] + 32 * ks;
+          auto frag = [&](int m) {
+            const int run = m / NM, i = m % NM;
+            return run < 2 ? addr.rows(run ? gp : qp, 0, i) : addr.cols(run == 2 ? gp : qp, 16 * (i / DB), i % DB);
+          };
+          bf16x8 f[AHEAD];
+          auto next = [&](int m) {
+            if (m + AHEAD < 4 * NM) f[m % AHEAD] = frag(m + AHEAD);
+          };
+          Half x;
+          x.s = start(st, 0), x.ds = start(st + 64, 0);
+#pragma unroll
+          for (int m = 0; m < AHEAD; ++m) f[m] = frag(m);
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int i = 0; i < NM; ++i) {
+            x.s = mma32(f[i % AHEAD], kf[i], x.s);
+            next(i);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+          auto sees = [&](int r) {
+            const int o = 8 * (r >> 2) + (r & 3);
+            return (o >= lo) & (o <= hi);
+          };
+#pragma unroll
+          for (int i = 0; i < NM; ++i) {
+            x.ds = mma32(f[(NM + i) % AHEAD], vf[i], x.ds);
+            next(NM + i);
+#pragma unroll
+            for (int r = i * E; r < i * E + E; ++r) {
+              const float e = __builtin_amdgcn_exp2f(x.s[r] * a.c);
+              x.s[r] = sees(r) ? e : 0.f;
+              if (r & 1) x.y[r / 2] = pack_bf16x2(x.s[r - 1], x.s[r]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+          }
+#pragma unroll
+          for (int i = 0; i < NM; ++i) {
+            dv[i % DB] = mma32(f[(2 * NM + i) % AHEAD], x.frag_s(i / DB), dv[i % DB]);
+            next(2 * NM + i);
+#pragma unroll
+            for (int r = i * E; r < i * E + E; ++r) {
+              x.ds[r] = sees(r) ? x.ds[r] * x.s[r] : 0.f;
+              if (r & 1) x.x[r / 2] = pack_bf16x2(x.ds[r - 1], x.ds[r]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+          }
+#pragma unroll
+          for (int i = 0; i < NM; ++i) {
+            dk[i % DB] = mma32(f[(3 * NM + i) % AHEAD], x.frag_ds(i / DB), dk[i % DB]);
+            next(3 * NM + i);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        };
+#pragma unroll 1
+        for (; rt < rend; ++rt, ++i) edge(h, rt, i & 1);
       } else {
         // a tile of which rows may see a part, 32 rows after another
         auto edge = [&](int h, int rt, int ring) {
@@ -1445,13 +1501,17 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dkv_kern
             const bool whole = u0 == q0 && u1 == q1 && wk1 <= q0 && wk0 + 31 == wk1 &&
                                (wk0 > q1 - a.window || wk1 < a.sinks);
             const f32x16 less_s = start(stats[ring][0], sb), less_ds = start(stats[ring][1], sb);
-            f32x16 s = sizeof(T) == 4 ? zero16() : less_s, ds = sizeof(T) == 4 ? zero16() : less_ds;
+            f32x16 s = zero16(), ds = zero16();
 #pragma unroll
             for (int st = 0; st < STEPS; ++st) {
               s = mma32(row_frag<T, DP>(t, sb, st, lane), kf[st], s);
               ds = mma32(row_frag<T, DP>(t + TB, sb, st, lane), vf[st], ds);
             }
-            gradients(s, ds, less_s, less_ds);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {  // fp32: the statistics are added last, see the dq kernel
+              s[r] = __builtin_amdgcn_exp2f(LOG2E * fmaf(s[r], a.scale, less_s[r]));
+              ds[r] = (ds[r] + less_ds[r]) * s[r];
+            }
             if (!whole) {
               // a row's position p = q0 + 4 (lane / 32) + o, against the key's own bounds
               const int base = q0 + 4 * (lane >> 5), lo = max(u0, key) - base,

@@ -149,7 +149,7 @@ void row_tiles(const lact_attention& p, int rows, AttnArgs& a) {
 // many as compute units (2 x 8 heads x 1024 tokens, d = 64: 52 us with one, 41
 // with two; 16 heads x 4096, 512 tiles: 126 and 133).  Of a padded batch's
 // tiles some are empty; 5/8 are counted (5 texts of up to 1777 tokens, 280 key
-// tiles: 218 and 209 us).  fp32 has no pipelined order to lose (16 heads x 4096:
+// tiles: 218 and 192 us).  fp32 has no pipelined order to lose (16 heads x 4096:
 // 528 and 471 us), but beyond d = 64 its tiles of 32 keys do not divide.
 int parts(const lact_attention& p, int64_t tiles, bool padded) {
   if (p.io_dtype == LACT_DTYPE_F32) return p.d <= 64 && tiles <= 4 * NCU ? 2 : 1;
