@@ -1538,6 +1538,10 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dkv_kern
     add_parts<RG, DB>(reinterpret_cast<float*>(lds), rg, ks, lane, dv);
     if (ks != 0) return;
   }
+  if (key >= klen) {  // masked to zeros, but zero times a NaN of a row that others see is none
+#pragma unroll
+    for (int db = 0; db < DB; ++db) dk[db] = dv[db] = zero16();
+  }
   const bool parts = tile < a.sink_tiles && a.splits > 1;
   // [batch x key head][sink tile][split][dk, dv][key][d]
   float* pk = a.part + (((int64_t)bk * a.sink_tiles + tile) * a.splits + split) * 2 * BK * a.d;

@@ -1,0 +1,50 @@
+"""The block's operators on the GPU where an input, a length or a caller is
+unusual: values that are not finite or near the type's largest beside lengths,
+parameters that a caller changes in place, views that grow from call to call.
+Tolerances as in test_gpu_block."""
+import numpy as np
+import pytest
+
+from oracle import lact_block as OB
+from test_gpu_block import DT, randn
+
+torch = pytest.importorskip("torch")
+pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a GPU")]
+
+
+@pytest.fixture(scope="module")
+def lact():
+    from test_layers_amd import lact as L
+    return L
+
+
+@pytest.mark.parametrize("t", ["bf16", "fp32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("batch", [1, 400])
+@pytest.mark.parametrize("n,sinks", [(237, 0), (237, 3), (20, 3)])
+def test_gradients_behind_the_lengths_are_zero(lact, t, d, batch, n, sinks):
+    """A NaN in a live row of dO or q, and a length that ends inside a group of
+    32 keys: the keys behind it take part in the products as masked places,
+    and their gradients are zeros all the same.  Once with two waves a tile,
+    once (stride 0 over a batch) with one; in a sink tile too."""
+    gen = torch.Generator("cuda").manual_seed(20)
+    L, dt = 300, DT[t]
+    one = [randn(gen, (1, 1, L, d), dt) for _ in range(4)]
+    lens = torch.full((batch,), n, dtype=torch.int64, device="cuda")
+    kw = dict(window=40, sinks=sinks, q_lens=lens, k_lens=lens)
+    rep = lambda x: x.expand((batch,) + x.shape[1:])
+    q, k, v, g = (rep(x) for x in one)
+    o, lse = lact.window_attention(q, k, v, return_lse=True, **kw)
+    see = OB.visible(n, n, 40, sinks)
+    for row in (n - 1, n - 7):
+        for spoilt in ("q", "dO"):
+            q2, g2 = one[0].clone(), one[3].clone()
+            (q2 if spoilt == "q" else g2)[0, 0, row, 5] = float("nan")
+            out = lact.window_attention_backward(rep(q2), k, v, o, lse, dO=rep(g2), **kw)
+            unseen = torch.from_numpy(~see[row]).cuda()
+            for name in ("dk", "dv"):
+                x = out[name]
+                assert (x[:, :, n:] == 0).all(), (name, row, spoilt)
+                assert torch.isfinite(x[:, :, :n][:, :, unseen]).all(), (name, row, spoilt)
+                assert (x[0] == x[-1]).logical_or(x[0].isnan()).all()
+            assert (out["dq"][:, :, n:] == 0).all()
