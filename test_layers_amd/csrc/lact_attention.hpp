@@ -429,12 +429,21 @@ __device__ __forceinline__ uint32_t not_finite(const f32x16 (&a)[DB]) {
   return (uint32_t)(b | (b >> 32));
 }
 
+// log2 of the sum l relative to m; where nothing was seen every weight is zero
+__device__ __forceinline__ float log2_sum(float m, float l) {
+  return l == 0.f ? __builtin_huge_valf() : m + log2f(l);
+}
+
 // a sum that is NaN in every column stays so
 __device__ __forceinline__ bool settled(const float (&x)[2], int d, int lane) {
   return __all((lane >= d || x[0] != x[0]) && (lane + 64 >= d || x[1] != x[1]));
 }
 
-// sum of exp2(c q.k - m) v over the visible keys of tiles i0, i0 + di .. < i1
+// sum of exp2(c q.k - m) v over the visible keys of tiles i0, i0 + di .. < i1.
+// m is log2 of the row's whole sum, so that the weights add up to one and no
+// value of the type's range leaves fp32 on the way: relative to the lagging
+// maximum of the products (see AttnRows::follow) a sum of values from 2^104 on
+// may have, which is one way to come here.
 template <typename T>
 __device__ __forceinline__ void slow_o(float (&x)[2], const char* q, const char* kb, int64_t kl, const char* vb,
                                        int64_t vl, const AttnArgs& a, int p, float m, const KeyTiles& kt, int i0,
@@ -765,11 +774,9 @@ __global__ __launch_bounds__(256, (attn_waves<T, DP>())) void attn_fwd_kernel(At
   }
   for (uint32_t bad = not_finite(w.o) & (uint32_t)__ballot(row < qlen && l == l); bad; bad &= bad - 1) {
     const int n = __builtin_ctz(bad), r = rw + n;
-    const float f = of_lane(inv, n);
     float x[2];
-    slow_o<T>(x, a.q + at.b * a.sq.b + at.h * a.sq.h + r * a.sq.l, kb, a.sk.l, vb, a.sv.l, a, off + r, of_lane(w.m, n),
-              kt, 0, kt.total, 1, BN, lane);
-    x[0] *= f, x[1] *= f;
+    slow_o<T>(x, a.q + at.b * a.sq.b + at.h * a.sq.h + r * a.sq.l, kb, a.sk.l, vb, a.sv.l, a, off + r,
+              of_lane(log2_sum(w.m, l), n), kt, 0, kt.total, 1, BN, lane);
     store_lane2<T>(out + r * a.so.l, x, a.d, lane);
   }
 }
@@ -833,12 +840,17 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(AttnArgs a) {
   for (int db = 0; db < DP / 32; ++db)
 #pragma unroll
     for (int r = 0; r < 16; ++r) mine[(32 * db + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) * 32 + n] = w.o[db][r];
-  const float lsum = pair_sum(w.l);
-  for (uint32_t bad = not_finite(w.o) & (uint32_t)__ballot(lsum == lsum); bad; bad &= bad - 1) {
+  float lsum = pair_sum(w.l);
+  uint32_t bad = not_finite(w.o) & (uint32_t)__ballot(lsum == lsum);
+  if (((bad >> n) & 1) && lsum > 0.f) {  // such a row's part is summed again with weights that add up to one
+    w.m = log2_sum(w.m, lsum);
+    lsum = 1.f;
+  }
+  for (; bad; bad &= bad - 1) {
     const int i = __builtin_ctz(bad), r = of_lane(row, i), t = min(r / a.G, qlen - 1);
     float x[2];
     slow_o<T>(x, a.q + b * a.sq.b + (int64_t)(hk * a.G + r % a.G) * a.sq.h + t * a.sq.l, kb, a.sk.l, vb, a.sv.l, a,
-              off + t, of_lane(w.m, i), kt, i0 + wave, i1, NW, 32, lane);
+              off + t, of_lane(lsum == 0.f ? __builtin_huge_valf() : w.m, i), kt, i0 + wave, i1, NW, 32, lane);
     mine[lane * 32 + i] = x[0];
     if (lane + 64 < DP) mine[(lane + 64) * 32 + i] = x[1];
   }
@@ -863,22 +875,23 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(AttnArgs a) {
   const int c0 = (int)(threadIdx.x >> 5) * PER;
   float* pr = a.part + (((int64_t)bk * rows + at) * a.splits + split) * a.d;
   char* orow = a.out + b * a.so.b + (int64_t)(hk * a.G + row % a.G) * a.so.h + (int64_t)tok * a.so.l;
+  // The waves' parts are divided by the sum before they are added, and a split
+  // leaves its part so: no larger than the largest value.
   const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+#pragma unroll
+  for (int v = 0; v < NW; ++v) f[v] *= inv;
 #pragma unroll
   for (int j = 0; j < PER; j += 4) {
     if (c0 + j >= a.d) break;
-    float x[4] = {0.f, 0.f, 0.f, 0.f};
+    float x[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
+    for (int e = 0; e < 4; ++e) {
+      x[e] = l == l ? 0.f : l;
 #pragma unroll
       for (int v = 0; v < NW; ++v) x[e] += f[v] == 0.f ? 0.f : f[v] * other(v)[(c0 + j + e) * 32 + n];
-    if (a.splits > 1) {
-      store4(pr + c0 + j, x);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] *= inv;
-      store_row4<T>(orow, c0 + j, x);
     }
+    if (a.splits > 1) store4(pr + c0 + j, x);
+    else store_row4<T>(orow, c0 + j, x);
   }
   if (threadIdx.x < 32) {
     if (a.splits > 1) {
@@ -892,7 +905,8 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(AttnArgs a) {
   }
 }
 
-// One workgroup a row: the splits' sums, rescaled to their common maximum.
+// One workgroup a row: the splits' results, weighted by their sums relative to
+// the common maximum.
 // All loads of a thread are independent: the kernel is as long as two trips
 // to memory.
 template <typename T, int DP>
@@ -913,9 +927,9 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
   __syncthreads();
   m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
   // a split without keys counts for nothing; one whose scores are all NaN has no maximum but a sum
-  const float w = ls == 0.f ? 0.f : ms == NONE ? 1.f : __builtin_amdgcn_exp2f(ms - m);
+  const float w = ls == 0.f ? 0.f : ms == NONE ? ls : ls * __builtin_amdgcn_exp2f(ms - m);
   f[t] = w;
-  const float s = wave_sum(ls == 0.f ? 0.f : ls * w);
+  const float s = wave_sum(w);
   __syncthreads();
   if (t % WAVE == 0) red[t / WAVE] = s;
   __syncthreads();
@@ -926,14 +940,14 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
 #pragma unroll 8
     for (int i = part; i < a.splits; i += PARTS) {
       const float v = pr[(int64_t)i * a.d + c];
-      x += f[i] == 0.f ? 0.f : f[i] * v;
+      x += f[i] == 0.f ? 0.f : f[i] * inv * v;
     }
   out[part][c] = x;
   __syncthreads();
   if (part == 0 && c < a.d) {
 #pragma unroll
     for (int i = 1; i < PARTS; ++i) x += out[i][c];
-    io_traits<T>::store(reinterpret_cast<T*>(a.out + b * a.so.b + (int64_t)h * a.so.h + (int64_t)tok * a.so.l) + c, x * inv);
+    io_traits<T>::store(reinterpret_cast<T*>(a.out + b * a.so.b + (int64_t)h * a.so.h + (int64_t)tok * a.so.l) + c, x);
   }
   if (a.lse && t == 0) a.lse[((int64_t)b * a.H + h) * a.Lq + tok] = l == 0.f ? NONE : m * LN2 + logf(l);
 }

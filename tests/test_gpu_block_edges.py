@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 
 from oracle import lact_block as OB
-from test_gpu_block import DT, randn
+from test_gpu_block import DT, check_attention, f64, randn
 
 torch = pytest.importorskip("torch")
 pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a GPU")]
@@ -48,3 +48,23 @@ def test_gradients_behind_the_lengths_are_zero(lact, t, d, batch, n, sinks):
                 assert torch.isfinite(x[:, :, :n][:, :, unseen]).all(), (name, row, spoilt)
                 assert (x[0] == x[-1]).logical_or(x[0].isnan()).all()
             assert (out["dq"][:, :, n:] == 0).all()
+
+
+@pytest.mark.parametrize("t", ["bf16", "fp32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,Lq,Lk", [(1, 150, 150), (200, 150, 150), (1, 3, 300), (1, 3, 4000), (300, 2, 300)])
+@pytest.mark.parametrize("size", [2.0 ** 104, 2.0 ** 125, 2.0 ** 127])
+def test_values_near_the_types_largest(lact, t, d, B, Lq, Lk, size):
+    """An average of values is no larger than the largest of them, also where
+    scores climb along the keys, so that sums are held relative to an earlier,
+    smaller maximum (by up to 2^24), and several parts are joined."""
+    dt = DT[t]
+    gen = torch.Generator("cuda").manual_seed(21)
+    q, k, v = (randn(gen, (1, 1, n, d), dt) for n in (Lq, Lk, Lk))
+    q[..., 0] = 8.0
+    k[..., 0] = (torch.arange(Lk, device="cuda") / Lk * 1.7).to(dt)   # times 8: 2^19.6 in the exponential
+    v = (torch.sign(v) * (1 + v.abs().clamp(max=3) / 4) * size).to(dt)   # up to 1.75 times the size
+    rep = lambda x: x.expand((B,) + x.shape[1:])
+    o = lact.window_attention(rep(q), rep(k), rep(v), scale=1.0)
+    ref = OB.window_attention(f64(q), f64(k), f64(v), 0, 0, 1.0)
+    check_attention(ref, {"o": o[-1:]}, dt, d, Lk, False)
