@@ -8,6 +8,7 @@ missing the import fails loudly -- there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 from typing import Optional, Sequence
 
@@ -512,6 +513,15 @@ def _plan(key, build):
     return plan
 
 
+def _int(x, name):
+    """A whole number given as any integer type (a tensor of one included):
+    its value now, which is what a plan's key has to hold."""
+    try:
+        return operator.index(x)
+    except TypeError:
+        raise ValueError(f"{name} must be a whole number, got {x!r}") from None
+
+
 def _one_device(*tensors):
     """The CUDA device that all given tensors share."""
     dev = tensors[0].device
@@ -673,6 +683,7 @@ def window_attention(q, k, v, o=None, *, window: int = 0, sinks: int = 0, scale:
     each sequence's own lengths; scale defaults to d^-1/2.  Returns o in q's
     layout, and with return_lse also lse [batch, heads, q_len] fp32; what is
     allocated here has zeros behind q_lens, given tensors keep what they held."""
+    window, sinks, scale = _int(window, "window"), _int(sinks, "sinks"), None if scale is None else float(scale)
     plan = _plan(("attention", window, sinks, scale, _meta(q), _meta(k), _meta(v), _meta(q_lens), _meta(k_lens)),
                  lambda: _attention_plan(q, k, v, window, sinks, scale, q_lens, k_lens, False))
     so = plan.rq
@@ -709,6 +720,7 @@ def window_attention_backward(q, k, v, o, lse, *, dO, window: int = 0, sinks: in
     as the forward returned them, dO [batch, heads, q_len, d] in q's dtype.
     Returns a dict of dq, dk, dv in the inputs' dtype and layout, zero behind
     the lengths; `out` (such a dict) is filled instead of allocating."""
+    window, sinks, scale = _int(window, "window"), _int(sinks, "sinks"), None if scale is None else float(scale)
     given = (None,) * 3 if out is None else (out["dq"], out["dk"], out["dv"])
     plan = _plan(("attention back", window, sinks, scale, _meta(q), _meta(k), _meta(v), _meta(q_lens), _meta(k_lens),
                   _meta(o), _meta(lse), _meta(dO), _meta(given[0]), _meta(given[1]), _meta(given[2])),
@@ -754,6 +766,7 @@ def _rotary_plan(q, k, freqs, positions, start, mscale, flags):
 
 
 def _rotary(q, k, freqs, positions, start, interleaved, mscale, q_out, k_out, stream, flags):
+    start, mscale = _int(start, "start"), float(mscale)
     if interleaved:
         flags |= ROTARY_INTERLEAVED
     plan = _plan(("rotary", _meta(q), _meta(k), _meta(freqs), _meta(positions), start, mscale, flags),
@@ -858,6 +871,7 @@ def add_rmsnorm(x, weight, residual=None, *, eps: float = 1e-6, y=None, h=None, 
     dimension (lact_add_rmsnorm_forward).  x, residual [..., cols] fp32 or
     bf16, weight [cols] fp32.  Returns (y, h); without a residual h is x
     itself.  h = residual or h = x updates the residual stream in place."""
+    eps = float(eps)
     plan = _plan(("norm", eps, _meta(x), _meta(weight), _meta(residual), _meta(y), _meta(h)),
                  lambda: _norm_plan(x, weight, eps, ("residual", residual, False), ("h", h, False), ("y", y, False)))
     ldx, ldr, ldh, ldy = plan.ld
@@ -881,7 +895,7 @@ def add_rmsnorm_quantised(x, weight, residual=None, *, eps: float = 1e-6, y8=Non
     float8_e4m3fn and scales [..., ceil(cols / 128)] fp32, so that y is about
     y8 * scale of its group of 128 columns.  Returns (y8, scales, h); a given
     y is filled too."""
-    torch = _torch()
+    torch, eps = _torch(), float(eps)
     plan = _plan(("norm 8", eps, _meta(x), _meta(weight), _meta(residual), _meta(y8), _meta(h), _meta(y)),
                  lambda: _norm_plan(x, weight, eps, ("residual", residual, False), ("h", h, False), ("y", y, False),
                                     ("y8", y8, True)))
@@ -912,7 +926,7 @@ def add_rmsnorm_backward(h, weight, *, dy, dh=None, eps: float = 1e-6, dx=None, 
     dy the gradient of y, dh that of h's other use (or None), in h's dtype.
     Returns (dx, dw): dx is the gradient of x and of residual alike, dw [cols]
     fp32 that of the weight."""
-    torch = _torch()
+    torch, eps = _torch(), float(eps)
     plan = _plan(("norm back", eps, _meta(h), _meta(weight), _meta(dy), _meta(dh), _meta(dx)),
                  lambda: _norm_plan(h, weight, eps, ("dy", dy, False), ("dh", dh, False), ("dx", dx, False)))
     ldh, ldy, lddh, lddx = plan.ld

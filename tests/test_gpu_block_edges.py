@@ -68,3 +68,38 @@ def test_values_near_the_types_largest(lact, t, d, B, Lq, Lk, size):
     o = lact.window_attention(rep(q), rep(k), rep(v), scale=1.0)
     ref = OB.window_attention(f64(q), f64(k), f64(v), 0, 0, 1.0)
     check_attention(ref, {"o": o[-1:]}, dt, d, Lk, False)
+
+
+def test_parameters_given_as_tensors_are_read_at_every_call(lact):
+    """A position counter or a scale that the caller keeps in a tensor and
+    changes in place: nothing of an earlier call's value is used."""
+    q, w = torch.randn(1, 2, 40, 64, device="cuda"), torch.ones(64, device="cuda")
+    fr, _ = lact.rotary_frequencies(32)
+    o, lse = lact.window_attention(q, q, q, return_lse=True)
+    flat = q.view(80, 64)
+    calls = {
+        "start": (3, 8, lambda x: lact.rotary(q, freqs=fr, start=x)),
+        "start back": (3, 8, lambda x: lact.rotary_backward(q, freqs=fr, start=x)),
+        "mscale": (0.5, 1.5, lambda x: lact.rotary(q, freqs=fr, mscale=x)),
+        "scale": (0.1, 0.7, lambda x: lact.window_attention(q, q, q, scale=x)),
+        "window": (2, 9, lambda x: lact.window_attention(q, q, q, window=x)),
+        "sinks": (0, 9, lambda x: lact.window_attention(q, q, q, window=3, sinks=x)),
+        "scale back": (0.1, 0.7, lambda x: lact.window_attention_backward(q, q, q, o, lse, dO=q, scale=x)["dk"]),
+        "window back": (2, 9, lambda x: lact.window_attention_backward(q, q, q, o, lse, dO=q, window=x)["dk"]),
+        "eps": (0.1, 0.9, lambda x: lact.add_rmsnorm(flat, w, eps=x)[0]),
+        "eps 8": (0.1, 0.9, lambda x: lact.add_rmsnorm_quantised(flat, w, eps=x)[1]),
+        "eps back": (0.1, 0.9, lambda x: lact.add_rmsnorm_backward(flat, w, dy=flat, eps=x)[0]),
+    }
+    for name, (first, then, call) in calls.items():
+        # powers of two and whole numbers apart, a float32 tensor holds another value than the float
+        x = torch.tensor(first)
+        one = call(x)
+        x.fill_(then)
+        two = call(x)
+        assert torch.equal(one, call(torch.tensor(first).item())), name
+        assert torch.equal(two, call(torch.tensor(then).item())) and not torch.equal(one, two), name
+    for kw in (dict(window=2.0), dict(sinks="4")):
+        with pytest.raises(ValueError):
+            lact.window_attention(q, q, q, **kw)
+    with pytest.raises(ValueError):
+        lact.rotary(q, freqs=fr, start=1.5)
