@@ -606,11 +606,13 @@ def _addr(t):
 
 
 def _like(t):
-    """An empty tensor of t's shape, in t's order of dimensions where t's rows are distinct."""
+    """The layout of a result like t, in t's order of dimensions where t's rows
+    are distinct: a tensor without memory, so that a plan costs none (k and v
+    may be a cache that fills the device)."""
     torch = _torch()
     if 0 in t.stride():   # an expanded input: its gradient or result has a place for every element
-        return torch.empty(t.shape, dtype=t.dtype, device=t.device)
-    return torch.empty_like(t)
+        return torch.empty(t.shape, dtype=t.dtype, device="meta")
+    return torch.empty_like(t, device="meta")
 
 
 def _new(t, meta):

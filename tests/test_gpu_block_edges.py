@@ -103,3 +103,22 @@ def test_parameters_given_as_tensors_are_read_at_every_call(lact):
             lact.window_attention(q, q, q, **kw)
     with pytest.raises(ValueError):
         lact.rotary(q, freqs=fr, start=1.5)
+
+
+def test_a_first_call_takes_no_memory_but_its_results(lact):
+    """The next token over a view of a cache that grows from call to call: each
+    shape is new to the binding, and none costs memory of the cache's size."""
+    n = 1 << 20
+    k = torch.zeros(1, 1, n, 128, dtype=torch.bfloat16, device="cuda")   # 256 MB
+    q = torch.zeros(1, 2, 1, 128, dtype=torch.bfloat16, device="cuda")
+    fr, _ = lact.rotary_frequencies(64)
+    for m in (n - 8, n):
+        kk = k[:, :, :m]
+        # results of [1, 2, 1, 128], and 256 splits' partial results of two rows
+        for call, most in ((lambda: lact.window_attention(q, kk, kk, window=4096), 1 << 20),
+                           (lambda: lact.rotary(kk, freqs=fr, q_out=kk), 0)):
+            torch.cuda.synchronize()
+            before = torch.cuda.memory_allocated()
+            torch.cuda.reset_peak_memory_stats()
+            call()
+            assert torch.cuda.max_memory_allocated() - before <= most
