@@ -743,7 +743,7 @@ def window_attention_backward(q, k, v, o, lse, *, dO, window: int = 0, sinks: in
     return _on(plan.device, stream, (q, k, v, o, lse, dO, q_lens, k_lens, workspace) + given, run)
 
 
-def _rotary_plan(q, k, freqs, positions, start, mscale, flags):
+def _rotary_plan(q, k, freqs, positions, mscale, flags):
     torch = _torch()
     if q.dim() != 4 or (k is not None and k.dim() != 4):
         raise ValueError("q and k must be [batch, heads, tokens, d]")
@@ -756,7 +756,7 @@ def _rotary_plan(q, k, freqs, positions, start, mscale, flags):
     _ptr(freqs, torch.float64, "freqs")
     _ptr(positions, torch.int64, "positions")
     plan.problem = RotaryProblem(b, h, 0 if k is None else k.shape[1], d, freqs.shape[0], _io_dtype(q), flags, mscale, l,
-                                 start)
+                                 0)
     plan.p = ctypes.byref(plan.problem)
     plan.dtype, plan.shape, plan.kshape = q.dtype, (b, h, l, d), None if k is None else (b, k.shape[1], l, d)
     given = [_strided(q, "q", plan.shape, q.dtype)] + ([] if k is None else [_strided(k, "k", plan.kshape, q.dtype)])
@@ -771,8 +771,12 @@ def _rotary(q, k, freqs, positions, start, interleaved, mscale, q_out, k_out, st
     start, mscale = _int(start, "start"), float(mscale)
     if interleaved:
         flags |= ROTARY_INTERLEAVED
-    plan = _plan(("rotary", _meta(q), _meta(k), _meta(freqs), _meta(positions), start, mscale, flags),
-                 lambda: _rotary_plan(q, k, freqs, positions, start, mscale, flags))
+    plan = _plan(("rotary", _meta(q), _meta(k), _meta(freqs), _meta(positions), mscale, flags),
+                 lambda: _rotary_plan(q, k, freqs, positions, mscale, flags))
+    p = plan.p
+    if positions is None and start:   # another one at every step of a decoding loop: not a part of the plan
+        problem = RotaryProblem.from_buffer_copy(plan.problem)
+        problem.start, p = start, ctypes.byref(problem)
     rq, rk = plan.rq, plan.rk
     if q_out is not None or k_out is not None:
         _one_device(q, q_out, k_out)
@@ -788,7 +792,7 @@ def _rotary(q, k, freqs, positions, start, interleaved, mscale, q_out, k_out, st
             q_out = _new(q, plan.results[0])
         if k is not None and k_out is None:
             k_out = _new(k, plan.results[1])
-        st = lib().lact_rotary(plan.p, q.data_ptr(), plan.sq, _addr(k), plan.sk, freqs.data_ptr(), _addr(positions),
+        st = lib().lact_rotary(p, q.data_ptr(), plan.sq, _addr(k), plan.sk, freqs.data_ptr(), _addr(positions),
                                q_out.data_ptr(), rq, _addr(k_out), rk, handle)
         check(st)
         return q_out if k is None else (q_out, k_out)

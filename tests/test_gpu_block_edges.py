@@ -122,3 +122,16 @@ def test_a_first_call_takes_no_memory_but_its_results(lact):
             torch.cuda.reset_peak_memory_stats()
             call()
             assert torch.cuda.max_memory_allocated() - before <= most
+
+
+def test_a_decoding_loop_plans_its_rotary_call_once(lact):
+    """The start moves on at every step; the plan does not depend on it."""
+    q, fr = torch.randn(1, 2, 1, 64, device="cuda"), lact.rotary_frequencies(32)[0]
+    lact.rotary(q, freqs=fr)
+    plans = dict(lact._PLANS)
+    for start in (0, 1, 2, 700, 1 << 40):
+        at = torch.full((1, 1), start, dtype=torch.int64, device="cuda")
+        want = lact.rotary(q, freqs=fr, positions=at, start=3)   # positions given: the start is not looked at
+        plans.update(lact._PLANS)
+        assert torch.equal(lact.rotary(q, freqs=fr, start=start), want)
+        assert lact._PLANS == plans
