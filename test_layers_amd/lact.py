@@ -517,9 +517,21 @@ def _int(x, name):
     """A whole number given as any integer type (a tensor of one included):
     its value now, which is what a plan's key has to hold."""
     try:
-        return operator.index(x)
+        n = operator.index(x)
     except TypeError:
         raise ValueError(f"{name} must be a whole number, got {x!r}") from None
+    if not -1 << 63 <= n < 1 << 63:
+        raise ValueError(f"{name} = {n} is not a 64-bit number")
+    return n
+
+
+def _struct(cls, *values):
+    """A C struct of the values, none of which ctypes may have cut to its field's width."""
+    s = cls(*values)
+    for (name, _), x in zip(cls._fields_, values):
+        if isinstance(x, int) and getattr(s, name) != x:
+            raise ValueError(f"{name} = {x}: more than the library takes")
+    return s
 
 
 def _one_device(*tensors):
@@ -631,7 +643,7 @@ def _attention_plan(q, k, v, window, sinks, scale, q_lens, k_lens, back):
     plan = _Plan()
     plan.device = _one_device(q, k, v, q_lens, k_lens)
     plan.shape, plan.kshape, plan.dtype = (b, h, lq, d), (b, hk, lk, d), q.dtype
-    plan.problem = Attention(b, h, hk, d, _io_dtype(q), d ** -0.5 if scale is None else scale, lq, lk, window, sinks)
+    plan.problem = _struct(Attention, b, h, hk, d, _io_dtype(q), d ** -0.5 if scale is None else scale, lq, lk, window, sinks)
     plan.p = ctypes.byref(plan.problem)
     plan.strides = [_strided(q, "q", plan.shape, q.dtype), _strided(k, "k", plan.kshape, q.dtype),
                     _strided(v, "v", plan.kshape, q.dtype)]
@@ -755,8 +767,8 @@ def _rotary_plan(q, k, freqs, positions, mscale, flags):
     plan.device = _one_device(q, k, freqs, positions)
     _ptr(freqs, torch.float64, "freqs")
     _ptr(positions, torch.int64, "positions")
-    plan.problem = RotaryProblem(b, h, 0 if k is None else k.shape[1], d, freqs.shape[0], _io_dtype(q), flags, mscale, l,
-                                 0)
+    plan.problem = _struct(RotaryProblem, b, h, 0 if k is None else k.shape[1], d, freqs.shape[0], _io_dtype(q), flags,
+                           mscale, l, 0)
     plan.p = ctypes.byref(plan.problem)
     plan.dtype, plan.shape, plan.kshape = q.dtype, (b, h, l, d), None if k is None else (b, k.shape[1], l, d)
     given = [_strided(q, "q", plan.shape, q.dtype)] + ([] if k is None else [_strided(k, "k", plan.kshape, q.dtype)])
@@ -861,7 +873,7 @@ def _norm_plan(x, weight, eps, *others):
     plan.device = _one_device(x, weight, *[t for _, t, _ in others])
     _check_shapes(weight=(weight, (cols,)))
     _ptr(weight, torch.float32, "weight")
-    plan.problem = NormProblem(x.numel() // cols, cols, _io_dtype(x), eps)
+    plan.problem = _struct(NormProblem, x.numel() // cols, cols, _io_dtype(x), eps)
     plan.p = ctypes.byref(plan.problem)
     plan.shape, plan.cols = tuple(x.shape), cols
     plan.groups = plan.shape[:-1] + ((cols + NORM_GROUP - 1) // NORM_GROUP,)
