@@ -884,11 +884,19 @@ def _norm_plan(x, weight, eps, *others):
     return plan
 
 
+def _stored(x, y, h):
+    """Where h is after a forward: in its own tensor, or in x unless y is there."""
+    if h is not None:
+        return h
+    return None if y is not None and y.data_ptr() == x.data_ptr() and x.numel() else x
+
+
 def add_rmsnorm(x, weight, residual=None, *, eps: float = 1e-6, y=None, h=None, stream=None):
     """h = x + residual and y = h weight / sqrt(mean(h^2) + eps) over the last
     dimension (lact_add_rmsnorm_forward).  x, residual [..., cols] fp32 or
     bf16, weight [cols] fp32.  Returns (y, h); without a residual h is x
-    itself.  h = residual or h = x updates the residual stream in place."""
+    itself, or None where y overwrites it (y = x and no h given).
+    h = residual or h = x updates the residual stream in place."""
     eps = float(eps)
     plan = _plan(("norm", eps, _meta(x), _meta(weight), _meta(residual), _meta(y), _meta(h)),
                  lambda: _norm_plan(x, weight, eps, ("residual", residual, False), ("h", h, False), ("y", y, False)))
@@ -902,7 +910,7 @@ def add_rmsnorm(x, weight, residual=None, *, eps: float = 1e-6, y=None, h=None, 
         st = lib().lact_add_rmsnorm_forward(plan.p, x.data_ptr(), ldx, _addr(residual), ldr, weight.data_ptr(), _addr(h),
                                             ldh, y.data_ptr(), ldy, None, 0, None, handle)
         check(st)
-        return y, (x if h is None else h)
+        return y, _stored(x, y, h)
 
     return _on(plan.device, stream, (x, weight, residual, y, h), run)
 
@@ -911,8 +919,8 @@ def add_rmsnorm_quantised(x, weight, residual=None, *, eps: float = 1e-6, y8=Non
                           stream=None):
     """As add_rmsnorm, with y in 8-bit floating point: y8 [..., cols]
     float8_e4m3fn and scales [..., ceil(cols / 128)] fp32, so that y is about
-    y8 * scale of its group of 128 columns.  Returns (y8, scales, h); a given
-    y is filled too."""
+    y8 * scale of its group of 128 columns.  Returns (y8, scales, h), h as
+    add_rmsnorm returns it; a given y is filled too."""
     torch, eps = _torch(), float(eps)
     plan = _plan(("norm 8", eps, _meta(x), _meta(weight), _meta(residual), _meta(y8), _meta(h), _meta(y)),
                  lambda: _norm_plan(x, weight, eps, ("residual", residual, False), ("h", h, False), ("y", y, False),
@@ -933,7 +941,7 @@ def add_rmsnorm_quantised(x, weight, residual=None, *, eps: float = 1e-6, y8=Non
         st = lib().lact_add_rmsnorm_forward(plan.p, x.data_ptr(), ldx, _addr(residual), ldr, weight.data_ptr(), _addr(h),
                                             ldh, _addr(y), ldy, y8.data_ptr(), ld8, scales.data_ptr(), handle)
         check(st)
-        return y8, scales, (x if h is None else h)
+        return y8, scales, _stored(x, y, h)
 
     return _on(plan.device, stream, (x, weight, residual, y8, scales, h, y), run)
 

@@ -135,3 +135,26 @@ def test_a_decoding_loop_plans_its_rotary_call_once(lact):
         plans.update(lact._PLANS)
         assert torch.equal(lact.rotary(q, freqs=fr, start=start), want)
         assert lact._PLANS == plans
+
+
+def test_a_norm_over_its_input_returns_no_h(lact):
+    """y = x without a residual: x holds y afterwards, and no h is handed out
+    that a backward pass would take for the norm's input."""
+    x, w = torch.randn(5, 64, device="cuda"), 2 * torch.ones(64, device="cuda")
+    want, _ = lact.add_rmsnorm(x, w)
+    q8, sc, h = lact.add_rmsnorm_quantised(x, w)
+    assert h is x
+    for given in (None, torch.empty_like(x)):
+        z = x.clone()
+        y, h = lact.add_rmsnorm(z, w, y=z, h=given)
+        assert y is z and torch.equal(z, want) and h is given
+        z = x.clone()
+        a, b, h = lact.add_rmsnorm_quantised(z, w, y=z, h=given)
+        assert torch.equal(a.float(), q8.float()) and torch.equal(b, sc) and torch.equal(z, want) and h is given
+        assert given is None or torch.equal(given, x)
+    # with a residual h has a place of its own
+    z = x.clone()
+    y, h = lact.add_rmsnorm(z, w, z, y=z)
+    assert torch.equal(h, x + x)
+    e = x[:0]
+    assert lact.add_rmsnorm(e, w)[1] is e
