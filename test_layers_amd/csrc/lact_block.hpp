@@ -79,10 +79,13 @@ lact_status validate(const lact_attention* p) {
   return LACT_OK;
 }
 
+// Whether some row may not see some key before it
+bool limited(const lact_attention& p) { return p.window && p.window < p.k_len && p.sinks < p.k_len; }
+
 // keys that the 32 rows of a tile of the few-row kernel can see
 int64_t few_keys(const lact_attention& p) {
   const int64_t tokens = std::min(p.q_len, ceil_div(31, p.heads / p.kv_heads) + 1);
-  return p.window ? std::min(p.k_len, std::min(p.window, MOST_TOKENS) + tokens - 1 + std::min(p.sinks, p.k_len)) : p.k_len;
+  return limited(p) ? std::min(p.k_len, p.window + tokens - 1 + p.sinks) : p.k_len;
 }
 
 // workgroups of the few-row kernel that run at once: their rings take 64 KB
@@ -124,8 +127,8 @@ AttnArgs attn_args(const lact_attention& p) {
   a.d = p.d;
   a.Lq = (int32_t)p.q_len;
   a.Lk = (int32_t)p.k_len;
-  a.window = (int32_t)(p.window == 0 ? MOST_TOKENS : std::min(p.window, MOST_TOKENS));
-  a.sinks = (int32_t)std::min(p.sinks, MOST_TOKENS);
+  a.window = (int32_t)(limited(p) ? p.window : MOST_TOKENS);
+  a.sinks = (int32_t)(limited(p) ? p.sinks : 0);
   a.c = p.scale * LOG2E;
   a.scale = p.scale;
   a.splits = 1;
@@ -162,19 +165,28 @@ int parts_k(const lact_attention& p, bool padded) {
   return parts(p, (int64_t)p.batch * p.kv_heads * ceil_div(p.k_len, 128), padded);
 }
 
-// key tiles of the dk, dv kernel, those of them with sinks, and the splits of
-// the rows behind a sink tile's window
+// Key tiles of the dk, dv kernel, those of them with sinks, and the splits of
+// the rows behind a sink tile's window: parts as long as what a window's tile
+// meets, at most 63 of them and no more than make SINK_JOBS of all sink tiles
+// together, two a compute unit.  More tiles fill the chip without being split,
+// and the workspace for their parts stays below 96 MiB.  Backward, window 128,
+// d = 128, as many parts as were allowed before and now (512, 1024 and 2048
+// jobs): 8 x 32 heads x 4096 tokens, 4 sinks: 1689 us with 552 MiB, and 1453,
+// 1449, 1530 with 104, 168, 296; 8 heads x 32K, 4096 sinks: 3690 us with 2 GiB,
+// and 2510, 2357, 2466 with 98, 162, 290 MiB; 1024 sinks: 1225, and 855, 895, 990.
+constexpr int64_t SINK_JOBS = 512;
 void sink_plan(const lact_attention& p, int64_t BK, AttnArgs& a) {
   a.tiles = (int32_t)ceil_div(p.k_len, BK);
   a.splits = 1;
   a.sink_tiles = 0;
-  if (p.sinks == 0 || p.window == 0 || p.k_len <= BK) return;
+  if (p.sinks == 0 || !limited(p) || p.k_len <= BK) return;
   const int64_t behind = p.k_len - (BK - 1) - p.window;  // rows behind the first sink tile's window
   if (behind <= 0) return;
-  // a split is as long as what a window's tile meets, and there are at most 64
-  const int64_t span = std::max(p.window + BK, ceil_div(behind, 63));
-  a.sink_tiles = (int32_t)ceil_div(std::min(p.sinks, p.k_len), BK);
-  a.span = (int32_t)std::min(span, MOST_TOKENS);
+  const int64_t tiles = ceil_div(p.sinks, BK), most = SINK_JOBS / std::max<int64_t>(1, p.batch * p.kv_heads * tiles);
+  if (most < 2) return;
+  const int64_t span = std::max(p.window + BK, ceil_div(behind, std::min<int64_t>(63, most)));
+  a.sink_tiles = (int32_t)tiles;
+  a.span = (int32_t)span;
   a.splits = 1 + (int32_t)ceil_div(behind, span);
 }
 

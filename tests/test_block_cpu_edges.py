@@ -45,3 +45,30 @@ def test_numbers_beyond_their_fields_are_refused():
             lact.window_attention_backward(q, q, q, q, q[..., 0], dO=q, **kw)
     with pytest.raises(ValueError, match="64-bit"):
         lact.rotary(q, freqs=torch.ones(4, dtype=torch.float64), start=1 << 63)
+
+
+def _back_ws(**kw):
+    a = dict(batch=1, heads=8, kv_heads=8, d=128, io_dtype=lact.DTYPE_BF16, scale=0.1, q_len=32768, k_len=32768,
+             window=128, sinks=4)
+    a.update(kw)
+    n = lact.lib().lact_window_attention_backward_workspace_size(ctypes.byref(lact.Attention(**a)))
+    assert n > 0
+    return n, 8 * a["batch"] * a["heads"] * a["q_len"] + 256   # all, and the rows' two statistics
+
+
+@pytest.mark.parametrize("kw", [
+    dict(sinks=32768), dict(sinks=1 << 40), dict(sinks=4096), dict(sinks=1024, window=1), dict(batch=64), dict(),
+    dict(batch=8, heads=32, kv_heads=32, q_len=4096, k_len=4096), dict(sinks=32767), dict(window=0, sinks=9),
+    dict(batch=8, heads=32, kv_heads=32, q_len=4096, k_len=4096, sinks=4096), dict(q_len=1 << 29, k_len=1 << 29),
+    dict(batch=4096, heads=64, kv_heads=64, q_len=500, k_len=500, window=3)])
+def test_workspace_of_the_backward_is_bounded(kw):
+    """At most 512 + 256 jobs of sink tiles, each with dk and dv of 128 keys by
+    d in fp32, beside the rows' statistics: whatever the sinks and the batch."""
+    need, stats = _back_ws(**kw)
+    assert need <= stats + 768 * 2 * 128 * 128 * 4 + 256
+    if kw.get("sinks", 0) >= kw.get("k_len", 32768) or kw.get("window") == 0:
+        assert need <= stats   # every row sees all keys before it: nothing to split
+
+
+def test_a_long_row_of_few_sinks_is_still_split():
+    assert _back_ws(sinks=4)[0] > _back_ws(sinks=0)[0] + 60 * 2 * 128 * 128 * 4 * 8

@@ -158,3 +158,17 @@ def test_a_norm_over_its_input_returns_no_h(lact):
     assert torch.equal(h, x + x)
     e = x[:0]
     assert lact.add_rmsnorm(e, w)[1] is e
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 7), (20, 300), (20, 1 << 40), (300, 5), (1 << 40, 0)])
+def test_limits_that_hide_nothing_are_no_limits(lact, window, sinks):
+    """A window or sinks over all keys: the bits of plain causal attention, and of its gradients."""
+    gen = torch.Generator("cuda").manual_seed(22)
+    q, k, v, g = (randn(gen, (2, 4, 300, 64), torch.bfloat16) for _ in range(4))
+    for rows in (300, 3):
+        qq, gg = q[:, :, :rows], g[:, :, :rows]
+        o, lse = lact.window_attention(qq, k, v, return_lse=True)
+        out = lact.window_attention_backward(qq, k, v, o, lse, dO=gg)
+        o2, lse2 = lact.window_attention(qq, k, v, return_lse=True, window=window, sinks=sinks)
+        out2 = lact.window_attention_backward(qq, k, v, o2, lse2, dO=gg, window=window, sinks=sinks)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2) and all(torch.equal(out[n], out2[n]) for n in out)
