@@ -782,6 +782,17 @@ __global__ __launch_bounds__(256, (attn_waves<T, DP>())) void attn_fwd_kernel(At
 }
 
 // ------------------------------------------------------------------ forward, few rows
+// waves of a workgroup, bytes of a tile of 32 keys, and the LDS of a workgroup:
+// a wave's ring of two tiles of K and V, where its O^T and statistics fit later
+template <typename T, int DP>
+constexpr int few_waves() { return DP * (int)sizeof(T) > 256 ? 2 : 4; }
+template <typename T, int DP>
+constexpr int few_tile() { return 32 * AttnTile<T, DP>::CPR * 16; }
+template <typename T, int DP>
+constexpr int few_lds() {
+  return few_waves<T, DP>() * (4 * few_tile<T, DP>() > 32 * DP * 4 + 256 ? 4 * few_tile<T, DP>() : 32 * DP * 4 + 256);
+}
+
 // Few rows a key head, 32 to a workgroup (row r is token r / G's query head r
 // % G, so that a workgroup's rows see the same keys): the work is reading
 // keys, so the keys are split, over workgroups and again over a workgroup's
@@ -790,11 +801,11 @@ __global__ __launch_bounds__(256, (attn_waves<T, DP>())) void attn_fwd_kernel(At
 // that it must read.  Where keys are few, by latency: one sequence of 16
 // heads, window 2048: 8.6 us, and 3.2 more for the join.  Each wave runs its own ring of 32-key tiles with no barrier; the
 // waves join in LDS, the workgroups through `part` in attn_join_kernel.
-template <typename T, int DP, int NW>
-__global__ __launch_bounds__(64 * NW) void attn_few_kernel(AttnArgs a) {
+template <typename T, int DP>
+__global__ __launch_bounds__(64 * (few_waves<T, DP>())) void attn_few_kernel(AttnArgs a) {
   using Tile = AttnTile<T, DP>;
-  constexpr int TB = 32 * Tile::CPR * 16, WB = 4 * TB > 32 * DP * 4 + 256 ? 4 * TB : 32 * DP * 4 + 256;
-  __shared__ __align__(1024) char lds[NW * WB];
+  constexpr int NW = few_waves<T, DP>(), TB = few_tile<T, DP>(), WB = few_lds<T, DP>() / NW;
+  __shared__ __align__(1024) char lds[few_lds<T, DP>()];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int split = blockIdx.x % a.splits, tile = blockIdx.x / a.splits % a.tiles, bk = blockIdx.x / a.splits / a.tiles;
   const int hk = bk % a.Hk, b = bk / a.Hk;

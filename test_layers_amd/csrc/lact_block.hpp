@@ -79,6 +79,13 @@ lact_status validate(const lact_attention* p) {
   return LACT_OK;
 }
 
+// calls fn with the element type and the padded head width
+template <class F>
+lact_status by_tile(const lact_attention& p, F&& fn) {
+  if (p.io_dtype == LACT_DTYPE_F32) return p.d <= 64 ? fn(float{}, IC<64>{}) : fn(float{}, IC<128>{});
+  return p.d <= 64 ? fn(bf16_t{}, IC<64>{}) : fn(bf16_t{}, IC<128>{});
+}
+
 // Whether some row may not see some key before it
 bool limited(const lact_attention& p) { return p.window && p.window < p.k_len && p.sinks < p.k_len; }
 
@@ -88,9 +95,17 @@ int64_t few_keys(const lact_attention& p) {
   return limited(p) ? std::min(p.k_len, p.window + tokens - 1 + p.sinks) : p.k_len;
 }
 
-// workgroups of the few-row kernel that run at once: their rings take 64 KB
-// of a compute unit's LDS, or 128
-int64_t few_room(const lact_attention& p) { return (p.d * size_of(p.io_dtype) > 128 ? 1 : 2) * NCU; }
+// workgroups of the few-row kernel that run at once, by its rings in LDS: 64 KB
+// (bf16, d <= 64), or 128 (16 heads of 32 in fp32 over 32K keys: in one round
+// of splits 65 us, in two 71)
+int64_t few_room(const lact_attention& p) {
+  int64_t n = 0;
+  (void)by_tile(p, [&](auto t, auto dp) {
+    n = LDS_MAX / few_lds<decltype(t), decltype(dp)::value>() * NCU;
+    return LACT_OK;
+  });
+  return n;
+}
 
 // Row tiles of the few-row kernel, 0 where the other kernel takes the problem.
 // A key head's rows in one tile: always.  More of them:
@@ -246,13 +261,6 @@ lact_status check_ws(const void* ws, size_t have, size_t need) {
   return LACT_OK;
 }
 
-// calls fn with the element type and the padded head width
-template <class F>
-lact_status by_tile(const lact_attention& p, F&& fn) {
-  if (p.io_dtype == LACT_DTYPE_F32) return p.d <= 64 ? fn(float{}, IC<64>{}) : fn(float{}, IC<128>{});
-  return p.d <= 64 ? fn(bf16_t{}, IC<64>{}) : fn(bf16_t{}, IC<128>{});
-}
-
 // calls fn with the number of waves that share a tile
 template <typename T, class DP, class F>
 void by_parts(T, DP, int ks, F&& fn) {
@@ -323,10 +331,10 @@ lact_status lact_window_attention_forward(const lact_attention* p, const void* q
     }
     return by_tile(*p, [&](auto t, auto dp) -> lact_status {
       using T = decltype(t);
-      constexpr int DP = decltype(dp)::value, NW = DP * sizeof(T) > 256 ? 2 : 4;
+      constexpr int DP = decltype(dp)::value, NW = few_waves<T, DP>();
       {
         KernelTimer kt(LACT_K_ATTN, s);
-        LACT_LAUNCH((attn_few_kernel<T, DP, NW>), dim3((unsigned)grid), dim3(64 * NW), s, a);
+        LACT_LAUNCH((attn_few_kernel<T, DP>), dim3((unsigned)grid), dim3(64 * NW), s, a);
       }
       KernelTimer kt(LACT_K_ATTN, s);
       if (a.splits > 1) LACT_LAUNCH((attn_join_kernel<T, DP>), dim3((unsigned)rows), dim3(256), s, a);

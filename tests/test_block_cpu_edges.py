@@ -72,3 +72,13 @@ def test_workspace_of_the_backward_is_bounded(kw):
 
 def test_a_long_row_of_few_sinks_is_still_split():
     assert _back_ws(sinks=4)[0] > _back_ws(sinks=0)[0] + 60 * 2 * 128 * 128 * 4 * 8
+
+
+@pytest.mark.parametrize("dtype,d,at_once", [("F32", 8, 256), ("F32", 32, 256), ("F32", 64, 256), ("F32", 128, 256),
+                                             ("BF16", 8, 512), ("BF16", 64, 512), ("BF16", 72, 256)])
+def test_key_splits_fill_the_chip_once(dtype, d, at_once):
+    """128 key heads' next tokens over long keys: as many splits as make one
+    round of workgroups, by the LDS that a workgroup of the padded width takes."""
+    a = lact.Attention(8, 16, 16, d, getattr(lact, "DTYPE_" + dtype), 0.1, 1, 1 << 20, 0, 0)
+    need = lact.lib().lact_window_attention_workspace_size(ctypes.byref(a))
+    assert need == 128 * (at_once // 128) * (d + 2) * 4   # a row's partial results and statistics, each a multiple of 256
