@@ -162,22 +162,41 @@ void row_tiles(const lact_attention& p, int rows, AttnArgs& a) {
   a.tiles = (int32_t)ceil_div(p.q_len, rows / a.hg);
 }
 
-// Waves that share the rows (keys) of a tile.  One wave a 32-row group has the
-// pipelined order, two fill the chip where there are few tiles of 128: bf16, as
-// many as compute units (2 x 8 heads x 1024 tokens, d = 64: 52 us with one, 41
-// with two; 16 heads x 4096, 512 tiles: 126 and 133).  Of a padded batch's
-// tiles some are empty; 5/8 are counted (5 texts of up to 1777 tokens, 280 key
-// tiles: 218 and 192 us).  fp32 has no pipelined order to lose (16 heads x 4096:
-// 528 and 471 us), but beyond d = 64 its tiles of 32 keys do not divide.
-int parts(const lact_attention& p, int64_t tiles, bool padded) {
+// Waves that share the rows (keys) of a tile: one wave a 32-row group, or two,
+// which make twice as many workgroups of half the work.  fp32 has no pipelined
+// order to lose by it (16 heads x 4096: 528 us with one, 471 with two), but
+// beyond d = 64 its tiles of 32 keys do not divide.  bf16, by the padded sizes,
+// since the host does not know the lengths:
+//
+// Rows (forward, dq).  d <= 64, two workgroups a compute unit: two waves up to
+// one and a half tiles of 128 a unit (1024 tokens, causal, forward: 32 - 128
+// tiles 17.7 us with one and 14.4 with two, 288: 23.2 and 21.0, 384: 23.8 and
+// 22.0, 448: 23.9 and 25.9; dq of 288 tiles 4 us less, of 512 4 more).  d > 64,
+// where one workgroup of dq has a unit: two up to half a tile a unit, beyond
+// that they run one after another (128 tiles: 23.2 and 19.0, 160: 23.5 and 25.0;
+// dq of 128 tiles 5 us less, of 160 8 more).
+int parts_q(const lact_attention& p) {
+  const int64_t tiles = (int64_t)p.batch * p.heads * ceil_div(p.q_len, 128);
   if (p.io_dtype == LACT_DTYPE_F32) return p.d <= 64 && tiles <= 4 * NCU ? 2 : 1;
-  return (padded ? tiles * 5 / 8 : tiles) <= NCU ? 2 : 1;
+  return 2 * tiles <= (p.d <= 64 ? 3 : 1) * NCU ? 2 : 1;
 }
-int parts_q(const lact_attention& p, bool padded) {
-  return parts(p, (int64_t)p.batch * p.heads * ceil_div(p.q_len, 128), padded);
-}
-int parts_k(const lact_attention& p, bool padded) {
-  return parts(p, (int64_t)p.batch * p.kv_heads * ceil_div(p.k_len, 128), padded);
+// Keys (dk, dv): two waves up to half a tile a unit (d = 128, 4 heads to a key
+// head: 8 - 27 us less; causal, 160 tiles of d = 64, 5 more).  With a window of
+// at most half the keys, whose tiles meet equally many rows, up to five quarters,
+// where a second round of whole tiles would be short (window 333, 4 heads to a
+// key head; the backward with one wave, and what two change.  d = 64: 224 tiles
+// of 1024 tokens 122 us, -26; 288: 133, -6, of 2048 tokens 142, +2; 352: 144,
+// +3.  d = 128: 256 tiles 216 and 242, -21 and -7; 288: 265 and 277, -12 and
+// -14; 352: 297 and 305, -13 and +14; but 160 to 224 tiles, one round, 0 to +6).
+// Padded, 280 tiles, window 333, 3 heads to a key head, d = 64 and 128: all
+// lengths full 114 and 222, -2 and -8; from a quarter to full 100 and 187, -18
+// and -26; half 94 and 137, -20 and +12; a quarter 72 and 110, -5 and -9.
+int parts_k(const lact_attention& p) {
+  const int64_t tiles = (int64_t)p.batch * p.kv_heads * ceil_div(p.k_len, 128);
+  if (p.io_dtype == LACT_DTYPE_F32) return p.d <= 64 && tiles <= 4 * NCU ? 2 : 1;
+  if (2 * tiles <= NCU) return 2;
+  if (!limited(p) || 2 * p.window > p.k_len || 4 * tiles > 5 * NCU) return 1;
+  return p.d <= 64 || 8 * tiles > 7 * NCU ? 2 : 1;
 }
 
 // Key tiles of the dk, dv kernel, those of them with sinks, and the splits of
@@ -222,12 +241,10 @@ AttnWs attn_back_ws(const lact_attention& p) {
   AttnWs w;
   w.part = align256((size_t)p.batch * p.heads * p.q_len * 2 * 4);
   w.total = w.part;
-  for (int64_t BK : {64, 128}) {  // the query does not know whether the batch is padded
-    AttnArgs a = attn_args(p);
-    sink_plan(p, BK, a);
-    if (a.splits > 1)
-      w.total = std::max(w.total, w.part + align256((size_t)p.batch * p.kv_heads * a.sink_tiles * a.splits * 2 * BK * p.d * 4));
-  }
+  const int64_t BK = 128 / parts_k(p);
+  AttnArgs a = attn_args(p);
+  sink_plan(p, BK, a);
+  if (a.splits > 1) w.total += align256((size_t)p.batch * p.kv_heads * a.sink_tiles * a.splits * 2 * BK * p.d * 4);
   return w;
 }
 
@@ -342,7 +359,7 @@ lact_status lact_window_attention_forward(const lact_attention* p, const void* q
       return LACT_OK;
     });
   }
-  const int ks = parts_q(*p, q_lens != nullptr);
+  const int ks = parts_q(*p);
   row_tiles(*p, 128 / ks, a);
   const int64_t grid = (int64_t)p->batch * (p->heads / a.hg) * a.tiles;
   TRY(check_grid(grid));
@@ -405,7 +422,7 @@ lact_status lact_window_attention_backward(const lact_attention* p, const void* 
   a.lse = const_cast<float*>(lse);
   a.stats = static_cast<float*>(ws);
   a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + w.part);
-  const int ksq = parts_q(*p, q_lens != nullptr), ksk = parts_k(*p, k_lens != nullptr);
+  const int ksq = parts_q(*p), ksk = parts_k(*p);
   AttnArgs kv = a;
   sink_plan(*p, 128 / ksk, kv);
   row_tiles(*p, 128 / ksq, a);

@@ -172,3 +172,30 @@ def test_limits_that_hide_nothing_are_no_limits(lact, window, sinks):
         o2, lse2 = lact.window_attention(qq, k, v, return_lse=True, window=window, sinks=sinks)
         out2 = lact.window_attention_backward(qq, k, v, o2, lse2, dO=gg, window=window, sinks=sinks)
         assert torch.equal(o, o2) and torch.equal(lse, lse2) and all(torch.equal(out[n], out2[n]) for n in out)
+
+
+# tiles of 128 rows and keys on both sides of every bound by which one wave or
+# two take a tile, with lengths that leave some of them empty
+# (batch, heads, kv_heads, d, tokens, window, lengths)
+SHARED = [
+    (1, 32, 32, 64, 500, 500, None), (1, 33, 33, 64, 500, 500, None), (1, 16, 16, 64, 1000, 300, None),
+    (1, 81, 81, 64, 500, 250, None), (1, 96, 96, 64, 500, 100, None), (1, 97, 97, 64, 500, 100, None),
+    (1, 32, 32, 72, 500, 100, None), (1, 33, 33, 72, 500, 100, None), (1, 57, 57, 128, 500, 100, None),
+    (1, 80, 80, 72, 500, 100, None), (1, 81, 81, 72, 500, 100, None), (2, 40, 40, 128, 500, 251, None),
+    (5, 32, 16, 64, 500, 100, [500, 1, 250, 0, 129]), (5, 32, 16, 96, 500, 100, [500, 1, 250, 0, 129]),
+    (3, 40, 40, 64, 400, 50, [400, 100, 0]),
+]
+
+
+@pytest.mark.parametrize("case", SHARED, ids=lambda c: "x".join(str(x) for x in c[:6]))
+def test_waves_that_share_tiles(lact, case):
+    B, H, Hk, d, L, window, lens = case
+    gen = torch.Generator("cuda").manual_seed(23)
+    q, k, v, g = (randn(gen, s, torch.bfloat16) for s in ((B, H, L, d), (B, Hk, L, d), (B, Hk, L, d), (B, H, L, d)))
+    n = None if lens is None else torch.tensor(lens, device="cuda")
+    kw = dict(window=window, sinks=3, q_lens=n, k_lens=n)
+    out = {}
+    out["o"], out["lse"] = lact.window_attention(q, k, v, return_lse=True, **kw)
+    out.update(lact.window_attention_backward(q, k, v, out["o"], out["lse"], dO=g, **kw))
+    ref = OB.window_attention(f64(q), f64(k), f64(v), window, 3, float(np.float32(d ** -0.5)), lens, lens, f64(g))
+    check_attention(ref, out, torch.bfloat16, d, 2 * L * H // Hk, True)
