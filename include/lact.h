@@ -295,7 +295,8 @@ lact_status lact_layer_forward_noalloc(const lact_problem* p, const void* q, con
  * asynchronous on `stream`, nothing allocated or kept, LACT_ERR_HIP leaves
  * the outputs undefined), with these of their own: all work runs on `stream`
  * itself, so that calls with workspaces of their own may overlap; every call
- * may be captured into a HIP graph; results are bitwise reproducible.
+ * may be captured into a HIP graph; results are bitwise reproducible.  A call
+ * that would need 2^32 threads of a launch is refused (LACT_ERR_UNSUPPORTED).
  *
  * A [batch, heads, tokens, d] tensor is a pointer and its strides in
  * elements, d contiguous: head-major memory, token-major memory and slices of

@@ -57,7 +57,7 @@ lact_status check_tensor(const char* name, const void* ptr, const lact_strides* 
 
 // ------------------------------------------------------------------ window attention
 constexpr int64_t MOST_TOKENS = INT64_C(1) << 30;
-constexpr int64_t MOST_GRID = 0x7fffffff;
+constexpr int64_t MOST_THREADS = (INT64_C(1) << 32) - 1;  // of a launch
 
 lact_status validate(const lact_attention* p) {
   if (!p) return fail(LACT_ERR_INVALID_ARG, "problem is NULL");
@@ -66,7 +66,7 @@ lact_status validate(const lact_attention* p) {
     return fail(LACT_ERR_INVALID_ARG, "heads = %d, kv_heads = %d: need a positive multiple", p->heads, p->kv_heads);
   if (p->d < 8 || p->d > 128 || p->d % 8)
     return fail(LACT_ERR_UNSUPPORTED, "d = %d: need a multiple of 8 in [8, 128]", p->d);
-  if ((int64_t)p->batch * p->heads > MOST_GRID)
+  if ((int64_t)p->batch * p->heads > INT32_MAX)
     return fail(LACT_ERR_UNSUPPORTED, "batch * heads = %lld: more than a launch takes", (long long)p->batch * p->heads);
   lact_status r = check_dtype(p->io_dtype);
   if (r) return r;
@@ -267,8 +267,9 @@ lact_status check_apart(std::initializer_list<const void*> outputs, std::initial
     if (s_) return s_;                 \
   } while (0)
 
-lact_status check_grid(int64_t n) {
-  if (n > MOST_GRID) return fail(LACT_ERR_UNSUPPORTED, "%lld workgroups: more than a launch takes", (long long)n);
+lact_status check_grid(int64_t n, int threads) {
+  if (n > MOST_THREADS / threads)
+    return fail(LACT_ERR_UNSUPPORTED, "%lld workgroups of %d: more than a launch takes", (long long)n, threads);
   return LACT_OK;
 }
 lact_status check_ws(const void* ws, size_t have, size_t need) {
@@ -340,7 +341,13 @@ lact_status lact_window_attention_forward(const lact_attention* p, const void* q
   if ((a.tiles = few_tiles(*p)) > 0) {
     a.splits = few_splits(*p);
     const int64_t grid = (int64_t)p->batch * p->kv_heads * a.tiles * a.splits;
-    TRY(check_grid(std::max(grid, rows)));
+    int threads = 0;
+    TRY(by_tile(*p, [&](auto t, auto dp) {
+      threads = 64 * few_waves<decltype(t), decltype(dp)::value>();
+      return LACT_OK;
+    }));
+    TRY(check_grid(grid, threads));
+    if (a.splits > 1) TRY(check_grid(rows, 256));
     TRY(check_device_again());
     if (a.splits > 1) {
       a.part = static_cast<float*>(ws);
@@ -362,7 +369,7 @@ lact_status lact_window_attention_forward(const lact_attention* p, const void* q
   const int ks = parts_q(*p);
   row_tiles(*p, 128 / ks, a);
   const int64_t grid = (int64_t)p->batch * (p->heads / a.hg) * a.tiles;
-  TRY(check_grid(grid));
+  TRY(check_grid(grid, 256));
   TRY(check_device_again());
   KernelTimer kt(LACT_K_ATTN, s);
   return by_tile(*p, [&](auto t, auto dp) -> lact_status {
@@ -429,7 +436,8 @@ lact_status lact_window_attention_backward(const lact_attention* p, const void* 
   const int64_t heads = (int64_t)p->batch * p->kv_heads, gq = (int64_t)p->batch * (p->heads / a.hg) * a.tiles,
                 gk = heads * (kv.tiles + (int64_t)kv.sink_tiles * (kv.splits - 1)),
                 gs = kv.splits > 1 ? heads * kv.sink_tiles * 2 * (128 / ksk) : 0;
-  TRY(check_grid(std::max(std::max(gq, gk), gs)));
+  TRY(check_grid(std::max(gq, gk), 256));
+  TRY(check_grid(gs, 128));
   TRY(check_device_again());
   const hipStream_t s = static_cast<hipStream_t>(stream);
   return by_tile(*p, [&](auto t, auto dp) -> lact_status {
@@ -526,7 +534,7 @@ lact_status lact_rotary(const lact_rotary_problem* p, const void* q, const lact_
   a.head_groups = (int32_t)std::max<int64_t>(a.head_groups, ceil_div((int64_t)a.tok * heads * p->d, 1 << 24));
   a.group = (int32_t)ceil_div(heads, a.head_groups);
   a.head_groups = (int32_t)ceil_div(heads, a.group);
-  TRY(check_grid(groups * a.head_groups));
+  TRY(check_grid(groups * a.head_groups, 256));
   TRY(check_device_again());
   const unsigned grid = (unsigned)(groups * a.head_groups);
   const hipStream_t s = static_cast<hipStream_t>(stream);

@@ -82,3 +82,34 @@ def test_key_splits_fill_the_chip_once(dtype, d, at_once):
     a = lact.Attention(8, 16, 16, d, getattr(lact, "DTYPE_" + dtype), 0.1, 1, 1 << 20, 0, 0)
     need = lact.lib().lact_window_attention_workspace_size(ctypes.byref(a))
     assert need == 128 * (at_once // 128) * (d + 2) * 4   # a row's partial results and statistics, each a multiple of 256
+
+
+FAKE = 1 << 20   # aligned, never dereferenced: every call here is refused first
+
+
+def test_grids_beyond_a_launch_are_refused():
+    """A launch ends at 2^32 - 1 threads, 2^24 - 1 workgroups of 256: what needs
+    more is refused before any device work, not left to fail there."""
+    U, L = lact.ERR_UNSUPPORTED, lact.lib()
+
+    def st(heads, rows, d=8):
+        return ctypes.byref(lact.Strides(heads * rows * d, rows * d, d))
+
+    def attention(B, H, q_len, k_len, d=8, dtype=lact.DTYPE_BF16, kv=None, **kw):
+        kv = kv or H
+        p = lact.Attention(B, H, kv, d, dtype, 0.1, q_len, k_len, kw.get("window", 0), 0)
+        a, b = st(H, q_len, d), st(kv, k_len, d)
+        f = L.lact_window_attention_forward(ctypes.byref(p), FAKE, a, FAKE, b, FAKE, b, None, None, FAKE * 8, a, None,
+                                            FAKE, 1 << 60, None)
+        g = L.lact_window_attention_backward(ctypes.byref(p), FAKE, a, FAKE, b, FAKE, b, None, None, FAKE, a, FAKE,
+                                             FAKE, a, FAKE * 8, a, FAKE * 9, b, FAKE * 10, b, FAKE, 1 << 60, None)
+        return f, g
+
+    assert attention(1 << 18, 1 << 6, 64, 64) == (U, U)            # 2^24 tiles of rows and of keys
+    assert attention(1 << 18, 1 << 6, 1, 64)[0] == U               # 2^24 workgroups of few rows, 256 threads each
+    assert attention(1 << 19, 1 << 6, 1, 64, 128, lact.DTYPE_F32)[0] == U   # 2^25, of 128 threads
+    for B, T in ((1, 1 << 29), (1 << 24, 1)):
+        p = lact.RotaryProblem(B, 1, 0, 8, 4, lact.DTYPE_BF16, 0, 1.0, T, 0)
+        assert L.lact_rotary(ctypes.byref(p), FAKE, st(1, T), None, None, FAKE, None, FAKE * 8, st(1, T), None, None,
+                             None) == U
+    assert "more than a launch" in lact.last_error()
