@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 
 from oracle import lact_block as OB
-from test_gpu_block import DT, check_attention, f64, randn
+from test_gpu_block import DT, check_attention, f64, half_step, randn
 
 torch = pytest.importorskip("torch")
 pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a GPU")]
@@ -199,3 +199,35 @@ def test_waves_that_share_tiles(lact, case):
     out.update(lact.window_attention_backward(q, k, v, out["o"], out["lse"], dO=g, **kw))
     ref = OB.window_attention(f64(q), f64(k), f64(v), window, 3, float(np.float32(d ** -0.5)), lens, lens, f64(g))
     check_attention(ref, out, torch.bfloat16, d, 2 * L * H // Hk, True)
+
+
+@pytest.mark.parametrize("t", ["bf16", "fp32"])
+def test_sines_of_turns(lact, t):
+    """A feature alone in its pair comes out as the sine and the cosine.  fp32:
+    right to 8 half steps of its own size also next to a zero: 4 of the sine
+    function (2 units in the last place), one each of mscale, the put-back
+    rounding of the turn and the result, and a quarter of the turn in fp64
+    (2^-50 of angle, for results from 2^-24 on).  bf16: one half step, and
+    2^-22 of what the hardware's sine and the turn's rounding are off."""
+    rng = np.random.default_rng(24)
+    sign = lambda n: rng.choice([-1.0, 1.0], n)
+    turns = np.concatenate([rng.random(4096) - 0.5, 2.0 ** -rng.uniform(1, 24, 2048) * sign(2048),
+                            0.25 + 2.0 ** -rng.uniform(4, 24, 2048) * sign(2048),
+                            0.5 + 2.0 ** -rng.uniform(4, 24, 2048) * sign(2048), 1e6 * rng.random(2048)])
+    u, fr = half_step(DT[t]), torch.from_numpy(2 * np.pi * turns)
+    for n in range(0, len(turns), 1024):
+        f = fr[n:n + 1024].cuda()
+        for interleaved in (False, True):
+            for axis in (0, 1):
+                q = torch.zeros(1, 1, 1, 2048, device="cuda", dtype=DT[t])
+                (q[..., axis::2] if interleaved else q[..., axis * 1024:(axis + 1) * 1024]).fill_(1.0)
+                y = f64(lact.rotary(q, freqs=f, start=1, interleaved=interleaved))[0, 0, 0]
+                a, b = (y[::2], y[1::2]) if interleaved else (y[:1024], y[1024:])
+                s, c = np.sin(f.cpu().numpy()), np.cos(f.cpu().numpy())
+                for got, ref in ((a, -s if axis else c), (b, c if axis else s)):
+                    tol = np.where(np.abs(ref) > 2.0 ** -24, 8 * u * np.abs(ref), 2.0 ** -24)
+                    if t == "bf16":
+                        tol = u * np.abs(ref) + 2.0 ** -22
+                    off = np.abs(got - ref) - tol
+                    i = np.argmax(off)
+                    assert off[i] <= 0, (got[i], ref[i], f[i].item())
