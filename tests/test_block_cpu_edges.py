@@ -5,6 +5,10 @@ import ctypes
 import numpy as np
 import pytest
 
+import block_precision as BP
+from oracle import lact_block as OB
+from test_gpu_block import ATTENTION
+
 lact = pytest.importorskip("test_layers_amd.lact", reason="liblact.so not built")
 torch = pytest.importorskip("torch")
 
@@ -113,3 +117,33 @@ def test_grids_beyond_a_launch_are_refused():
         assert L.lact_rotary(ctypes.byref(p), FAKE, st(1, T), None, None, FAKE, None, FAKE * 8, st(1, T), None, None,
                              None) == U
     assert "more than a launch" in lact.last_error()
+
+
+# ------------------------------------------------------------------ what fp32 results are held to
+def _fp32_inputs(case):
+    B, H, Hk, d, Lq, Lk = case[:6]
+    rng = np.random.default_rng(sum(case[:8]))
+    return [rng.standard_normal(s).astype(np.float32).astype(np.float64)
+            for s in ((B, H, Lq, d), (B, Hk, Lk, d), (B, Hk, Lk, d), (B, H, Lq, d))]
+
+
+@pytest.mark.parametrize("case", ATTENTION, ids=lambda c: "x".join(str(x) for x in c[:8]))
+def test_bounds_of_fp32_attention_tell_lesser_paths(case):
+    """The bounds that fp32 results are held to pass the formulas themselves,
+    and neither probabilities rounded to bf16's 8 bits nor scores from operands
+    of 11 bits."""
+    B, H, Hk, d, Lq, Lk, window, sinks, ql, kl = case
+    q, k, v, g = _fp32_inputs(case)
+    ref = OB.window_attention(q, k, v, window, sinks, 0.3, ql, kl, g)
+    limits = BP.bounds(q, k, v, g, window, sinks, 0.3, ql, kl, ref)
+    args = (q, k, v, g, window, sinks, 0.3, ql, kl)
+    single, rms = BP.excess(BP.attention(*args), ref, limits)
+    assert max([*single.values(), *rms.values(), 0]) < 0.01
+    sees = [OB.visible(Lq if ql is None else ql[b], Lk if kl is None else kl[b], window, sinks).sum(1)
+            for b in range(B)]
+    if max((int(n.max()) for n in sees if n.size), default=0) < 2:
+        return   # a probability of one is one in any number of bits
+    for name, lesser in (("weights", dict(weight=lambda x: BP.rounded(x, 8))),
+                         ("operands", dict(operand=lambda x: BP.rounded(x, 11)))):
+        _, rms = BP.excess(BP.attention(*args, **lesser), ref, limits)
+        assert min(rms.values()) > 5, (name, rms)
