@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 
 from oracle import lact_block as OB
-from test_gpu_block import DT, check_attention, f64, half_step, randn
+from test_gpu_block import DT, _graph, check_attention, f64, half_step, randn
 
 torch = pytest.importorskip("torch")
 pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a GPU")]
@@ -231,3 +231,47 @@ def test_sines_of_turns(lact, t):
                     off = np.abs(got - ref) - tol
                     i = np.argmax(off)
                     assert off[i] <= 0, (got[i], ref[i], f[i].item())
+
+
+@pytest.mark.parametrize("t", ["bf16", "fp32"])
+@pytest.mark.parametrize("L,lens", [(1, [2000, 77]), (40, [40, 11]), (500, [500, 130])])
+def test_graph_with_rotary_keys_and_lengths(lact, t, L, lens):
+    """q and k turned in one call, k into a cache's slots, a padded batch and its
+    gradients back through rotary, with a workspace of the caller's, captured:
+    every replay is the eager call bit for bit, after the inputs changed too."""
+    gen = torch.Generator("cuda").manual_seed(25)
+    B, H, Hk, d, Lk, dt = 2, 4, 2, 64, 2000, DT[t]
+    q, kn, vn, g = (randn(gen, (B, h, L, d), dt, "tokens") for h in (H, Hk, Hk, H))
+    cache = [randn(gen, (B, Hk, Lk, d), dt) for _ in range(2)]
+    kl = torch.tensor(lens if L == 1 else [Lk - L, Lk - L], device="cuda")
+    ql = None if L == 1 else torch.tensor(lens, device="cuda")
+    fr, _ = lact.rotary_frequencies(d // 2)
+    pos = torch.arange(L, device="cuda").expand(B, L).contiguous() + 5
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+    kw = dict(window=300, sinks=4, q_lens=ql, k_lens=kl)
+    s = {}
+
+    def call():
+        slots = cache[0][:, :, Lk - L:]
+        qr, kr = lact.rotary(q, kn, freqs=fr, positions=pos, k_out=slots)
+        cache[1][:, :, Lk - L:].copy_(vn)
+        o, lse = lact.window_attention(qr, *cache, return_lse=True, workspace=ws, **kw)
+        out = lact.window_attention_backward(qr, *cache, o, lse, dO=g, workspace=ws, **kw)
+        dq, dk = lact.rotary_backward(out["dq"], out["dk"][:, :, Lk - L:], freqs=fr, positions=pos)
+        for n, x in dict(o=o, lse=lse, dq=dq, dk=dk, dv=out["dv"], cache=cache[0]).items():
+            s.setdefault(n, torch.empty_like(x)).copy_(x)
+
+    _graph(call, lambda: list(s.values()))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for _ in range(3):
+        for x in (q, kn, vn, g):
+            x.copy_(torch.randn(x.shape, generator=gen, device="cuda"))
+        kl.sub_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = {n: x.clone() for n, x in s.items()}
+        call()
+        torch.cuda.synchronize()
+        assert all(torch.equal(got[n], s[n]) for n in s)
