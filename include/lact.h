@@ -340,8 +340,13 @@ typedef struct {
  * row, head or sequence), outputs' rows distinct.  q_lens, k_lens: device
  * arrays [batch] of each sequence's rows and keys (clamped to q_len and k_len), NULL: all.
  * Rows of o and lse behind a sequence's q_lens are left as they were; q, k
- * and v behind the lengths are not read.  A NaN or infinity in k or v reaches
- * only rows that see it.  lse [batch, heads, q_len] float32, or NULL.
+ * and v behind the lengths are not read.  Scores, statistics and sums are
+ * float32; for bf16 tensors a probability is rounded to bf16 once, as an
+ * operand of its product with v.  A NaN or infinity in k or v reaches only
+ * rows that see it: rows that are not finite are summed again one key after
+ * another, about 5 ns of the call for each row and key that it sees (one
+ * infinite value that 8192 rows see in windows of 2048 keys: 88 ms).
+ * lse [batch, heads, q_len] float32, or NULL.
  * ws: lact_window_attention_workspace_size bytes, 256-B aligned (may be NULL
  * where that is 0).  o must not overlap an input.
  */
@@ -356,9 +361,11 @@ lact_status lact_window_attention_forward(const lact_attention* p, const void* q
  * Gradients of sum(dO * o) with respect to q, k, v, from the forward's o and
  * lse (lse's own gradient is zero).  dq, dk, dv in io_dtype, shapes of q, k,
  * v, fully written: zero behind the lengths.  Sums are held in float32 and
- * rounded once; a key head's gradient is the sum over its query heads.  dO
- * behind q_lens is not read.  Non-finite inputs give non-finite gradients to
- * what they reach.
+ * rounded once; for bf16 tensors the probabilities P and dS = P (dO.v - dO.o)
+ * are rounded to bf16 once more, as operands of the products with dO, q and k.
+ * A key head's gradient is the sum over its query heads.  dO behind q_lens is
+ * not read.  Non-finite inputs give non-finite gradients to what they reach
+ * and to nothing else, at the forward's price for such rows and keys.
  */
 size_t lact_window_attention_backward_workspace_size(const lact_attention* p);
 lact_status lact_window_attention_backward(const lact_attention* p, const void* q, const lact_strides* sq,

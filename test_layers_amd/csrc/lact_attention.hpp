@@ -799,8 +799,9 @@ constexpr int few_lds() {
 // waves.  Bound by memory: next tokens of 96 sequences of up to 8192 keys,
 // window 4096, 32 heads (8 key heads) of 128: 265 us, 5.6 TB/s of the 1.48 GB
 // that it must read.  Where keys are few, by latency: one sequence of 16
-// heads, window 2048: 8.6 us, and 3.2 more for the join.  Each wave runs its own ring of 32-key tiles with no barrier; the
-// waves join in LDS, the workgroups through `part` in attn_join_kernel.
+// heads, window 2048: 8.7 us, and 3.0 more for the join.  Each wave runs its
+// own ring of 32-key tiles with no barrier; the waves join in LDS, the
+// workgroups through `part` in attn_join_kernel.
 template <typename T, int DP>
 __global__ __launch_bounds__(64 * (few_waves<T, DP>())) void attn_few_kernel(AttnArgs a) {
   using Tile = AttnTile<T, DP>;

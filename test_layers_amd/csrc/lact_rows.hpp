@@ -44,7 +44,8 @@ struct RotaryTensor {
   int32_t heads;
 };
 // n / d for 0 <= n < 2^31 and a divisor that the host knows: a multiplication
-// and a shift (four divisions of every 8-byte item took as long as its memory)
+// and a shift, by the method of Granlund and Montgomery, "Division by invariant
+// integers using multiplication", 1994 (four divisions of every 8-byte item took as long as its memory)
 struct FastDiv {
   uint32_t d, m, s;
   FastDiv() = default;
