@@ -99,9 +99,13 @@ struct AttnTile {
 };
 
 // One direct load of 16 bytes a lane from a uniform base and a lane's offset.
+// The base is moved by the scalar unit first: a vector instruction that wrote
+// it (a spilled one's v_readlane) has to be five wait states before the load,
+// which the compiler does not see here; a scalar move waits for it by itself.
 __device__ __forceinline__ void dma16_at(uint32_t off, const char* base, uint32_t m0) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
-               :
+  const char* at;
+  asm volatile("s_mov_b32 m0, %3\n\ts_mov_b64 %0, %2\n\tglobal_load_lds_dwordx4 %1, %0"
+               : "=&s"(at)
                : "v"(off), "s"(base), "s"(m0)
                : "memory", "m0");
 }
