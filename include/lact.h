@@ -467,6 +467,144 @@ lact_status lact_add_rmsnorm_backward(const lact_norm_problem* p, const void* h,
                                       const void* dy, int64_t ldy, const void* dh, int64_t lddh, void* dx,
                                       int64_t lddx, float* dw, void* ws, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------
+ * Batches of sequences of different lengths.  Their rows lie one after
+ * another: a [heads, tokens, d] tensor (a pointer and strides, of which
+ * `batch` is not looked at) holds the rows of sequence b at tokens
+ * offsets[b] .. offsets[b + 1].  offsets: device int64 [batch + 1], not
+ * decreasing, 0 .. tokens; others are cut to that, and no memory outside the
+ * tensors is touched whatever they hold.
+ *
+ * Packed attention: whole prompts, or texts of a training step, from their
+ * first token on.  Row r of a sequence sees its keys 0 <= j <= r with
+ * j > r - window or j < sinks (window = 0: j <= r), as in window attention
+ * with q_len = k_len.
+ */
+#define LACT_CLEAR_REST 1u   /* rows of o and lse that are no sequence's become zero, not left as they were */
+typedef struct {
+    int32_t batch;      /* sequences, 0 .. 2^24 */
+    int32_t heads, kv_heads, d, io_dtype;   /* as in lact_attention */
+    float scale;
+    int64_t tokens;     /* rows of q, k, v and o, 0 <= tokens < 2^30 */
+    int64_t longest;    /* at least the rows of the longest sequence (those behind are not looked at); <= tokens */
+    int64_t window;     /* >= 0; 0: no limit */
+    int64_t sinks;      /* >= 0 */
+    uint32_t flags;     /* LACT_CLEAR_REST */
+} lact_packed;
+
+/*
+ * q, o [heads, tokens, d], k, v [kv_heads, tokens, d]: 16-byte aligned,
+ * strides as in window attention.  lse [heads, tokens] float32, or NULL.
+ * Numbers, and NaN or infinity in k or v, as in window attention.
+ */
+lact_status lact_packed_attention_forward(const lact_packed* p, const void* q, const lact_strides* sq, const void* k,
+                                          const lact_strides* sk, const void* v, const lact_strides* sv,
+                                          const int64_t* offsets, void* o, const lact_strides* so, float* lse,
+                                          void* stream);
+
+/* Gradients, from the forward's o and lse; rows that are no sequence's are zero.
+ * ws: lact_packed_attention_backward_workspace_size bytes, 256-B aligned. */
+size_t lact_packed_attention_backward_workspace_size(const lact_packed* p);
+lact_status lact_packed_attention_backward(const lact_packed* p, const void* q, const lact_strides* sq, const void* k,
+                                           const lact_strides* sk, const void* v, const lact_strides* sv,
+                                           const int64_t* offsets, const void* o, const lact_strides* so,
+                                           const float* lse, const void* dO, const lact_strides* sdo, void* dq,
+                                           const lact_strides* sdq, void* dk, const lact_strides* sdk, void* dv,
+                                           const lact_strides* sdv, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Paged attention: new tokens of many requests over the keys that each has so
+ * far, which lie in pages of a common pool.  Sequence b has k_lens[b] keys
+ * with its new ones; key j lies in page table[b][j / page], place j % page.
+ * Its row r stands at position p = k_lens[b] - rows + r and sees the keys
+ * j <= p as in window attention.  One row a sequence and chunks of thousands
+ * may come in one batch.
+ */
+typedef struct {
+    int32_t batch;      /* sequences, 0 .. 2^24 */
+    int32_t heads, kv_heads, d, io_dtype;   /* as in lact_attention */
+    float scale;
+    int64_t tokens;     /* rows of q and o, 0 <= tokens < 2^30 */
+    int64_t longest;    /* at least the rows of the longest sequence (those behind are not looked at); <= tokens */
+    int64_t k_len;      /* at least its keys (those behind are not looked at); <= width * page */
+    int64_t window;     /* >= 0; 0: no limit */
+    int64_t sinks;      /* >= 0 */
+    int32_t pages;      /* of the pool, >= 0 */
+    int32_t page;       /* tokens of a page: a multiple of 8 in [8, 65536]; pages * page < 2^31 */
+    int32_t width;      /* entries of a sequence in the table, >= 0; width * page < 2^30 */
+    uint32_t flags;     /* LACT_CLEAR_REST */
+} lact_paged;
+
+/*
+ * q, o [heads, tokens, d] as in packed attention; k_pages, v_pages [pages,
+ * kv_heads, page, d] (batch: the stride of a page), 16-byte aligned, strides
+ * multiples of 16 bytes, a token's at most 2^27 bytes: pages of token-major
+ * and of head-major rows alike.  offsets as above; k_lens: device int64
+ * [batch]; table: device int32 [batch, width].  Entries of pages that no row
+ * sees, before a window or behind the last key, are not used (any value; one
+ * outside the pool never leads outside it), nor what lies in places behind
+ * the last key.  lse [heads, tokens] float32, or NULL.
+ * ws: lact_paged_attention_workspace_size bytes, 256-B aligned (may be NULL
+ * where that is 0).
+ */
+size_t lact_paged_attention_workspace_size(const lact_paged* p);
+lact_status lact_paged_attention(const lact_paged* p, const void* q, const lact_strides* sq, const void* k_pages,
+                                 const lact_strides* sk, const void* v_pages, const lact_strides* sv,
+                                 const int64_t* offsets, const int64_t* k_lens, const int32_t* table, void* o,
+                                 const lact_strides* so, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Places of a step's new tokens.  Request b holds lens[b] tokens (negative: 0)
+ * in the pages table[b][0 .. ceil(lens[b] / page)) and gets counts[b] more
+ * (negative: none), at rows offsets[b] .. offsets[b + 1] of the step's
+ * `tokens` rows: offsets is the sum of the counts, cut where the rows end.
+ * The pages that it needs more are the last of free[0 .. have), request by
+ * request, and are entered in the table.  A request whose tokens do not fit
+ * its row of the table, or whose pages with those that requests before it
+ * asked for are more than `have`, gets none: its k_lens stays lens[b], its
+ * rows have slot -1.  Outputs, all device arrays:
+ *   offsets [batch + 1], k_lens [batch]: lens[b] and what was added;
+ *   slots [tokens]: page * (tokens of a page) + place of each row, -1 for rows
+ *     that have none (behind the last request's, too);
+ *   positions [tokens]: lens[b] + its number among the request's rows, 0
+ *     behind the last request's;
+ *   left [2]: free pages that are left (free[0 .. left[0])), requests that
+ *     got none.  `have` may be left itself.
+ * lens, counts and free are only read: a call repeated gives the same.
+ */
+typedef struct {
+    int32_t batch;      /* requests, 0 .. 2^24 */
+    int32_t page;       /* as in lact_paged */
+    int32_t width;      /* entries of a request in the table, >= 0; width * page < 2^30 */
+    int32_t entries;    /* of `free`, >= 0: `have` is cut to that */
+    int64_t tokens;     /* rows of the step, 0 <= tokens < 2^30 */
+} lact_slots;
+/* int64 arrays 8-byte, table and free 4-byte aligned.
+ * ws: lact_page_slots_workspace_size bytes, 256-B aligned (may be NULL where that is 0). */
+size_t lact_page_slots_workspace_size(const lact_slots* p);
+lact_status lact_page_slots(const lact_slots* p, const int64_t* lens, const int64_t* counts, int32_t* table,
+                            const int32_t* free, const int64_t* have, int64_t* offsets, int64_t* k_lens,
+                            int64_t* slots, int64_t* positions, int64_t* left, void* ws, size_t ws_bytes,
+                            void* stream);
+
+/*
+ * Rows of k and v [kv_heads, tokens, d] into their slots of k_pages and
+ * v_pages [pages, kv_heads, page, d], all in io_dtype, 16-byte aligned with
+ * strides in multiples of 16 bytes.  Rows whose slot is negative or behind the
+ * pool are not written.  Of rows with the same slot one is kept, in each
+ * 16 bytes any of them.
+ */
+typedef struct {
+    int32_t kv_heads;   /* 1 .. 65536 */
+    int32_t d;          /* width of a head: a multiple of 16 bytes, at most 8192 elements */
+    int32_t io_dtype;
+    int32_t pages, page;   /* as in lact_paged */
+    int64_t tokens;     /* 0 <= tokens < 2^30 */
+} lact_write;
+lact_status lact_page_write(const lact_write* p, const void* k, const lact_strides* sk, const void* v,
+                            const lact_strides* sv, const int64_t* slots, void* k_pages, const lact_strides* skp,
+                            void* v_pages, const lact_strides* svp, void* stream);
+
 /* Static text for a status code. */
 const char* lact_status_str(lact_status s);
 
@@ -498,11 +636,12 @@ const char* lact_last_error(void);
 #define LACT_K_BWD_ELEM 9  /* backward: elementwise, row and reduction kernels */
 #define LACT_K_NSRED 10    /* Newton-Schulz input: the sum of the split partials with its row
                               sums of squares (and, with momentum, the new momentum) */
-#define LACT_K_ATTN 11     /* window attention forward (the join of split keys included) */
-#define LACT_K_ATTN_BWD 12 /* window attention backward */
+#define LACT_K_ATTN 11     /* window, packed and paged attention forward (the join of split keys included) */
+#define LACT_K_ATTN_BWD 12 /* window and packed attention backward */
 #define LACT_K_ROTARY 13   /* rotary positions */
 #define LACT_K_NORM 14     /* add and norm, forward and backward */
-#define LACT_K_COUNT 15
+#define LACT_K_PAGES 15    /* page slots and page writes */
+#define LACT_K_COUNT 16
 lact_status lact_timing_enable(int32_t kclass, int32_t on);
 lact_status lact_timing_read(int32_t kclass, double* total_ms, int64_t* launches);
 

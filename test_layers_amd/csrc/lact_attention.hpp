@@ -41,7 +41,14 @@ struct AttnStride {
   int64_t b, h, l;
 };
 
+// How a batch lies in memory.  PADDED: [batch, heads, tokens, d] and lengths.
+// PACKED: [heads, tokens, d], with the rows and keys of sequence b at tokens
+// offsets[b] .. offsets[b + 1].  PAGED: rows so, keys in pages of a pool
+// [pages, heads, page, d] that each sequence's row of a table names.
+enum class Lie { PADDED, PACKED, PAGED };
+
 struct AttnArgs {
+  static constexpr Lie LIE = Lie::PADDED;
   const char *q, *k, *v, *o, *dO;
   char *out, *dq, *dk, *dv;
   AttnStride sq, sk, sv, so, sdo, sdq, sdk, sdv;
@@ -59,6 +66,22 @@ struct AttnArgs {
   int32_t sink_tiles, span;        // backward: key tiles with sinks; rows of one of their splits
   float c;                         // scale * log2(e): exp(scale s) = exp2(c s)
   float scale;
+};
+struct PackedArgs : AttnArgs {   // Lq: tokens of all sequences, the strides' b unused
+  static constexpr Lie LIE = Lie::PACKED;
+  const int64_t* offsets;  // [B + 1], device
+  int32_t most;            // rows of a sequence (and its keys, packed) that are looked at
+  int32_t slots;           // tiles of all sequences together, see find_tile; 0: `tiles` for each
+  int32_t main;            // workgroups that compute; those behind them clear rows of no sequence
+  int32_t rest;            // how many those are
+};
+struct PagedArgs : PackedArgs {  // Lk: keys of a sequence that are looked at
+  static constexpr Lie LIE = Lie::PAGED;
+  const int32_t* table;    // [B, width]
+  int32_t width, pages;
+  FastDiv by_page;
+  int32_t few;             // sequences of up to so many rows are the few-row kernel's, others the forward's
+  int32_t by_token;        // join: one workgroup for each row of the forward's sequences, not of the few-row kernel's
 };
 
 // ------------------------------------------------------------------ tiles
@@ -140,6 +163,102 @@ struct Stager {
       Tile::template stage<R, NW>(tile, base, stride, row0, rmax, cmax, wave, lane);
     }
   }
+};
+
+// The copies of a K and a V tile, and single rows of both.
+template <typename T, int DP, int R, int NW>
+struct KeyRows {
+  static constexpr int TB = R * AttnTile<T, DP>::CPR * 16;
+  Stager<T, DP, R, NW> sk, sv;
+  __device__ __forceinline__ KeyRows(const char* kb, int64_t kl, const char* vb, int64_t vl, int rmax, int cmax,
+                                     int wave, int lane)
+      : sk(kb, kl, rmax, cmax, wave, lane), sv(vb, vl, rmax, cmax, wave, lane) {}
+  __device__ __forceinline__ void issue(char* tile, int row0) const {
+    sk.issue(tile, row0);
+    sv.issue(tile + TB, row0);
+  }
+  __device__ __forceinline__ const char* k(int j) const { return sk.base + j * sk.stride; }
+  __device__ __forceinline__ const char* v(int j) const { return sv.base + j * sv.stride; }
+};
+
+// The same with the offsets formed for every tile, for waves that need the registers.
+template <typename T, int DP, int R>
+struct LooseRows {
+  using Tile = AttnTile<T, DP>;
+  const char *kb, *vb;
+  int64_t kl, vl;
+  int rmax, cmax, lane;
+  __device__ __forceinline__ void issue(char* tile, int row0) const {
+    Tile::template stage<R, 1>(tile, kb, kl, row0, rmax, cmax, 0, lane);
+    Tile::template stage<R, 1>(tile + R * Tile::CPR * 16, vb, vl, row0, rmax, cmax, 0, lane);
+  }
+  __device__ __forceinline__ const char* k(int j) const { return kb + j * kl; }
+  __device__ __forceinline__ const char* v(int j) const { return vb + j * vl; }
+};
+
+// The same out of pages.  The rows that a wave copies at once, 64 / CPR <= 8
+// of them at a multiple of as many, lie in one page, since pages are multiples
+// of 8 rows: their page is a scalar, and a copy has a scalar base and the
+// lanes' kept offsets, as in a dense matrix.  An entry outside the pool is
+// taken as the nearest page inside: what it holds is masked (entries before a
+// window, say), and no memory outside the pool is touched.
+template <typename T, int DP, int R, int NW>
+struct PageRows {
+  using Tile = AttnTile<T, DP>;
+  static constexpr int TB = R * Tile::CPR * 16, N = R * Tile::CPR / (WAVE * NW), GROUP = WAVE / Tile::CPR;
+  static_assert(GROUP <= 8, "a group of rows lies in one page");
+  typedef const __attribute__((address_space(4))) int32_t* Entries;  // scalar loads: written before the kernel
+  const char *kb, *vb;
+  AttnStride ks, vs;
+  Entries table;
+  FastDiv by_page;
+  int last, rmax, cmax, wave, lane;
+  uint32_t ko[N], vo[N];
+  __device__ __forceinline__ PageRows(const PagedArgs& a, int b, int hk, int rmax_, int wave_, int lane_)
+      : kb(a.k + hk * a.sk.h), vb(a.v + hk * a.sv.h), ks(a.sk), vs(a.sv),
+        table((Entries)(uintptr_t)(a.table + (int64_t)b * a.width)), by_page(a.by_page), last(a.pages - 1), rmax(rmax_),
+        cmax(a.d * (int)sizeof(T) / 16 - 1), wave(wave_), lane(lane_) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int row = (i * NW + wave) * GROUP + lane / Tile::CPR;
+      const uint32_t c = (uint32_t)min((lane % Tile::CPR) ^ Tile::f(row), cmax) * 16u;
+      ko[i] = (uint32_t)(lane / Tile::CPR) * (uint32_t)ks.l + c;
+      vo[i] = (uint32_t)(lane / Tile::CPR) * (uint32_t)vs.l + c;
+    }
+  }
+  __device__ __forceinline__ void issue(char* tile, int row0) const {
+    const uint32_t m0 = __builtin_amdgcn_readfirstlane(lds_off(tile) + (uint32_t)(wave * WAVE * 16));
+    if (row0 + R - 1 <= rmax) {
+      int page[N], in[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int row = __builtin_amdgcn_readfirstlane(row0 + (i * NW + wave) * GROUP), n = (int)by_page.div((uint32_t)row);
+        in[i] = row - n * (int)by_page.d;
+        page[i] = table[n];
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int64_t e = max(0, min(page[i], last));
+        dma16_at(ko[i], kb + e * ks.b + in[i] * ks.l, m0 + (uint32_t)(i * NW * WAVE * 16));
+        dma16_at(vo[i], vb + e * vs.b + in[i] * vs.l, m0 + (uint32_t)(TB + i * NW * WAVE * 16));
+      }
+    } else {  // rows behind the last are read from it
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int row = (i * NW + wave) * GROUP + lane / Tile::CPR, gr = min(row0 + row, rmax);
+        const int c = min((lane % Tile::CPR) ^ Tile::f(row), cmax) * 16;
+        dma16(k(gr) + c, m0 + (uint32_t)(i * NW * WAVE * 16));
+        dma16(v(gr) + c, m0 + (uint32_t)(TB + i * NW * WAVE * 16));
+      }
+    }
+  }
+  __device__ __forceinline__ const char* row(const char* base, const AttnStride& s, int j) const {
+    const int n = (int)by_page.div((uint32_t)j);
+    const int64_t e = max(0, min(table[n], last));
+    return base + e * s.b + (int64_t)(j - n * (int)by_page.d) * s.l;
+  }
+  __device__ __forceinline__ const char* k(int j) const { return row(kb, ks, j); }
+  __device__ __forceinline__ const char* v(int j) const { return row(vb, vs, j); }
 };
 
 // ------------------------------------------------------------------ products
@@ -319,6 +438,89 @@ __device__ __forceinline__ int seq_len(const int64_t* lens, int b, int most) {
   return (int)(n < 0 ? 0 : n > most ? most : n);
 }
 
+// A sequence: its lengths, and in a packed batch the token of its first row.
+struct AttnSeq {
+  int b, qlen, klen, first;
+  __device__ AttnSeq(const AttnArgs& a, int b_)
+      : b(b_), qlen(seq_len(a.q_lens, b_, a.Lq)), klen(seq_len(a.k_lens, b_, a.Lk)), first(0) {}
+  __device__ AttnSeq(const PackedArgs& a, int b_) : b(b_) {
+    first = __builtin_amdgcn_readfirstlane(seq_len(a.offsets, b, a.Lq));
+    qlen = __builtin_amdgcn_readfirstlane(min(max(seq_len(a.offsets, b + 1, a.Lq) - first, 0), a.most));
+    klen = qlen;
+  }
+  __device__ AttnSeq(const PagedArgs& a, int b_) : AttnSeq(static_cast<const PackedArgs&>(a), b_) {
+    klen = __builtin_amdgcn_readfirstlane(seq_len(a.k_lens, b, a.Lk));
+  }
+  // bytes before the sequence's first row, or before its statistics of a head
+  template <class A>
+  __device__ __forceinline__ int64_t at(const A&, const AttnStride& s) const {
+    if constexpr (A::LIE == Lie::PADDED) return b * s.b;
+    else return first * s.l;
+  }
+  template <class A>
+  __device__ __forceinline__ int64_t stat(const A& a, int h) const {
+    if constexpr (A::LIE == Lie::PADDED) return ((int64_t)b * a.H + h) * a.Lq;
+    else return (int64_t)h * a.Lq + first;
+  }
+};
+template <class A>
+__device__ __forceinline__ int64_t stats_of(const A& a) {  // statistics of all rows and heads
+  return (int64_t)(A::LIE == Lie::PADDED ? a.B : 1) * a.H * a.Lq;
+}
+
+// The last of the numbers 0 .. n - 1 for which `upto` holds, which is true of
+// none or of the first ones: 64 of them are tried at once.  -1: none.
+template <class F>
+__device__ __forceinline__ int find_last(int n, int lane, F&& upto) {
+  int lo = 0;
+  while (n > 0) {
+    const int step = (n + WAVE - 1) / WAVE;
+    const int i = lane * step;
+    const int hits = (int)__popcll(__ballot(i < n && upto(lo + min(i, n - 1))));
+    if (hits == 0) return lo - 1;
+    lo += (hits - 1) * step;
+    if (step == 1) return lo;
+    n = min(step, n - (hits - 1) * step);
+    lo += 1, n -= 1;  // the first of them is known
+  }
+  return lo - 1;
+}
+
+// The sequence (b < 0: none) and its tile of BM rows that workgroup `id` of a
+// packed batch takes.  The host does not know the lengths: it numbers slots,
+// of which sequence b has those from offsets[b] / BM + b on.  Rounded down,
+// these leave room for its tiles and at most one more, and T / BM + B are
+// enough for all.  Where rows have unequal work the long ones go first.
+template <class A>
+__device__ __forceinline__ void find_tile(const A& a, int id, int BM, int lane, bool long_last, int& b, int& tile) {
+  if (a.slots == 0) {
+    tile = long_last ? id / a.B : a.tiles - 1 - id / a.B;
+    b = id % a.B;
+    return;
+  }
+  const int s = long_last ? id : a.slots - 1 - id;
+  auto slot = [&](int i) { return seq_len(a.offsets, i, a.Lq) / BM + i; };
+  b = __builtin_amdgcn_readfirstlane(find_last(a.B, lane, [&](int i) { return slot(i) <= s; }));
+  tile = b < 0 ? 0 : __builtin_amdgcn_readfirstlane(s - slot(b));
+}
+
+// Clears rows of no sequence, those before the first and behind the last: part
+// `part` of `parts`, by a workgroup.  x [heads, tokens, d], lse [heads, tokens]
+// (null: none).
+template <class A>
+__device__ __forceinline__ void clear_rest(const A& a, char* x, const AttnStride& s, int heads, int bytes, float* lse,
+                                           int part, int parts) {
+  const int before = seq_len(a.offsets, 0, a.Lq), behind = max(before, seq_len(a.offsets, a.B, a.Lq));
+  const int64_t rows = before + a.Lq - behind, per = bytes / 16;
+  auto token = [&](int64_t r) { return r < before ? r : behind + (r - before); };
+  for (int64_t i = (int64_t)part * blockDim.x + threadIdx.x; x && i < rows * heads * per; i += (int64_t)parts * blockDim.x) {
+    const int64_t r = i / per / heads, h = i / per % heads;
+    *reinterpret_cast<uint4*>(x + h * s.h + token(r) * s.l + i % per * 16) = zero4();
+  }
+  for (int64_t i = (int64_t)part * blockDim.x + threadIdx.x; lse && i < rows * heads; i += (int64_t)parts * blockDim.x)
+    lse[i / rows * a.Lq + token(i % rows)] = 0.f;
+}
+
 // Whether the row at position p sees key k + o, for a run of offsets o
 struct Seen {
   int hi, lo, first;
@@ -448,10 +650,9 @@ __device__ __forceinline__ bool settled(const float (&x)[2], int d, int lane) {
 // value of the type's range leaves fp32 on the way: relative to the lagging
 // maximum of the products (see AttnRows::follow) a sum of values from 2^104 on
 // may have, which is one way to come here.
-template <typename T>
-__device__ __forceinline__ void slow_o(float (&x)[2], const char* q, const char* kb, int64_t kl, const char* vb,
-                                       int64_t vl, const AttnArgs& a, int p, float m, const KeyTiles& kt, int i0,
-                                       int i1, int di, int bn, int lane) {
+template <typename T, class Keys>
+__device__ __forceinline__ void slow_o(float (&x)[2], const char* q, const Keys& keys, const AttnArgs& a, int p,
+                                       float m, const KeyTiles& kt, int i0, int i1, int di, int bn, int lane) {
   const Lane2<T> qq(q, a.d, lane);
   x[0] = x[1] = 0.f;
 #pragma unroll 1
@@ -459,8 +660,8 @@ __device__ __forceinline__ void slow_o(float (&x)[2], const char* q, const char*
 #pragma unroll 1
     for (int j = kt.at(i) * bn; j < kt.at(i) * bn + bn && j <= p; ++j) {
       if (j <= p - a.window && j >= a.sinks) continue;
-      const float pr = __builtin_amdgcn_exp2f(fmaf(qq.dot(Lane2<T>(kb + j * kl, a.d, lane)), a.c, -m));
-      const Lane2<T> v(vb + j * vl, a.d, lane);
+      const float pr = __builtin_amdgcn_exp2f(fmaf(qq.dot(Lane2<T>(keys.k(j), a.d, lane)), a.c, -m));
+      const Lane2<T> v(keys.v(j), a.d, lane);
 #pragma unroll
       for (int e = 0; e < 2; ++e) x[e] = fmaf(pr, v.x[e], x[e]);
       if (settled(x, a.d, lane)) return;
@@ -647,9 +848,23 @@ constexpr int attn_bn() { return DP * (int)sizeof(T) > 256 ? 32 : 64; }
 // Where a workgroup works: head and tile.  Query heads that share a key head
 // come next to each other, then tiles, so that those reading the same keys
 // run together, and (xcd_remap) mostly on one XCD with its L2.
+//
+// In a packed batch key heads are innermost instead, so that consecutive
+// workgroups, which go to the XCDs in turn, put the same ones on an XCD and
+// leave each with as many long tiles as the others.
 struct AttnPlace {
-  int b, hk, h, tile;
-  __device__ AttnPlace(int id, const AttnArgs& a) {
+  int b, hk, h, tile, split = 0;
+  __device__ AttnPlace(int id, int BM, int lane, const PackedArgs& a, int splits = 1) {
+    const int groups = a.G / a.hg;
+    hk = id % a.Hk;
+    id /= a.Hk;
+    h = hk * a.G + id % groups * a.hg;
+    id /= groups;
+    split = id % splits;
+    find_tile(a, id / splits, BM, lane, false, b, tile);
+  }
+  __device__ AttnPlace(int id, int, int lane, const AttnArgs& a, int = 1) {
+    id = xcd_remap(id, gridDim.x);
     const int groups = a.G / a.hg;
     h = id % groups * a.hg;
     id /= groups;
@@ -675,57 +890,72 @@ struct AttnPlace {
 // 55 % of the time; 16 heads, d = 64: 325 us, 820 TFLOP/s, 45 %; no LDS bank
 // conflicts.  Tiles of 32 keys with three waves a SIMD took 1.47 ms for 1.17
 // of these at the time: too few products between a tile's waits.
-template <typename T, int DP, int KS>
-__global__ __launch_bounds__(256, (attn_waves<T, DP>())) void attn_fwd_kernel(AttnArgs a) {
+template <typename T, int DP, int KS, class A = AttnArgs>
+__global__ __launch_bounds__(256, (attn_waves<T, DP>())) void attn_fwd_kernel(A a) {
   using Tile = AttnTile<T, DP>;
+  constexpr bool PAGED = A::LIE == Lie::PAGED;
   constexpr int NW = 4, RG = NW / KS, BN = attn_bn<T, DP>(), TB = BN * Tile::CPR * 16;
   __shared__ __align__(1024) char lds[4 * TB];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  AttnPlace at(xcd_remap(blockIdx.x, gridDim.x), a);
-  const int qlen = seq_len(a.q_lens, at.b, a.Lq), klen = seq_len(a.k_lens, at.b, a.Lk);
+  if constexpr (A::LIE != Lie::PADDED)
+    if ((int)blockIdx.x >= a.main)
+      return clear_rest(a, a.out, a.so, a.H, a.d * (int)sizeof(T), a.lse, (int)blockIdx.x - a.main, a.rest);
   const int rg = wave % RG, ks = wave / RG;  // head and rows of the wave; its part of a tile
   const int BM = 32 * RG / a.hg;             // rows of the workgroup
+  AttnPlace at(blockIdx.x, BM, lane, a, a.splits);
+  if (A::LIE != Lie::PADDED && at.b < 0) return;
+  const AttnSeq seq(a, at.b);
+  const int qlen = seq.qlen, klen = seq.klen;
+  if constexpr (PAGED)
+    if (qlen <= a.few) return;
   at.h += rg % a.hg;
   const int r0 = at.tile * BM, rw = r0 + 32 * (rg / a.hg), off = klen - qlen;
   if (r0 >= qlen) return;
   const int row = rw + (lane & 31), cmax = a.d * (int)sizeof(T) / 16 - 1;
-  const char* kb = a.k + at.b * a.sk.b + at.hk * a.sk.h;
-  const char* vb = a.v + at.b * a.sv.b + at.hk * a.sv.h;
+  const char* qb = a.q + seq.at(a, a.sq) + at.h * a.sq.h;
   AttnRows<T, DP> w;
   w.clear();
-  load_rows(w.q, a.q + at.b * a.sq.b + at.h * a.sq.h + (int64_t)min(row, qlen - 1) * a.sq.l, cmax, lane);
+  load_rows(w.q, qb + (int64_t)min(row, qlen - 1) * a.sq.l, cmax, lane);
   w.p = off + row;
   w.w = {off + rw, off + min(rw + 31, qlen - 1)};
   const KeyTiles kt(off + r0, off + min(r0 + BM, qlen) - 1, a.window, a.sinks, BN);
-  const Stager<T, DP, BN, NW> sk(kb, a.sk.l, klen - 1, cmax, wave, lane), sv(vb, a.sv.l, klen - 1, cmax, wave, lane);
+  const auto keys = [&] {
+    if constexpr (PAGED) return PageRows<T, DP, BN, NW>(a, at.b, at.hk, klen - 1, wave, lane);
+    else return KeyRows<T, DP, BN, NW>(a.k + seq.at(a, a.sk) + at.hk * a.sk.h, a.sk.l, a.v + seq.at(a, a.sv) + at.hk * a.sv.h,
+                                       a.sv.l, klen - 1, cmax, wave, lane);
+  }();
   const AttnAddr<DP> addr(lane);
+  // the workgroup's tiles: all, or a split's (from an even one on: the ring's first place)
+  int i0 = 0, i1 = kt.total;
+  if constexpr (PAGED) {
+    auto cut = [&](int s) { return (int)((int64_t)kt.total * s / a.splits) & ~1; };
+    if (a.splits > 1) {
+      i0 = cut(at.split);
+      if (at.split + 1 < a.splits) i1 = cut(at.split + 1);
+    }
+  }
   // ring of two: tile i + 1 is copied while tile i is computed
   auto arrive = [&](int i, char* other) {
     wait_lgkm0();
     wait_vm<0>();
     bar();
-    if (i + 1 < kt.total) {
-      sk.issue(other, kt.at(i + 1) * BN);
-      sv.issue(other + TB, kt.at(i + 1) * BN);
-    }
+    if (i + 1 < i1) keys.issue(other, kt.at(i + 1) * BN);
   };
   auto edge = [&](int i) {
     char* t = lds + (i & 1) * 2 * TB;
     arrive(i, lds + (2 - 2 * (i & 1)) * TB);
     if (w.w.lo <= w.w.hi) w.template tile<BN, KS>(t, t + TB, ks, kt.at(i) * BN, a.window, a.sinks, a.c, lane);
   };
-  if (kt.total > 0) {
-    sk.issue(lds, kt.at(0) * BN);
-    sv.issue(lds + TB, kt.at(0) * BN);
-  }
+  if (i0 < i1) keys.issue(lds, kt.at(i0) * BN);
   // Tiles that all rows of the workgroup see whole run in a loop of their own,
   // two a round: with nothing but straight code in it the sums stay in their
   // registers (with the edges' branches inside the loop the compiler copied
   // all 64 twice a tile).
-  int i = 0;
+  int i = i0;
   if constexpr (sizeof(T) == 2 && KS == 1) {
     int lo, hi;
     kt.whole(off + r0, off + min(r0 + BM, qlen) - 1, a.window, BN, r0 + BM <= qlen, lo, hi);
+    if constexpr (PAGED) lo = min(lo, i1), hi = min(hi, i1);
     for (; i < lo; ++i) edge(i);
     for (; i + 1 < hi; i += 2) {
       arrive(i, lds + 2 * TB);
@@ -735,7 +965,7 @@ __global__ __launch_bounds__(256, (attn_waves<T, DP>())) void attn_fwd_kernel(At
     }
   }
 #pragma unroll 1
-  for (; i < kt.total; ++i) edge(i);
+  for (; i < i1; ++i) edge(i);
   float l = pair_sum(w.l);
   if constexpr (KS == 2) {
     static_assert(RG * (32 * DP + 64) * 4 <= 4 * TB, "the join's place");
@@ -770,18 +1000,25 @@ __global__ __launch_bounds__(256, (attn_waves<T, DP>())) void attn_fwd_kernel(At
       }
   }
   const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-  char* out = a.out + at.b * a.so.b + at.h * a.so.h;
+  char* out = a.out + seq.at(a, a.so) + at.h * a.so.h;
+  // a split's result and statistics, by token, head and split
+  auto part = [&](int r) { return (((int64_t)(seq.first + r) * a.H + at.h) * a.splits + at.split); };
   if (row < qlen) {
-    store_rows<T, DP>(w.o, inv, out + row * a.so.l, a.d, lane);
-    if (a.lse && lane < 32)
-      a.lse[((int64_t)at.b * a.H + at.h) * a.Lq + row] = l == 0.f ? -__builtin_huge_valf() : w.m * LN2 + logf(l);
+    if (PAGED && a.splits > 1) {
+      store_rows<float, DP>(w.o, inv, reinterpret_cast<char*>(a.part + part(row) * a.d), a.d, lane);
+      if (lane < 32) *reinterpret_cast<float2*>(a.part_ml + part(row) * 2) = make_float2(w.m, l);
+    } else {
+      store_rows<T, DP>(w.o, inv, out + row * a.so.l, a.d, lane);
+      if (a.lse && lane < 32)
+        a.lse[seq.stat(a, at.h) + row] = l == 0.f ? -__builtin_huge_valf() : w.m * LN2 + logf(l);
+    }
   }
   for (uint32_t bad = not_finite(w.o) & (uint32_t)__ballot(row < qlen && l == l); bad; bad &= bad - 1) {
     const int n = __builtin_ctz(bad), r = rw + n;
     float x[2];
-    slow_o<T>(x, a.q + at.b * a.sq.b + at.h * a.sq.h + r * a.sq.l, kb, a.sk.l, vb, a.sv.l, a, off + r,
-              of_lane(log2_sum(w.m, l), n), kt, 0, kt.total, 1, BN, lane);
-    store_lane2<T>(out + r * a.so.l, x, a.d, lane);
+    slow_o<T>(x, qb + r * a.sq.l, keys, a, off + r, of_lane(log2_sum(w.m, l), n), kt, i0, i1, 1, BN, lane);
+    if (PAGED && a.splits > 1) store_lane2<float>(reinterpret_cast<char*>(a.part + part(r) * a.d), x, a.d, lane);
+    else store_lane2<T>(out + r * a.so.l, x, a.d, lane);
   }
 }
 
@@ -806,35 +1043,40 @@ constexpr int few_lds() {
 // heads, window 2048: 8.7 us, and 3.0 more for the join.  Each wave runs its
 // own ring of 32-key tiles with no barrier; the waves join in LDS, the
 // workgroups through `part` in attn_join_kernel.
-template <typename T, int DP>
-__global__ __launch_bounds__(64 * (few_waves<T, DP>())) void attn_few_kernel(AttnArgs a) {
+template <typename T, int DP, class A = AttnArgs>
+__global__ __launch_bounds__(64 * (few_waves<T, DP>())) void attn_few_kernel(A a) {
   using Tile = AttnTile<T, DP>;
+  constexpr bool PAGED = A::LIE == Lie::PAGED;
   constexpr int NW = few_waves<T, DP>(), TB = few_tile<T, DP>(), WB = few_lds<T, DP>() / NW;
   __shared__ __align__(1024) char lds[few_lds<T, DP>()];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int split = blockIdx.x % a.splits, tile = blockIdx.x / a.splits % a.tiles, bk = blockIdx.x / a.splits / a.tiles;
   const int hk = bk % a.Hk, b = bk / a.Hk;
-  const int qlen = seq_len(a.q_lens, b, a.Lq), klen = seq_len(a.k_lens, b, a.Lk);
+  if constexpr (PAGED)
+    if ((int)blockIdx.x >= a.main)
+      return clear_rest(a, a.out, a.so, a.H, a.d * (int)sizeof(T), a.lse, (int)blockIdx.x - a.main, a.rest);
+  const AttnSeq seq(a, b);
+  const int qlen = seq.qlen, klen = seq.klen;
+  if constexpr (PAGED)
+    if (qlen > a.few) return;
   const int t0 = 32 * tile / a.G;  // the first row's token
   if (t0 >= qlen) return;
-  const int off = klen - qlen, rows = a.G * a.Lq, n = lane & 31, at = 32 * tile + n;
+  const int off = klen - qlen, rows = a.G * (PAGED ? qlen : a.Lq), n = lane & 31, at = 32 * tile + n;
   const int row = min(at, rows - 1), tok = row / a.G, cmax = a.d * (int)sizeof(T) / 16 - 1;
-  const char* kb = a.k + b * a.sk.b + hk * a.sk.h;
-  const char* vb = a.v + b * a.sv.b + hk * a.sv.h;
+  const char* qb = a.q + seq.at(a, a.sq);
   AttnRows<T, DP> w;
   w.clear();
-  load_rows(w.q, a.q + b * a.sq.b + (int64_t)(hk * a.G + row % a.G) * a.sq.h +
-                            (int64_t)min(tok, qlen - 1) * a.sq.l, cmax, lane);
+  load_rows(w.q, qb + (int64_t)(hk * a.G + row % a.G) * a.sq.h + (int64_t)min(tok, qlen - 1) * a.sq.l, cmax, lane);
   w.p = off + min(tok, qlen - 1);
   w.w = {off + t0, off + min((32 * tile + 31) / a.G, qlen - 1)};
   const KeyTiles kt(w.w.lo, w.w.hi, a.window, a.sinks, 32);
   const int i0 = (int)((int64_t)kt.total * split / a.splits), i1 = (int)((int64_t)kt.total * (split + 1) / a.splits);
   char* ring = lds + wave * WB;
-  auto issue = [&](int i, int buf) {
-    char* t = ring + buf * 2 * TB;
-    Tile::template stage<32, 1>(t, kb, a.sk.l, kt.at(i) * 32, klen - 1, cmax, 0, lane);
-    Tile::template stage<32, 1>(t + TB, vb, a.sv.l, kt.at(i) * 32, klen - 1, cmax, 0, lane);
-  };
+  const auto keys = [&] {
+    if constexpr (PAGED) return PageRows<T, DP, 32, 1>(a, b, hk, klen - 1, 0, lane);
+    else return LooseRows<T, DP, 32>{a.k + b * a.sk.b + hk * a.sk.h, a.v + b * a.sv.b + hk * a.sv.h, a.sk.l, a.sv.l, klen - 1, cmax, lane};
+  }();
+  auto issue = [&](int i, int buf) { keys.issue(ring + buf * 2 * TB, kt.at(i) * 32); };
   if (i0 + wave < i1) issue(i0 + wave, 0);
   int buf = 0;
   for (int i = i0 + wave; i < i1; i += NW, buf ^= 1) {
@@ -865,8 +1107,8 @@ __global__ __launch_bounds__(64 * (few_waves<T, DP>())) void attn_few_kernel(Att
   for (; bad; bad &= bad - 1) {
     const int i = __builtin_ctz(bad), r = of_lane(row, i), t = min(r / a.G, qlen - 1);
     float x[2];
-    slow_o<T>(x, a.q + b * a.sq.b + (int64_t)(hk * a.G + r % a.G) * a.sq.h + t * a.sq.l, kb, a.sk.l, vb, a.sv.l, a,
-              off + t, of_lane(lsum == 0.f ? __builtin_huge_valf() : w.m, i), kt, i0 + wave, i1, NW, 32, lane);
+    slow_o<T>(x, qb + (int64_t)(hk * a.G + r % a.G) * a.sq.h + t * a.sq.l, keys, a, off + t,
+              of_lane(lsum == 0.f ? __builtin_huge_valf() : w.m, i), kt, i0 + wave, i1, NW, 32, lane);
     mine[lane * 32 + i] = x[0];
     if (lane + 64 < DP) mine[(lane + 64) * 32 + i] = x[1];
   }
@@ -889,8 +1131,9 @@ __global__ __launch_bounds__(64 * (few_waves<T, DP>())) void attn_few_kernel(Att
   if (at >= rows || tok >= qlen) return;
   constexpr int PER = DP / (2 * NW);  // columns of a thread
   const int c0 = (int)(threadIdx.x >> 5) * PER;
-  float* pr = a.part + (((int64_t)bk * rows + at) * a.splits + split) * a.d;
-  char* orow = a.out + b * a.so.b + (int64_t)(hk * a.G + row % a.G) * a.so.h + (int64_t)tok * a.so.l;
+  const int64_t place = PAGED ? (int64_t)(seq.first + tok) * a.H + hk * a.G + row % a.G : (int64_t)bk * rows + at;
+  float* pr = a.part + (place * a.splits + split) * a.d;
+  char* orow = a.out + seq.at(a, a.so) + (int64_t)(hk * a.G + row % a.G) * a.so.h + (int64_t)tok * a.so.l;
   // The waves' parts are divided by the sum before they are added, and a split
   // leaves its part so: no larger than the largest value.
   const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
@@ -911,12 +1154,11 @@ __global__ __launch_bounds__(64 * (few_waves<T, DP>())) void attn_few_kernel(Att
   }
   if (threadIdx.x < 32) {
     if (a.splits > 1) {
-      float* ml = a.part_ml + (((int64_t)bk * rows + at) * a.splits + split) * 2;
+      float* ml = a.part_ml + (place * a.splits + split) * 2;
       ml[0] = m;
       ml[1] = l;
     } else if (a.lse) {
-      a.lse[((int64_t)b * a.H + hk * a.G + row % a.G) * a.Lq + tok] =
-          l == 0.f ? -__builtin_huge_valf() : m * LN2 + logf(l);
+      a.lse[seq.stat(a, hk * a.G + row % a.G) + tok] = l == 0.f ? -__builtin_huge_valf() : m * LN2 + logf(l);
     }
   }
 }
@@ -925,15 +1167,34 @@ __global__ __launch_bounds__(64 * (few_waves<T, DP>())) void attn_few_kernel(Att
 // the common maximum.
 // All loads of a thread are independent: the kernel is as long as two trips
 // to memory.
-template <typename T, int DP>
-__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
+template <typename T, int DP, class A = AttnArgs>
+__global__ __launch_bounds__(256) void attn_join_kernel(A a) {
+  constexpr bool PAGED = A::LIE == Lie::PAGED;
   constexpr int PARTS = 256 / DP;  // threads that share a column
   __shared__ float f[256], red[4], out[PARTS][DP];
-  const int rows = a.G * a.Lq, n = blockIdx.x % rows, bk = blockIdx.x / rows, t = threadIdx.x;
-  const int hk = bk % a.Hk, b = bk / a.Hk, tok = n / a.G, h = hk * a.G + n % a.G;
-  if (tok >= seq_len(a.q_lens, b, a.Lq)) return;
-  const float* ml = a.part_ml + ((int64_t)bk * rows + n) * a.splits * 2;
-  const float* pr = a.part + ((int64_t)bk * rows + n) * a.splits * a.d;
+  const int t = threadIdx.x;
+  int b = 0, h = blockIdx.x % a.H, tok = blockIdx.x / a.H;
+  bool by_token = false;
+  if constexpr (PAGED) by_token = a.by_token;
+  if (by_token) {
+    if constexpr (PAGED) b = find_last(a.B, t % WAVE, [&](int i) { return seq_len(a.offsets, i, a.Lq) <= tok; });
+    if (b < 0) return;
+  } else {
+    int rows = a.G * a.Lq;
+    if constexpr (PAGED) rows = a.G * a.few;
+    const int n = blockIdx.x % rows, bk = blockIdx.x / rows;
+    b = bk / a.Hk, tok = n / a.G, h = bk % a.Hk * a.G + n % a.G;
+  }
+  const AttnSeq seq(a, b);
+  int64_t place = blockIdx.x;
+  if constexpr (PAGED) {
+    if (by_token) tok -= seq.first;
+    else place = (int64_t)(seq.first + tok) * a.H + h;
+    if ((seq.qlen > a.few) != by_token) return;
+  }
+  if (tok >= seq.qlen) return;
+  const float* ml = a.part_ml + place * a.splits * 2;
+  const float* pr = a.part + place * a.splits * a.d;
   constexpr float NONE = -__builtin_huge_valf();
   const float ms = t < a.splits ? ml[2 * t] : NONE, ls = t < a.splits ? ml[2 * t + 1] : 0.f;
   float m = ms;
@@ -963,9 +1224,9 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
   if (part == 0 && c < a.d) {
 #pragma unroll
     for (int i = 1; i < PARTS; ++i) x += out[i][c];
-    io_traits<T>::store(reinterpret_cast<T*>(a.out + b * a.so.b + (int64_t)h * a.so.h + (int64_t)tok * a.so.l) + c, x);
+    io_traits<T>::store(reinterpret_cast<T*>(a.out + seq.at(a, a.so) + (int64_t)h * a.so.h + (int64_t)tok * a.so.l) + c, x);
   }
-  if (a.lse && t == 0) a.lse[((int64_t)b * a.H + h) * a.Lq + tok] = l == 0.f ? NONE : m * LN2 + logf(l);
+  if (a.lse && t == 0) a.lse[seq.stat(a, h) + tok] = l == 0.f ? NONE : m * LN2 + logf(l);
 }
 
 // ------------------------------------------------------------------ backward: dq
@@ -987,28 +1248,34 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
 // 32K step of 16 heads, d = 64, window 2048: 585 us, matrix pipes busy 50 % of
 // the time with the four products of a score (three are dq's own, one is the
 // mean key's); the rest is the vector pipe's share, as in the forward.
-template <typename T, int DP, int KS>
-__global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dq_kernel(AttnArgs a) {
+template <typename T, int DP, int KS, class A = AttnArgs>
+__global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dq_kernel(A a) {
   using Tile = AttnTile<T, DP>;
   constexpr int NW = 4, RG = NW / KS, BN = attn_bn<T, DP>(), TB = BN * Tile::CPR * 16, STEPS = Tile::STEPS, DB = DP / 32;
   constexpr bool CENTRE = sizeof(T) == 2;
   __shared__ __align__(1024) char lds[4 * TB];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  AttnPlace at(xcd_remap(blockIdx.x, gridDim.x), a);
-  const int qlen = seq_len(a.q_lens, at.b, a.Lq), klen = seq_len(a.k_lens, at.b, a.Lk);
+  if constexpr (A::LIE != Lie::PADDED)
+    if ((int)blockIdx.x >= a.main)
+      return clear_rest(a, a.dq, a.sdq, a.H, a.d * (int)sizeof(T), nullptr, (int)blockIdx.x - a.main, a.rest);
   const int rg = wave % RG, ks = wave / RG;  // head and rows of the wave; its part of a tile
   const int BM = 32 * RG / a.hg;             // rows of the workgroup
+  AttnPlace at(blockIdx.x, BM, lane, a);
+  if (A::LIE != Lie::PADDED && at.b < 0) return;
+  const AttnSeq seq(a, at.b);
+  const int qlen = seq.qlen, klen = seq.klen;
   at.h += rg % a.hg;
   const int r0 = at.tile * BM, rw = r0 + 32 * (rg / a.hg), off = klen - qlen, n = lane & 31;
   const int row = rw + n, cmax = a.d * (int)sizeof(T) / 16 - 1;
-  const int64_t stat = ((int64_t)at.b * a.H + at.h) * a.Lq + row;
+  const int64_t stat = seq.stat(a, at.h) + row;
+  if (A::LIE != Lie::PADDED && r0 >= qlen) return;
   f32x16 dq[DB];
 #pragma unroll
   for (int db = 0; db < DB; ++db) dq[db] = zero16();
-  const char* kb = a.k + at.b * a.sk.b + at.hk * a.sk.h;
-  const char* vb = a.v + at.b * a.sv.b + at.hk * a.sv.h;
-  const char* qb = a.q + at.b * a.sq.b + at.h * a.sq.h;
-  const char* gb = a.dO + at.b * a.sdo.b + at.h * a.sdo.h;
+  const char* kb = a.k + seq.at(a, a.sk) + at.hk * a.sk.h;
+  const char* vb = a.v + seq.at(a, a.sv) + at.hk * a.sv.h;
+  const char* qb = a.q + seq.at(a, a.sq) + at.h * a.sq.h;
+  const char* gb = a.dO + seq.at(a, a.sdo) + at.h * a.sdo.h;
   float delta = 0.f, lse = 0.f, lse2 = 0.f;
   const KeyTiles kt(off + r0, off + min(r0 + BM, qlen) - 1, a.window, a.sinks, BN);
   if (r0 < qlen) {
@@ -1018,7 +1285,7 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dq_kerne
       Frag<T> o[STEPS];
       load_rows(q, qb + rc * a.sq.l, cmax, lane);
       load_rows(g, gb + rc * a.sdo.l, cmax, lane);
-      load_rows(o, a.o + at.b * a.so.b + at.h * a.so.h + rc * a.so.l, cmax, lane);
+      load_rows(o, a.o + seq.at(a, a.so) + at.h * a.so.h + rc * a.so.l, cmax, lane);
 #pragma unroll
       for (int s = 0; s < STEPS; ++s)
 #pragma unroll
@@ -1232,7 +1499,7 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dq_kerne
     // what the dk, dv kernel's products start from: exp2(c (q.k - lse / scale)), dO.v - D
     if (ks == 0 && row < qlen && lane < 32) {
       a.stats[stat] = sizeof(T) == 4 ? -lse : -lse / a.scale;
-      a.stats[(int64_t)a.B * a.H * a.Lq + stat] = -delta;
+      a.stats[stats_of(a) + stat] = -delta;
     }
   }
   if (ks != 0) return;
@@ -1240,8 +1507,8 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dq_kerne
 #pragma unroll
     for (int db = 0; db < DB; ++db) dq[db] = zero16();
   }
-  char* out = a.dq + at.b * a.sdq.b + at.h * a.sdq.h;
-  if (row < a.Lq) store_rows<T, DP>(dq, a.scale, out + (int64_t)row * a.sdq.l, a.d, lane);
+  char* out = a.dq + seq.at(a, a.sdq) + at.h * a.sdq.h;
+  if (row < (A::LIE == Lie::PADDED ? a.Lq : qlen)) store_rows<T, DP>(dq, a.scale, out + (int64_t)row * a.sdq.l, a.d, lane);
   for (uint32_t bad = not_finite(dq) & (uint32_t)__ballot(lse2 == lse2 && delta == delta); bad; bad &= bad - 1) {
     const int i = __builtin_ctz(bad), r = rw + i;
     const float ls = of_lane(lse2, i), de = of_lane(delta, i);
@@ -1275,30 +1542,54 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dq_kerne
 // window's; the rows behind the window of a sink tile's last key are split
 // over further workgroups of `span` rows each, and the fp32 partial sums of a
 // sink tile are added in a fixed order by attn_sink_sum_kernel.
-template <typename T, int DP, int KS>
-__global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dkv_kernel(AttnArgs a) {
+template <typename T, int DP, int KS, class A = AttnArgs>
+__global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dkv_kernel(A a) {
   using Tile = AttnTile<T, DP>;
   constexpr int NW = 4, RG = NW / KS, BK = 32 * RG, BQ = attn_bn<T, DP>(), TB = BQ * Tile::CPR * 16, STEPS = Tile::STEPS, DB = DP / 32;
   __shared__ __align__(1024) char lds[4 * TB];
   __shared__ __align__(1024) float stats[2][2][64];  // [ring][-lse / scale, -D][row]
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 31;
-  int id = xcd_remap(blockIdx.x, gridDim.x);
-  const int jobs = a.tiles + a.sink_tiles * (a.splits - 1);
-  const int job = id % jobs, bk = id / jobs, hk = bk % a.Hk, b = bk / a.Hk;
-  int tile, split = 0;
-  if (job < a.sink_tiles * a.splits) {
-    tile = job / a.splits;
-    split = job % a.splits;
+  int tile, split = 0, hk, b;
+  if constexpr (A::LIE == Lie::PADDED) {
+    int id = xcd_remap(blockIdx.x, gridDim.x);
+    const int jobs = a.tiles + a.sink_tiles * (a.splits - 1);
+    const int job = id % jobs, bk = id / jobs;
+    hk = bk % a.Hk, b = bk / a.Hk;
+    if (job < a.sink_tiles * a.splits) {
+      tile = job / a.splits;
+      split = job % a.splits;
+    } else {
+      tile = job - a.sink_tiles * (a.splits - 1);
+    }
   } else {
-    tile = job - a.sink_tiles * (a.splits - 1);
+    // split sink tiles of all sequences, then the tiles by slots, early keys first: most rows see them
+    int id = blockIdx.x;
+    if (id >= a.main) {
+      clear_rest(a, a.dk, a.sdk, a.Hk, a.d * (int)sizeof(T), nullptr, id - a.main, a.rest);
+      return clear_rest(a, a.dv, a.sdv, a.Hk, a.d * (int)sizeof(T), nullptr, id - a.main, a.rest);
+    }
+    hk = id % a.Hk, id /= a.Hk;
+    const int jobs = a.splits > 1 ? a.B * a.sink_tiles * a.splits : 0;
+    if (id < jobs) {
+      split = id % a.splits, id /= a.splits;
+      tile = id % a.sink_tiles, b = id / a.sink_tiles;
+    } else {
+      find_tile(a, id - jobs, BK, lane, true, b, tile);
+      if (b < 0 || (a.splits > 1 && tile < a.sink_tiles)) return;
+    }
   }
-  const int qlen = seq_len(a.q_lens, b, a.Lq), klen = seq_len(a.k_lens, b, a.Lk), off = klen - qlen;
+  const int bk = b * a.Hk + hk;
+  const AttnSeq seq(a, b);
+  const int qlen = seq.qlen, klen = seq.klen, off = klen - qlen;
+  if (A::LIE != Lie::PADDED && tile * BK >= klen) return;
   const int k0 = tile * BK, cmax = a.d * (int)sizeof(T) / 16 - 1;
   const int rg = wave % RG, ks = wave / RG;  // keys of the wave; its part of a row tile (see the forward)
   const int key = k0 + 32 * rg + n;
-  const char* qh = a.q + b * a.sq.b + (int64_t)hk * a.G * a.sq.h;
-  const char* gh = a.dO + b * a.sdo.b + (int64_t)hk * a.G * a.sdo.h;
-  const int64_t sh = ((int64_t)b * a.H + hk * a.G) * a.Lq, sn = (int64_t)a.B * a.H * a.Lq;
+  const char* qh = a.q + seq.at(a, a.sq) + (int64_t)hk * a.G * a.sq.h;
+  const char* gh = a.dO + seq.at(a, a.sdo) + (int64_t)hk * a.G * a.sdo.h;
+  const char* kh = a.k + seq.at(a, a.sk) + hk * a.sk.h;
+  const char* vh = a.v + seq.at(a, a.sv) + hk * a.sv.h;
+  const int64_t sh = seq.stat(a, hk * a.G), sn = stats_of(a);
   f32x16 dk[DB], dv[DB];
 #pragma unroll
   for (int db = 0; db < DB; ++db) dk[db] = dv[db] = zero16();
@@ -1319,8 +1610,8 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dkv_kern
     const int rend = rz / BQ + 1;  // behind the last row tile
     Frag<T> kf[STEPS], vf[STEPS];
     const int64_t kc = min(key, klen - 1);
-    load_rows(kf, a.k + b * a.sk.b + hk * a.sk.h + kc * a.sk.l, cmax, lane);
-    load_rows(vf, a.v + b * a.sv.b + hk * a.sv.h + kc * a.sv.l, cmax, lane);
+    load_rows(kf, kh + kc * a.sk.l, cmax, lane);
+    load_rows(vf, vh + kc * a.sv.l, cmax, lane);
     const int wk0 = k0 + 32 * rg, wk1 = min(wk0 + 31, klen - 1);
     Stager<T, DP, BQ, NW> sq(qh, a.sq.l, qlen - 1, cmax, wave, lane), sg(gh, a.sdo.l, qlen - 1, cmax, wave, lane);
     auto issue = [&](int h, int rt, char* t, float* st) {
@@ -1575,20 +1866,19 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dkv_kern
   const bool parts = tile < a.sink_tiles && a.splits > 1;
   // [batch x key head][sink tile][split][dk, dv][key][d]
   float* pk = a.part + (((int64_t)bk * a.sink_tiles + tile) * a.splits + split) * 2 * BK * a.d;
-  char* ok = a.dk + b * a.sdk.b + hk * a.sdk.h;
-  char* ov = a.dv + b * a.sdv.b + hk * a.sdv.h;
+  char* ok = a.dk + seq.at(a, a.sdk) + hk * a.sdk.h;
+  char* ov = a.dv + seq.at(a, a.sdv) + hk * a.sdv.h;
   if (parts) {
     float* to = pk + (32 * rg + n) * a.d;
     store_rows<float, DP>(dk, 1.f, reinterpret_cast<char*>(to), a.d, lane);
     store_rows<float, DP>(dv, 1.f, reinterpret_cast<char*>(to + BK * a.d), a.d, lane);
-  } else if (key < a.Lk) {
+  } else if (key < (A::LIE == Lie::PADDED ? a.Lk : klen)) {
     store_rows<T, DP>(dk, a.scale, ok + (int64_t)key * a.sdk.l, a.d, lane);
     store_rows<T, DP>(dv, 1.f, ov + (int64_t)key * a.sdv.l, a.d, lane);
   }
   for (uint32_t bad = (not_finite(dk) | not_finite(dv)) & (uint32_t)__ballot(key < klen); bad; bad &= bad - 1) {
     const int i = __builtin_ctz(bad), j = k0 + 32 * rg + i;
-    const Lane2<T> k(a.k + b * a.sk.b + hk * a.sk.h + j * a.sk.l, a.d, lane);
-    const Lane2<T> v(a.v + b * a.sv.b + hk * a.sv.h + j * a.sv.l, a.d, lane);
+    const Lane2<T> k(kh + j * a.sk.l, a.d, lane), v(vh + j * a.sv.l, a.d, lane);
     float x[2] = {0.f, 0.f}, y[2] = {0.f, 0.f};
 #pragma unroll 1
     for (int h = 0; h < a.G; ++h)
@@ -1623,18 +1913,19 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dkv_kern
 }
 
 // dk, dv of the sink tiles, BK keys each: the splits' partial sums, in order
-template <typename T, int BK>
-__global__ __launch_bounds__(128) void attn_sink_sum_kernel(AttnArgs a) {
+template <typename T, int BK, class A = AttnArgs>
+__global__ __launch_bounds__(128) void attn_sink_sum_kernel(A a) {
   const int keys = a.sink_tiles * BK;
   const int x = blockIdx.x % (2 * keys), bk = blockIdx.x / (2 * keys), what = x / keys, key = x % keys;
   const int hk = bk % a.Hk, b = bk / a.Hk, c = threadIdx.x;
-  if (key >= a.Lk || c >= a.d) return;
+  const AttnSeq seq(a, b);
+  if (key >= (A::LIE == Lie::PADDED ? a.Lk : seq.klen) || c >= a.d) return;
   const float* pr = a.part + ((((int64_t)bk * a.sink_tiles + key / BK) * a.splits * 2 + what) * BK + key % BK) * a.d + c;
   float sum = 0.f;
   for (int s = 0; s < a.splits; ++s) sum += pr[(int64_t)s * 2 * BK * a.d];
-  if (key >= seq_len(a.k_lens, b, a.Lk)) sum = 0.f;
-  char* to = what ? a.dv + b * a.sdv.b + hk * a.sdv.h + (int64_t)key * a.sdv.l
-                  : a.dk + b * a.sdk.b + hk * a.sdk.h + (int64_t)key * a.sdk.l;
+  if (key >= seq.klen) sum = 0.f;
+  char* to = what ? a.dv + seq.at(a, a.sdv) + hk * a.sdv.h + (int64_t)key * a.sdv.l
+                  : a.dk + seq.at(a, a.sdk) + hk * a.sdk.h + (int64_t)key * a.sdk.l;
   io_traits<T>::store(reinterpret_cast<T*>(to) + c, what ? sum : sum * a.scale);
 }
 

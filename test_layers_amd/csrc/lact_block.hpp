@@ -158,7 +158,7 @@ AttnArgs attn_args(const lact_attention& p) {
 // 128 rows of one head a workgroup, 611 us with 32 rows of four).
 void row_tiles(const lact_attention& p, int rows, AttnArgs& a) {
   a.hg = 1;
-  while (a.hg < rows / 32 && a.G % (2 * a.hg) == 0) a.hg *= 2;
+  while (a.hg < rows / 32 && p.heads / p.kv_heads % (2 * a.hg) == 0) a.hg *= 2;
   a.tiles = (int32_t)ceil_div(p.q_len, rows / a.hg);
 }
 

@@ -43,18 +43,6 @@ struct RotaryTensor {
   int64_t ib, ih, il, ob, oh, ol;  // byte strides
   int32_t heads;
 };
-// n / d for 0 <= n < 2^31 and a divisor that the host knows: a multiplication
-// and a shift, by the method of Granlund and Montgomery, "Division by invariant
-// integers using multiplication", 1994 (four divisions of every 8-byte item took as long as its memory)
-struct FastDiv {
-  uint32_t d, m, s;
-  FastDiv() = default;
-  explicit FastDiv(uint32_t d_) : d(d_), m(0), s(0) {
-    while ((uint64_t(1) << s) < d) ++s;
-    m = (uint32_t)(((uint64_t(1) << 32) * ((uint64_t(1) << s) - d)) / d + 1);
-  }
-  __device__ __forceinline__ uint32_t div(uint32_t n) const { return (__umulhi(n, m) + n) >> s; }
-};
 
 struct RotaryArgs {
   RotaryTensor t[2];         // q and k (k.heads 0: none)

@@ -3,3 +3,4 @@
 // timing, device check).
 #include "lact.hip"
 #include "lact_block.hpp"
+#include "lact_pages_host.hpp"

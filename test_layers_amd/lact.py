@@ -39,21 +39,25 @@ QK_PREP = 2
 ROTARY_INTERLEAVED = 1
 ROTARY_INVERSE = 2
 ROTARY_SCALING = {"plain": 0, "linear": 1, "ntk": 2, "yarn": 3}
+CLEAR_REST = 1
 NORM_GROUP = 128   # LACT_NORM_GROUP: columns that share a scale of the 8-bit output
 
 (K_UPD, K_APP, K_OUT, K_DW, K_OPT, K_NS, K_SNAP, K_PREP, K_BWD_GEMM, K_BWD_ELEM, K_NSRED, K_ATTN, K_ATTN_BWD,
- K_ROTARY, K_NORM) = range(15)
+ K_ROTARY, K_NORM, K_PAGES) = range(16)
 K_NAMES = {K_UPD: "update_fwd", K_APP: "apply_fwd", K_OUT: "apply_out", K_DW: "dw", K_OPT: "opt",
            K_NS: "newton_schulz", K_SNAP: "snapshot", K_PREP: "qk_prep", K_BWD_GEMM: "bwd_gemm",
            K_BWD_ELEM: "bwd_elem", K_NSRED: "ns_reduce", K_ATTN: "attention", K_ATTN_BWD: "attention_bwd",
-           K_ROTARY: "rotary", K_NORM: "norm"}
+           K_ROTARY: "rotary", K_NORM: "norm", K_PAGES: "pages"}
 
 EXPORTS = ["lact_workspace_size", "lact_chunk_update", "lact_apply", "lact_layer_forward",
            "lact_layer_forward_scaled", "lact_layer_forward_noalloc", "lact_backward_workspace_size",
            "lact_layer_backward", "lact_window_attention_workspace_size", "lact_window_attention_forward",
            "lact_window_attention_backward_workspace_size", "lact_window_attention_backward", "lact_rotary",
            "lact_rotary_frequencies", "lact_add_rmsnorm_forward", "lact_add_rmsnorm_backward_workspace_size",
-           "lact_add_rmsnorm_backward", "lact_status_str", "lact_last_error", "lact_timing_enable", "lact_timing_read"]
+           "lact_add_rmsnorm_backward", "lact_packed_attention_forward",
+           "lact_packed_attention_backward_workspace_size", "lact_packed_attention_backward",
+           "lact_paged_attention_workspace_size", "lact_paged_attention", "lact_page_slots_workspace_size",
+           "lact_page_slots", "lact_page_write", "lact_status_str", "lact_last_error", "lact_timing_enable", "lact_timing_read"]
 
 NOALLOC_SCRATCH_BYTES = 128 << 20   # LACT_NOALLOC_SCRATCH_BYTES
 
@@ -91,6 +95,31 @@ class RotaryProblem(ctypes.Structure):
 class NormProblem(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int32), ("io_dtype", ctypes.c_int32),
                 ("eps", ctypes.c_float)]
+
+
+class Packed(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("d", ctypes.c_int32), ("io_dtype", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("tokens", ctypes.c_int64), ("longest", ctypes.c_int64), ("window", ctypes.c_int64),
+                ("sinks", ctypes.c_int64), ("flags", ctypes.c_uint32)]
+
+
+class Paged(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("d", ctypes.c_int32), ("io_dtype", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("tokens", ctypes.c_int64), ("longest", ctypes.c_int64), ("k_len", ctypes.c_int64),
+                ("window", ctypes.c_int64), ("sinks", ctypes.c_int64), ("pages", ctypes.c_int32),
+                ("page", ctypes.c_int32), ("width", ctypes.c_int32), ("flags", ctypes.c_uint32)]
+
+
+class Slots(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("page", ctypes.c_int32), ("width", ctypes.c_int32),
+                ("entries", ctypes.c_int32), ("tokens", ctypes.c_int64)]
+
+
+class Write(ctypes.Structure):
+    _fields_ = [("kv_heads", ctypes.c_int32), ("d", ctypes.c_int32), ("io_dtype", ctypes.c_int32),
+                ("pages", ctypes.c_int32), ("page", ctypes.c_int32), ("tokens", ctypes.c_int64)]
 
 
 _lib = None
@@ -155,6 +184,23 @@ def lib() -> ctypes.CDLL:
     L.lact_add_rmsnorm_backward_workspace_size.argtypes = [N]
     L.lact_add_rmsnorm_backward.restype = i32
     L.lact_add_rmsnorm_backward.argtypes = [N, vp, i64, vp, vp, i64, vp, i64, vp, i64, vp, vp, sz, vp]
+    K, G, S, W = (ctypes.POINTER(x) for x in (Packed, Paged, Slots, Write))
+    L.lact_packed_attention_forward.restype = i32
+    L.lact_packed_attention_forward.argtypes = [K] + [vp] * 11
+    L.lact_packed_attention_backward_workspace_size.restype = sz
+    L.lact_packed_attention_backward_workspace_size.argtypes = [K]
+    L.lact_packed_attention_backward.restype = i32
+    L.lact_packed_attention_backward.argtypes = [K] + [vp] * 19 + [sz, vp]
+    L.lact_paged_attention_workspace_size.restype = sz
+    L.lact_paged_attention_workspace_size.argtypes = [G]
+    L.lact_paged_attention.restype = i32
+    L.lact_paged_attention.argtypes = [G] + [vp] * 13 + [sz, vp]
+    L.lact_page_slots_workspace_size.restype = sz
+    L.lact_page_slots_workspace_size.argtypes = [S]
+    L.lact_page_slots.restype = i32
+    L.lact_page_slots.argtypes = [S] + [vp] * 11 + [sz, vp]
+    L.lact_page_write.restype = i32
+    L.lact_page_write.argtypes = [W] + [vp] * 10
     L.lact_status_str.restype = ctypes.c_char_p
     L.lact_status_str.argtypes = [i32]
     L.lact_last_error.restype = ctypes.c_char_p
@@ -973,6 +1019,310 @@ def add_rmsnorm_backward(h, weight, *, dy, dh=None, eps: float = 1e-6, dx=None, 
         return dx, dw
 
     return _on(plan.device, stream, (h, weight, dy, dh, dx, dw, workspace), run)
+
+
+# ----------------------------------------------------------------- batches of sequences of different lengths
+def _strided3(t, name, shape, dtype):
+    """Strides of a [heads, tokens, d] tensor with d contiguous."""
+    if t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    h, l, e = t.stride()
+    if e != 1 and shape[2] > 1 and t.numel():
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return Strides(0, h, l)
+
+
+def _bound(x, name, default, most):
+    """A bound that the caller may give on what the device holds."""
+    if x is None:
+        return default
+    x = _int(x, name)
+    if x < 0:
+        raise ValueError(f"{name} = {x} < 0")
+    return min(x, most)
+
+
+def _packed_rows(plan, q, offsets):
+    if q.dim() != 3:
+        raise ValueError("q must be [heads, tokens, d]")
+    plan.shape, plan.dtype = tuple(q.shape), q.dtype
+    if offsets.dim() != 1 or offsets.shape[0] < 1:
+        raise ValueError("offsets must be [batch + 1]")
+    _ptr(offsets, _torch().int64, "offsets")
+    plan.batch = offsets.shape[0] - 1
+    plan.lse = (_torch().float32, None, plan.shape[:2], (plan.shape[1], 1))
+    plan.strides = [_strided3(q, "q", plan.shape, q.dtype)]
+
+
+def _packed_plan(q, k, v, offsets, longest, window, sinks, scale):
+    if k.dim() != 3:
+        raise ValueError("k must be [kv_heads, tokens, d]")
+    plan = _Plan()
+    plan.device = _one_device(q, k, v, offsets)
+    _packed_rows(plan, q, offsets)
+    h, t, d = plan.shape
+    plan.kshape = (k.shape[0], t, d)
+    plan.strides += [_strided3(k, "k", plan.kshape, q.dtype), _strided3(v, "v", plan.kshape, q.dtype)]
+    plan.sq, plan.sk, plan.sv = (ctypes.byref(x) for x in plan.strides)
+    values = [plan.batch, h, k.shape[0], d, _io_dtype(q), d ** -0.5 if scale is None else scale, t,
+              _bound(longest, "longest", t, t), window, sinks]
+    plan.problem, plan.clear = _struct(Packed, *values, 0), _struct(Packed, *values, CLEAR_REST)
+    plan.p, plan.pc = ctypes.byref(plan.problem), ctypes.byref(plan.clear)
+    plan.results = [_meta(_like(x)) for x in (q, k, v)]
+    plan.rstrides = [Strides(0, *m[3][:2]) for m in plan.results]
+    plan.rq, plan.rk, plan.rv = (ctypes.byref(x) for x in plan.rstrides)
+    return plan
+
+
+def _packed_back_plan(q, k, v, offsets, longest, window, sinks, scale, o, lse, dO, given):
+    plan = _packed_plan(q, k, v, offsets, longest, window, sinks, scale)
+    _one_device(q, o, lse, dO, *given)
+    _check_shapes(lse=(lse, plan.shape[:2]))
+    _ptr(lse, _torch().float32, "lse")
+    more = [_strided3(o, "o", plan.shape, plan.dtype), _strided3(dO, "dO", plan.shape, plan.dtype)]
+    plan.so, plan.sg = (ctypes.byref(x) for x in more)
+    if given[0] is not None:
+        more += [_strided3(t, f"out[{n}]", s, plan.dtype)
+                 for t, n, s in zip(given, ("dq", "dk", "dv"), (plan.shape, plan.kshape, plan.kshape))]
+        plan.rq, plan.rk, plan.rv = (ctypes.byref(x) for x in more[2:])
+    plan.strides += more
+    plan.need = lib().lact_packed_attention_backward_workspace_size(plan.p)
+    return plan
+
+
+def _given_rows(plan, q, o, lse):
+    """The strides of o, a given one's or the result's."""
+    if o is None and lse is None:
+        return plan.rq
+    _one_device(q, o, lse)
+    _check_shapes(lse=(lse, plan.shape[:2]))
+    _ptr(lse, _torch().float32, "lse")
+    return plan.rq if o is None else ctypes.byref(_strided3(o, "o", plan.shape, plan.dtype))
+
+
+def _new_rows(plan, q, o, lse, return_lse):
+    """(the problem, o, lse): results to allocate get zeros in rows of no
+    sequence, by the call itself where that touches no given tensor."""
+    own_o, own_lse = o is None, lse is None and return_lse
+    if own_o:
+        o = _new(q, plan.results[0])
+    given = not own_o or lse is not None
+    if own_lse:
+        lse = _new(q, plan.lse)
+    if given:
+        for x, own in ((o, own_o), (lse, own_lse)):
+            if own:
+                x.zero_()
+    return plan.p if given else plan.pc, o, lse
+
+
+def packed_attention(q, k, v, o=None, *, offsets, longest: Optional[int] = None, window: int = 0, sinks: int = 0,
+                     scale: Optional[float] = None, return_lse: bool = False, lse=None, stream=None):
+    """Causal attention of sequences packed one after another
+    (lact_packed_attention_forward): q [heads, tokens, d], k, v [kv_heads,
+    tokens, d], fp32 or bf16, any strides in multiples of 16 bytes with d
+    contiguous: token-major tensors come as transposed views.  Sequence b has
+    the tokens offsets[b] .. offsets[b + 1] (int64 [batch + 1] on the device),
+    `longest` at most (None: it may be all).  window, sinks and scale as in
+    window_attention.  Returns o in q's layout, and with return_lse also lse
+    [heads, tokens] fp32; rows of no sequence are zero in what is allocated
+    here and left as they were in given tensors."""
+    window, sinks, scale = _int(window, "window"), _int(sinks, "sinks"), None if scale is None else float(scale)
+    longest = None if longest is None else _int(longest, "longest")
+    plan = _plan(("packed", window, sinks, scale, longest, _meta(q), _meta(k), _meta(v), _meta(offsets)),
+                 lambda: _packed_plan(q, k, v, offsets, longest, window, sinks, scale))
+    so = _given_rows(plan, q, o, lse)
+
+    def run(handle, o=o, lse=lse):
+        p, o, lse = _new_rows(plan, q, o, lse, return_lse)
+        check(lib().lact_packed_attention_forward(p, q.data_ptr(), plan.sq, k.data_ptr(), plan.sk, v.data_ptr(), plan.sv,
+                                                  offsets.data_ptr(), o.data_ptr(), so, _addr(lse), handle))
+        return (o, lse) if return_lse else o
+
+    return _on(plan.device, stream, (q, k, v, offsets, o, lse), run)
+
+
+def packed_attention_backward(q, k, v, o, lse, *, dO, offsets, longest: Optional[int] = None, window: int = 0,
+                              sinks: int = 0, scale: Optional[float] = None, out=None, workspace=None, stream=None):
+    """Backward of packed_attention (lact_packed_attention_backward): o and lse
+    as the forward returned them, dO [heads, tokens, d] in q's dtype.  Returns a
+    dict of dq, dk, dv in the inputs' dtype and layout, zero in rows of no
+    sequence; `out` (such a dict) is filled instead of allocating."""
+    window, sinks, scale = _int(window, "window"), _int(sinks, "sinks"), None if scale is None else float(scale)
+    longest = None if longest is None else _int(longest, "longest")
+    given = (None,) * 3 if out is None else (out["dq"], out["dk"], out["dv"])
+    plan = _plan(("packed back", window, sinks, scale, longest, _meta(q), _meta(k), _meta(v), _meta(offsets), _meta(o),
+                  _meta(lse), _meta(dO), _meta(given[0]), _meta(given[1]), _meta(given[2])),
+                 lambda: _packed_back_plan(q, k, v, offsets, longest, window, sinks, scale, o, lse, dO, given))
+
+    def run(handle, out=out):
+        if out is None:
+            m = plan.results
+            out = {"dq": _new(q, m[0]), "dk": _new(k, m[1]), "dv": _new(v, m[2])}
+        ws, ws_bytes, _held = _scratch(plan.need, workspace, q.device)
+        check(lib().lact_packed_attention_backward(
+            plan.p, q.data_ptr(), plan.sq, k.data_ptr(), plan.sk, v.data_ptr(), plan.sv, offsets.data_ptr(), o.data_ptr(),
+            plan.so, lse.data_ptr(), dO.data_ptr(), plan.sg, out["dq"].data_ptr(), plan.rq, out["dk"].data_ptr(),
+            plan.rk, out["dv"].data_ptr(), plan.rv, ws, ws_bytes, handle))
+        return out
+
+    return _on(plan.device, stream, (q, k, v, o, lse, dO, offsets, workspace) + given, run)
+
+
+def _paged_plan(q, k_pages, v_pages, table, offsets, k_lens, longest, k_len, window, sinks, scale):
+    torch = _torch()
+    if k_pages.dim() != 4:
+        raise ValueError("k_pages must be [pages, kv_heads, page, d]")
+    plan = _Plan()
+    plan.device = _one_device(q, k_pages, v_pages, table, offsets, k_lens)
+    _packed_rows(plan, q, offsets)
+    h, t, d = plan.shape
+    pages, hk, page, _ = k_pages.shape
+    pool = (pages, hk, page, d)
+    plan.strides += [_strided(k_pages, "k_pages", pool, q.dtype), _strided(v_pages, "v_pages", pool, q.dtype)]
+    plan.sq, plan.sk, plan.sv = (ctypes.byref(x) for x in plan.strides)
+    _check_shapes(k_lens=(k_lens, (plan.batch,)))
+    _ptr(k_lens, torch.int64, "k_lens")
+    if table.dim() != 2 or table.shape[0] != plan.batch:
+        raise ValueError(f"table has shape {tuple(table.shape)}, expected {(plan.batch, 'width')}")
+    _ptr(table, torch.int32, "table")
+    width = table.shape[1]
+    values = [plan.batch, h, hk, d, _io_dtype(q), d ** -0.5 if scale is None else scale, t,
+              _bound(longest, "longest", t, t), _bound(k_len, "k_len", width * page, width * page), window, sinks, pages,
+              page, width]
+    plan.problem, plan.clear = _struct(Paged, *values, 0), _struct(Paged, *values, CLEAR_REST)
+    plan.p, plan.pc = ctypes.byref(plan.problem), ctypes.byref(plan.clear)
+    plan.results = [_meta(_like(q))]
+    plan.rstrides = Strides(0, *plan.results[0][3][:2])
+    plan.rq = ctypes.byref(plan.rstrides)
+    plan.need = lib().lact_paged_attention_workspace_size(plan.p)
+    return plan
+
+
+def paged_attention(q, k_pages, v_pages, o=None, *, table, offsets, k_lens, longest: Optional[int] = None,
+                    k_len: Optional[int] = None, window: int = 0, sinks: int = 0, scale: Optional[float] = None,
+                    return_lse: bool = False, lse=None, workspace=None, stream=None):
+    """Attention of new tokens over a paged cache (lact_paged_attention): q
+    [heads, tokens, d], of which sequence b has the rows offsets[b] ..
+    offsets[b + 1] (int64 [batch + 1]); k_pages, v_pages [pages, kv_heads, page,
+    d], page a multiple of 8: token-major pages come as transposed views.
+    Sequence b has k_lens[b] keys (int64 [batch]), its new ones among them, in
+    the pages table[b] (int32 [batch, width]).  One row a sequence and long
+    chunks may be mixed; `longest` and `k_len` bound the rows and keys of a
+    sequence (None: all rows, the table's width) and choose how the work is
+    split.  window, sinks and scale as in window_attention, results as in
+    packed_attention."""
+    window, sinks, scale = _int(window, "window"), _int(sinks, "sinks"), None if scale is None else float(scale)
+    longest = None if longest is None else _int(longest, "longest")
+    k_len = None if k_len is None else _int(k_len, "k_len")
+    plan = _plan(("paged", window, sinks, scale, longest, k_len, _meta(q), _meta(k_pages), _meta(v_pages), _meta(table),
+                  _meta(offsets), _meta(k_lens)),
+                 lambda: _paged_plan(q, k_pages, v_pages, table, offsets, k_lens, longest, k_len, window, sinks, scale))
+    so = _given_rows(plan, q, o, lse)
+
+    def run(handle, o=o, lse=lse):
+        p, o, lse = _new_rows(plan, q, o, lse, return_lse)
+        ws, ws_bytes, _held = _scratch(plan.need, workspace, q.device)
+        check(lib().lact_paged_attention(p, q.data_ptr(), plan.sq, k_pages.data_ptr(), plan.sk, v_pages.data_ptr(),
+                                         plan.sv, offsets.data_ptr(), k_lens.data_ptr(), table.data_ptr(), o.data_ptr(),
+                                         so, _addr(lse), ws, ws_bytes, handle))
+        return (o, lse) if return_lse else o
+
+    return _on(plan.device, stream, (q, k_pages, v_pages, table, offsets, k_lens, o, lse, workspace), run)
+
+
+def _slots_plan(lens, counts, table, free, have, page, tokens, given):
+    torch = _torch()
+    if lens.dim() != 1:
+        raise ValueError("lens must be [batch]")
+    b = lens.shape[0]
+    plan = _Plan()
+    plan.device = _one_device(lens, counts, table, free, have, *given.values())
+    plan.shapes = {"offsets": (b + 1,), "k_lens": (b,), "slots": (tokens,), "positions": (tokens,), "left": (2,)}
+    _check_shapes(counts=(counts, (b,)), **{n: (t, plan.shapes[n]) for n, t in given.items()})
+    if table.dim() != 2 or table.shape[0] != b:
+        raise ValueError(f"table has shape {tuple(table.shape)}, expected {(b, 'width')}")
+    if free.dim() != 1 or have.dim() != 1 or have.shape[0] not in (1, 2):
+        raise ValueError("free must be [entries], free_count [1] or [2]")
+    for t, n in [(lens, "lens"), (counts, "counts"), (have, "free_count")] + [(t, n) for n, t in given.items()]:
+        _ptr(t, torch.int64, n)
+    _ptr(table, torch.int32, "table")
+    _ptr(free, torch.int32, "free")
+    plan.problem = _struct(Slots, b, page, table.shape[1], free.shape[0], tokens)
+    plan.p = ctypes.byref(plan.problem)
+    plan.need = lib().lact_page_slots_workspace_size(plan.p)
+    return plan
+
+
+def page_slots(lens, counts, table, free, free_count, *, page: int, tokens: int, out=None, workspace=None, stream=None):
+    """Places of a step's new tokens in a paged cache (lact_page_slots).
+    Request b holds lens[b] tokens (int64 [batch]) in the pages table[b] (int32
+    [batch, width], extended in place) and gets counts[b] more (int64 [batch]),
+    in the step's `tokens` rows one request after another.  Pages come off the
+    end of free[: free_count] (int32 [entries], int64 [1]; both only read).
+    Returns a dict of int64 tensors, what the other operators of a step take:
+    offsets [batch + 1] and k_lens [batch] for paged_attention, slots [tokens]
+    for page_write, positions [tokens] for rotary, and left [2]: the free pages
+    that are left, the next step's free_count, and how many requests got none
+    because the pool or their row of the table is full (their slots are -1).
+    `out` (such a dict) is filled instead of allocating; its left may be
+    free_count itself, of shape [2]."""
+    torch, page, tokens = _torch(), _int(page, "page"), _int(tokens, "tokens")
+    given = {} if out is None else {n: out[n] for n in ("offsets", "k_lens", "slots", "positions", "left")}
+    if tokens < 0:
+        raise ValueError(f"tokens = {tokens} < 0")
+    plan = _plan(("slots", page, tokens, _meta(lens), _meta(counts), _meta(table), _meta(free), _meta(free_count)) +
+                 tuple(_meta(t) for t in given.values()),
+                 lambda: _slots_plan(lens, counts, table, free, free_count, page, tokens, given))
+
+    def run(handle, out=out):
+        if out is None:
+            out = {n: lens.new_empty(s) for n, s in plan.shapes.items()}
+        ws, ws_bytes, _held = _scratch(plan.need, workspace, lens.device)
+        check(lib().lact_page_slots(plan.p, lens.data_ptr(), counts.data_ptr(), table.data_ptr(), free.data_ptr(),
+                                    free_count.data_ptr(), out["offsets"].data_ptr(), out["k_lens"].data_ptr(),
+                                    out["slots"].data_ptr(), out["positions"].data_ptr(), out["left"].data_ptr(), ws,
+                                    ws_bytes, handle))
+        return out
+
+    return _on(plan.device, stream, (lens, counts, table, free, free_count, workspace) + tuple(given.values()), run)
+
+
+def _write_plan(k, v, k_pages, v_pages, slots):
+    if k.dim() != 3 or k_pages.dim() != 4:
+        raise ValueError("k must be [kv_heads, tokens, d] and k_pages [pages, kv_heads, page, d]")
+    h, t, d = k.shape
+    plan = _Plan()
+    plan.device = _one_device(k, v, k_pages, v_pages, slots)
+    pool = (k_pages.shape[0], h, k_pages.shape[2], d)
+    plan.strides = [_strided3(x, n, (h, t, d), k.dtype) for x, n in ((k, "k"), (v, "v"))]
+    plan.strides += [_strided(x, n, pool, k.dtype) for x, n in ((k_pages, "k_pages"), (v_pages, "v_pages"))]
+    plan.refs = [ctypes.byref(x) for x in plan.strides]
+    _check_shapes(slots=(slots, (t,)))
+    _ptr(slots, _torch().int64, "slots")
+    plan.problem = _struct(Write, h, d, _io_dtype(k), pool[0], pool[2], t)
+    plan.p = ctypes.byref(plan.problem)
+    return plan
+
+
+def page_write(k, v, k_pages, v_pages, *, slots, stream=None):
+    """Rows of k and v [kv_heads, tokens, d] into a paged cache
+    (lact_page_write): token t goes to slot slots[t] (int64 [tokens], as
+    page_slots gives them; -1: nowhere) of k_pages and v_pages [pages, kv_heads,
+    page, d], all of one type, any strides in multiples of 16 bytes with d
+    contiguous.  Returns (k_pages, v_pages), changed in place."""
+    plan = _plan(("write", _meta(k), _meta(v), _meta(k_pages), _meta(v_pages), _meta(slots)),
+                 lambda: _write_plan(k, v, k_pages, v_pages, slots))
+    a, b, c, d = plan.refs
+
+    def run(handle):
+        check(lib().lact_page_write(plan.p, k.data_ptr(), a, v.data_ptr(), b, slots.data_ptr(), k_pages.data_ptr(), c,
+                                    v_pages.data_ptr(), d, handle))
+        return k_pages, v_pages
+
+    return _on(plan.device, stream, (k, v, k_pages, v_pages, slots), run)
 
 
 lib()  # fail at import time if the library is missing
