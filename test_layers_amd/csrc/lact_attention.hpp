@@ -80,8 +80,13 @@ struct PagedArgs : PackedArgs {  // Lk: keys of a sequence that are looked at
   const int32_t* table;    // [B, width]
   int32_t width, pages;
   FastDiv by_page;
-  int32_t few;             // sequences of up to so many rows are the few-row kernel's, others the forward's
-  int32_t by_token;        // join: one workgroup for each row of the forward's sequences, not of the few-row kernel's
+  int32_t few;             // sequences of up to so many rows are the streams', others the forward's
+  int32_t chunk;           // forward: tiles of a key split, of which there are at most `splits`
+  int32_t waves, share;    // streams: waves of the launch, fewest units of one
+  int32_t unit;            // tiles of a unit of work
+  int32_t rows;            // rows of a partial result: of an item, at most 32
+  int32_t* upto;           // [B + 1]: work of the sequences before each, null: summed by every workgroup
+  struct StreamJoin* joins;  // [waves]
 };
 
 // ------------------------------------------------------------------ tiles
@@ -181,17 +186,10 @@ struct KeyRows {
   __device__ __forceinline__ const char* v(int j) const { return sv.base + j * sv.stride; }
 };
 
-// The same with the offsets formed for every tile, for waves that need the registers.
-template <typename T, int DP, int R>
-struct LooseRows {
-  using Tile = AttnTile<T, DP>;
+// Single rows of dense K and V.
+struct TokenRows {
   const char *kb, *vb;
   int64_t kl, vl;
-  int rmax, cmax, lane;
-  __device__ __forceinline__ void issue(char* tile, int row0) const {
-    Tile::template stage<R, 1>(tile, kb, kl, row0, rmax, cmax, 0, lane);
-    Tile::template stage<R, 1>(tile + R * Tile::CPR * 16, vb, vl, row0, rmax, cmax, 0, lane);
-  }
   __device__ __forceinline__ const char* k(int j) const { return kb + j * kl; }
   __device__ __forceinline__ const char* v(int j) const { return vb + j * vl; }
 };
@@ -448,6 +446,7 @@ struct AttnSeq {
     qlen = __builtin_amdgcn_readfirstlane(min(max(seq_len(a.offsets, b + 1, a.Lq) - first, 0), a.most));
     klen = qlen;
   }
+  __device__ AttnSeq(int b_, int qlen_, int klen_, int first_) : b(b_), qlen(qlen_), klen(klen_), first(first_) {}
   __device__ AttnSeq(const PagedArgs& a, int b_) : AttnSeq(static_cast<const PackedArgs&>(a), b_) {
     klen = __builtin_amdgcn_readfirstlane(seq_len(a.k_lens, b, a.Lk));
   }
@@ -578,6 +577,12 @@ struct KeyTiles {
     lo = min(lo, total);
   }
 };
+
+// Key splits of a row tile of the forward over pages: of about a chunk's tiles,
+// no more than the host allowed.
+__device__ __forceinline__ int key_splits(const PagedArgs& a, const KeyTiles& kt) {
+  return max(1, min(a.splits, (kt.total + a.chunk / 2) / a.chunk));
+}
 
 // the lowest and highest position of a wave's rows
 struct AttnWave {
@@ -851,17 +856,24 @@ constexpr int attn_bn() { return DP * (int)sizeof(T) > 256 ? 32 : 64; }
 //
 // In a packed batch key heads are innermost instead, so that consecutive
 // workgroups, which go to the XCDs in turn, put the same ones on an XCD and
-// leave each with as many long tiles as the others.
+// leave each with as many long tiles as the others.  Key splits are outermost:
+// an XCD deals its workgroups to its shader engines in turn, too, and with
+// every fourth split in use and three empty ones beside it, a quarter of them
+// had all the work (eight chunks of 1024 rows among 20 sequences, two of eight
+// splits in use: 2.1 ms innermost, 1.0 when all splits are).
 struct AttnPlace {
   int b, hk, h, tile, split = 0;
   __device__ AttnPlace(int id, int BM, int lane, const PackedArgs& a, int splits = 1) {
     const int groups = a.G / a.hg;
+    if (splits > 1) {
+      const int one = a.main / splits;
+      split = id / one;
+      id -= split * one;
+    }
     hk = id % a.Hk;
     id /= a.Hk;
     h = hk * a.G + id % groups * a.hg;
-    id /= groups;
-    split = id % splits;
-    find_tile(a, id / splits, BM, lane, false, b, tile);
+    find_tile(a, id / groups, BM, lane, false, b, tile);
   }
   __device__ AttnPlace(int id, int, int lane, const AttnArgs& a, int = 1) {
     id = xcd_remap(id, gridDim.x);
@@ -926,13 +938,12 @@ __global__ __launch_bounds__(256, (attn_waves<T, DP>())) void attn_fwd_kernel(A 
   }();
   const AttnAddr<DP> addr(lane);
   // the workgroup's tiles: all, or a split's (from an even one on: the ring's first place)
-  int i0 = 0, i1 = kt.total;
+  int i0 = 0, i1 = kt.total, splits = 1;
   if constexpr (PAGED) {
-    auto cut = [&](int s) { return (int)((int64_t)kt.total * s / a.splits) & ~1; };
-    if (a.splits > 1) {
-      i0 = cut(at.split);
-      if (at.split + 1 < a.splits) i1 = cut(at.split + 1);
-    }
+    splits = key_splits(a, kt);
+    if (at.split >= splits) return;
+    i0 = (int)((int64_t)i1 * at.split / splits) & ~1;
+    if (at.split + 1 < splits) i1 = (int)((int64_t)i1 * (at.split + 1) / splits) & ~1;
   }
   // ring of two: tile i + 1 is copied while tile i is computed
   auto arrive = [&](int i, char* other) {
@@ -1004,7 +1015,7 @@ __global__ __launch_bounds__(256, (attn_waves<T, DP>())) void attn_fwd_kernel(A 
   // a split's result and statistics, by token, head and split
   auto part = [&](int r) { return (((int64_t)(seq.first + r) * a.H + at.h) * a.splits + at.split); };
   if (row < qlen) {
-    if (PAGED && a.splits > 1) {
+    if (PAGED && splits > 1) {
       store_rows<float, DP>(w.o, inv, reinterpret_cast<char*>(a.part + part(row) * a.d), a.d, lane);
       if (lane < 32) *reinterpret_cast<float2*>(a.part_ml + part(row) * 2) = make_float2(w.m, l);
     } else {
@@ -1017,7 +1028,7 @@ __global__ __launch_bounds__(256, (attn_waves<T, DP>())) void attn_fwd_kernel(A 
     const int n = __builtin_ctz(bad), r = rw + n;
     float x[2];
     slow_o<T>(x, qb + r * a.sq.l, keys, a, off + r, of_lane(log2_sum(w.m, l), n), kt, i0, i1, 1, BN, lane);
-    if (PAGED && a.splits > 1) store_lane2<float>(reinterpret_cast<char*>(a.part + part(r) * a.d), x, a.d, lane);
+    if (PAGED && splits > 1) store_lane2<float>(reinterpret_cast<char*>(a.part + part(r) * a.d), x, a.d, lane);
     else store_lane2<T>(out + r * a.so.l, x, a.d, lane);
   }
 }
@@ -1043,40 +1054,35 @@ constexpr int few_lds() {
 // heads, window 2048: 8.7 us, and 3.0 more for the join.  Each wave runs its
 // own ring of 32-key tiles with no barrier; the waves join in LDS, the
 // workgroups through `part` in attn_join_kernel.
-template <typename T, int DP, class A = AttnArgs>
-__global__ __launch_bounds__(64 * (few_waves<T, DP>())) void attn_few_kernel(A a) {
+template <typename T, int DP>
+__global__ __launch_bounds__(64 * (few_waves<T, DP>())) void attn_few_kernel(AttnArgs a) {
   using Tile = AttnTile<T, DP>;
-  constexpr bool PAGED = A::LIE == Lie::PAGED;
   constexpr int NW = few_waves<T, DP>(), TB = few_tile<T, DP>(), WB = few_lds<T, DP>() / NW;
   __shared__ __align__(1024) char lds[few_lds<T, DP>()];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int split = blockIdx.x % a.splits, tile = blockIdx.x / a.splits % a.tiles, bk = blockIdx.x / a.splits / a.tiles;
   const int hk = bk % a.Hk, b = bk / a.Hk;
-  if constexpr (PAGED)
-    if ((int)blockIdx.x >= a.main)
-      return clear_rest(a, a.out, a.so, a.H, a.d * (int)sizeof(T), a.lse, (int)blockIdx.x - a.main, a.rest);
-  const AttnSeq seq(a, b);
-  const int qlen = seq.qlen, klen = seq.klen;
-  if constexpr (PAGED)
-    if (qlen > a.few) return;
+  const int qlen = seq_len(a.q_lens, b, a.Lq), klen = seq_len(a.k_lens, b, a.Lk);
   const int t0 = 32 * tile / a.G;  // the first row's token
   if (t0 >= qlen) return;
-  const int off = klen - qlen, rows = a.G * (PAGED ? qlen : a.Lq), n = lane & 31, at = 32 * tile + n;
+  const int off = klen - qlen, rows = a.G * a.Lq, n = lane & 31, at = 32 * tile + n;
   const int row = min(at, rows - 1), tok = row / a.G, cmax = a.d * (int)sizeof(T) / 16 - 1;
-  const char* qb = a.q + seq.at(a, a.sq);
+  const char* kb = a.k + b * a.sk.b + hk * a.sk.h;
+  const char* vb = a.v + b * a.sv.b + hk * a.sv.h;
   AttnRows<T, DP> w;
   w.clear();
-  load_rows(w.q, qb + (int64_t)(hk * a.G + row % a.G) * a.sq.h + (int64_t)min(tok, qlen - 1) * a.sq.l, cmax, lane);
+  load_rows(w.q, a.q + b * a.sq.b + (int64_t)(hk * a.G + row % a.G) * a.sq.h +
+                            (int64_t)min(tok, qlen - 1) * a.sq.l, cmax, lane);
   w.p = off + min(tok, qlen - 1);
   w.w = {off + t0, off + min((32 * tile + 31) / a.G, qlen - 1)};
   const KeyTiles kt(w.w.lo, w.w.hi, a.window, a.sinks, 32);
   const int i0 = (int)((int64_t)kt.total * split / a.splits), i1 = (int)((int64_t)kt.total * (split + 1) / a.splits);
   char* ring = lds + wave * WB;
-  const auto keys = [&] {
-    if constexpr (PAGED) return PageRows<T, DP, 32, 1>(a, b, hk, klen - 1, 0, lane);
-    else return LooseRows<T, DP, 32>{a.k + b * a.sk.b + hk * a.sk.h, a.v + b * a.sv.b + hk * a.sv.h, a.sk.l, a.sv.l, klen - 1, cmax, lane};
-  }();
-  auto issue = [&](int i, int buf) { keys.issue(ring + buf * 2 * TB, kt.at(i) * 32); };
+  auto issue = [&](int i, int buf) {
+    char* t = ring + buf * 2 * TB;
+    Tile::template stage<32, 1>(t, kb, a.sk.l, kt.at(i) * 32, klen - 1, cmax, 0, lane);
+    Tile::template stage<32, 1>(t + TB, vb, a.sv.l, kt.at(i) * 32, klen - 1, cmax, 0, lane);
+  };
   if (i0 + wave < i1) issue(i0 + wave, 0);
   int buf = 0;
   for (int i = i0 + wave; i < i1; i += NW, buf ^= 1) {
@@ -1107,8 +1113,8 @@ __global__ __launch_bounds__(64 * (few_waves<T, DP>())) void attn_few_kernel(A a
   for (; bad; bad &= bad - 1) {
     const int i = __builtin_ctz(bad), r = of_lane(row, i), t = min(r / a.G, qlen - 1);
     float x[2];
-    slow_o<T>(x, qb + (int64_t)(hk * a.G + r % a.G) * a.sq.h + t * a.sq.l, keys, a, off + t,
-              of_lane(lsum == 0.f ? __builtin_huge_valf() : w.m, i), kt, i0 + wave, i1, NW, 32, lane);
+    slow_o<T>(x, a.q + b * a.sq.b + (int64_t)(hk * a.G + r % a.G) * a.sq.h + t * a.sq.l, TokenRows{kb, vb, a.sk.l, a.sv.l}, a,
+              off + t, of_lane(lsum == 0.f ? __builtin_huge_valf() : w.m, i), kt, i0 + wave, i1, NW, 32, lane);
     mine[lane * 32 + i] = x[0];
     if (lane + 64 < DP) mine[(lane + 64) * 32 + i] = x[1];
   }
@@ -1131,9 +1137,8 @@ __global__ __launch_bounds__(64 * (few_waves<T, DP>())) void attn_few_kernel(A a
   if (at >= rows || tok >= qlen) return;
   constexpr int PER = DP / (2 * NW);  // columns of a thread
   const int c0 = (int)(threadIdx.x >> 5) * PER;
-  const int64_t place = PAGED ? (int64_t)(seq.first + tok) * a.H + hk * a.G + row % a.G : (int64_t)bk * rows + at;
-  float* pr = a.part + (place * a.splits + split) * a.d;
-  char* orow = a.out + seq.at(a, a.so) + (int64_t)(hk * a.G + row % a.G) * a.so.h + (int64_t)tok * a.so.l;
+  float* pr = a.part + (((int64_t)bk * rows + at) * a.splits + split) * a.d;
+  char* orow = a.out + b * a.so.b + (int64_t)(hk * a.G + row % a.G) * a.so.h + (int64_t)tok * a.so.l;
   // The waves' parts are divided by the sum before they are added, and a split
   // leaves its part so: no larger than the largest value.
   const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
@@ -1154,11 +1159,12 @@ __global__ __launch_bounds__(64 * (few_waves<T, DP>())) void attn_few_kernel(A a
   }
   if (threadIdx.x < 32) {
     if (a.splits > 1) {
-      float* ml = a.part_ml + (place * a.splits + split) * 2;
+      float* ml = a.part_ml + (((int64_t)bk * rows + at) * a.splits + split) * 2;
       ml[0] = m;
       ml[1] = l;
     } else if (a.lse) {
-      a.lse[seq.stat(a, hk * a.G + row % a.G) + tok] = l == 0.f ? -__builtin_huge_valf() : m * LN2 + logf(l);
+      a.lse[((int64_t)b * a.H + hk * a.G + row % a.G) * a.Lq + tok] =
+          l == 0.f ? -__builtin_huge_valf() : m * LN2 + logf(l);
     }
   }
 }
@@ -1167,34 +1173,15 @@ __global__ __launch_bounds__(64 * (few_waves<T, DP>())) void attn_few_kernel(A a
 // the common maximum.
 // All loads of a thread are independent: the kernel is as long as two trips
 // to memory.
-template <typename T, int DP, class A = AttnArgs>
-__global__ __launch_bounds__(256) void attn_join_kernel(A a) {
-  constexpr bool PAGED = A::LIE == Lie::PAGED;
+template <typename T, int DP>
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
   constexpr int PARTS = 256 / DP;  // threads that share a column
   __shared__ float f[256], red[4], out[PARTS][DP];
-  const int t = threadIdx.x;
-  int b = 0, h = blockIdx.x % a.H, tok = blockIdx.x / a.H;
-  bool by_token = false;
-  if constexpr (PAGED) by_token = a.by_token;
-  if (by_token) {
-    if constexpr (PAGED) b = find_last(a.B, t % WAVE, [&](int i) { return seq_len(a.offsets, i, a.Lq) <= tok; });
-    if (b < 0) return;
-  } else {
-    int rows = a.G * a.Lq;
-    if constexpr (PAGED) rows = a.G * a.few;
-    const int n = blockIdx.x % rows, bk = blockIdx.x / rows;
-    b = bk / a.Hk, tok = n / a.G, h = bk % a.Hk * a.G + n % a.G;
-  }
-  const AttnSeq seq(a, b);
-  int64_t place = blockIdx.x;
-  if constexpr (PAGED) {
-    if (by_token) tok -= seq.first;
-    else place = (int64_t)(seq.first + tok) * a.H + h;
-    if ((seq.qlen > a.few) != by_token) return;
-  }
-  if (tok >= seq.qlen) return;
-  const float* ml = a.part_ml + place * a.splits * 2;
-  const float* pr = a.part + place * a.splits * a.d;
+  const int rows = a.G * a.Lq, n = blockIdx.x % rows, bk = blockIdx.x / rows, t = threadIdx.x;
+  const int hk = bk % a.Hk, b = bk / a.Hk, tok = n / a.G, h = hk * a.G + n % a.G;
+  if (tok >= seq_len(a.q_lens, b, a.Lq)) return;
+  const float* ml = a.part_ml + ((int64_t)bk * rows + n) * a.splits * 2;
+  const float* pr = a.part + ((int64_t)bk * rows + n) * a.splits * a.d;
   constexpr float NONE = -__builtin_huge_valf();
   const float ms = t < a.splits ? ml[2 * t] : NONE, ls = t < a.splits ? ml[2 * t + 1] : 0.f;
   float m = ms;
@@ -1224,9 +1211,249 @@ __global__ __launch_bounds__(256) void attn_join_kernel(A a) {
   if (part == 0 && c < a.d) {
 #pragma unroll
     for (int i = 1; i < PARTS; ++i) x += out[i][c];
-    io_traits<T>::store(reinterpret_cast<T*>(a.out + seq.at(a, a.so) + (int64_t)h * a.so.h + (int64_t)tok * a.so.l) + c, x);
+    io_traits<T>::store(reinterpret_cast<T*>(a.out + b * a.so.b + (int64_t)h * a.so.h + (int64_t)tok * a.so.l) + c, x);
   }
-  if (a.lse && t == 0) a.lse[seq.stat(a, h) + tok] = l == 0.f ? NONE : m * LN2 + logf(l);
+  if (a.lse && t == 0) a.lse[((int64_t)b * a.H + h) * a.Lq + tok] = l == 0.f ? NONE : m * LN2 + logf(l);
+}
+
+// The same for the forward's key splits over pages, a row (token and head) a wave.
+template <typename T, int DP>
+__global__ __launch_bounds__(256) void split_join_kernel(PagedArgs a) {
+  constexpr float NONE = -__builtin_huge_valf();
+  constexpr int BN = attn_bn<T, DP>();
+  const int lane = threadIdx.x % WAVE, c = 2 * lane;
+  const int64_t place = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
+  const int h = (int)(place % a.H), token = (int)(place / a.H), BM = 128 / a.hg;
+  if (token >= a.Lq) return;
+  const int b = __builtin_amdgcn_readfirstlane(find_last(a.B, lane, [&](int i) { return seq_len(a.offsets, i, a.Lq) <= token; }));
+  if (b < 0) return;
+  const AttnSeq seq(a, b);
+  const int row = token - seq.first, r0 = row / BM * BM, off = seq.klen - seq.qlen;
+  if (seq.qlen <= a.few || row >= seq.qlen) return;
+  const int splits = key_splits(a, KeyTiles(off + r0, off + min(r0 + BM, seq.qlen) - 1, a.window, a.sinks, BN));
+  if (splits == 1) return;
+  const float* ml = a.part_ml + place * a.splits * 2;
+  const float* pr = a.part + place * a.splits * a.d;
+  const float2 s = lane < splits ? *reinterpret_cast<const float2*>(ml + 2 * lane) : make_float2(NONE, 0.f);
+  float m = s.x;
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, WAVE));
+  // a split without keys counts for nothing; one whose scores are all NaN has no maximum but a sum
+  const float f = s.y == 0.f ? 0.f : s.x == NONE ? s.y : s.y * __builtin_amdgcn_exp2f(s.x - m), l = wave_sum(f);
+  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+  float2 x = make_float2(0.f, 0.f);
+#pragma unroll 8
+  for (int i = 0; i < splits; ++i) {
+    const float g = of_lane(f, i) * inv;
+    float2 v = make_float2(0.f, 0.f);
+    if (c < a.d) v = *reinterpret_cast<const float2*>(pr + (int64_t)i * a.d + c);
+    x.x += g == 0.f ? 0.f : g * v.x;
+    x.y += g == 0.f ? 0.f : g * v.y;
+  }
+  T* out = reinterpret_cast<T*>(a.out + seq.at(a, a.so) + (int64_t)h * a.so.h + (int64_t)row * a.so.l);
+  if (c < a.d) io_traits<T>::store(out + c, x.x), io_traits<T>::store(out + c + 1, x.y);
+  if (a.lse && lane == 0) a.lse[seq.stat(a, h) + row] = l == 0.f ? NONE : m * LN2 + logf(l);
+}
+
+// ------------------------------------------------------------------ pages, few rows
+// Next tokens over pages.  The work is reading keys, of sequences whose lengths
+// only the device knows: all tiles of 32 keys that some sequence's rows see,
+// one after another -- by sequence, 32 of its rows (ordered by token, as in
+// attn_few_kernel) and key head, an item -- are dealt to the launch's waves in
+// equal runs.  Each wave goes along its run alone, with its own ring and no
+// barrier: while one begins an item the others read on.  An item that lies in
+// one run is finished there; of others each wave leaves its part (at most two
+// a wave: its first and its last), which stream_join_kernel adds up.
+constexpr int STREAM_SCAN = 256;  // sequences whose work a workgroup sums itself
+
+// The rows of a sequence in tiles of 32, and the units of each, at least one:
+// an item that sees no key is written too.
+struct StreamItem {
+  KeyTiles kt;
+  int rtiles, units;
+  __device__ __forceinline__ StreamItem(const PagedArgs& a, const AttnSeq& s)
+      : kt(s.klen - s.qlen, s.klen - 1, a.window, a.sinks, 32), rtiles(s.qlen > a.few ? 0 : (a.G * s.qlen + 31) / 32),
+        units(a.unit == 1 ? max(1, kt.total) : max(1, (kt.total + a.unit - 1) / a.unit)) {}
+};
+// The sequences that a workgroup has summed the work of
+struct StreamScan {
+  int upto[STREAM_SCAN + 1], first[STREAM_SCAN], qlen[STREAM_SCAN], klen[STREAM_SCAN];
+};
+// upto[i]: work of the sequences before i, for i = 0 .. B, by a workgroup of NT threads
+template <int NT>
+__device__ __forceinline__ void stream_scan(const PagedArgs& a, int* upto, StreamScan* keep) {
+  __shared__ int sums[NT / WAVE];
+  const int lane = threadIdx.x % WAVE, wave = threadIdx.x / WAVE;
+  int before = 0;
+  for (int b0 = 0; b0 < a.B; b0 += NT) {
+    const int b = b0 + threadIdx.x;
+    int x = 0;
+    if (b < a.B) {
+      const int first = seq_len(a.offsets, b, a.Lq);
+      const AttnSeq s(b, min(max(seq_len(a.offsets, b + 1, a.Lq) - first, 0), a.most), seq_len(a.k_lens, b, a.Lk), first);
+      const StreamItem it(a, s);
+      x = it.rtiles * it.units * a.Hk;
+      if (keep) keep->first[b] = first, keep->qlen[b] = s.qlen, keep->klen[b] = s.klen;
+    }
+    for (int o = 1; o < WAVE && o < a.B; o *= 2) {
+      const int y = __shfl_up(x, o, WAVE);
+      if (lane >= o) x += y;
+    }
+    if (b0) __syncthreads();
+    if (lane == WAVE - 1) sums[wave] = x;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NT / WAVE; ++i)
+      if (i < wave) x += sums[i];
+    if (b < a.B) upto[b + 1] = before + x;
+#pragma unroll
+    for (int i = 0; i < NT / WAVE; ++i) before += sums[i];
+  }
+  if (threadIdx.x == 0) upto[0] = 0;
+  __syncthreads();
+}
+__global__ __launch_bounds__(1024) void stream_plan_kernel(PagedArgs a) { stream_scan<1024>(a, a.upto, nullptr); }
+
+// An item that lies in several runs, noted by the wave of the second of them
+// (parts = 0: none begins so): its first row's place, rows and heads, and where
+// its first part is.
+struct StreamJoin {
+  int first, row, rows, head;  // the sequence's first token; rows row .. row + rows - 1, ordered by token; first head
+  int part, parts;             // of parts part, part + 2 (or + 1, see below), + 4 ..
+};
+
+template <typename T, int DP>
+__global__ __launch_bounds__(64 * (few_waves<T, DP>())) void stream_kernel(PagedArgs a) {
+  using Tile = AttnTile<T, DP>;
+  constexpr int NW = few_waves<T, DP>(), TB = few_tile<T, DP>(), WB = 4 * TB;
+  __shared__ __align__(1024) char lds[NW * WB];
+  __shared__ StreamScan scan;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 31;
+  if ((int)blockIdx.x >= a.main)
+    return clear_rest(a, a.out, a.so, a.H, a.d * (int)sizeof(T), a.lse, (int)blockIdx.x - a.main, a.rest);
+  if (!a.upto) stream_scan<64 * NW>(a, scan.upto, &scan);
+  const int* upto = a.upto ? a.upto : scan.upto;
+  const int work = __builtin_amdgcn_readfirstlane(upto[a.B]), run = max(a.share, (work + a.waves - 1) / a.waves);
+  const int me = blockIdx.x * NW + wave, cmax = a.d * (int)sizeof(T) / 16 - 1;
+  const int t0 = min(work, me * run), t1 = min(work, t0 + run);
+  char* ring = lds + wave * WB;
+  StreamJoin join = {0, 0, 0, 0, 0, 0};
+#pragma unroll 1
+  for (int t = t0; t < t1;) {
+    const int b = __builtin_amdgcn_readfirstlane(find_last(a.B, lane, [&](int i) { return upto[i] <= t; }));
+    auto of = [&](const int(&x)[STREAM_SCAN]) { return __builtin_amdgcn_readfirstlane(x[b]); };
+    const AttnSeq seq = a.upto ? AttnSeq(a, b) : AttnSeq(b, of(scan.qlen), of(scan.klen), of(scan.first));
+    const int qlen = seq.qlen, klen = seq.klen, off = klen - qlen;
+    const StreamItem it(a, seq);
+    const KeyTiles& kt = it.kt;
+    const int local = t - __builtin_amdgcn_readfirstlane(upto[b]), item = local / it.units, u0 = local - item * it.units;
+    const int u1 = min(it.units, u0 + (t1 - t)), hk = item % a.Hk, r0 = 32 * (item / a.Hk);
+    const int i0 = u0 * a.unit, i1 = min(kt.total, u1 * a.unit);
+    const int rows = a.G * qlen, row = min(r0 + n, rows - 1), tok = row / a.G, h = hk * a.G + row % a.G;
+    const char* qb = a.q + seq.at(a, a.sq);
+    AttnRows<T, DP> w;
+    w.clear();
+    const PageRows<T, DP, 32, 1> keys(a, b, hk, klen - 1, 0, lane);
+    auto issue = [&](int i, int buf) { keys.issue(ring + buf * 2 * TB, kt.at(i) * 32); };
+    wait_lgkm0();  // the item before has been read
+    if (i0 < i1) issue(i0, 0);
+    load_rows(w.q, qb + (int64_t)h * a.sq.h + (int64_t)tok * a.sq.l, cmax, lane);
+    w.p = off + tok;
+    w.w = {off + r0 / a.G, off + min(r0 + 31, rows - 1) / a.G};
+    int buf = 0;
+#pragma unroll 1
+    for (int i = i0; i < i1; ++i, buf ^= 1) {
+      wait_lgkm0();  // the tile that the next copies overwrite has been read
+      if (i + 1 < i1) {
+        issue(i + 1, buf ^ 1);
+        wait_vm<Tile::CPR>();  // the 2 x CPR / 2 copies of the tile before them have landed
+      } else {
+        wait_vm<0>();
+      }
+      asm volatile("" ::: "memory");
+      const char* x = ring + buf * 2 * TB;
+      w.template tile<32, 1>(x, x + TB, 0, kt.at(i) * 32, a.window, a.sinks, a.c, lane);
+    }
+    const bool whole = u0 == 0 && u1 == it.units;
+    const float l = pair_sum(w.l), inv = l > 0.f || l != l ? 1.f / l : 0.f;
+    const int64_t part = (int64_t)(2 * me + (t == t0 ? 0 : 1)) * a.rows;
+    char* out = a.out + seq.at(a, a.so) + (int64_t)h * a.so.h + (int64_t)tok * a.so.l;
+    if (r0 + n < rows) {
+      if (whole) {
+        store_rows<T, DP>(w.o, inv, out, a.d, lane);
+        if (a.lse && lane < 32) a.lse[seq.stat(a, h) + tok] = l == 0.f ? -__builtin_huge_valf() : w.m * LN2 + logf(l);
+      } else {
+        store_rows<float, DP>(w.o, inv, reinterpret_cast<char*>(a.part + (part + n) * a.d), a.d, lane);
+        if (lane < 32) *reinterpret_cast<float2*>(a.part_ml + (part + n) * 2) = make_float2(w.m, l);
+      }
+    }
+    for (uint32_t bad = not_finite(w.o) & (uint32_t)__ballot(r0 + n < rows && l == l); bad; bad &= bad - 1) {
+      const int i = __builtin_ctz(bad), r = r0 + i;
+      float x[2];
+      slow_o<T>(x, qb + (int64_t)(hk * a.G + r % a.G) * a.sq.h + (int64_t)(r / a.G) * a.sq.l, keys, a, off + r / a.G,
+                of_lane(log2_sum(w.m, l), i), kt, i0, i1, 1, 32, lane);
+      if (whole) store_lane2<T>(a.out + seq.at(a, a.so) + (int64_t)(hk * a.G + r % a.G) * a.so.h + (int64_t)(r / a.G) * a.so.l, x, a.d, lane);
+      else store_lane2<float>(reinterpret_cast<char*>(a.part + (part + i) * a.d), x, a.d, lane);
+    }
+    // the item began in the run before this one, there as its first item or a later one
+    if (t == t0 && u0 > 0 && u0 <= run)
+      join = {seq.first, r0, min(32, rows - r0), hk * a.G, 2 * (me - 1) + (u0 < run ? 1 : 0), 2 + (it.units - u0 - 1) / run};
+    t += u1 - u0;
+  }
+  if (lane == 0) a.joins[me] = join;
+}
+
+// Items that lie in several runs: the parts, weighted by their sums relative to
+// the common maximum.  Workgroup (w, y) takes rows y, y + 4 .. of the item that
+// wave w + 1 noted; its waves share a row's parts.  Its length is that of its
+// trips to memory: the note, the statistics, 16 parts at a time of each wave.
+constexpr int JOIN_ROWS = 4;
+template <typename T>
+__global__ __launch_bounds__(256) void stream_join_kernel(PagedArgs a) {
+  constexpr float NONE = -__builtin_huge_valf();
+  __shared__ float2 other[4][WAVE];
+  const StreamJoin j = a.joins[blockIdx.x + 1];
+  const int lane = threadIdx.x % WAVE, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE), c = 2 * lane;
+  for (int n = blockIdx.y; j.parts > 0 && n < j.rows; n += JOIN_ROWS) {
+    // all parts but the first are the first ones of their waves
+    auto place = [&](int i) { return (int64_t)(i == 0 ? j.part : (j.part & ~1) + 2 * i) * a.rows + n; };
+    auto stat = [&](int i) { return i < j.parts ? *reinterpret_cast<const float2*>(a.part_ml + place(i) * 2) : make_float2(NONE, 0.f); };
+    // a part without keys counts for nothing; one whose scores are all NaN has no maximum but a sum
+    auto weight = [&](float2 x, float m) { return x.y == 0.f ? 0.f : x.x == NONE ? x.y : x.y * __builtin_amdgcn_exp2f(x.x - m); };
+    const float2 head = stat(lane);
+    float m = head.x;
+    for (int i = lane + WAVE; i < j.parts; i += WAVE) m = fmaxf(m, stat(i).x);
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, WAVE));
+    float l = weight(head, m);
+    for (int i = lane + WAVE; i < j.parts; i += WAVE) l += weight(stat(i), m);
+    l = wave_sum(l);
+    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+    float2 x = make_float2(0.f, 0.f);
+    for (int i0 = 0; i0 < j.parts; i0 += WAVE) {
+      const float f = weight(i0 == 0 ? head : stat(i0 + lane), m) * inv;
+      const int most = min(WAVE, j.parts - i0);
+#pragma unroll
+      for (int k = 0; k < WAVE / 4; ++k) {  // a wave's 16 of 64 parts: all loads before the first is waited for
+        const int i = 4 * k + wave;
+        const float g = of_lane(f, i);
+        float2 v = make_float2(0.f, 0.f);
+        if (i < most && c < a.d) v = *reinterpret_cast<const float2*>(a.part + place(i0 + i) * a.d + c);
+        x.x += g == 0.f ? 0.f : g * v.x;
+        x.y += g == 0.f ? 0.f : g * v.y;
+      }
+    }
+    __syncthreads();
+    other[wave][lane] = x;
+    __syncthreads();
+    if (wave != 0) continue;
+#pragma unroll
+    for (int i = 1; i < 4; ++i) x.x += other[i][lane].x, x.y += other[i][lane].y;
+    const int tok = (j.row + n) / a.G, h = j.head + (j.row + n) % a.G;
+    T* out = reinterpret_cast<T*>(a.out + (int64_t)h * a.so.h + (int64_t)(j.first + tok) * a.so.l);
+    if (c < a.d) io_traits<T>::store(out + c, x.x), io_traits<T>::store(out + c + 1, x.y);
+    if (a.lse && lane == 0) a.lse[(int64_t)h * a.Lq + j.first + tok] = l == 0.f ? NONE : m * LN2 + logf(l);
+  }
 }
 
 // ------------------------------------------------------------------ backward: dq

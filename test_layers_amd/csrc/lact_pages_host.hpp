@@ -67,61 +67,103 @@ lact_status check_offsets(const void* offsets) {
 // ------------------------------------------------------------------ paged attention
 // Which kernels take a batch.  The host knows the longest sequence's rows, not
 // whether others have as many: sequences of few rows (one 32-row tile of a key
-// head, `few`) go to the few-row kernel with split keys, longer ones to the
-// forward's, in two launches where both may come.  A batch that the few-row
-// kernel would take whole (few_tiles) goes there.
+// head, `few`) go to the streams of tiles, longer ones to the forward's kernel,
+// in two launches where both may come.  (Sequences of a few 32-row tiles read
+// their keys once for each in the streams: 64 and 128 rows of 32 (8) heads over
+// 16384 keys 90 and 149 us there.)
 struct PagedPlan {
-  int64_t few = 0;         // rows of a sequence up to which the few-row kernel has it
-  int few_tiles = 0, few_splits = 1;
+  int64_t few = 0;         // rows of a sequence up to which the streams have it
+  int64_t items = 0;       // of the streams, at most
   int64_t few_grid = 0, big_grid = 0;  // workgroups, 0: not launched
-  int hg = 1, big_splits = 1;
-  size_t few_part = 0, few_ml = 0, big_part = 0, big_ml = 0, total = 0;  // the workspace
+  int waves = 0, rows = 0, unit = 1, big_splits = 1, chunk = 1;
+  size_t upto = 0, joins = 0, few_part = 0, few_ml = 0, big_part = 0, big_ml = 0, total = 0;  // the workspace
 };
 
-// Key splits of the forward for `groups` workgroups over up to `keys` keys
-int split_keys(const lact_attention& w, int64_t groups) {
-  const int64_t at_once = (w.io_dtype == LACT_DTYPE_F32 && w.d > 64 ? 1 : 2) * NCU;
-  const int64_t keys = limited(w) ? std::min(w.k_len, w.window + w.sinks + w.q_len) : w.k_len;
-  if (groups <= 0 || 2 * groups > at_once) return 1;
-  return (int)std::max<int64_t>(1, std::min<int64_t>({at_once / groups, keys / 512, 32}));
+// Key splits of the forward's row tiles: `groups` workgroups (as far as the
+// host can tell) of `rows` rows a head.
+//
+// One sequence: all tiles have about as many keys.  A workgroup alone on its
+// compute unit takes `alone` us a tile, two take `both`, a join about 6 us, and
+// the parts pass memory twice.  Over 16384 keys, 32 (8) heads of 128, us with
+// 1, 2, 3, 4, 5, 8 splits: 256 rows (64 workgroups) 319, 177, 127, 102, 107, 87;
+// 512 rows 321, 188, 175, 153, 183, 162; 1200 rows 414, 408, 357, 359, 357, 368;
+// 2048 rows, one round of two a unit, 493, 522, 527, 533, 543, 584; the model
+// chooses 8, 4, 5 and 1.
+//
+// Several, whose keys only the device knows, while one round holds them: a
+// quarter of the most keys a split (less where there are few workgroups), so
+// that long ones are split and short ones are not.  40 sequences, 4 of them of
+// 512 rows, of up to 12000 keys: with splits of 48 tiles 519 us, of 16 540, none
+// 544; one of 512 rows among 64 of one: 352, none 400; 4 of 100: 189, none 493.
+// Beyond one round (8 of 1024 rows among 20) none is best: 946, and 1023 with a
+// quarter.
+void split_keys(const lact_attention& w, int64_t groups, int64_t rows, int& splits, int& chunk) {
+  const bool fp32 = w.io_dtype == LACT_DTYPE_F32, wide = w.d > 64;
+  const int64_t room = (fp32 && wide ? 1 : 2) * NCU;
+  const int64_t keys = limited(w) ? std::min(w.k_len, w.window + w.sinks + rows) : w.k_len;
+  const int64_t tiles = ceil_div(keys, fp32 && wide ? 32 : 64);
+  splits = chunk = 1;
+  if (w.batch == 1) {
+    const double alone = fp32 ? 3.7 : wide ? 1.25 : 0.7, both = fp32 && wide ? alone : fp32 ? 7.4 : wide ? 1.93 : 1.1;
+    const double part = (double)groups * 128 * (double)(w.d + 2) * 8 / 4e6;  // us of one split's parts
+    double best = 1e30;
+    for (int64_t s = 1; s <= 64 && (s == 1 || tiles / s >= 4); ++s) {
+      const int64_t full = groups * s / room, left = groups * s % room;
+      const double round = (double)full * both + (left == 0 ? 0.0 : left <= NCU ? alone : both);
+      const double cost = round * (double)ceil_div(tiles, s) + (s > 1 ? 6.0 + part * (double)s : 0.0);
+      if (cost < best) best = cost, splits = (int)s;
+    }
+    if (splits > 1) chunk = 4;  // of a tile of early rows, which has fewer keys
+  } else if (groups <= room) {
+    const int64_t s = std::max<int64_t>(4, std::min<int64_t>(32, room / std::max<int64_t>(1, groups)));
+    chunk = (int)std::max<int64_t>(8, ceil_div(tiles, s));
+    splits = (int)std::max<int64_t>(1, (tiles + chunk / 2) / chunk);
+  }
 }
+
+// Fewest units of a wave's run, and the units of a batch, which are counted in 32 bits
+constexpr int STREAM_SHARE = 2;
+constexpr int64_t STREAM_MOST = INT64_C(1) << 30;
 
 PagedPlan paged_plan(const lact_paged& p, const lact_attention& w) {
   PagedPlan x;
   if (w.batch == 0 || p.tokens == 0 || w.q_len == 0) return x;
   const int64_t G = w.heads / w.kv_heads, small = std::max<int64_t>(1, 32 / G);
   lact_attention f = w;
-  x.few_tiles = few_tiles(w);
-  if (x.few_tiles > 0 || w.q_len <= small) {
-    x.few = w.q_len;
-  } else if (w.batch > 1) {
-    x.few = f.q_len = small;
-  }
-  if (x.few > 0) {
-    x.few_tiles = (int)ceil_div(G * x.few, 32);
-    const int64_t most = std::max<int64_t>(1, ceil_div(few_keys(f), 256)),
-                  want = few_room(f) / std::max<int64_t>(1, (int64_t)w.batch * w.kv_heads * x.few_tiles);
-    x.few_splits = (int)std::min<int64_t>(std::min(most, std::max<int64_t>(1, want)), 256);
-    x.few_grid = (int64_t)w.batch * w.kv_heads * x.few_tiles * x.few_splits;
-  }
-  if (x.few < w.q_len) {
-    PackedArgs a;
-    memset(&a, 0, sizeof(a));
-    row_tiles(w, 128, a);
-    x.hg = a.hg;
-    const int64_t groups = count_tiles(w, p.tokens, 128 / x.hg, a) * (w.heads / x.hg);
-    x.big_splits = split_keys(w, groups);
-    x.big_grid = groups * x.big_splits;
-  }
+  if (w.q_len <= small) x.few = w.q_len;
+  else if (w.batch > 1) x.few = small;
+  f.q_len = x.few;
+  int waves = 0;  // of a workgroup of the streams
+  (void)by_tile(w, [&](auto t, auto dp) {
+    waves = few_waves<decltype(t), decltype(dp)::value>();
+    return LACT_OK;
+  });
   const size_t rows = (size_t)p.tokens * w.heads;
   auto place = [&](size_t bytes) {
     const size_t at = x.total;
     x.total += align256(bytes);
     return at;
   };
-  if (x.few_splits > 1) {
-    x.few_part = place(rows * x.few_splits * w.d * 4);
-    x.few_ml = place(rows * x.few_splits * 2 * 4);
+  if (x.few > 0) {
+    // no more workgroups than run at once, nor than have a share of the tiles that there can be
+    const int64_t items = x.items = std::min((int64_t)w.batch * ceil_div(G * x.few, 32), p.tokens * ceil_div(G, 32)) * w.kv_heads;
+    const int64_t tiles = ceil_div(few_keys(f), 32) + 2;  // the sinks' and the window's may be cut anew
+    while (items * ceil_div(tiles, x.unit) > STREAM_MOST && x.unit < tiles) x.unit *= 2;
+    x.few_grid = std::min(few_room(f), ceil_div(items, waves * STREAM_SHARE) * tiles);
+    x.waves = (int)(x.few_grid * waves);
+    x.rows = (int)std::min<int64_t>(32, G * x.few);
+    if (w.batch > STREAM_SCAN) x.upto = place((size_t)(w.batch + 1) * 4);
+    x.joins = place((size_t)x.waves * sizeof(StreamJoin));
+    x.few_part = place((size_t)x.waves * 2 * x.rows * w.d * 4);
+    x.few_ml = place((size_t)x.waves * 2 * x.rows * 2 * 4);
+  }
+  if (x.few < w.q_len) {
+    PackedArgs a;
+    memset(&a, 0, sizeof(a));
+    row_tiles(w, 128, a);
+    const int64_t tile = 128 / a.hg, groups = count_tiles(w, p.tokens, tile, a), heads = w.heads / a.hg;
+    split_keys(w, std::min(groups, ceil_div(p.tokens, tile)) * heads, tile, x.big_splits, x.chunk);
+    x.big_grid = groups * heads * x.big_splits;
   }
   if (x.big_splits > 1) {
     x.big_part = place(rows * x.big_splits * w.d * 4);
@@ -167,6 +209,8 @@ lact_status lact_paged_attention(const lact_paged* p, const void* q, const lact_
   if (!aligned(lse, 4)) return fail(LACT_ERR_INVALID_ARG, "lse is not 4-byte aligned");
   TRY(check_apart({o, lse}, {q, k_pages, v_pages, offsets, k_lens, table}));
   const PagedPlan x = paged_plan(*p, w);
+  if (x.items > STREAM_MOST)
+    return fail(LACT_ERR_UNSUPPORTED, "%lld sequences and key heads: more than a launch takes", (long long)x.items);
   TRY(check_ws(ws, ws_bytes, x.total));
   a.q = static_cast<const char*>(q);
   a.k = static_cast<const char*>(k_pages);
@@ -181,13 +225,11 @@ lact_status lact_paged_attention(const lact_paged* p, const void* q, const lact_
   a.few = (int32_t)x.few;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const int64_t rows = p->tokens * w.heads, clear = p->flags & LACT_CLEAR_REST ? rest_groups(rows * w.d * es) : 0;
-  const int64_t few_rows = (int64_t)w.batch * w.heads * x.few;
   // what is cleared is cleared beside the kernel of the longer sequences, if there is one
   const int64_t few_clear = x.big_grid > 0 ? 0 : clear, big_grid = x.big_grid + (clear - few_clear);
   TRY(by_tile(w, [&](auto t, auto dp) { return check_grid(x.few_grid + few_clear, 64 * few_waves<decltype(t), decltype(dp)::value>()); }));
   TRY(check_grid(big_grid, 256));
-  if (x.few_splits > 1) TRY(check_grid(few_rows, 256));
-  if (x.big_splits > 1) TRY(check_grid(rows, 256));
+  if (x.big_splits > 1) TRY(check_grid(ceil_div(rows, 4), 256));
   TRY(check_device_again());
   char* const base = static_cast<char*>(ws);
   return by_tile(w, [&](auto t, auto dp) -> lact_status {
@@ -196,32 +238,40 @@ lact_status lact_paged_attention(const lact_paged* p, const void* q, const lact_
     a.rest = (int32_t)clear;
     PagedArgs f = a;
     if (x.few_grid + few_clear > 0) {
-      f.tiles = std::max(1, x.few_tiles);
-      f.splits = x.few_splits;
       f.main = (int32_t)x.few_grid;
+      f.waves = x.waves;
+      f.share = STREAM_SHARE;
+      f.unit = x.unit;
+      f.rows = x.rows;
+      f.upto = w.batch > STREAM_SCAN ? reinterpret_cast<int32_t*>(base + x.upto) : nullptr;
+      f.joins = reinterpret_cast<StreamJoin*>(base + x.joins);
       f.part = reinterpret_cast<float*>(base + x.few_part);
       f.part_ml = reinterpret_cast<float*>(base + x.few_ml);
+      if (f.upto && x.few_grid > 0) {
+        KernelTimer kt(LACT_K_ATTN, s);
+        LACT_LAUNCH(stream_plan_kernel, dim3(1), dim3(1024), s, f);
+      }
       KernelTimer kt(LACT_K_ATTN, s);
-      LACT_LAUNCH((attn_few_kernel<T, DP, PagedArgs>), dim3((unsigned)(x.few_grid + few_clear)), dim3(64 * (few_waves<T, DP>())), s, f);
+      LACT_LAUNCH((stream_kernel<T, DP>), dim3((unsigned)(x.few_grid + few_clear)), dim3(64 * (few_waves<T, DP>())), s, f);
     }
     if (big_grid > 0) {
       row_tiles(w, 128, a);
       (void)count_tiles(w, p->tokens, 128 / a.hg, a);
       a.splits = x.big_splits;
+      a.chunk = x.chunk;
       a.main = (int32_t)x.big_grid;
       a.part = reinterpret_cast<float*>(base + x.big_part);
       a.part_ml = reinterpret_cast<float*>(base + x.big_ml);
       KernelTimer kt(LACT_K_ATTN, s);
       LACT_LAUNCH((attn_fwd_kernel<T, DP, 1, PagedArgs>), dim3((unsigned)big_grid), dim3(256), s, a);
     }
-    if (x.few_splits > 1) {
+    if (x.waves > 1) {
       KernelTimer kt(LACT_K_ATTN, s);
-      LACT_LAUNCH((attn_join_kernel<T, DP, PagedArgs>), dim3((unsigned)few_rows), dim3(256), s, f);
+      LACT_LAUNCH((stream_join_kernel<T>), dim3((unsigned)(x.waves - 1), (unsigned)std::min(x.rows, JOIN_ROWS)), dim3(256), s, f);
     }
     if (x.big_splits > 1) {
-      a.by_token = 1;
       KernelTimer kt(LACT_K_ATTN, s);
-      LACT_LAUNCH((attn_join_kernel<T, DP, PagedArgs>), dim3((unsigned)rows), dim3(256), s, a);
+      LACT_LAUNCH((split_join_kernel<T, DP>), dim3((unsigned)ceil_div(rows, 4)), dim3(256), s, a);
     }
     HIP_TRY(hipGetLastError());
     return LACT_OK;

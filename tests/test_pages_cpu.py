@@ -176,19 +176,23 @@ def test_workspace_of_the_backward_is_bounded(kw):
     assert stats - 512 <= need <= stats + 768 * 2 * 128 * 128 * 4 + 256
 
 
-def _parts(**kw):
-    a = dict(heads=32, kv_heads=8, d=128, k_len=32768, pages=1 << 16, page=128, width=256, window=0)
+def _paged_ws(**kw):
+    a = dict(heads=32, kv_heads=8, d=128, k_len=32768, pages=1 << 15, page=128, width=256, window=0)
     a.update(kw)
-    return lact.lib().lact_paged_attention_workspace_size(R(_paged(**a))) / (a["tokens"] * 32 * 130 * 4)
+    return lact.lib().lact_paged_attention_workspace_size(R(_paged(**a)))
 
 
-def test_keys_are_split_where_rows_are_few():
-    """In parts of one result and two statistics a row and head."""
-    assert _parts(batch=1, tokens=1, longest=1) >= 16 and _parts(batch=4, tokens=4, longest=1) >= 4
-    assert _parts(batch=1, tokens=256, longest=256) >= 2                         # a chunk that fills half the chip
-    assert _parts(batch=1, tokens=1, longest=1, k_len=100) == 0
-    assert _parts(batch=0, tokens=1, longest=1) == 0 and _parts(batch=4, tokens=64, longest=0) == 0
-    assert _parts(batch=1, tokens=1, longest=1, pages=0) == 0                    # no keys
+def test_workspace_of_paged_attention():
+    """Few rows: two parts a wave, of at most 2048 waves and 32 rows; a chunk
+    that fills half the chip: parts of its rows; no more, whatever the batch."""
+    part = 130 * 4   # a row's result and two statistics
+    for kw, rows in ((dict(batch=1, tokens=1, longest=1), 4), (dict(batch=96, tokens=96, longest=1), 4),
+                     (dict(batch=300, tokens=2400, longest=8), 32), (dict(batch=1 << 20, tokens=1 << 20, longest=1), 4)):
+        need = _paged_ws(**kw)
+        assert 512 * part < need <= 2048 * 2 * rows * part + 8 * (kw["batch"] + 1) + 1024, kw
+    assert _paged_ws(batch=1, tokens=256, longest=256) >= 2 * 256 * 32 * part
+    assert _paged_ws(batch=1, tokens=4096, longest=4096) == 0
+    assert _paged_ws(batch=0, tokens=1, longest=1) == 0 and _paged_ws(batch=4, tokens=64, longest=0) == 0
 
 
 def test_grids_beyond_a_launch_are_refused():
@@ -196,7 +200,7 @@ def test_grids_beyond_a_launch_are_refused():
     st = _st(1 << 40, 8, 1024)
     assert _fwd(_packed(**big), q=(FAKE, st), k=(FAKE * 2, st), v=(FAKE * 3, st), o=(FAKE * 4, st)) == U
     assert "launch" in lact.last_error()
-    huge = dict(batch=1 << 24, heads=64, kv_heads=64, d=8, tokens=1 << 24, longest=1)
+    huge = dict(batch=1 << 24, heads=64, kv_heads=64, d=8, tokens=1 << 24, longest=99)
     st = _st(1 << 40, 8, 512)
     assert _pgd(_paged(**huge), q=(FAKE, st), o=(FAKE * 4, st), k=(FAKE * 2, _st(1 << 20, 8, 512)),
                 v=(FAKE * 3, _st(1 << 20, 8, 512))) == U and "launch" in lact.last_error()
