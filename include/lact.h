@@ -576,7 +576,7 @@ typedef struct {
     int32_t batch;      /* requests, 0 .. 2^24 */
     int32_t page;       /* as in lact_paged */
     int32_t width;      /* entries of a request in the table, >= 0; width * page < 2^30 */
-    int32_t entries;    /* of `free`, >= 0: `have` is cut to that */
+    int32_t entries;    /* of `free`, 0 .. 2^28 - 1: `have` is cut to that */
     int64_t tokens;     /* rows of the step, 0 <= tokens < 2^30 */
 } lact_slots;
 /* int64 arrays 8-byte, table and free 4-byte aligned.

@@ -23,7 +23,7 @@ struct SlotArgs {
   int64_t *offsets, *k_lens;     // [B + 1], [B]
   int64_t *slots, *positions;    // [T]
   int64_t* left;                 // [2]: free pages left, requests not served
-  int64_t* base;                 // [B] workspace: place in `free` of a request's first new page; -1: not served
+  int32_t* base;                 // [B] workspace: place in `free` of a request's first new page; -1: not served
   int32_t B, T, width, entries;
   FastDiv by_page;
 };
@@ -33,75 +33,84 @@ __device__ __forceinline__ int64_t slot_len(const SlotArgs& a, int b) {
   const int64_t n = a.lens[b];
   return n < 0 ? 0 : n;
 }
-__device__ __forceinline__ int64_t pages_of(int64_t tokens, int64_t page) { return (tokens + page - 1) / page; }
-
-// inclusive sum over the workgroup's threads, and over all of them
-__device__ __forceinline__ int64_t block_sum(int64_t x, int64_t (&lds)[PLAN_THREADS / WAVE], int64_t& total) {
-  const int lane = threadIdx.x % WAVE, wave = threadIdx.x / WAVE;
-#pragma unroll
-  for (int o = 1; o < WAVE; o *= 2) {
-    const int64_t y = __shfl_up(x, o, WAVE);
-    if (lane >= o) x += y;
-  }
-  __syncthreads();
-  if (lane == WAVE - 1) lds[wave] = x;
-  __syncthreads();
-  total = 0;
-  int64_t before = 0;
-#pragma unroll
-  for (int i = 0; i < PLAN_THREADS / WAVE; ++i) {
-    if (i == wave) before = total;
-    total += lds[i];
-  }
-  return before + x;
+__device__ __forceinline__ int pages_of(const SlotArgs& a, int tokens) {
+  return (int)a.by_page.div((uint32_t)(tokens + (int)a.by_page.d - 1));
 }
 
-// One workgroup: offsets, k_lens and left; keep(b, first row, length, base) for each request.
+// Inclusive sum over the first `waves` waves of the workgroup, cut at `most`
+// (x and most at most 2^30: no step leaves 32 bits), and in `total` over all.
+__device__ __forceinline__ int cut_sum(int x, int most, int waves, int (&lds)[PLAN_THREADS / WAVE], int& total) {
+  const int lane = threadIdx.x % WAVE, wave = threadIdx.x / WAVE;
+  for (int o = 1; o < WAVE; o *= 2) {
+    const int y = __shfl_up(x, o, WAVE);
+    if (lane >= o) x = min(x + y, most);
+  }
+  if (lane == WAVE - 1) lds[wave] = x;
+  __syncthreads();
+  int before = 0;
+  total = 0;
+  for (int i = 0; i < waves; ++i) {
+    if (i == wave) before = total;
+    total = min(total + lds[i], most);
+  }
+  return wave < waves ? min(before + x, most) : total;
+}
+
+// A workgroup's sums over all requests: keep(b, first row, rows, length, base,
+// whether it is served) for each, and in a.left (where `write`) what is left.
 template <class F>
-__device__ __forceinline__ void plan_slots(const SlotArgs& a, F&& keep) {
-  __shared__ int64_t lds[PLAN_THREADS / WAVE];
-  const int64_t page = a.by_page.d, have = min(max(a.have[0], (int64_t)0), (int64_t)a.entries), T = a.T;
-  int64_t rows = 0, wanted = 0, taken = 0, refused = 0, sum;
+__device__ __forceinline__ void plan_slots(const SlotArgs& a, bool write, F&& keep) {
+  __shared__ int lds[2][PLAN_THREADS / WAVE], taken, refused;
+  const int have = (int)min(max(a.have[0], (int64_t)0), (int64_t)a.entries), T = a.T, room = a.width * (int)a.by_page.d;
+  int rows = 0, wanted = 0;
+  if (threadIdx.x == 0) taken = refused = 0;
   for (int b0 = 0; b0 < a.B; b0 += PLAN_THREADS) {
-    const int b = b0 + threadIdx.x;
+    const int b = b0 + threadIdx.x, waves = min(PLAN_THREADS, a.B - b0 + WAVE - 1) / WAVE;
     const bool live = b < a.B;
     const int64_t len = live ? slot_len(a, b) : 0;
-    int64_t count = live ? min(max(a.counts[b], (int64_t)0), T) : 0;
-    const int64_t upto_row = rows + block_sum(count, lds, sum);
-    rows += sum;
-    const int64_t first = min(upto_row - count, T), end = min(upto_row, T);
+    int count = live ? (int)min(max(a.counts[b], (int64_t)0), (int64_t)T) : 0, sum;
+    if (b0) __syncthreads();
+    const int end = min(rows + cut_sum(count, T, waves, lds[0], sum), T);
+    // the sum before this request, which is not the difference where the sum was cut
+    int first = __shfl_up(end, 1, WAVE);
+    if (threadIdx.x % WAVE == 0) {
+      first = rows;
+      for (int i = 0; i < (int)threadIdx.x / WAVE; ++i) first = min(first + lds[0][i], T);
+    }
+    rows = min(rows + sum, T);
     count = end - first;
-    const bool fits = len <= a.width * page - count;
-    const int64_t need = live && fits ? pages_of(len + count, page) - pages_of(len, page) : 0;
-    const int64_t upto = wanted + block_sum(need, lds, sum);
-    wanted += sum;
+    const bool fits = len <= room - count;
+    const int need = live && fits ? pages_of(a, (int)len + count) - pages_of(a, (int)len) : 0;
+    const int upto = min(wanted + cut_sum(need, have + 1, waves, lds[1], sum), have + 1);
+    wanted = min(wanted + sum, have + 1);
     const bool good = fits && (need == 0 || upto <= have);
-    block_sum(good ? need : 0, lds, sum);
-    taken += sum;
-    block_sum(live && !good ? 1 : 0, lds, sum);
-    refused += sum;
-    if (live) {
-      a.offsets[b + 1] = end;
-      a.k_lens[b] = good ? len + count : len;
-      keep(b, first, len, !good ? -1 : need ? have - 1 - (upto - need) : 0);
+    if (live) keep(b, first, end, len, !good ? -1 : need ? have - 1 - (upto - need) : 0);
+    // what those that are served take is the largest sum that is not too much
+    if (write && live) {
+      if (good && need) atomicMax(&taken, upto);
+      if (!good) atomicAdd(&refused, 1);
     }
   }
   __syncthreads();  // `left` may be what all have read `have` from
-  if (threadIdx.x == 0) {
+  if (write && threadIdx.x == 0) {
     a.offsets[0] = 0;
     a.left[0] = have - taken;
     a.left[1] = refused;
   }
 }
+__device__ __forceinline__ void plan_write(const SlotArgs& a, int b, int first, int end, int64_t len, int base) {
+  a.offsets[b + 1] = end;
+  a.k_lens[b] = base >= 0 ? len + (end - first) : len;
+}
 
 // Row t, which is request b's (b < 0: none's)
-__device__ __forceinline__ void place_row(const SlotArgs& a, int t, int b, int64_t first, int64_t len, int64_t base) {
+__device__ __forceinline__ void place_row(const SlotArgs& a, int t, int b, int first, int64_t len, int base) {
   int64_t slot = -1, at = 0;
   if (b >= 0) {
     at = len + (t - first);
     if (base >= 0) {
       const int page = (int)a.by_page.d, n = (int)a.by_page.div((uint32_t)at), in = (int)at - n * page;
-      const int held = (int)a.by_page.div((uint32_t)(len + page - 1));
+      const int held = pages_of(a, (int)len);
       int32_t* entry = a.table + (int64_t)b * a.width + n;
       int32_t e;
       if (n < held) {
@@ -117,14 +126,24 @@ __device__ __forceinline__ void place_row(const SlotArgs& a, int t, int b, int64
   a.positions[t] = at;
 }
 
-// Both in one workgroup, for steps of few rows: all latency.
+// Steps of few requests: every workgroup sums them itself and places its rows,
+// 1024 or, of a launch of one, all.  All latency: the sums (two loads, two
+// barriers a sum), the table's or the free list's entry.  64 requests of one
+// token 4.0 us, 1024 requests with 32768 tokens 6.8 us (summed by one workgroup
+// and placed by others in a second launch 7.3 and 3.4).
 constexpr int ONE_GROUP = 1024;  // requests
 __global__ __launch_bounds__(PLAN_THREADS) void slots_one_kernel(SlotArgs a) {
-  __shared__ int64_t first[ONE_GROUP], len[ONE_GROUP], base[ONE_GROUP];
-  plan_slots(a, [&](int b, int64_t f, int64_t l, int64_t x) { first[b] = f, len[b] = l, base[b] = x; });
-  __syncthreads();
-  const int64_t rows = a.B > 0 ? a.offsets[a.B] : 0;  // written by this workgroup before the barrier
-  for (int t = threadIdx.x; t < a.T; t += PLAN_THREADS) {
+  __shared__ int first[ONE_GROUP], base[ONE_GROUP];
+  __shared__ int64_t len[ONE_GROUP];
+  __shared__ int rows;
+  if (threadIdx.x == 0) rows = 0;
+  const bool write = blockIdx.x == 0;
+  plan_slots(a, write, [&](int b, int f, int e, int64_t l, int x) {
+    first[b] = f, len[b] = l, base[b] = x;
+    if (b == a.B - 1) rows = e;
+    if (write) plan_write(a, b, f, e, l, x);
+  });
+  for (int t = blockIdx.x * PLAN_THREADS + threadIdx.x; t < a.T; t += gridDim.x * PLAN_THREADS) {
     int lo = 0, hi = a.B;  // the last request that begins at t or before it
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
@@ -136,8 +155,12 @@ __global__ __launch_bounds__(PLAN_THREADS) void slots_one_kernel(SlotArgs a) {
   }
 }
 
+// Many requests: one workgroup sums, the others place in a second launch.
 __global__ __launch_bounds__(PLAN_THREADS) void slots_plan_kernel(SlotArgs a) {
-  plan_slots(a, [&](int b, int64_t, int64_t, int64_t x) { a.base[b] = x; });
+  plan_slots(a, true, [&](int b, int f, int e, int64_t l, int x) {
+    a.base[b] = x;
+    plan_write(a, b, f, e, l, x);
+  });
 }
 // A row a thread; a wave finds its first and last rows' requests by 64 tries at
 // once, and each lane its own among those.
@@ -152,7 +175,7 @@ __global__ __launch_bounds__(256) void slots_fill_kernel(SlotArgs a) {
     if (a.offsets[mid] <= t) lo = mid;
     else hi = mid;
   }
-  if (a.B > 0 && t < a.offsets[a.B]) place_row(a, t, lo, a.offsets[lo], slot_len(a, lo), a.base[lo]);
+  if (a.B > 0 && t < a.offsets[a.B]) place_row(a, t, lo, (int)a.offsets[lo], slot_len(a, lo), a.base[lo]);
   else place_row(a, t, -1, 0, 0, 0);
 }
 

@@ -7,6 +7,7 @@
 namespace {
 
 constexpr int32_t MOST_BATCH = 1 << 24;
+constexpr int32_t MOST_PAGES = 1 << 28;         // of a pool, by its places
 constexpr int64_t MOST_ROW = INT64_C(1) << 27;  // bytes from a token's row to the next in a page
 
 lact_status check_page(int32_t page, int32_t pages, int32_t width) {
@@ -453,13 +454,13 @@ lact_status validate(const lact_slots* p) {
   if (!p) return fail(LACT_ERR_INVALID_ARG, "problem is NULL");
   if (p->batch < 0 || p->batch > MOST_BATCH) return fail(LACT_ERR_INVALID_ARG, "batch = %d", p->batch);
   TRY(check_page(p->page, 0, p->width));
-  if (p->entries < 0) return fail(LACT_ERR_INVALID_ARG, "entries = %d < 0", p->entries);
+  if (p->entries < 0 || p->entries >= MOST_PAGES) return fail(LACT_ERR_INVALID_ARG, "entries = %d", p->entries);
   if (p->tokens < 0 || p->tokens >= MOST_TOKENS) return fail(LACT_ERR_INVALID_ARG, "tokens = %lld", (long long)p->tokens);
   return LACT_OK;
 }
 
-// Steps that one workgroup places whole, which saves a launch
-bool slots_in_one(const lact_slots& p) { return p.batch <= ONE_GROUP && p.tokens <= 8192; }
+// Whether every workgroup sums the requests itself
+bool slots_in_one(const lact_slots& p) { return p.batch <= ONE_GROUP; }
 
 }  // namespace
 
@@ -468,7 +469,7 @@ extern "C" {
 size_t lact_page_slots_workspace_size(const lact_slots* p) {
   g_err.clear();
   if (validate(p)) return 0;
-  return slots_in_one(*p) ? 0 : align256((size_t)p->batch * 8);
+  return slots_in_one(*p) ? 0 : align256((size_t)p->batch * 4);
 }
 
 lact_status lact_page_slots(const lact_slots* p, const int64_t* lens, const int64_t* counts, int32_t* table,
@@ -494,19 +495,21 @@ lact_status lact_page_slots(const lact_slots* p, const int64_t* lens, const int6
   TRY(check_apart({offsets, k_lens, slots, positions, left, table}, {lens, counts, free}));
   TRY(check_apart({offsets, k_lens, slots, positions, table}, {have}));
   const bool one = slots_in_one(*p);
-  if (!one) TRY(check_ws(ws, ws_bytes, align256((size_t)p->batch * 8)));
+  if (!one) TRY(check_ws(ws, ws_bytes, align256((size_t)p->batch * 4)));
   TRY(check_device_again());
   SlotArgs a;
   memset(&a, 0, sizeof(a));
   a.lens = lens, a.counts = counts, a.table = table, a.free = free, a.have = have;
   a.offsets = offsets, a.k_lens = k_lens, a.slots = slots, a.positions = positions, a.left = left;
-  a.base = static_cast<int64_t*>(ws);
+  a.base = static_cast<int32_t*>(ws);
   a.B = p->batch, a.T = (int32_t)p->tokens, a.width = p->width, a.entries = p->entries;
   a.by_page = FastDiv((uint32_t)p->page);
   const hipStream_t s = static_cast<hipStream_t>(stream);
   if (one) {
     KernelTimer kt(LACT_K_PAGES, s);
-    LACT_LAUNCH(slots_one_kernel, dim3(1), dim3(PLAN_THREADS), s, a);
+    // `left` in place of `have` is written by the only workgroup that reads it
+    const unsigned grid = left == have ? 1 : (unsigned)std::max<int64_t>(1, ceil_div(p->tokens, PLAN_THREADS));
+    LACT_LAUNCH(slots_one_kernel, dim3(grid), dim3(PLAN_THREADS), s, a);
   } else {
     {
       KernelTimer kt(LACT_K_PAGES, s);

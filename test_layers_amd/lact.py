@@ -1241,6 +1241,8 @@ def _slots_plan(lens, counts, table, free, have, page, tokens, given):
     plan = _Plan()
     plan.device = _one_device(lens, counts, table, free, have, *given.values())
     plan.shapes = {"offsets": (b + 1,), "k_lens": (b,), "slots": (tokens,), "positions": (tokens,), "left": (2,)}
+    plan.sizes = [s[0] for s in plan.shapes.values()]
+    plan.numbers = sum(plan.sizes)
     _check_shapes(counts=(counts, (b,)), **{n: (t, plan.shapes[n]) for n, t in given.items()})
     if table.dim() != 2 or table.shape[0] != b:
         raise ValueError(f"table has shape {tuple(table.shape)}, expected {(b, 'width')}")
@@ -1278,8 +1280,8 @@ def page_slots(lens, counts, table, free, free_count, *, page: int, tokens: int,
                  lambda: _slots_plan(lens, counts, table, free, free_count, page, tokens, given))
 
     def run(handle, out=out):
-        if out is None:
-            out = {n: lens.new_empty(s) for n, s in plan.shapes.items()}
+        if out is None:   # views of one allocation: five would be half of the call's time
+            out = dict(zip(plan.shapes, lens.new_empty(plan.numbers).split_with_sizes(plan.sizes)))
         ws, ws_bytes, _held = _scratch(plan.need, workspace, lens.device)
         check(lib().lact_page_slots(plan.p, lens.data_ptr(), counts.data_ptr(), table.data_ptr(), free.data_ptr(),
                                     free_count.data_ptr(), out["offsets"].data_ptr(), out["k_lens"].data_ptr(),
