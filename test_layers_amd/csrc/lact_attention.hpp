@@ -74,6 +74,7 @@ struct PackedArgs : AttnArgs {   // Lq: tokens of all sequences, the strides' b 
   int32_t slots;           // tiles of all sequences together, see find_tile; 0: `tiles` for each
   int32_t main;            // workgroups that compute; those behind them clear rows of no sequence
   int32_t rest;            // how many those are
+  int32_t rs;              // dk, dv: parts that the rows of a tile are split in
 };
 struct PagedArgs : PackedArgs {  // Lk: keys of a sequence that are looked at
   static constexpr Lie LIE = Lie::PAGED;
@@ -88,6 +89,10 @@ struct PagedArgs : PackedArgs {  // Lk: keys of a sequence that are looked at
   int32_t* upto;           // [B + 1]: work of the sequences before each, null: summed by every workgroup
   struct StreamJoin* joins;  // [waves]
 };
+
+// An LDS location's byte offset: the low half of its generic address (a cast to
+// the LDS address space would test for null every time).
+__device__ __forceinline__ uint32_t lds_at(const void* p) { return (uint32_t)(uintptr_t)p; }
 
 // ------------------------------------------------------------------ tiles
 // One LDS tile holds R rows of DP elements (DP = d rounded up to 64 or 128)
@@ -115,7 +120,7 @@ struct AttnTile {
                                                int cmax, int wave, int lane) {
     constexpr int N = R * CPR / (WAVE * NW);
     static_assert(R * CPR % (WAVE * NW) == 0, "whole copies");
-    const uint32_t m0 = __builtin_amdgcn_readfirstlane(lds_off(tile) + (uint32_t)(wave * WAVE * 16));
+    const uint32_t m0 = __builtin_amdgcn_readfirstlane(lds_at(tile) + (uint32_t)(wave * WAVE * 16));
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int s = (i * NW + wave) * WAVE + lane;
@@ -161,7 +166,7 @@ struct Stager {
   __device__ __forceinline__ void issue(char* tile, int row0) const {
     if (row0 >= 0 && row0 + R - 1 <= rmax && stride < FAR) {
       const char* b = base + (int64_t)row0 * stride;
-      const uint32_t m0 = __builtin_amdgcn_readfirstlane(lds_off(tile) + (uint32_t)(wave * WAVE * 16));
+      const uint32_t m0 = __builtin_amdgcn_readfirstlane(lds_at(tile) + (uint32_t)(wave * WAVE * 16));
 #pragma unroll
       for (int i = 0; i < N; ++i) dma16_at(off[i], b, m0 + (uint32_t)(i * NW * WAVE * 16));
     } else {
@@ -225,7 +230,7 @@ struct PageRows {
     }
   }
   __device__ __forceinline__ void issue(char* tile, int row0) const {
-    const uint32_t m0 = __builtin_amdgcn_readfirstlane(lds_off(tile) + (uint32_t)(wave * WAVE * 16));
+    const uint32_t m0 = __builtin_amdgcn_readfirstlane(lds_at(tile) + (uint32_t)(wave * WAVE * 16));
     if (row0 + R - 1 <= rmax) {
       int page[N], in[N];
 #pragma unroll
@@ -366,14 +371,30 @@ __device__ __forceinline__ void mma_trans(f32x16 (&acc)[DP / 32], const bf16x8 (
 #pragma unroll
     for (int db = 0; db < DP / 32; ++db) acc[db] = mma32(trans_frag<DP>(tile, row0, kb, db, lane), b[kb], acc[db]);
 }
+// (fp32, see row_steps: blocks of d behind its last are left out)
 template <int DP>
 __device__ __forceinline__ void mma_trans(f32x16 (&acc)[DP / 32], const f32x16& p, const char* tile, int row0,
-                                          int lane) {
+                                          int lane, int d) {
 #pragma unroll
-  for (int r = 0; r < 16; ++r)
+  for (int db = 0; db < DP / 32; ++db)
+    if (DP <= 64 || 32 * db < d) {
 #pragma unroll
-    for (int db = 0; db < DP / 32; ++db)
-      acc[db] = __builtin_amdgcn_mfma_f32_32x32x2f32(trans_elem<DP>(tile, row0, r, db, lane), p[r], acc[db], 0, 0, 0);
+      for (int r = 0; r < 16; ++r)
+        acc[db] = __builtin_amdgcn_mfma_f32_32x32x2f32(trans_elem<DP>(tile, row0, r, db, lane), p[r], acc[db], 0, 0, 0);
+    }
+}
+// The steps of a row product, fn(s): fp32 tiles of 128 leave out 32-wide blocks
+// behind d (5 texts of up to 1777 tokens, 12 (4) heads of 96: forward 171 -> 141
+// us, backward 751 -> 596; at d <= 64 the branch cost 4 % and d <= 32 is rare)
+template <typename T, int STEPS, class F>
+__device__ __forceinline__ void row_steps(int d, F&& fn) {
+  constexpr int N = sizeof(T) == 2 || STEPS <= 8 ? STEPS : 4;
+#pragma unroll
+  for (int g = 0; g < STEPS; g += N)
+    if (N == STEPS || 8 * g < d) {
+#pragma unroll
+      for (int s = g; s < g + N; ++s) fn(s);
+    }
 }
 
 // p as the operand of mma_trans: rounded to bf16 (registers 8 i .. 8 i + 7 are
@@ -413,9 +434,10 @@ struct Half {
 };
 
 template <typename T, int DP>
-__device__ __forceinline__ void acc_trans(f32x16 (&acc)[DP / 32], const f32x16& p, const char* tile, int row0, int lane) {
+__device__ __forceinline__ void acc_trans(f32x16 (&acc)[DP / 32], const f32x16& p, const char* tile, int row0, int lane,
+                                          int d) {
   if constexpr (sizeof(T) == 2) mma_trans<DP>(acc, round_pair(p).f, tile, row0, lane);
-  else mma_trans<DP>(acc, p, tile, row0, lane);
+  else mma_trans<DP>(acc, p, tile, row0, lane, d);
 }
 
 // maximum and sum of a lane and its partner 32 away
@@ -485,22 +507,34 @@ __device__ __forceinline__ int find_last(int n, int lane, F&& upto) {
   return lo - 1;
 }
 
-// The sequence (b < 0: none) and its tile of BM rows that workgroup `id` of a
+// The sequence (none: b < 0) and its tile of BM rows that workgroup `id` of a
 // packed batch takes.  The host does not know the lengths: it numbers slots,
 // of which sequence b has those from offsets[b] / BM + b on.  Rounded down,
 // these leave room for its tiles and at most one more, and T / BM + B are
-// enough for all.  Where rows have unequal work the long ones go first.
+// enough for all.  Where rows have unequal work the long ones go first.  Of up
+// to 63 sequences a wave holds all offsets: one trip to memory.
 template <class A>
-__device__ __forceinline__ void find_tile(const A& a, int id, int BM, int lane, bool long_last, int& b, int& tile) {
+__device__ __forceinline__ AttnSeq find_tile(const A& a, int id, int BM, int lane, bool long_last, int& tile) {
   if (a.slots == 0) {
     tile = long_last ? id / a.B : a.tiles - 1 - id / a.B;
-    b = id % a.B;
-    return;
+    return AttnSeq(a, id % a.B);
   }
   const int s = long_last ? id : a.slots - 1 - id;
+  if (a.B < WAVE) {
+    const int at = seq_len(a.offsets, min(lane, a.B), a.Lq);
+    const int b = (int)__popcll(__ballot(lane < a.B && at / BM + lane <= s)) - 1;
+    if (b < 0) return AttnSeq(b, 0, 0, 0);
+    const int first = __builtin_amdgcn_readlane(at, b), rows = __builtin_amdgcn_readlane(at, b + 1) - first;
+    tile = s - (first / BM + b);
+    const int qlen = min(max(rows, 0), a.most);
+    if constexpr (A::LIE == Lie::PACKED) return AttnSeq(b, qlen, qlen, first);
+    else return AttnSeq(b, qlen, __builtin_amdgcn_readfirstlane(seq_len(a.k_lens, b, a.Lk)), first);
+  }
   auto slot = [&](int i) { return seq_len(a.offsets, i, a.Lq) / BM + i; };
-  b = __builtin_amdgcn_readfirstlane(find_last(a.B, lane, [&](int i) { return slot(i) <= s; }));
-  tile = b < 0 ? 0 : __builtin_amdgcn_readfirstlane(s - slot(b));
+  const int b = __builtin_amdgcn_readfirstlane(find_last(a.B, lane, [&](int i) { return slot(i) <= s; }));
+  if (b < 0) return AttnSeq(b, 0, 0, 0);
+  tile = __builtin_amdgcn_readfirstlane(s - slot(b));
+  return AttnSeq(a, b);
 }
 
 // Clears rows of no sequence, those before the first and behind the last: part
@@ -693,10 +727,9 @@ struct AttnRows {
   }
 
   // scores of the 32 keys from row `at` of a tile
-  __device__ __forceinline__ f32x16 scores(const char* kt, int at, int lane) const {
+  __device__ __forceinline__ f32x16 scores(const char* kt, int at, int lane, int d) const {
     f32x16 s = zero16();
-#pragma unroll
-    for (int t = 0; t < STEPS; ++t) s = mma32(row_frag<T, DP>(kt, at, t, lane), q[t], s);
+    row_steps<T, STEPS>(d, [&](int t) { s = mma32(row_frag<T, DP>(kt, at, t, lane), q[t], s); });
     return s;
   }
   __device__ __forceinline__ void mask(f32x16& s, int k0, int window, int sinks, int lane) const {
@@ -739,12 +772,12 @@ struct AttnRows {
   }
   // 32 keys, in LDS tiles of as many rows
   __device__ __forceinline__ void step(const char* kt, const char* vt, int k0, int window, int sinks, float c,
-                                       int lane) {
-    f32x16 s = scores(kt, 0, lane);
+                                       int lane, int d) {
+    f32x16 s = scores(kt, 0, lane, d);
     if (!w.whole(k0, k0 + 31, window, sinks)) mask(s, k0, window, sinks, lane);
     follow(s, c, nullptr);
     exps(s, c);
-    acc_trans<T, DP>(o, s, vt, 0, lane);
+    acc_trans<T, DP>(o, s, vt, 0, lane, d);
   }
   // 64 keys that every row sees.  Four runs of products: the scores of one
   // half and of the other, then each half's sums.  The exponentials of a half
@@ -812,11 +845,11 @@ struct AttnRows {
   // BN keys of which a row may see some or none; of KS waves' parts, part ks
   template <int BN, int KS>
   __device__ __forceinline__ void tile(const char* kt, const char* vt, int ks, int k0, int window, int sinks, float c,
-                                       int lane) {
+                                       int lane, int d) {
 #pragma unroll 1
     for (int i = 32 * ks; i < BN; i += 32 * KS)
       if (w.some(k0 + i, k0 + i + 31, window, sinks))
-        step(kt + i * AttnTile<T, DP>::CPR * 16, vt + i * AttnTile<T, DP>::CPR * 16, k0 + i, window, sinks, c, lane);
+        step(kt + i * AttnTile<T, DP>::CPR * 16, vt + i * AttnTile<T, DP>::CPR * 16, k0 + i, window, sinks, c, lane, d);
   }
 };
 
@@ -863,19 +896,20 @@ constexpr int attn_bn() { return DP * (int)sizeof(T) > 256 ? 32 : 64; }
 // splits in use: 2.1 ms innermost, 1.0 when all splits are).
 struct AttnPlace {
   int b, hk, h, tile, split = 0;
-  __device__ AttnPlace(int id, int BM, int lane, const PackedArgs& a, int splits = 1) {
+  // of a packed batch: without the sequence (find_tile), whose number is left in b
+  __device__ AttnPlace(int id, const PackedArgs& a) {
     const int groups = a.G / a.hg;
-    if (splits > 1) {
-      const int one = a.main / splits;
+    if (a.splits > 1) {
+      const int one = a.main / a.splits;
       split = id / one;
       id -= split * one;
     }
     hk = id % a.Hk;
     id /= a.Hk;
     h = hk * a.G + id % groups * a.hg;
-    find_tile(a, id / groups, BM, lane, false, b, tile);
+    b = id / groups, tile = 0;
   }
-  __device__ AttnPlace(int id, int, int lane, const AttnArgs& a, int = 1) {
+  __device__ AttnPlace(int id, const AttnArgs& a) {
     id = xcd_remap(id, gridDim.x);
     const int groups = a.G / a.hg;
     h = id % groups * a.hg;
@@ -887,6 +921,12 @@ struct AttnPlace {
     h += hk * a.G;
   }
 };
+
+template <class A>
+__device__ __forceinline__ AttnSeq place_seq(const A& a, int BM, int lane, AttnPlace& at) {
+  if constexpr (A::LIE == Lie::PADDED) return AttnSeq(a, at.b);
+  else return find_tile(a, at.b, BM, lane, false, at.tile);
+}
 
 // Four waves x 32 rows; K and V tiles in a two-deep ring of direct loads: a
 // tile's 32 KB serve 128 rows, and Q and O never leave the registers.
@@ -914,9 +954,9 @@ __global__ __launch_bounds__(256, (attn_waves<T, DP>())) void attn_fwd_kernel(A 
       return clear_rest(a, a.out, a.so, a.H, a.d * (int)sizeof(T), a.lse, (int)blockIdx.x - a.main, a.rest);
   const int rg = wave % RG, ks = wave / RG;  // head and rows of the wave; its part of a tile
   const int BM = 32 * RG / a.hg;             // rows of the workgroup
-  AttnPlace at(blockIdx.x, BM, lane, a, a.splits);
-  if (A::LIE != Lie::PADDED && at.b < 0) return;
-  const AttnSeq seq(a, at.b);
+  AttnPlace at(blockIdx.x, a);
+  const AttnSeq seq = place_seq(a, BM, lane, at);
+  if (A::LIE != Lie::PADDED && seq.b < 0) return;
   const int qlen = seq.qlen, klen = seq.klen;
   if constexpr (PAGED)
     if (qlen <= a.few) return;
@@ -932,7 +972,7 @@ __global__ __launch_bounds__(256, (attn_waves<T, DP>())) void attn_fwd_kernel(A 
   w.w = {off + rw, off + min(rw + 31, qlen - 1)};
   const KeyTiles kt(off + r0, off + min(r0 + BM, qlen) - 1, a.window, a.sinks, BN);
   const auto keys = [&] {
-    if constexpr (PAGED) return PageRows<T, DP, BN, NW>(a, at.b, at.hk, klen - 1, wave, lane);
+    if constexpr (PAGED) return PageRows<T, DP, BN, NW>(a, seq.b, at.hk, klen - 1, wave, lane);
     else return KeyRows<T, DP, BN, NW>(a.k + seq.at(a, a.sk) + at.hk * a.sk.h, a.sk.l, a.v + seq.at(a, a.sv) + at.hk * a.sv.h,
                                        a.sv.l, klen - 1, cmax, wave, lane);
   }();
@@ -955,7 +995,7 @@ __global__ __launch_bounds__(256, (attn_waves<T, DP>())) void attn_fwd_kernel(A 
   auto edge = [&](int i) {
     char* t = lds + (i & 1) * 2 * TB;
     arrive(i, lds + (2 - 2 * (i & 1)) * TB);
-    if (w.w.lo <= w.w.hi) w.template tile<BN, KS>(t, t + TB, ks, kt.at(i) * BN, a.window, a.sinks, a.c, lane);
+    if (w.w.lo <= w.w.hi) w.template tile<BN, KS>(t, t + TB, ks, kt.at(i) * BN, a.window, a.sinks, a.c, lane, a.d);
   };
   if (i0 < i1) keys.issue(lds, kt.at(i0) * BN);
   // Tiles that all rows of the workgroup see whole run in a loop of their own,
@@ -1095,7 +1135,7 @@ __global__ __launch_bounds__(64 * (few_waves<T, DP>())) void attn_few_kernel(Att
     }
     asm volatile("" ::: "memory");
     const char* t = ring + buf * 2 * TB;
-    w.template tile<32, 1>(t, t + TB, 0, kt.at(i) * 32, a.window, a.sinks, a.c, lane);
+    w.template tile<32, 1>(t, t + TB, 0, kt.at(i) * 32, a.window, a.sinks, a.c, lane, a.d);
   }
   // join the waves: O as [d][row] and the statistics behind it
   wait_lgkm0();
@@ -1372,7 +1412,7 @@ __global__ __launch_bounds__(64 * (few_waves<T, DP>())) void stream_kernel(Paged
       }
       asm volatile("" ::: "memory");
       const char* x = ring + buf * 2 * TB;
-      w.template tile<32, 1>(x, x + TB, 0, kt.at(i) * 32, a.window, a.sinks, a.c, lane);
+      w.template tile<32, 1>(x, x + TB, 0, kt.at(i) * 32, a.window, a.sinks, a.c, lane, a.d);
     }
     const bool whole = u0 == 0 && u1 == it.units;
     const float l = pair_sum(w.l), inv = l > 0.f || l != l ? 1.f / l : 0.f;
@@ -1487,9 +1527,9 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dq_kerne
       return clear_rest(a, a.dq, a.sdq, a.H, a.d * (int)sizeof(T), nullptr, (int)blockIdx.x - a.main, a.rest);
   const int rg = wave % RG, ks = wave / RG;  // head and rows of the wave; its part of a tile
   const int BM = 32 * RG / a.hg;             // rows of the workgroup
-  AttnPlace at(blockIdx.x, BM, lane, a);
-  if (A::LIE != Lie::PADDED && at.b < 0) return;
-  const AttnSeq seq(a, at.b);
+  AttnPlace at(blockIdx.x, a);
+  const AttnSeq seq = place_seq(a, BM, lane, at);
+  if (A::LIE != Lie::PADDED && seq.b < 0) return;
   const int qlen = seq.qlen, klen = seq.klen;
   at.h += rg % a.hg;
   const int r0 = at.tile * BM, rw = r0 + 32 * (rg / a.hg), off = klen - qlen, n = lane & 31;
@@ -1679,11 +1719,10 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dq_kerne
           const int k0 = kt.at(i) * BN + sb;
           if (w.lo > w.hi || !w.some(k0, k0 + 31, a.window, a.sinks)) continue;
           f32x16 s = zero16(), ds = less;
-#pragma unroll
-          for (int st = 0; st < STEPS; ++st) {
+          row_steps<T, STEPS>(a.d, [&](int st) {
             s = mma32(row_frag<T, DP>(t, sb, st, lane), q[st], s);
             ds = mma32(row_frag<T, DP>(t + TB, sb, st, lane), g[st], ds);
-          }
+          });
           gradients(s, ds);
           if (!w.whole(k0, k0 + 31, a.window, a.sinks)) {
             const Seen seen(p, k0 + 4 * (lane >> 5), a.window, a.sinks);
@@ -1700,7 +1739,7 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dq_kerne
             mma_trans<DP>(dq, x.f, t, sb, lane);
             mma_trans<DP>(kbar, round_pair(s).f, t, sb, lane);
           } else {
-            mma_trans<DP>(dq, ds, t, sb, lane);
+            mma_trans<DP>(dq, ds, t, sb, lane, a.d);
           }
         }
       };
@@ -1769,14 +1808,30 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dq_kerne
 // window's; the rows behind the window of a sink tile's last key are split
 // over further workgroups of `span` rows each, and the fp32 partial sums of a
 // sink tile are added in a fixed order by attn_sink_sum_kernel.
+//
+// Packed: the rows that a tile meets, over all its query heads, may be split in
+// `rs` equal parts, where tiles are few; attn_row_sum_kernel adds them.
+//
+// The number of a part, of [dk, dv][key][d] each: of a sink tile's splits, and
+// behind those of the other tiles by slot.
+__device__ __forceinline__ int64_t dkv_part(const PackedArgs& a, int b, int hk, int tile, int split) {
+  return ((((int64_t)b * a.Hk + hk) * a.sink_tiles + tile) * a.splits + split) * a.rs;
+}
+__device__ __forceinline__ int64_t dkv_part(const PackedArgs& a, int slot, int hk) {
+  const int64_t sinks = a.splits > 1 ? (int64_t)a.B * a.Hk * a.sink_tiles * a.splits : 0;
+  return (sinks + (int64_t)slot * a.Hk + hk) * a.rs;
+}
+
 template <typename T, int DP, int KS, class A = AttnArgs>
 __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dkv_kernel(A a) {
+  constexpr bool PACKED = A::LIE != Lie::PADDED;
   using Tile = AttnTile<T, DP>;
   constexpr int NW = 4, RG = NW / KS, BK = 32 * RG, BQ = attn_bn<T, DP>(), TB = BQ * Tile::CPR * 16, STEPS = Tile::STEPS, DB = DP / 32;
   __shared__ __align__(1024) char lds[4 * TB];
   __shared__ __align__(1024) float stats[2][2][64];  // [ring][-lse / scale, -D][row]
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 31;
-  int tile, split = 0, hk, b;
+  int tile = 0, split = 0, hk, b, rpart = 0, slot = 0;
+  AttnSeq seq(0, 0, 0, 0);
   if constexpr (A::LIE == Lie::PADDED) {
     int id = xcd_remap(blockIdx.x, gridDim.x);
     const int jobs = a.tiles + a.sink_tiles * (a.splits - 1);
@@ -1788,6 +1843,7 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dkv_kern
     } else {
       tile = job - a.sink_tiles * (a.splits - 1);
     }
+    seq = AttnSeq(a, b);
   } else {
     // split sink tiles of all sequences, then the tiles by slots, early keys first: most rows see them
     int id = blockIdx.x;
@@ -1796,17 +1852,20 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dkv_kern
       return clear_rest(a, a.dv, a.sdv, a.Hk, a.d * (int)sizeof(T), nullptr, id - a.main, a.rest);
     }
     hk = id % a.Hk, id /= a.Hk;
+    if (a.rs > 1) rpart = id % a.rs, id /= a.rs;
     const int jobs = a.splits > 1 ? a.B * a.sink_tiles * a.splits : 0;
+    slot = id - jobs;
     if (id < jobs) {
       split = id % a.splits, id /= a.splits;
       tile = id % a.sink_tiles, b = id / a.sink_tiles;
+      seq = AttnSeq(a, b);
     } else {
-      find_tile(a, id - jobs, BK, lane, true, b, tile);
+      seq = find_tile(a, slot, BK, lane, true, tile);
+      b = seq.b;
       if (b < 0 || (a.splits > 1 && tile < a.sink_tiles)) return;
     }
   }
   const int bk = b * a.Hk + hk;
-  const AttnSeq seq(a, b);
   const int qlen = seq.qlen, klen = seq.klen, off = klen - qlen;
   if (A::LIE != Lie::PADDED && tile * BK >= klen) return;
   const int k0 = tile * BK, cmax = a.d * (int)sizeof(T) / 16 - 1;
@@ -1833,8 +1892,23 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dkv_kern
     p_hi = reach;
   }
   const int ra = max(0, p_lo - off) / BQ, rz = p_hi - off;  // first row tile, last row
-  if (k0 < klen && rz >= ra * BQ && p_hi >= p_lo) {
-    const int rend = rz / BQ + 1;  // behind the last row tile
+  // of each head's row tiles ra .. rend - 1, those from tile r0 of head h0 to tile r1 - 1 of head h1
+  // (PADDED: all, in expressions that leave nothing of the choice in the code: a
+  // comparison with head 0 peeled its round off the loop and spilled 100 registers)
+  int h0 = 0, h1 = a.G - 1, r0 = ra, rend = rz / BQ + 1, r1 = rend;
+  auto from = [&](int h) { return PACKED && h == h0 ? r0 : ra; };
+  auto to = [&](int h) { return PACKED && h == h1 ? r1 : rend; };
+  if constexpr (PACKED)
+    if (a.rs > 1) {
+      const int64_t n = max(0, rend - ra), all = n * a.G, s0 = all * rpart / a.rs, s1 = all * (rpart + 1) / a.rs;
+      if (s1 > s0) {
+        h0 = __builtin_amdgcn_readfirstlane((int)(s0 / n)), h1 = __builtin_amdgcn_readfirstlane((int)((s1 - 1) / n));
+        r0 = ra + (int)(s0 - h0 * n), r1 = ra + (int)(s1 - h1 * n);
+      } else {
+        rend = ra;
+      }
+    }
+  if (k0 < klen && rz >= ra * BQ && p_hi >= p_lo && (!PACKED || rend > ra)) {
     Frag<T> kf[STEPS], vf[STEPS];
     const int64_t kc = min(key, klen - 1);
     load_rows(kf, kh + kc * a.sk.l, cmax, lane);
@@ -1848,14 +1922,14 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dkv_kern
       sg.issue(t + TB, rt * BQ);
       if (wave < 2)
         dma4(a.stats + wave * sn + sh + (int64_t)h * a.Lq + min(rt * BQ + lane, qlen - 1),
-             __builtin_amdgcn_readfirstlane(lds_off(st) + (uint32_t)wave * 256u));
+             __builtin_amdgcn_readfirstlane(lds_at(st) + (uint32_t)wave * 256u));
     };
     auto arrive = [&](int h, int rt, char* other, float* st) {
       wait_lgkm0();
       wait_vm<0>();
       bar();
-      if (rt + 1 < rend) issue(h, rt + 1, other, st);
-      else if (h + 1 < a.G) issue(h + 1, ra, other, st);
+      if (rt + 1 < to(h)) issue(h, rt + 1, other, st);
+      else if (h + 1 < (PACKED ? h1 + 1 : a.G)) issue(h + 1, ra, other, st);
     };
     // -lse / scale or -D of 32 rows, as a product leaves them
     auto start = [&](const float* st, int row0) {
@@ -1868,16 +1942,17 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dkv_kern
       }
       return x;
     };
-    issue(0, ra, lds, stats[0][0]);
+    issue(h0, r0, lds, stats[0][0]);
     int i = 0;  // tiles done: the ring's place
 #pragma unroll 1
-    for (int h = 0; h < a.G; ++h) {
-      int rt = ra;
+    for (int h = h0; h < (PACKED ? h1 + 1 : a.G); ++h) {
+      int rt = from(h);
+      const int re = to(h);
       if constexpr (sizeof(T) == 2 && BQ == 64 && KS == 1) {
         // row tiles that see all keys of the workgroup
         const int last = k0 + BK - 1 < a.sinks ? p_hi : min(p_hi, k0 + a.window - 1);
         const int wa = max(ra, (max(max(k0 + BK - 1, p_lo) - off, 0) + BQ - 1) / BQ);
-        const int wz = k0 + BK <= klen && last >= off ? min(rend, (last - off + 1) / BQ) : 0;
+        const int wz = k0 + BK <= klen && last >= off ? min(re, (last - off + 1) / BQ) : 0;
         const AttnAddr<DP> addr(lane);
         // 64 rows that see every key (see AttnRows::step2)
         auto pair = [&](lds_ptr qp, lds_ptr gp, const float* st, auto masked, int lo, int hi) {
@@ -1957,7 +2032,7 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dkv_kern
           pair(t, t + TB, stats[ring][0], std::true_type{}, lo, hi);
         };
 #pragma unroll 1
-        for (; rt < rend && (rt < wa || (rt < wz && (i & 1))); ++rt, ++i) edge(h, rt, i & 1);
+        for (; rt < re && (rt < wa || (rt < wz && (i & 1))); ++rt, ++i) edge(h, rt, i & 1);
         for (; rt + 1 < wz; rt += 2, i += 2) {
           arrive(h, rt, lds + 2 * TB, stats[1][0]);
           pair((lds_ptr)lds, (lds_ptr)lds + TB, stats[0][0], std::false_type{}, 0, 0);
@@ -1965,7 +2040,7 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dkv_kern
           pair((lds_ptr)lds + 2 * TB, (lds_ptr)lds + 3 * TB, stats[1][0], std::false_type{}, 0, 0);
         }
 #pragma unroll 1
-        for (; rt < rend; ++rt, ++i) edge(h, rt, i & 1);
+        for (; rt < re; ++rt, ++i) edge(h, rt, i & 1);
       } else if constexpr (sizeof(T) == 2) {
         // the wave's 32 rows of a tile in four runs of products, S, dP, dv and
         // dk, with P formed between those of dP and dS between those of dv (5
@@ -2035,7 +2110,7 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dkv_kern
           }
         };
 #pragma unroll 1
-        for (; rt < rend; ++rt, ++i) edge(h, rt, i & 1);
+        for (; rt < re; ++rt, ++i) edge(h, rt, i & 1);
       } else {
         // a tile of which rows may see a part, 32 rows after another
         auto edge = [&](int h, int rt, int ring) {
@@ -2050,11 +2125,10 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dkv_kern
                                (wk0 > q1 - a.window || wk1 < a.sinks);
             const f32x16 less_s = start(stats[ring][0], sb), less_ds = start(stats[ring][1], sb);
             f32x16 s = zero16(), ds = zero16();
-#pragma unroll
-            for (int st = 0; st < STEPS; ++st) {
+            row_steps<T, STEPS>(a.d, [&](int st) {
               s = mma32(row_frag<T, DP>(t, sb, st, lane), kf[st], s);
               ds = mma32(row_frag<T, DP>(t + TB, sb, st, lane), vf[st], ds);
-            }
+            });
 #pragma unroll
             for (int r = 0; r < 16; ++r) {  // fp32: the statistics are added last, see the dq kernel
               s[r] = __builtin_amdgcn_exp2f(LOG2E * fmaf(s[r], a.scale, less_s[r]));
@@ -2072,12 +2146,12 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dkv_kern
                 ds[r] = see ? ds[r] : 0.f;
               }
             }
-            acc_trans<T, DP>(dv, s, t + TB, sb, lane);
-            acc_trans<T, DP>(dk, ds, t, sb, lane);
+            acc_trans<T, DP>(dv, s, t + TB, sb, lane, a.d);
+            acc_trans<T, DP>(dk, ds, t, sb, lane, a.d);
           }
         };
 #pragma unroll 1
-        for (; rt < rend; ++rt, ++i) edge(h, rt, i & 1);
+        for (; rt < re; ++rt, ++i) edge(h, rt, i & 1);
       }
     }
   }
@@ -2090,9 +2164,16 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dkv_kern
 #pragma unroll
     for (int db = 0; db < DB; ++db) dk[db] = dv[db] = zero16();
   }
-  const bool parts = tile < a.sink_tiles && a.splits > 1;
+  const bool sink = tile < a.sink_tiles && a.splits > 1;
+  bool parts = sink;
   // [batch x key head][sink tile][split][dk, dv][key][d]
-  float* pk = a.part + (((int64_t)bk * a.sink_tiles + tile) * a.splits + split) * 2 * BK * a.d;
+  int64_t place = ((int64_t)bk * a.sink_tiles + tile) * a.splits + split;
+  if constexpr (PACKED)
+    if (a.rs > 1) {
+      parts = true;
+      place = (sink ? dkv_part(a, b, hk, tile, split) : dkv_part(a, slot, hk)) + rpart;
+    }
+  float* pk = a.part + place * 2 * BK * a.d;
   char* ok = a.dk + seq.at(a, a.sdk) + hk * a.sdk.h;
   char* ov = a.dv + seq.at(a, a.sdv) + hk * a.sdv.h;
   if (parts) {
@@ -2108,9 +2189,9 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dkv_kern
     const Lane2<T> k(kh + j * a.sk.l, a.d, lane), v(vh + j * a.sv.l, a.d, lane);
     float x[2] = {0.f, 0.f}, y[2] = {0.f, 0.f};
 #pragma unroll 1
-    for (int h = 0; h < a.G; ++h)
+    for (int h = h0; h < (PACKED ? h1 + 1 : a.G); ++h)
 #pragma unroll 1
-      for (int p = max(max(p_lo, j), off); p <= p_hi; ++p) {
+      for (int p = max(max(p_lo, j), off + (PACKED ? from(h) * BQ : 0)); p <= (PACKED ? min(p_hi, off + to(h) * BQ - 1) : p_hi); ++p) {
         if (j <= p - a.window && j >= a.sinks) break;
         const int64_t r = p - off, st = sh + (int64_t)h * a.Lq + r;
         const Lane2<T> q(qh + h * a.sq.h + r * a.sq.l, a.d, lane), g(gh + h * a.sdo.h + r * a.sdo.l, a.d, lane);
@@ -2139,21 +2220,66 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dkv_kern
   }
 }
 
-// dk, dv of the sink tiles, BK keys each: the splits' partial sums, in order
-template <typename T, int BK, class A = AttnArgs>
-__global__ __launch_bounds__(128) void attn_sink_sum_kernel(A a) {
-  const int keys = a.sink_tiles * BK;
-  const int x = blockIdx.x % (2 * keys), bk = blockIdx.x / (2 * keys), what = x / keys, key = x % keys;
-  const int hk = bk % a.Hk, b = bk / a.Hk, c = threadIdx.x;
-  const AttnSeq seq(a, b);
-  if (key >= (A::LIE == Lie::PADDED ? a.Lk : seq.klen) || c >= a.d) return;
-  const float* pr = a.part + ((((int64_t)bk * a.sink_tiles + key / BK) * a.splits * 2 + what) * BK + key % BK) * a.d + c;
-  float sum = 0.f;
-  for (int s = 0; s < a.splits; ++s) sum += pr[(int64_t)s * 2 * BK * a.d];
-  if (key >= seq.klen) sum = 0.f;
+// Four columns of a key's dk or dv: `n` parts, `step` floats apart, in order
+__device__ __forceinline__ void sum_parts(float (&sum)[4], const float* pr, int64_t step, int n) {
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const float4 v = *reinterpret_cast<const float4*>(pr + i * step);
+    sum[0] += v.x, sum[1] += v.y, sum[2] += v.z, sum[3] += v.w;
+  }
+}
+template <typename T, class A>
+__device__ __forceinline__ void store_key(const A& a, const AttnSeq& seq, int hk, int key, int what, int c, float (&sum)[4]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) sum[e] = key >= seq.klen ? 0.f : what ? sum[e] : sum[e] * a.scale;
   char* to = what ? a.dv + seq.at(a, a.sdv) + hk * a.sdv.h + (int64_t)key * a.sdv.l
                   : a.dk + seq.at(a, a.sdk) + hk * a.sdk.h + (int64_t)key * a.sdk.l;
-  io_traits<T>::store(reinterpret_cast<T*>(to) + c, what ? sum : sum * a.scale);
+  store4(reinterpret_cast<T*>(to) + c, sum);
+}
+
+// dk, dv of the sink tiles, BK keys each: the splits' partial sums, in order
+// (behind the first split's rows only sinks are seen: other keys' sums are whole
+// with it).  32 threads a key, four columns each.
+template <typename T, int BK, class A = AttnArgs>
+__global__ __launch_bounds__(256) void attn_sink_sum_kernel(A a) {
+  const int keys = a.sink_tiles * BK, place = blockIdx.x * 8 + threadIdx.x / 32;
+  const int x = place % (2 * keys), bk = place / (2 * keys), what = x / keys, key = x % keys;
+  const int hk = bk % a.Hk, b = bk / a.Hk, c = threadIdx.x % 32 * 4;
+  const AttnSeq seq(a, b);
+  if (key >= (A::LIE == Lie::PADDED ? a.Lk : seq.klen) || c >= a.d) return;
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+  sum_parts(sum, a.part + ((((int64_t)bk * a.sink_tiles + key / BK) * a.splits * 2 + what) * BK + key % BK) * a.d + c,
+            (int64_t)2 * BK * a.d, key < a.sinks ? a.splits : 1);
+  store_key<T>(a, seq, hk, key, what, c, sum);
+}
+
+// dk, dv of a packed batch whose tiles' rows are split: a tile's parts, in
+// order.  Workgroups as in the dk, dv kernel, one for eight rows of a tile's dk
+// or dv.
+template <typename T, int BK>
+__global__ __launch_bounds__(256) void attn_row_sum_kernel(PackedArgs a) {
+  constexpr int PER = 2 * BK / 8;
+  const int lane = threadIdx.x % WAVE, x = blockIdx.x % PER * 8 + threadIdx.x / 32, what = x / BK, c = threadIdx.x % 32 * 4;
+  int id = blockIdx.x / PER, tile = 0, n = a.rs;
+  const int hk = id % a.Hk, sink = a.splits > 1 ? a.B * a.sink_tiles : 0;
+  id /= a.Hk;
+  int64_t first;
+  AttnSeq seq(0, 0, 0, 0);
+  if (id < sink) {
+    tile = id % a.sink_tiles;
+    seq = AttnSeq(a, id / a.sink_tiles);
+    first = dkv_part(a, seq.b, hk, tile, 0);
+    if (tile * BK + x % BK < a.sinks) n *= a.splits;
+  } else {
+    seq = find_tile(a, id - sink, BK, lane, true, tile);
+    if (seq.b < 0 || (a.splits > 1 && tile < a.sink_tiles)) return;
+    first = dkv_part(a, id - sink, hk);
+  }
+  const int key = tile * BK + x % BK;
+  if (key >= seq.klen || c >= a.d) return;
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+  sum_parts(sum, a.part + ((first * 2 + what) * BK + x % BK) * a.d + c, (int64_t)2 * BK * a.d, n);
+  store_key<T>(a, seq, hk, key, what, c, sum);
 }
 
 }  // namespace lact

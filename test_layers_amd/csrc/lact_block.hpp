@@ -435,9 +435,8 @@ lact_status lact_window_attention_backward(const lact_attention* p, const void* 
   row_tiles(*p, 128 / ksq, a);
   const int64_t heads = (int64_t)p->batch * p->kv_heads, gq = (int64_t)p->batch * (p->heads / a.hg) * a.tiles,
                 gk = heads * (kv.tiles + (int64_t)kv.sink_tiles * (kv.splits - 1)),
-                gs = kv.splits > 1 ? heads * kv.sink_tiles * 2 * (128 / ksk) : 0;
-  TRY(check_grid(std::max(gq, gk), 256));
-  TRY(check_grid(gs, 128));
+                gs = kv.splits > 1 ? heads * kv.sink_tiles * 2 * (128 / ksk) / 8 : 0;
+  TRY(check_grid(std::max({gq, gk, gs}), 256));
   TRY(check_device_again());
   const hipStream_t s = static_cast<hipStream_t>(stream);
   return by_tile(*p, [&](auto t, auto dp) -> lact_status {
@@ -457,8 +456,8 @@ lact_status lact_window_attention_backward(const lact_attention* p, const void* 
     }
     if (gs > 0) {
       KernelTimer kt(LACT_K_ATTN_BWD, s);
-      if (ksk == 2) LACT_LAUNCH((attn_sink_sum_kernel<T, 64>), dim3((unsigned)gs), dim3(128), s, kv);
-      else LACT_LAUNCH((attn_sink_sum_kernel<T, 128>), dim3((unsigned)gs), dim3(128), s, kv);
+      if (ksk == 2) LACT_LAUNCH((attn_sink_sum_kernel<T, 64>), dim3((unsigned)gs), dim3(256), s, kv);
+      else LACT_LAUNCH((attn_sink_sum_kernel<T, 128>), dim3((unsigned)gs), dim3(256), s, kv);
     }
     HIP_TRY(hipGetLastError());
     return LACT_OK;

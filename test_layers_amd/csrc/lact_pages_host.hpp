@@ -336,9 +336,34 @@ namespace {
 struct PackedBack {
   PackedArgs q, kv;          // tile fields of the two kernels
   int ksq = 1, ksk = 1;
-  int64_t gq = 0, gk = 0, gs = 0;  // workgroups: dq; dk, dv; sums of sink tiles
+  int64_t gq = 0, gk = 0, gs = 0;  // workgroups: dq; dk, dv; sums of parts
   size_t part = 0, total = 0;
 };
+// Parts of the rows of a key tile, of `work` tiles a key head (as far as the
+// host can tell) and `jobs` workgroups at most: shared work and half of the
+// longest workgroup, or all of it, against a launch more and the parts' way
+// through memory.  Training steps, us with 1, 2, 3, 5, 8 parts: fp32, 6 texts of
+// 4001 tokens, window 333, 12 (4) heads of 96: 721, 680, 598, 583, 584; bf16:
+// 135, 141, 145, 169, 203; 4 texts of 8000 tokens, 8 (2) heads of 128, causal:
+// 599, 437, 429, 445, 474; 4000 tokens, 32 (8) heads of 128: 413, 351, 355, 381,
+// 452; 16 heads of 64: 146, 168, 173, 190, 249.  Of these it takes 5, 1, 5, 3, 1.
+int row_splits(const lact_attention& w, int64_t work, int64_t jobs, int64_t BK) {
+  const bool fp32 = w.io_dtype == LACT_DTYPE_F32, wide = w.d > 64;
+  const int64_t room = (fp32 || wide ? 1 : 2) * NCU, BQ = fp32 && wide ? 32 : 64, G = w.heads / w.kv_heads;
+  const int64_t most = G * ceil_div(limited(w) ? std::min(w.k_len, w.window + BK) : w.k_len, BQ);  // row tiles of a key tile
+  const double mean = limited(w) ? (double)most : 0.5 * (double)most;
+  const double t = (fp32 ? 7.0 : wide ? 3.5 : 1.8) * (BK == 64 ? 0.5 : 1.0);  // us a row tile
+  double best = 1e30;
+  int parts = 1;
+  for (int64_t s = 1; s <= 16 && s <= most && (s == 1 || jobs * w.kv_heads * s <= 8 * NCU); ++s) {
+    const double sums = s > 1 ? 8.0 + (double)(jobs * w.kv_heads * s) * (double)(2 * BK * w.d * 8) / 4e6 : 0.0;
+    const double longest = (double)most / (double)s, share = (double)(work * w.kv_heads) * mean / (double)room;
+    const double cost = std::max(longest, share + 0.5 * longest) * t + sums;
+    if (cost < best) best = cost, parts = (int)s;
+  }
+  return parts;
+}
+
 PackedBack packed_back(const lact_packed& p, const lact_attention& w) {
   PackedBack x;
   memset(&x.q, 0, sizeof(x.q));
@@ -356,9 +381,12 @@ PackedBack packed_back(const lact_packed& p, const lact_attention& w) {
   sink_plan(w, BK, x.kv);
   const int64_t tiles = count_tiles(w, p.tokens, BK, x.kv);
   const int64_t split = x.kv.splits > 1 ? (int64_t)w.batch * x.kv.sink_tiles : 0;  // sink tiles in parts, a key head
-  x.gk = (tiles + split * x.kv.splits) * w.kv_heads;
-  x.gs = split * w.kv_heads * 2 * BK;
-  if (split) x.total += align256((size_t)split * w.kv_heads * x.kv.splits * 2 * BK * w.d * 4);
+  const int64_t jobs = tiles + split * x.kv.splits;
+  x.kv.rs = row_splits(w, std::min(tiles, ceil_div(p.tokens, BK)) + split, jobs, BK);
+  x.gk = jobs * w.kv_heads * x.kv.rs;
+  x.gs = (x.kv.rs > 1 ? tiles + split : split) * w.kv_heads * (2 * BK / 8);
+  const int64_t parts = x.kv.rs > 1 ? jobs * x.kv.rs : split * x.kv.splits;  // a key head
+  x.total += align256((size_t)parts * w.kv_heads * 2 * BK * w.d * 4);
   return x;
 }
 
@@ -415,9 +443,9 @@ lact_status lact_packed_attention_backward(const lact_packed* p, const void* q, 
   PackedArgs kv = a;
   a.hg = x.q.hg, a.tiles = x.q.tiles, a.slots = x.q.slots, a.main = (int32_t)x.gq;
   kv.tiles = x.kv.tiles, kv.slots = x.kv.slots, kv.main = (int32_t)x.gk;
-  kv.splits = std::max(1, x.kv.splits), kv.sink_tiles = x.kv.sink_tiles, kv.span = x.kv.span;
+  kv.rs = std::max(1, x.kv.rs), kv.splits = std::max(1, x.kv.splits), kv.sink_tiles = x.kv.sink_tiles, kv.span = x.kv.span;
   TRY(check_grid(std::max(x.gq, x.gk) + a.rest, 256));
-  TRY(check_grid(x.gs, 128));
+  TRY(check_grid(x.gs, 256));
   TRY(check_device_again());
   const hipStream_t s = static_cast<hipStream_t>(stream);
   return by_tile(w, [&](auto t, auto dp) -> lact_status {
@@ -436,9 +464,12 @@ lact_status lact_packed_attention_backward(const lact_packed* p, const void* q, 
       });
     }
     if (x.gs > 0) {
+      const dim3 grid((unsigned)x.gs);
       KernelTimer kt(LACT_K_ATTN_BWD, s);
-      if (x.ksk == 2) LACT_LAUNCH((attn_sink_sum_kernel<T, 64, PackedArgs>), dim3((unsigned)x.gs), dim3(128), s, kv);
-      else LACT_LAUNCH((attn_sink_sum_kernel<T, 128, PackedArgs>), dim3((unsigned)x.gs), dim3(128), s, kv);
+      if (x.kv.rs > 1 && x.ksk == 2) LACT_LAUNCH((attn_row_sum_kernel<T, 64>), grid, dim3(256), s, kv);
+      else if (x.kv.rs > 1) LACT_LAUNCH((attn_row_sum_kernel<T, 128>), grid, dim3(256), s, kv);
+      else if (x.ksk == 2) LACT_LAUNCH((attn_sink_sum_kernel<T, 64, PackedArgs>), grid, dim3(256), s, kv);
+      else LACT_LAUNCH((attn_sink_sum_kernel<T, 128, PackedArgs>), grid, dim3(256), s, kv);
     }
     HIP_TRY(hipGetLastError());
     return LACT_OK;
