@@ -1256,14 +1256,18 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
   if (a.lse && t == 0) a.lse[((int64_t)b * a.H + h) * a.Lq + tok] = l == 0.f ? NONE : m * LN2 + logf(l);
 }
 
-// The same for the forward's key splits over pages, a row (token and head) a wave.
+// The same for the forward's key splits over pages, four heads of a token a
+// wave: what it looks up serves all, and their loads are in flight together (36
+// next tokens and 4 chunks of 512 rows, 32 heads of 128: a head a wave 31.6 us,
+// so 21.9).
+constexpr int JOIN_HEADS = 4;
 template <typename T, int DP>
 __global__ __launch_bounds__(256) void split_join_kernel(PagedArgs a) {
   constexpr float NONE = -__builtin_huge_valf();
-  constexpr int BN = attn_bn<T, DP>();
-  const int lane = threadIdx.x % WAVE, c = 2 * lane;
-  const int64_t place = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
-  const int h = (int)(place % a.H), token = (int)(place / a.H), BM = 128 / a.hg;
+  constexpr int BN = attn_bn<T, DP>(), N = JOIN_HEADS;
+  const int lane = threadIdx.x % WAVE, c = 2 * lane, quads = (a.H + N - 1) / N, BM = 128 / a.hg;
+  const int64_t id = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
+  const int h0 = (int)(id % quads) * N, token = (int)(id / quads);
   if (token >= a.Lq) return;
   const int b = __builtin_amdgcn_readfirstlane(find_last(a.B, lane, [&](int i) { return seq_len(a.offsets, i, a.Lq) <= token; }));
   if (b < 0) return;
@@ -1272,27 +1276,43 @@ __global__ __launch_bounds__(256) void split_join_kernel(PagedArgs a) {
   if (seq.qlen <= a.few || row >= seq.qlen) return;
   const int splits = key_splits(a, KeyTiles(off + r0, off + min(r0 + BM, seq.qlen) - 1, a.window, a.sinks, BN));
   if (splits == 1) return;
-  const float* ml = a.part_ml + place * a.splits * 2;
-  const float* pr = a.part + place * a.splits * a.d;
-  const float2 s = lane < splits ? *reinterpret_cast<const float2*>(ml + 2 * lane) : make_float2(NONE, 0.f);
-  float m = s.x;
+  // a head behind the last is the last again: the same is stored twice
+  auto place = [&](int i) { return ((int64_t)token * a.H + min(h0 + i, a.H - 1)) * a.splits; };
+  float2 s[N];
 #pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, WAVE));
-  // a split without keys counts for nothing; one whose scores are all NaN has no maximum but a sum
-  const float f = s.y == 0.f ? 0.f : s.x == NONE ? s.y : s.y * __builtin_amdgcn_exp2f(s.x - m), l = wave_sum(f);
-  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-  float2 x = make_float2(0.f, 0.f);
-#pragma unroll 8
-  for (int i = 0; i < splits; ++i) {
-    const float g = of_lane(f, i) * inv;
-    float2 v = make_float2(0.f, 0.f);
-    if (c < a.d) v = *reinterpret_cast<const float2*>(pr + (int64_t)i * a.d + c);
-    x.x += g == 0.f ? 0.f : g * v.x;
-    x.y += g == 0.f ? 0.f : g * v.y;
+  for (int i = 0; i < N; ++i) s[i] = lane < splits ? *reinterpret_cast<const float2*>(a.part_ml + (place(i) + lane) * 2) : make_float2(NONE, 0.f);
+  float f[N], m[N], l[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    m[i] = s[i].x;
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) m[i] = fmaxf(m[i], __shfl_xor(m[i], o, WAVE));
+    // a split without keys counts for nothing; one whose scores are all NaN has no maximum but a sum
+    f[i] = s[i].y == 0.f ? 0.f : s[i].x == NONE ? s[i].y : s[i].y * __builtin_amdgcn_exp2f(s[i].x - m[i]);
+    l[i] = wave_sum(f[i]);
+    f[i] *= l[i] > 0.f || l[i] != l[i] ? 1.f / l[i] : 0.f;
   }
-  T* out = reinterpret_cast<T*>(a.out + seq.at(a, a.so) + (int64_t)h * a.so.h + (int64_t)row * a.so.l);
-  if (c < a.d) io_traits<T>::store(out + c, x.x), io_traits<T>::store(out + c + 1, x.y);
-  if (a.lse && lane == 0) a.lse[seq.stat(a, h) + row] = l == 0.f ? NONE : m * LN2 + logf(l);
+  float2 x[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = make_float2(0.f, 0.f);
+#pragma unroll 4
+  for (int k = 0; k < splits; ++k) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float g = of_lane(f[i], k);
+      float2 v = make_float2(0.f, 0.f);
+      if (c < a.d) v = *reinterpret_cast<const float2*>(a.part + (place(i) + k) * a.d + c);
+      x[i].x += g == 0.f ? 0.f : g * v.x;
+      x[i].y += g == 0.f ? 0.f : g * v.y;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int h = min(h0 + i, a.H - 1);
+    T* out = reinterpret_cast<T*>(a.out + seq.at(a, a.so) + (int64_t)h * a.so.h + (int64_t)row * a.so.l);
+    if (c < a.d) io_traits<T>::store(out + c, x[i].x), io_traits<T>::store(out + c + 1, x[i].y);
+    if (a.lse && lane == 0) a.lse[seq.stat(a, h) + row] = l[i] == 0.f ? NONE : m[i] * LN2 + logf(l[i]);
+  }
 }
 
 // ------------------------------------------------------------------ pages, few rows

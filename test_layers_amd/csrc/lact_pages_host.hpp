@@ -230,7 +230,8 @@ lact_status lact_paged_attention(const lact_paged* p, const void* q, const lact_
   const int64_t few_clear = x.big_grid > 0 ? 0 : clear, big_grid = x.big_grid + (clear - few_clear);
   TRY(by_tile(w, [&](auto t, auto dp) { return check_grid(x.few_grid + few_clear, 64 * few_waves<decltype(t), decltype(dp)::value>()); }));
   TRY(check_grid(big_grid, 256));
-  if (x.big_splits > 1) TRY(check_grid(ceil_div(rows, 4), 256));
+  const int64_t joins = ceil_div(p->tokens * ceil_div(w.heads, JOIN_HEADS), 4);
+  if (x.big_splits > 1) TRY(check_grid(joins, 256));
   TRY(check_device_again());
   char* const base = static_cast<char*>(ws);
   return by_tile(w, [&](auto t, auto dp) -> lact_status {
@@ -272,7 +273,7 @@ lact_status lact_paged_attention(const lact_paged* p, const void* q, const lact_
     }
     if (x.big_splits > 1) {
       KernelTimer kt(LACT_K_ATTN, s);
-      LACT_LAUNCH((split_join_kernel<T, DP>), dim3((unsigned)ceil_div(rows, 4)), dim3(256), s, a);
+      LACT_LAUNCH((split_join_kernel<T, DP>), dim3((unsigned)joins), dim3(256), s, a);
     }
     HIP_TRY(hipGetLastError());
     return LACT_OK;
