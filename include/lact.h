@@ -472,15 +472,16 @@ lact_status lact_add_rmsnorm_backward(const lact_norm_problem* p, const void* h,
  * another: a [heads, tokens, d] tensor (a pointer and strides, of which
  * `batch` is not looked at) holds the rows of sequence b at tokens
  * offsets[b] .. offsets[b + 1].  offsets: device int64 [batch + 1], not
- * decreasing, 0 .. tokens; others are cut to that, and no memory outside the
- * tensors is touched whatever they hold.
+ * decreasing; values are cut to 0 .. tokens.  Decreasing ones give undefined
+ * results, but no memory outside the tensors is touched whatever they hold.
  *
  * Packed attention: whole prompts, or texts of a training step, from their
  * first token on.  Row r of a sequence sees its keys 0 <= j <= r with
  * j > r - window or j < sinks (window = 0: j <= r), as in window attention
  * with q_len = k_len.
  */
-#define LACT_CLEAR_REST 1u   /* rows of o and lse that are no sequence's become zero, not left as they were */
+#define LACT_CLEAR_REST 1u   /* rows of o and lse that are no sequence's, or behind `longest`, become zero and
+                                are not left as they were */
 typedef struct {
     int32_t batch;      /* sequences, 0 .. 2^24 */
     int32_t heads, kv_heads, d, io_dtype;   /* as in lact_attention */
@@ -502,7 +503,7 @@ lact_status lact_packed_attention_forward(const lact_packed* p, const void* q, c
                                           const int64_t* offsets, void* o, const lact_strides* so, float* lse,
                                           void* stream);
 
-/* Gradients, from the forward's o and lse; rows that are no sequence's are zero.
+/* Gradients, from the forward's o and lse; rows that are no sequence's, or behind `longest`, are zero.
  * ws: lact_packed_attention_backward_workspace_size bytes, 256-B aligned. */
 size_t lact_packed_attention_backward_workspace_size(const lact_packed* p);
 lact_status lact_packed_attention_backward(const lact_packed* p, const void* q, const lact_strides* sq, const void* k,

@@ -526,6 +526,7 @@ __device__ __forceinline__ AttnSeq find_tile(const A& a, int id, int BM, int lan
     if (b < 0) return AttnSeq(b, 0, 0, 0);
     const int first = __builtin_amdgcn_readlane(at, b), rows = __builtin_amdgcn_readlane(at, b + 1) - first;
     tile = s - (first / BM + b);
+    if (tile < 0) return AttnSeq(-1, 0, 0, 0);  // offsets that decrease
     const int qlen = min(max(rows, 0), a.most);
     if constexpr (A::LIE == Lie::PACKED) return AttnSeq(b, qlen, qlen, first);
     else return AttnSeq(b, qlen, __builtin_amdgcn_readfirstlane(seq_len(a.k_lens, b, a.Lk)), first);
@@ -534,11 +535,13 @@ __device__ __forceinline__ AttnSeq find_tile(const A& a, int id, int BM, int lan
   const int b = __builtin_amdgcn_readfirstlane(find_last(a.B, lane, [&](int i) { return slot(i) <= s; }));
   if (b < 0) return AttnSeq(b, 0, 0, 0);
   tile = __builtin_amdgcn_readfirstlane(s - slot(b));
+  if (tile < 0) return AttnSeq(-1, 0, 0, 0);
   return AttnSeq(a, b);
 }
 
-// Clears rows of no sequence, those before the first and behind the last: part
-// `part` of `parts`, by a workgroup.  x [heads, tokens, d], lse [heads, tokens]
+// Clears rows of no sequence, those before the first and behind the last, and
+// those of a sequence that are not looked at: part `part` of `parts`, by a
+// workgroup.  x [heads, tokens, d], lse [heads, tokens]
 // (null: none).
 template <class A>
 __device__ __forceinline__ void clear_rest(const A& a, char* x, const AttnStride& s, int heads, int bytes, float* lse,
@@ -552,6 +555,16 @@ __device__ __forceinline__ void clear_rest(const A& a, char* x, const AttnStride
   }
   for (int64_t i = (int64_t)part * blockDim.x + threadIdx.x; lse && i < rows * heads; i += (int64_t)parts * blockDim.x)
     lse[i / rows * a.Lq + token(i % rows)] = 0.f;
+  // rows behind `most`, which the caller has promised not to have: a sequence a thread
+  if (a.most < a.Lq)
+    for (int64_t b = (int64_t)part * blockDim.x + threadIdx.x; b < a.B; b += (int64_t)parts * blockDim.x) {
+      const int end = seq_len(a.offsets, (int)b + 1, a.Lq);
+      for (int64_t r = (int64_t)seq_len(a.offsets, (int)b, a.Lq) + a.most; r < end; ++r)
+        for (int h = 0; h < heads; ++h) {
+          for (int64_t c = 0; x && c < per; ++c) *reinterpret_cast<uint4*>(x + h * s.h + r * s.l + c * 16) = zero4();
+          if (lse) lse[(int64_t)h * a.Lq + r] = 0.f;
+        }
+    }
 }
 
 // Whether the row at position p sees key k + o, for a run of offsets o
@@ -940,7 +953,8 @@ __device__ __forceinline__ AttnSeq place_seq(const A& a, int BM, int lane, AttnP
 // two waves of a SIMD overlap as far as they can.  32K prompt of 32 heads
 // (8 key heads), d = 128, window 2048: 1.08 ms, 990 TFLOP/s, matrix pipes busy
 // 55 % of the time; 16 heads, d = 64: 325 us, 820 TFLOP/s, 45 %; no LDS bank
-// conflicts.  Tiles of 32 keys with three waves a SIMD took 1.47 ms for 1.17
+// conflicts.  Packed: 8 prompts of 32768 tokens, causal, the same heads: 1.32 ms,
+// 1.05 PFLOP/s; paged: 2048 rows over 32768 keys 1.02 ms, 1.05 PFLOP/s.  Tiles of 32 keys with three waves a SIMD took 1.47 ms for 1.17
 // of these at the time: too few products between a tile's waits.
 template <typename T, int DP, int KS, class A = AttnArgs>
 __global__ __launch_bounds__(256, (attn_waves<T, DP>())) void attn_fwd_kernel(A a) {
@@ -1273,7 +1287,7 @@ __global__ __launch_bounds__(256) void split_join_kernel(PagedArgs a) {
   if (b < 0) return;
   const AttnSeq seq(a, b);
   const int row = token - seq.first, r0 = row / BM * BM, off = seq.klen - seq.qlen;
-  if (seq.qlen <= a.few || row >= seq.qlen) return;
+  if (seq.qlen <= a.few || row < 0 || row >= seq.qlen) return;
   const int splits = key_splits(a, KeyTiles(off + r0, off + min(r0 + BM, seq.qlen) - 1, a.window, a.sinks, BN));
   if (splits == 1) return;
   // a head behind the last is the last again: the same is stored twice
@@ -1324,6 +1338,12 @@ __global__ __launch_bounds__(256) void split_join_kernel(PagedArgs a) {
 // barrier: while one begins an item the others read on.  An item that lies in
 // one run is finished there; of others each wave leaves its part (at most two
 // a wave: its first and its last), which stream_join_kernel adds up.
+//
+// Bound by memory: 96 requests of 2.1K to 8.2K keys, 32 (8) heads of 128: 367 us,
+// 5.5 TB/s of the 2.03 GB (a workgroup for each key head, by attn_few_kernel's
+// scheme: 456, two splits of the keys 435 and more of them longer: a workgroup's
+// beginning and end took 5 us in which its compute unit read nothing).  Where keys
+// are few, by latency: 16 heads of 64, window 2048: 11.0 us, and 3.9 the join.
 constexpr int STREAM_SCAN = 256;  // sequences whose work a workgroup sums itself
 
 // The rows of a sequence in tiles of 32, and the units of each, at least one:

@@ -1125,7 +1125,8 @@ def packed_attention(q, k, v, o=None, *, offsets, longest: Optional[int] = None,
     tokens, d], fp32 or bf16, any strides in multiples of 16 bytes with d
     contiguous: token-major tensors come as transposed views.  Sequence b has
     the tokens offsets[b] .. offsets[b + 1] (int64 [batch + 1] on the device),
-    `longest` at most (None: it may be all).  window, sinks and scale as in
+    `longest` at most (None: it may be all; rows behind are not looked at and
+    count as no sequence's).  window, sinks and scale as in
     window_attention.  Returns o in q's layout, and with return_lse also lse
     [heads, tokens] fp32; rows of no sequence are zero in what is allocated
     here and left as they were in given tensors."""
@@ -1211,8 +1212,8 @@ def paged_attention(q, k_pages, v_pages, o=None, *, table, offsets, k_lens, long
     Sequence b has k_lens[b] keys (int64 [batch]), its new ones among them, in
     the pages table[b] (int32 [batch, width]).  One row a sequence and long
     chunks may be mixed; `longest` and `k_len` bound the rows and keys of a
-    sequence (None: all rows, the table's width) and choose how the work is
-    split.  window, sinks and scale as in window_attention, results as in
+    sequence (None: all rows, the table's width; rows and keys behind them are
+    not looked at) and choose how the work is split.  window, sinks and scale as in window_attention, results as in
     packed_attention."""
     window, sinks, scale = _int(window, "window"), _int(sinks, "sinks"), None if scale is None else float(scale)
     longest = None if longest is None else _int(longest, "longest")

@@ -56,6 +56,11 @@ PACKED = [
     (32, 16, 128, 330, 4, [600, 513, 100, 700], 0, 40),
     (64, 64, 40, 0, 0, [515, 300, 131], 0, 0),
     (32, 8, 96, 0, 0, [260, 1290], 0, 0),
+    # few key tiles with many rows, which are split: over heads, and beside sinks' own splits
+    (8, 1, 128, 0, 0, [1500, 700, 3, 0, 130], 1, 2),
+    (12, 2, 96, 333, 17, [1400, 383, 0, 200, 800], 0, 3),
+    (4, 1, 64, 256, 200, [1900, 31, 900], 0, 0),
+    (3, 1, 40, 0, 0, [2100], 0, 0),
 ]
 
 
@@ -284,6 +289,108 @@ def test_numbers_on_the_device_are_cut_to_the_arrays(lact):
     assert torch.equal(got[:, :20], one[:, :20])
     check_attention(OP.packed_attention(f64(q), f64(k), f64(k), [0, 20, 50], 0, 0, 0.125), {"o": torch.cat(
         [got[:, :50], torch.zeros_like(got[:, 50:])], 1), }, torch.float32, 64, 60, False)
+
+
+def test_offsets_out_of_order_stay_inside(lact):
+    """Offsets that jump about: whatever they give, nothing outside the tensors is touched."""
+    gen = torch.Generator("cuda").manual_seed(14)
+    T, d = 4000, 64
+    around = [torch.full((T + 200, h, d), 7.0, device="cuda", dtype=torch.bfloat16) for h in (4, 4, 2, 2)]
+    o, dq, dk, dv = (x[100 : T + 100].transpose(0, 1) for x in around)
+    q = rows(gen, 4, T, d, torch.bfloat16, "tokens")
+    k = rows(gen, 2, T, d, torch.bfloat16, "tokens")
+    kp, vp, table = _cache(gen, [900] * 90, 2, 32, d, torch.bfloat16, "heads")
+    for B in (20, 90):
+        # found by slots: one long sequence, then numbers in any order
+        jump = torch.randint(-10, T + 10, (B - 1,), generator=gen, device="cuda").tolist()
+        off = whole([0, 3000] + jump)
+        _, lse = lact.packed_attention(q, k, k, o, offsets=off, longest=3000, return_lse=True)
+        lact.packed_attention_backward(q, k, k, o, lse, dO=q, offsets=off, longest=3000, out=dict(dq=dq, dk=dk, dv=dv))
+        lact.paged_attention(q, kp, vp, o, table=whole(table[:B], torch.int32), offsets=off, k_lens=whole([900] * B))
+        torch.cuda.synchronize()
+        assert all((x[:100] == 7).all() and (x[T + 100 :] == 7).all() for x in around)
+
+
+@pytest.mark.parametrize("longest", [1, 30])
+def test_rows_behind_the_longest_are_no_sequences(lact, longest):
+    gen = torch.Generator("cuda").manual_seed(15)
+    off, n = [3, 63, 64, 164], 170
+    q, k = rows(gen, 4, n, 64, torch.float32, "heads"), rows(gen, 2, n, 64, torch.float32, "heads")
+    live = torch.zeros(n, dtype=torch.bool, device="cuda")
+    for a, z in zip(off[:-1], off[1:]):
+        live[a : min(z, a + longest)] = True
+    kw = dict(offsets=whole(off), longest=longest)
+    o, lse = lact.packed_attention(q, k, k, return_lse=True, **kw)
+    g = lact.packed_attention_backward(q, k, k, o, lse, dO=q, **kw)
+    kp, vp, table = _cache(gen, [70, 9, 200], 2, 8, 64, torch.float32, "tokens")
+    p = lact.paged_attention(q, kp, vp, table=whole(table, torch.int32), k_lens=whole([70, 9, 200]), **kw)
+    for x in (o, lse, p, *g.values()):
+        assert (x[:, ~live] == 0).all() and x[:, live].any()
+    given = torch.full_like(q, 7.0)
+    lact.packed_attention(q, k, k, given, **kw)
+    assert (given[:, ~live] == 7).all() and torch.equal(given[:, live], o[:, live])
+
+
+@pytest.mark.parametrize("t", ["bf16", "fp32"])
+@pytest.mark.parametrize("seqs", [[(1, 1900), (1, 700)], [(90, 1900), (1, 700), (70, 90)]])
+def test_pages_before_the_window_may_be_gone(lact, t, seqs):
+    """Entries between the sinks and what the window of any row reaches lead nowhere, or to pages that hold NaN."""
+    dt, window, sinks, page = DT[t], 200, 5, 16
+    gen = torch.Generator("cuda").manual_seed(16)
+    new, lens = [n for n, _ in seqs], [m for _, m in seqs]
+    q = rows(gen, 4, sum(new), 64, dt, "tokens")
+    kp, vp, table = _cache(gen, lens, 2, page, 64, dt, "heads", spare=8)
+    used = {int(x) for b, m in enumerate(lens) for x in table[b, : -(-m // page)]}
+    spare = [x for x in range(kp.shape[0]) if x not in used]
+    kp[spare], vp[spare] = float("nan"), float("inf")
+    kw = dict(offsets=whole(sums(new)), k_lens=whole(lens), window=window, sinks=sinks, longest=max(new))
+    want = lact.paged_attention(q, kp, vp, table=whole(table, torch.int32), **kw)
+    for b, (n, m) in enumerate(seqs):
+        first, last = -(-sinks // page), max(0, m - n - window + 1) // page   # pages that no row sees
+        for i in range(first, last):
+            table[b, i] = (-1, 2 ** 31 - 1, -2 ** 31, spare[i % len(spare)])[i % 4]
+    got = lact.paged_attention(q, kp, vp, table=whole(table, torch.int32), **kw)
+    # a row that a NaN passed is summed again, in another order
+    ref = _paged_ref(q, kp, vp, np.clip(table, 0, kp.shape[0] - 1), sums(new), lens, window, sinks, 0.125)
+    check_attention(ref, {"o": got}, dt, 64, max(lens), False)
+    assert torch.isfinite(got).all() and float((got - want).abs().max()) < 0.1
+
+
+@pytest.mark.parametrize("t,d,B", [("bf16", 64, 300), ("fp32", 128, 200), ("bf16", 128, 700), ("fp32", 40, 257)])
+@pytest.mark.parametrize("chunk", [0, 60])
+def test_many_requests(lact, t, d, B, chunk):
+    """More sequences than a workgroup sums in one round, and than it sums itself; some without rows or keys."""
+    rng, dt = np.random.default_rng([B, chunk]), DT[t]
+    gen = torch.Generator("cuda").manual_seed(17)
+    new = [int(x) for x in rng.integers(0, 3, B)]
+    if chunk:
+        new[B // 2] = chunk
+    lens = [int(x) for x in rng.integers(0, 200, B)]
+    lens[B // 2], lens[3] = 900, 0
+    q = rows(gen, 8, sum(new), d, dt, "tokens")
+    kp, vp, table = _cache(gen, lens, 2, 16, d, dt, "tokens")
+    kw = dict(table=whole(table, torch.int32), offsets=whole(sums(new)), k_lens=whole(lens), longest=max(new), window=150,
+              sinks=3, scale=0.3)
+    print("many", t, d, B, chunk, flush=True)
+    ref = _paged_ref(q, kp, vp, table, sums(new), lens, 150, 3, float(np.float32(0.3)))
+    for _ in range(2):
+        o, lse = lact.paged_attention(q, kp, vp, return_lse=True, **kw)
+        check_attention(ref, {"o": o, "lse": lse}, dt, d, 900, False)
+
+
+def test_work_counted_in_several_tiles(lact):
+    """A table so wide that the tiles it could hold pass 2^30: the same results."""
+    gen = torch.Generator("cuda").manual_seed(18)
+    B, page, width = 40, 65536, 16383
+    kp, vp = (torch.randn(3, 1, page, 8, generator=gen, device="cuda").bfloat16() for _ in range(2))
+    table = torch.full((B, width), -1, dtype=torch.int32, device="cuda")
+    table[:, 0], table[:, 1] = torch.arange(B, device="cuda") % 3, (torch.arange(B, device="cuda") + 1) % 3
+    lens = [1, 31, 32, 33, 65536, 65537, 70000, 0] * 5
+    q = rows(gen, 2, B, 8, torch.bfloat16, "heads")
+    kw = dict(table=table, offsets=whole(list(range(B + 1))), k_lens=whole(lens), longest=1)
+    ref = _paged_ref(q, kp, vp, table.cpu().numpy()[:, :2], list(range(B + 1)), lens, 0, 0, 8 ** -0.5)
+    for bound in (None, 70000):
+        check_attention(ref, {"o": lact.paged_attention(q, kp, vp, k_len=bound, **kw)}, torch.bfloat16, 8, 70000, False)
 
 
 def test_a_cache_beyond_32_bit_offsets(lact):
