@@ -229,8 +229,11 @@ struct PageRows {
       vo[i] = (uint32_t)(lane / Tile::CPR) * (uint32_t)vs.l + c;
     }
   }
-  __device__ __forceinline__ void issue(char* tile, int row0) const {
-    const uint32_t m0 = __builtin_amdgcn_readfirstlane(lds_at(tile) + (uint32_t)(wave * WAVE * 16));
+  __device__ __forceinline__ void issue(char* tile, int row0) const { issue(tile, tile + TB, row0); }
+  // (a null tile is left out)
+  __device__ __forceinline__ void issue(char* ktile, char* vtile, int row0) const {
+    const uint32_t at = (uint32_t)(wave * WAVE * 16);
+    const uint32_t mk = __builtin_amdgcn_readfirstlane(lds_at(ktile) + at), mv = __builtin_amdgcn_readfirstlane(lds_at(vtile) + at);
     if (row0 + R - 1 <= rmax) {
       int page[N], in[N];
 #pragma unroll
@@ -242,16 +245,16 @@ struct PageRows {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const int64_t e = max(0, min(page[i], last));
-        dma16_at(ko[i], kb + e * ks.b + in[i] * ks.l, m0 + (uint32_t)(i * NW * WAVE * 16));
-        dma16_at(vo[i], vb + e * vs.b + in[i] * vs.l, m0 + (uint32_t)(TB + i * NW * WAVE * 16));
+        if (ktile) dma16_at(ko[i], kb + e * ks.b + in[i] * ks.l, mk + (uint32_t)(i * NW * WAVE * 16));
+        if (vtile) dma16_at(vo[i], vb + e * vs.b + in[i] * vs.l, mv + (uint32_t)(i * NW * WAVE * 16));
       }
     } else {  // rows behind the last are read from it
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const int row = (i * NW + wave) * GROUP + lane / Tile::CPR, gr = min(row0 + row, rmax);
         const int c = min((lane % Tile::CPR) ^ Tile::f(row), cmax) * 16;
-        dma16(k(gr) + c, m0 + (uint32_t)(i * NW * WAVE * 16));
-        dma16(v(gr) + c, m0 + (uint32_t)(TB + i * NW * WAVE * 16));
+        if (ktile) dma16(k(gr) + c, mk + (uint32_t)(i * NW * WAVE * 16));
+        if (vtile) dma16(v(gr) + c, mv + (uint32_t)(i * NW * WAVE * 16));
       }
     }
   }
@@ -784,12 +787,16 @@ struct AttnRows {
     }
   }
   // 32 keys, in LDS tiles of as many rows
-  __device__ __forceinline__ void step(const char* kt, const char* vt, int k0, int window, int sinks, float c,
-                                       int lane, int d) {
+  __device__ __forceinline__ f32x16 weights(const char* kt, int k0, int window, int sinks, float c, int lane, int d) {
     f32x16 s = scores(kt, 0, lane, d);
     if (!w.whole(k0, k0 + 31, window, sinks)) mask(s, k0, window, sinks, lane);
     follow(s, c, nullptr);
     exps(s, c);
+    return s;
+  }
+  __device__ __forceinline__ void step(const char* kt, const char* vt, int k0, int window, int sinks, float c,
+                                       int lane, int d) {
+    const f32x16 s = weights(kt, k0, window, sinks, c, lane, d);
     acc_trans<T, DP>(o, s, vt, 0, lane, d);
   }
   // 64 keys that every row sees.  Four runs of products: the scores of one
@@ -1402,10 +1409,24 @@ struct StreamJoin {
   int part, parts;             // of parts part, part + 2 (or + 1, see below), + 4 ..
 };
 
+// A wave keeps one tile of K and one of V: the next K is on its way from the
+// scores on, the next V from the sums on, so that each has the other's half of
+// the work to land in, and twice as many waves find room as with rings of two
+// tiles (fp32, the same requests: 1.94 ms with rings, 1.01 so, 4.0 TB/s; heads of
+// 64 580 and 413 us; bf16, one request of 16 heads of 64: 16.4 and 15.5 us with
+// the join).  bf16 tiles of 128, whose work is short beside their way, have the
+// ring (386 us and 402; one request of 32768 keys 40 and 46).
+constexpr int STREAM_GROUP = 4;  // waves of a workgroup
 template <typename T, int DP>
-__global__ __launch_bounds__(64 * (few_waves<T, DP>())) void stream_kernel(PagedArgs a) {
+constexpr bool stream_ring() { return sizeof(T) == 2 && DP > 64; }
+template <typename T, int DP>
+constexpr int stream_groups() { return DP <= 64 ? 2 : 1; }  // workgroups of a compute unit, by LDS
+template <typename T, int DP>
+__global__ __launch_bounds__(64 * STREAM_GROUP, (stream_groups<T, DP>())) void stream_kernel(PagedArgs a) {
   using Tile = AttnTile<T, DP>;
-  constexpr int NW = few_waves<T, DP>(), TB = few_tile<T, DP>(), WB = 4 * TB;
+  constexpr bool RING = stream_ring<T, DP>();
+  constexpr int NW = STREAM_GROUP, TB = few_tile<T, DP>(), WB = (RING ? 4 : 2) * TB;
+  static_assert(NW * WB * stream_groups<T, DP>() <= 128 * 1024, "LDS of the workgroups of a compute unit");
   __shared__ __align__(1024) char lds[NW * WB];
   __shared__ StreamScan scan;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 31;
@@ -1416,7 +1437,7 @@ __global__ __launch_bounds__(64 * (few_waves<T, DP>())) void stream_kernel(Paged
   const int work = __builtin_amdgcn_readfirstlane(upto[a.B]), run = max(a.share, (work + a.waves - 1) / a.waves);
   const int me = blockIdx.x * NW + wave, cmax = a.d * (int)sizeof(T) / 16 - 1;
   const int t0 = min(work, me * run), t1 = min(work, t0 + run);
-  char* ring = lds + wave * WB;
+  char *const kt_lds = lds + wave * WB, *const vt_lds = kt_lds + TB;
   StreamJoin join = {0, 0, 0, 0, 0, 0};
 #pragma unroll 1
   for (int t = t0; t < t1;) {
@@ -1434,25 +1455,46 @@ __global__ __launch_bounds__(64 * (few_waves<T, DP>())) void stream_kernel(Paged
     AttnRows<T, DP> w;
     w.clear();
     const PageRows<T, DP, 32, 1> keys(a, b, hk, klen - 1, 0, lane);
-    auto issue = [&](int i, int buf) { keys.issue(ring + buf * 2 * TB, kt.at(i) * 32); };
     wait_lgkm0();  // the item before has been read
-    if (i0 < i1) issue(i0, 0);
+    if (i0 < i1) keys.issue(kt_lds, vt_lds, kt.at(i0) * 32);
     load_rows(w.q, qb + (int64_t)h * a.sq.h + (int64_t)tok * a.sq.l, cmax, lane);
     w.p = off + tok;
     w.w = {off + r0 / a.G, off + min(r0 + 31, rows - 1) / a.G};
-    int buf = 0;
+    // a copy of 32 rows is CPR / 2 instructions of a wave
 #pragma unroll 1
-    for (int i = i0; i < i1; ++i, buf ^= 1) {
-      wait_lgkm0();  // the tile that the next copies overwrite has been read
-      if (i + 1 < i1) {
-        issue(i + 1, buf ^ 1);
-        wait_vm<Tile::CPR>();  // the 2 x CPR / 2 copies of the tile before them have landed
+    for (int i = i0; i < i1; ++i) {
+      const int k0 = kt.at(i) * 32;
+      if constexpr (RING) {
+        const int at = ((i - i0) & 1) * 2 * TB;
+        wait_lgkm0();  // the tile that the next copies overwrite has been read
+        if (i + 1 < i1) {
+          char* next = kt_lds + 2 * TB - at;
+          keys.issue(next, next + TB, kt.at(i + 1) * 32);
+          wait_vm<Tile::CPR>();
+        } else {
+          wait_vm<0>();
+        }
+        asm volatile("" ::: "memory");
+        w.template tile<32, 1>(kt_lds + at, vt_lds + at, 0, k0, a.window, a.sinks, a.c, lane, a.d);
+        continue;
+      }
+      const bool some = w.w.some(k0, k0 + 31, a.window, a.sinks), more = i + 1 < i1;
+      if (i == i0) wait_vm<0>();
+      else wait_vm<Tile::CPR / 2>();  // K is here, V may not be
+      asm volatile("" ::: "memory");
+      f32x16 p = zero16();
+      if (some) p = w.weights(kt_lds, k0, a.window, a.sinks, a.c, lane, a.d);
+      wait_lgkm0();  // K has been read
+      if (more) {
+        keys.issue(kt_lds, nullptr, kt.at(i + 1) * 32);
+        wait_vm<Tile::CPR / 2>();
       } else {
         wait_vm<0>();
       }
       asm volatile("" ::: "memory");
-      const char* x = ring + buf * 2 * TB;
-      w.template tile<32, 1>(x, x + TB, 0, kt.at(i) * 32, a.window, a.sinks, a.c, lane, a.d);
+      if (some) acc_trans<T, DP>(w.o, p, vt_lds, 0, lane, a.d);
+      wait_lgkm0();  // V has been read
+      if (more) keys.issue(nullptr, vt_lds, kt.at(i + 1) * 32);
     }
     const bool whole = u0 == 0 && u1 == it.units;
     const float l = pair_sum(w.l), inv = l > 0.f || l != l ? 1.f / l : 0.f;

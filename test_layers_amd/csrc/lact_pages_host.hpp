@@ -134,9 +134,9 @@ PagedPlan paged_plan(const lact_paged& p, const lact_attention& w) {
   if (w.q_len <= small) x.few = w.q_len;
   else if (w.batch > 1) x.few = small;
   f.q_len = x.few;
-  int waves = 0;  // of a workgroup of the streams
+  int64_t room = 0;  // workgroups of the streams that run at once
   (void)by_tile(w, [&](auto t, auto dp) {
-    waves = few_waves<decltype(t), decltype(dp)::value>();
+    room = (int64_t)stream_groups<decltype(t), decltype(dp)::value>() * NCU;
     return LACT_OK;
   });
   const size_t rows = (size_t)p.tokens * w.heads;
@@ -150,8 +150,8 @@ PagedPlan paged_plan(const lact_paged& p, const lact_attention& w) {
     const int64_t items = x.items = std::min((int64_t)w.batch * ceil_div(G * x.few, 32), p.tokens * ceil_div(G, 32)) * w.kv_heads;
     const int64_t tiles = ceil_div(few_keys(f), 32) + 2;  // the sinks' and the window's may be cut anew
     while (items * ceil_div(tiles, x.unit) > STREAM_MOST && x.unit < tiles) x.unit *= 2;
-    x.few_grid = std::min(few_room(f), ceil_div(items, waves * STREAM_SHARE) * tiles);
-    x.waves = (int)(x.few_grid * waves);
+    x.few_grid = std::min(room, ceil_div(items, STREAM_GROUP * STREAM_SHARE) * tiles);
+    x.waves = (int)(x.few_grid * STREAM_GROUP);
     x.rows = (int)std::min<int64_t>(32, G * x.few);
     if (w.batch > STREAM_SCAN) x.upto = place((size_t)(w.batch + 1) * 4);
     x.joins = place((size_t)x.waves * sizeof(StreamJoin));
@@ -228,7 +228,7 @@ lact_status lact_paged_attention(const lact_paged* p, const void* q, const lact_
   const int64_t rows = p->tokens * w.heads, clear = p->flags & LACT_CLEAR_REST ? rest_groups(rows * w.d * es) : 0;
   // what is cleared is cleared beside the kernel of the longer sequences, if there is one
   const int64_t few_clear = x.big_grid > 0 ? 0 : clear, big_grid = x.big_grid + (clear - few_clear);
-  TRY(by_tile(w, [&](auto t, auto dp) { return check_grid(x.few_grid + few_clear, 64 * few_waves<decltype(t), decltype(dp)::value>()); }));
+  TRY(check_grid(x.few_grid + few_clear, 64 * STREAM_GROUP));
   TRY(check_grid(big_grid, 256));
   const int64_t joins = ceil_div(p->tokens * ceil_div(w.heads, JOIN_HEADS), 4);
   if (x.big_splits > 1) TRY(check_grid(joins, 256));
@@ -254,7 +254,7 @@ lact_status lact_paged_attention(const lact_paged* p, const void* q, const lact_
         LACT_LAUNCH(stream_plan_kernel, dim3(1), dim3(1024), s, f);
       }
       KernelTimer kt(LACT_K_ATTN, s);
-      LACT_LAUNCH((stream_kernel<T, DP>), dim3((unsigned)(x.few_grid + few_clear)), dim3(64 * (few_waves<T, DP>())), s, f);
+      LACT_LAUNCH((stream_kernel<T, DP>), dim3((unsigned)(x.few_grid + few_clear)), dim3(64 * STREAM_GROUP), s, f);
     }
     if (big_grid > 0) {
       row_tiles(w, 128, a);
