@@ -1341,7 +1341,7 @@ __global__ __launch_bounds__(256) void split_join_kernel(PagedArgs a) {
 // only the device knows: all tiles of 32 keys that some sequence's rows see,
 // one after another -- by sequence, 32 of its rows (ordered by token, as in
 // attn_few_kernel) and key head, an item -- are dealt to the launch's waves in
-// equal runs.  Each wave goes along its run alone, with its own ring and no
+// equal runs.  Each wave goes along its run alone, with its own tiles and no
 // barrier: while one begins an item the others read on.  An item that lies in
 // one run is finished there; of others each wave leaves its part (at most two
 // a wave: its first and its last), which stream_join_kernel adds up.
@@ -1350,7 +1350,7 @@ __global__ __launch_bounds__(256) void split_join_kernel(PagedArgs a) {
 // 5.5 TB/s of the 2.03 GB (a workgroup for each key head, by attn_few_kernel's
 // scheme: 456, two splits of the keys 435 and more of them longer: a workgroup's
 // beginning and end took 5 us in which its compute unit read nothing).  Where keys
-// are few, by latency: 16 heads of 64, window 2048: 11.0 us, and 3.9 the join.
+// are few, by latency: 16 heads of 64, window 2048: 9.9 us, and 4.0 the join.
 constexpr int STREAM_SCAN = 256;  // sequences whose work a workgroup sums itself
 
 // The rows of a sequence in tiles of 32, and the units of each, at least one:
