@@ -23,6 +23,7 @@
 // every product is an fp32 MFMA and nothing is rounded.
 #pragma once
 #include "lact_direct.hpp"
+#include "lact_stream_work.hpp"
 
 namespace lact {
 
@@ -1379,22 +1380,22 @@ __device__ __forceinline__ void stream_scan(const PagedArgs& a, int* upto, Strea
       const int first = seq_len(a.offsets, b, a.Lq);
       const AttnSeq s(b, min(max(seq_len(a.offsets, b + 1, a.Lq) - first, 0), a.most), seq_len(a.k_lens, b, a.Lk), first);
       const StreamItem it(a, s);
-      x = it.rtiles * it.units * a.Hk;
+      x = stream_work(it.rtiles, it.units, a.Hk);
       if (keep) keep->first[b] = first, keep->qlen[b] = s.qlen, keep->klen[b] = s.klen;
     }
     for (int o = 1; o < WAVE && o < a.B; o *= 2) {
       const int y = __shfl_up(x, o, WAVE);
-      if (lane >= o) x += y;
+      if (lane >= o) x = stream_add(x, y);
     }
     if (b0) __syncthreads();
     if (lane == WAVE - 1) sums[wave] = x;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < NT / WAVE; ++i)
-      if (i < wave) x += sums[i];
-    if (b < a.B) upto[b + 1] = before + x;
+      if (i < wave) x = stream_add(x, sums[i]);
+    if (b < a.B) upto[b + 1] = stream_add(before, x);
 #pragma unroll
-    for (int i = 0; i < NT / WAVE; ++i) before += sums[i];
+    for (int i = 0; i < NT / WAVE; ++i) before = stream_add(before, sums[i]);
   }
   if (threadIdx.x == 0) upto[0] = 0;
   __syncthreads();
@@ -1434,7 +1435,7 @@ __global__ __launch_bounds__(64 * STREAM_GROUP, (stream_groups<T, DP>())) void s
     return clear_rest(a, a.out, a.so, a.H, a.d * (int)sizeof(T), a.lse, (int)blockIdx.x - a.main, a.rest);
   if (!a.upto) stream_scan<64 * NW>(a, scan.upto, &scan);
   const int* upto = a.upto ? a.upto : scan.upto;
-  const int work = __builtin_amdgcn_readfirstlane(upto[a.B]), run = max(a.share, (work + a.waves - 1) / a.waves);
+  const int work = __builtin_amdgcn_readfirstlane(upto[a.B]), run = stream_run(work, a.waves, a.share);
   const int me = blockIdx.x * NW + wave, cmax = a.d * (int)sizeof(T) / 16 - 1;
   const int t0 = min(work, me * run), t1 = min(work, t0 + run);
   char *const kt_lds = lds + wave * WB, *const vt_lds = kt_lds + TB;
@@ -1447,8 +1448,8 @@ __global__ __launch_bounds__(64 * STREAM_GROUP, (stream_groups<T, DP>())) void s
     const int qlen = seq.qlen, klen = seq.klen, off = klen - qlen;
     const StreamItem it(a, seq);
     const KeyTiles& kt = it.kt;
-    const int local = t - __builtin_amdgcn_readfirstlane(upto[b]), item = local / it.units, u0 = local - item * it.units;
-    const int u1 = min(it.units, u0 + (t1 - t)), hk = item % a.Hk, r0 = 32 * (item / a.Hk);
+    const StreamTake take(t, t1, __builtin_amdgcn_readfirstlane(upto[b]), it.units);
+    const int u0 = take.u0, u1 = take.u1, hk = take.item % a.Hk, r0 = 32 * (take.item / a.Hk);
     const int i0 = u0 * a.unit, i1 = min(kt.total, u1 * a.unit);
     const int rows = a.G * qlen, row = min(r0 + n, rows - 1), tok = row / a.G, h = hk * a.G + row % a.G;
     const char* qb = a.q + seq.at(a, a.sq);
@@ -1517,9 +1518,8 @@ __global__ __launch_bounds__(64 * STREAM_GROUP, (stream_groups<T, DP>())) void s
       if (whole) store_lane2<T>(a.out + seq.at(a, a.so) + (int64_t)(hk * a.G + r % a.G) * a.so.h + (int64_t)(r / a.G) * a.so.l, x, a.d, lane);
       else store_lane2<float>(reinterpret_cast<char*>(a.part + (part + i) * a.d), x, a.d, lane);
     }
-    // the item began in the run before this one, there as its first item or a later one
-    if (t == t0 && u0 > 0 && u0 <= run)
-      join = {seq.first, r0, min(32, rows - r0), hk * a.G, 2 * (me - 1) + (u0 < run ? 1 : 0), 2 + (it.units - u0 - 1) / run};
+    const StreamParts p(me, u0, it.units, run, work - t);
+    if (t == t0 && p.begins) join = {seq.first, r0, min(32, rows - r0), hk * a.G, p.part, p.parts};
     t += u1 - u0;
   }
   if (lane == 0) a.joins[me] = join;

@@ -122,9 +122,8 @@ void split_keys(const lact_attention& w, int64_t groups, int64_t rows, int& spli
   }
 }
 
-// Fewest units of a wave's run, and the units of a batch, which are counted in 32 bits
+// Fewest units of a wave's run
 constexpr int STREAM_SHARE = 2;
-constexpr int64_t STREAM_MOST = INT64_C(1) << 30;
 
 PagedPlan paged_plan(const lact_paged& p, const lact_attention& w) {
   PagedPlan x;
@@ -149,7 +148,7 @@ PagedPlan paged_plan(const lact_paged& p, const lact_attention& w) {
     // no more workgroups than run at once, nor than have a share of the tiles that there can be
     const int64_t items = x.items = std::min((int64_t)w.batch * ceil_div(G * x.few, 32), p.tokens * ceil_div(G, 32)) * w.kv_heads;
     const int64_t tiles = ceil_div(few_keys(f), 32) + 2;  // the sinks' and the window's may be cut anew
-    while (items * ceil_div(tiles, x.unit) > STREAM_MOST && x.unit < tiles) x.unit *= 2;
+    x.unit = stream_unit(items, tiles);
     x.few_grid = std::min(room, ceil_div(items, STREAM_GROUP * STREAM_SHARE) * tiles);
     x.waves = (int)(x.few_grid * STREAM_GROUP);
     x.rows = (int)std::min<int64_t>(32, G * x.few);
