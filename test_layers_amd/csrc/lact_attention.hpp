@@ -1943,8 +1943,10 @@ __global__ __launch_bounds__(256, (attn_back_waves<T, DP>())) void attn_dkv_kern
     // split sink tiles of all sequences, then the tiles by slots, early keys first: most rows see them
     int id = blockIdx.x;
     if (id >= a.main) {
-      clear_rest(a, a.dk, a.sdk, a.Hk, a.d * (int)sizeof(T), nullptr, id - a.main, a.rest);
-      return clear_rest(a, a.dv, a.sdv, a.Hk, a.d * (int)sizeof(T), nullptr, id - a.main, a.rest);
+#pragma unroll 1  // (once in the code: twice, fp32 dk, dv of 12 (4) heads of 96 took 274 us for 263)
+      for (int i = 0; i < 2; ++i)
+        clear_rest(a, i ? a.dv : a.dk, i ? a.sdv : a.sdk, a.Hk, a.d * (int)sizeof(T), nullptr, id - a.main, a.rest);
+      return;
     }
     hk = id % a.Hk, id /= a.Hk;
     if (a.rs > 1) rpart = id % a.rs, id /= a.rs;
