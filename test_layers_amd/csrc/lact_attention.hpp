@@ -1433,8 +1433,14 @@ struct StreamJoin {
 constexpr int STREAM_GROUP = 4;  // waves of a workgroup
 template <typename T, int DP>
 constexpr bool stream_ring() { return sizeof(T) == 2 && DP > 64; }
+// Workgroups of a compute unit: what its LDS holds, except for bf16 heads of up
+// to 64, of which it would hold four and two are fastest.  Two, three, four of
+// them, us with the join: 96 requests of 2.1K to 8.2K keys, 32 (8) heads of 64, 219,
+// 233, 231; 400 of 1000 keys 144, 150, 159; 8 of 4000 keys 24.5, 25.7, 27.8; one of
+// 32768 keys 37.7, 39.8, 45.4, with window 2048 15.4, 15.5, 16.0; 32 requests of 16
+// heads with that window 64.8, 63.2, 67.2.
 template <typename T, int DP>
-constexpr int stream_groups() { return DP <= 64 ? 2 : 1; }  // workgroups of a compute unit, by LDS
+constexpr int stream_groups() { return DP <= 64 ? 2 : 1; }
 template <typename T, int DP>
 __global__ __launch_bounds__(64 * STREAM_GROUP, (stream_groups<T, DP>())) void stream_kernel(PagedArgs a) {
   using Tile = AttnTile<T, DP>;

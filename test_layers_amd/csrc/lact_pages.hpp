@@ -130,7 +130,9 @@ __device__ __forceinline__ void place_row(const SlotArgs& a, int t, int b, int f
 // 1024 or, of a launch of one, all.  All latency: the sums (two loads, two
 // barriers a sum), the table's or the free list's entry.  64 requests of one
 // token 4.0 us, 1024 requests with 32768 tokens 6.8 us (summed by one workgroup
-// and placed by others in a second launch 7.3 and 3.4).
+// and placed by others in a second launch 7.3 and 3.4).  One launch and two, of
+// rows as many as requests: 64 5.8 and 7.5 us, 256 6.4 and 8.4, 1000 8.2 and 9.9;
+// up to here 16 KB of LDS; with 64, 2000 11.3 and 13.5, 4096 17.8 and 20.0.
 constexpr int ONE_GROUP = 1024;  // requests
 __global__ __launch_bounds__(PLAN_THREADS) void slots_one_kernel(SlotArgs a) {
   __shared__ int first[ONE_GROUP], base[ONE_GROUP];

@@ -97,7 +97,11 @@ struct PagedPlan {
 // 512 rows, of up to 12000 keys: with splits of 48 tiles 519 us, of 16 540, none
 // 544; one of 512 rows among 64 of one: 352, none 400; 4 of 100: 189, none 493.
 // Beyond one round (8 of 1024 rows among 20) none is best: 946, and 1023 with a
-// quarter.
+// quarter.  The most keys are the caller's bound, and without one the table's
+// width: these figures are of tables two pages wider than the longest sequence.
+// With tables of 2, 4, 16 times the width and no bound less is split, in the end
+// nothing: 40 sequences 547, 540, 538 us (527 with a bound), one chunk among 64
+// 546, 636, 618 (508), 4 of 100 360, 490, 493 (196 - 204).
 void split_keys(const lact_attention& w, int64_t groups, int64_t rows, int& splits, int& chunk) {
   const bool fp32 = w.io_dtype == LACT_DTYPE_F32, wide = w.d > 64;
   const int64_t room = (fp32 && wide ? 1 : 2) * NCU;
@@ -122,7 +126,12 @@ void split_keys(const lact_attention& w, int64_t groups, int64_t rows, int& spli
   }
 }
 
-// Fewest units of a wave's run
+// Fewest units of a wave's run: with 1, 2, 4, 8, 16, us with the join, one request
+// of 16 heads of 64, window 2048, 15.1, 15.4, 17.2, 21.3, 29.3; 4 of 300 keys, 32 (8)
+// heads of 128, 15.9, 20.7, 23.8, 34.4, 51.8; 8 of 4000 keys 34.8, 34.4, 34.3, 36.9, 49.4;
+// 400 of 1000, 96 of 8192 and one of 32768 keys the same up to 8 (246, 376, 41).  So
+// few units are right; one would do as well as two, and better where all keys
+// are few.
 constexpr int STREAM_SHARE = 2;
 
 PagedPlan paged_plan(const lact_paged& p, const lact_attention& w) {
@@ -539,6 +548,7 @@ lact_status lact_page_slots(const lact_slots* p, const int64_t* lens, const int6
   if (one) {
     KernelTimer kt(LACT_K_PAGES, s);
     // `left` in place of `have` is written by the only workgroup that reads it
+    // (1024 requests, 32768 tokens: 45 us for 8)
     const unsigned grid = left == have ? 1 : (unsigned)std::max<int64_t>(1, ceil_div(p->tokens, PLAN_THREADS));
     LACT_LAUNCH(slots_one_kernel, dim3(grid), dim3(PLAN_THREADS), s, a);
   } else {
